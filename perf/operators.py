@@ -268,6 +268,8 @@ def _plain_distill(s):
     loss = torch.where(t > 0, t * (log_t - log_q), 0.0).sum(1, keepdim=True)
     if c["tail"] == "bucket":
         t_tail = (1.0 - t.sum(1, keepdim=True)).clamp(min=0.0)
+        # with no tail in the student, the teacher's is rounding
+        t_tail = torch.where((q_tail > 0) | (t_tail > 2.0**-16), t_tail, 0.0)
         loss = loss + torch.where(t_tail > 0, t_tail * (t_tail.log() - q_tail.log()), 0.0)
     else:
         t_tail = torch.zeros_like(q_tail)
@@ -423,6 +425,7 @@ def _exact_distill(s):
         if c["tail"] == "bucket":
             rest = (1.0 - mass).clamp(min=0.0)
             log_rest = torch.logsumexp(log_q.masked_fill(named, NEG_INF), 1, keepdim=True)
+            rest = torch.where((log_rest > NEG_INF) | (rest > 2.0**-16), rest, 0.0)
             loss = loss + torch.where(rest > 0, torch.special.xlogy(rest, rest) - rest * log_rest, 0.0)
             # the bucket's mass, spread as the student spreads it, makes the same gradient
             spread = rest * (log_q - log_rest).exp()
