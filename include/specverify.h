@@ -81,6 +81,12 @@ typedef enum {
 
 typedef enum { SPEC_OP_LINEAR = 0, SPEC_OP_TREE = 1 } spec_op;
 
+/* What a teacher's top-K log probabilities stand for (spec_distill_topk). */
+typedef enum {
+    SPEC_TAIL_RENORM = 0, /* the whole teacher: renormalised over the K tokens */
+    SPEC_TAIL_BUCKET = 1  /* a part of it: what is left of 1 is one bucket over all other tokens */
+} spec_tail_mode;
+
 /* Philox purposes (counter word 2, low byte). */
 #define SPEC_PURPOSE_ACCEPT 1
 #define SPEC_PURPOSE_RESIDUAL 2
@@ -95,6 +101,7 @@ typedef enum { SPEC_OP_LINEAR = 0, SPEC_OP_TREE = 1 } spec_op;
 #define SPEC_DEVERR_LENGTH 8     /* compaction: accepted length or source row out of range */
 #define SPEC_DEVERR_TIMEOUT 16   /* a wait for a bulk copy ran out (2 s); the rows it left were
                                     recomputed by the two-pass route, so the results stand */
+#define SPEC_DEVERR_CAPACITY 32  /* cache blocks: the free list or a request's table row ran out */
 
 typedef struct {
     float temperature;  /* 0 => greedy (argmax, ties to the lowest index); > 0 => sampled */
@@ -371,6 +378,140 @@ spec_status spec_compact_accepted(const void* hidden, int B, int T, int H, const
 spec_status spec_sample_rows(const void* logits, spec_dtype dtype, int R, int V, const int64_t* request_ids,
                              const int64_t* positions, const spec_sampling_params* params, int32_t* out_tokens,
                              int32_t* dev_error, spec_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the top
+ * alternatives of every row: what a server answers with beside the emitted
+ * tokens, and what a target model hands to the training of its draft
+ * (spec_distill_topk).  With the target logits of a verification as
+ * [B * (k+1), V] and its out_tokens as [B * (k+1)], every emitted token is
+ * scored by the row that emitted it and the -1 entries cost nothing.
+ *
+ *  logits       R rows of V elements; row r starts row_stride * r elements
+ *               after logits (row_stride >= V; rows need not be aligned).
+ *  tokens       [R] int32 or NULL (no given tokens).  A row whose token is
+ *               -1 is skipped and not read.
+ *  temperature  T > 0: p = softmax(row / T), over the whole row.
+ *  top_k        0 .. min(V, 128).
+ *  logprob      [R] out: log p(token).  NULL only when tokens is NULL.
+ *  rank         [R] out or NULL: 1 + the number of v before the token in
+ *               (logit descending, index ascending) order.
+ *  entropy      [R] out or NULL: -sum p log p, in nats.
+ *  top_ids, top_logprobs  [R, top_k] out: the first top_k tokens in that
+ *               order and log p of each (-inf where the logit is).
+ *  A skipped row gets logprob 0, entropy 0, rank -1, top_ids -1 and
+ *  top_logprobs -inf.  A token outside [0, V) other than -1
+ *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it
+ *  (SPEC_DEVERR_NONFINITE) gives the same, with logprob -inf.  With tokens
+ *  NULL, logprob (if given) is 0 and rank -1 in every row.
+ *  R == 0 is valid and enqueues only the clearing of dev_error.
+ *  Limits: V <= 524,280, top_k <= 128 (SPEC_ERR_UNSUPPORTED above).
+ */
+spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int V, int64_t row_stride,
+                                const int32_t* tokens, float temperature, int top_k, float* logprob, int32_t* rank,
+                                float* entropy, int32_t* top_ids, float* top_logprobs, int32_t* dev_error,
+                                spec_stream_t stream);
+
+/*
+ * Distillation of a draft model from a teacher's top-K log probabilities:
+ * the loss of every row and, in the same call, its gradient.
+ *
+ *  student          R rows of V logits, as in spec_token_logprobs.
+ *  teacher_ids      [R, K] int32: distinct tokens; -1 marks an absent entry.
+ *  teacher_logprobs [R, K] float: l_j (any constant may be added under
+ *                   SPEC_TAIL_RENORM); -inf counts as probability zero.
+ *  weights          [R] or NULL (=> 1): a row of weight 0 is not read and
+ *                   has loss 0 and gradient 0.
+ *  temperature      T > 0 of the student: q = softmax(row / T).
+ *  With t_j = exp(l_j), M = sum t_j and q_T = sum of q over the tokens not
+ *  listed:
+ *    SPEC_TAIL_RENORM: t_j <- t_j / M,  t_T = 0   (M = 0: loss 0, gradient 0)
+ *    SPEC_TAIL_BUCKET: t_T = max(0, 1 - M), and 0 where q_T = 0 and 1 - M
+                      <= 2^-16 (the rounding of the l_j)
+ *    loss = sum_j t_j (log t_j - log q_j) + t_T (log t_T - log q_T), terms
+ *    with t = 0 being 0, and q_T summed over the tail itself, never as
+ *    1 - sum q_j.
+ *  loss       [R] out, not multiplied by the weight.
+ *  row_stats  [R, 8] out or NULL: what spec_distill_topk_backward needs.
+ *  grad       R rows of V elements of student's type, grad_stride apart, or
+ *             NULL: d(sum_r weights[r] loss[r]) / d student,
+ *               listed tokens   w (S q_j - t_j) / T
+ *               other tokens    w (S q_T - t_T) / T * q_v / q_T
+ *             with S = sum t_j + t_T; may be student's own buffer.
+ *  An id outside [0, V) other than -1, or one listed twice
+ *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it,
+ *  a NaN or +inf teacher value of a listed token (SPEC_DEVERR_NONFINITE):
+ *  the row has loss 0 and gradient 0.  A listed token of t_j > 0 whose
+ *  student logit is -inf makes the loss +inf; the gradient stays finite.
+ *  R == 0 is valid.  Limits: 1 <= K <= 128, V <= 524,280.
+ */
+spec_status spec_distill_topk(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,
+                              const int32_t* teacher_ids, const float* teacher_logprobs, int K, const float* weights,
+                              float temperature, spec_tail_mode tail, float* loss, float* row_stats, void* grad,
+                              int64_t grad_stride, int32_t* dev_error, spec_stream_t stream);
+
+/*
+ * The gradient of spec_distill_topk for upstream gradients that are known
+ * only after the losses: grad = grad_loss[r] * d loss[r] / d student, from
+ * the row_stats that call wrote for the same student, teacher_ids,
+ * teacher_logprobs, temperature and tail.  grad_loss [R] or NULL (=> 1); a
+ * row with grad_loss 0, or one the first call skipped or refused, has
+ * gradient 0 and is not read.  grad may be student's own buffer.
+ */
+spec_status spec_distill_topk_backward(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,
+                                       const int32_t* teacher_ids, const float* teacher_logprobs, int K,
+                                       const float* row_stats, const float* grad_loss, float temperature, void* grad,
+                                       int64_t grad_stride, spec_stream_t stream);
+
+/*
+ * The cache slots of the next step, from the lengths of the last one: the
+ * accepted tokens of a verification become part of every request's
+ * sequence, requests that need them get cache blocks from a free list, and
+ * every new token gets its slot.
+ *
+ *  seq_lens      [B] tokens of each request in the cache before the last
+ *                step; accepted_len [B] a_b of that step (spec_verify_linear)
+ *                or NULL: len_b = seq_lens[b] + a_b + 1 (NULL: seq_lens[b]).
+ *                The last step fed its last token and the k drafts, so a_b
+ *                accepted drafts leave a_b + 1 valid entries.  a_b = -1
+ *                keeps the length.
+ *  new_tokens    [B] n_b >= 0: tokens that the next step feeds.
+ *  block_table   [B, max_blocks], rows table_stride apart, in/out: block j
+ *                of request b holds its positions j * page_size ...; only
+ *                the entries held[b] .. out_held[b] - 1 are written.
+ *  held          [B] blocks each request has.
+ *  free_blocks   the free list, a stack of *free_count <= free_capacity
+ *                entries; read only.
+ *  Request b needs max(held, ceil((len_b + n_b) / page_size)) blocks.  In
+ *  request order, each takes what it lacks from the end of the free list:
+ *  it is served iff all that it and the requests before it lack fits in
+ *  *free_count.
+ *  out_seq_lens [B] len_b, out_held [B], out_free_count [1]: the state for
+ *  the next call; distinct from the input buffers.
+ *  cu_tokens [B+1]: cu_tokens[0] = 0, cu_tokens[b+1] = cu_tokens[b] + n_b.
+ *  slots     [max_tokens] int64: token i of request b is at
+ *            slots[cu_tokens[b] + i] = block * page_size + offset of
+ *            position len_b + i; positions [max_tokens] int32 that position
+ *            (NULL: not written).  Entries past cu_tokens[B] get slot -1 and
+ *            position 0.
+ *  A request that is not served, or needs more than max_blocks blocks
+ *  (SPEC_DEVERR_CAPACITY; it then lacks nothing in the rule above), keeps its
+ *  blocks and its new tokens get slot -1.  seq_lens, held or new_tokens
+ *  negative, accepted_len below -1, held above max_blocks, len_b above
+ *  held * page_size or len_b + n_b above 2^31 - 1 (SPEC_DEVERR_LENGTH): the request keeps seq_lens[b] and
+ *  held[b] and its new tokens (negative: none) get slot -1 and position 0.
+ *  More than max_tokens new tokens set SPEC_DEVERR_LENGTH too; those past the
+ *  end are not written.  A *free_count outside 0 .. free_capacity sets it
+ *  and counts as 0.
+ *  Limits: 1 <= B <= 16384, B * max_blocks < 2^31 (SPEC_ERR_UNSUPPORTED
+ *  above), the sum of new_tokens below 2^31.
+ */
+spec_status spec_advance_blocks(const int32_t* seq_lens, const int32_t* accepted_len, const int32_t* new_tokens,
+                                int B, int page_size, int32_t* block_table, int max_blocks, int64_t table_stride,
+                                const int32_t* held, const int32_t* free_blocks, int free_capacity,
+                                const int32_t* free_count, int32_t* out_seq_lens, int32_t* out_held, int32_t* out_free_count,
+                                int32_t* cu_tokens, int64_t* slots, int32_t* positions, int max_tokens,
+                                int32_t* dev_error, spec_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* spec_status_string(spec_status status);

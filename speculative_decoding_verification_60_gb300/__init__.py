@@ -9,6 +9,7 @@ from ._binding import (  # noqa: F401
     CHILD_DETERMINISTIC,
     CHILD_IID,
     CHILD_WOR,
+    DEVERR_CAPACITY,
     DEVERR_LENGTH,
     DEVERR_NONFINITE,
     DEVERR_PARENT,
@@ -17,12 +18,18 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     SPEC_OP_LINEAR,
     SPEC_OP_TREE,
+    TAIL_BUCKET,
+    TAIL_RENORM,
     SamplingParams,
     SpecError,
+    advance_blocks,
     compact_accepted,
+    distill_topk,
+    distill_topk_backward,
     load,
     sample_rows,
     status_string,
+    token_logprobs,
     verify_linear,
     verify_linear_compact,
     verify_tree,

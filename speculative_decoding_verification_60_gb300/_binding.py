@@ -20,13 +20,15 @@ SPEC_OK = 0
 SPEC_BF16, SPEC_F32 = 0, 1
 SPEC_OP_LINEAR, SPEC_OP_TREE = 0, 1
 CHILD_WOR, CHILD_IID, CHILD_DETERMINISTIC = 0, 1, 2
-DEVERR_TOKEN, DEVERR_NONFINITE, DEVERR_PARENT, DEVERR_LENGTH = 1, 2, 4, 8
+DEVERR_TOKEN, DEVERR_NONFINITE, DEVERR_PARENT, DEVERR_LENGTH, DEVERR_CAPACITY = 1, 2, 4, 8, 32
+TAIL_RENORM, TAIL_BUCKET = 0, 1
 
 # Every symbol declared in include/specverify.h.
 EXPORTS = ("spec_workspace_size", "spec_verify_linear", "spec_verify_linear_compact", "spec_linear_stats_decide",
            "spec_linear_draw", "spec_verify_linear_noalloc", "spec_verify_tree", "spec_verify_tree_dynamic",
            "spec_compact_accepted",
-           "spec_sample_rows", "spec_status_string")
+           "spec_sample_rows", "spec_token_logprobs", "spec_distill_topk", "spec_distill_topk_backward",
+           "spec_advance_blocks", "spec_status_string")
 
 
 class SamplingParams(ctypes.Structure):
@@ -80,6 +82,15 @@ def load() -> ctypes.CDLL:
     lib.spec_compact_accepted.restype = I
     lib.spec_sample_rows.argtypes = [P, I, I, I, P, P, ctypes.POINTER(SamplingParams), P, P, P]
     lib.spec_sample_rows.restype = I
+    L, F = ctypes.c_int64, ctypes.c_float
+    lib.spec_token_logprobs.argtypes = [P, I, I, I, L, P, F, I, P, P, P, P, P, P, P]
+    lib.spec_token_logprobs.restype = I
+    lib.spec_distill_topk.argtypes = [P, I, I, I, L, P, P, I, P, F, I, P, P, P, L, P, P]
+    lib.spec_distill_topk.restype = I
+    lib.spec_distill_topk_backward.argtypes = [P, I, I, I, L, P, P, I, P, P, F, P, L, P]
+    lib.spec_distill_topk_backward.restype = I
+    lib.spec_advance_blocks.argtypes = [P, P, P, I, I, P, I, L, P, P, I, P, P, P, P, P, P, P, I, P, P]
+    lib.spec_advance_blocks.restype = I
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -332,4 +343,212 @@ def sample_rows(logits, temperature: float, top_p: float = 1.0, seed: int = 0, r
                               _ptr(out["out_tokens"]), _ptr(out.get("dev_error")), _stream(stream))
     if st != SPEC_OK:
         raise SpecError("spec_sample_rows", st)
+    return out
+
+
+def _rows(t, name):
+    """(R, V, row stride) of a tensor [..., V] whose rows are contiguous and
+    evenly spaced (a slice of a wider buffer counts)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2:
+        raise ValueError(f"{name} must have shape [..., V], got {tuple(shape)}")
+    V = shape[-1]
+    if V > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    R, step = 1, None
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n > 1:
+            if step is None:
+                step = s
+            elif s != step * R:
+                raise ValueError(f"{name} must have evenly spaced rows")
+        R *= n
+    if step is None:
+        step = V
+    if step < V:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return R, V, step
+
+
+class _On:
+    """Stream of a call: the given one, or the current one of the tensor's
+    device.  With a given stream, outputs are allocated on it and `use` marks
+    the caller's tensors as used there, so that the allocator does not hand
+    their memory on before the call's work is done."""
+
+    def __init__(self, stream, t):
+        self.given = stream
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+
+    def empty(self, *shape, dtype, device):
+        if self.given is None:
+            return torch.empty(*shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.given):
+            return torch.empty(*shape, dtype=dtype, device=device)
+
+    def use(self, *tensors):
+        if self.given is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.given)
+
+    @property
+    def handle(self):
+        return self.stream.cuda_stream
+
+
+def _out(out, key, dtype, shape, on, device):
+    """Entry `key` of the outputs: the caller's, checked, or a new tensor."""
+    t = out.get(key)
+    if t is None:
+        t = out[key] = on.empty(*shape, dtype=dtype, device=device)
+    else:
+        _check(t, key, dtype, shape)
+        on.use(t)
+    return t.data_ptr()
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def token_logprobs(logits, tokens=None, temperature: float = 1.0, top_k: int = 0, out=None, stream=None) -> dict:
+    """``spec_token_logprobs`` on torch tensors: log probability, rank and
+    entropy for one token per row of logits [..., V] (bf16 or fp32; rows may
+    be slices of a wider buffer), and the row's top_k alternatives.  tokens
+    int32 of logits' leading shape, -1 skipping a row, or None (entropy and
+    alternatives only).  With logits = target [B, k+1, V] and tokens =
+    out_tokens of a verification, every emitted token is scored.  Returns a
+    dict of device tensors in the leading shape: logprob, rank, entropy,
+    top_ids and top_logprobs [..., top_k], dev_error [1]; tensors given in
+    out are written in place."""
+    lib = load()
+    dt = _dtype_code(logits)
+    R, V, step = _rows(logits, "logits")
+    lead, dev = tuple(logits.shape[:-1]), logits.device
+    _check(tokens, "tokens", torch.int32, lead)
+    on = _On(stream, logits)
+    on.use(logits, tokens)
+    out = {} if out is None else out
+    K = int(top_k)
+    wide = (*lead, max(K, 0))
+    st = lib.spec_token_logprobs(
+        logits.data_ptr(), dt, R, V, step, _data(tokens), float(temperature), K,
+        _out(out, "logprob", torch.float32, lead, on, dev), _out(out, "rank", torch.int32, lead, on, dev),
+        _out(out, "entropy", torch.float32, lead, on, dev), _out(out, "top_ids", torch.int32, wide, on, dev),
+        _out(out, "top_logprobs", torch.float32, wide, on, dev), _out(out, "dev_error", torch.int32, (1,), on, dev),
+        on.handle)
+    if st != SPEC_OK:
+        raise SpecError("spec_token_logprobs", st)
+    return out
+
+
+def _grad_rows(out, student, V, on):
+    """The gradient tensor of a call: the caller's (student's own counts), checked, or a new one."""
+    grad = out.get("grad")
+    if grad is None:
+        grad = out["grad"] = on.empty(*student.shape, dtype=student.dtype, device=student.device)
+    if grad.dtype != student.dtype or grad.shape != student.shape:
+        raise ValueError(f"grad must be {student.dtype} of shape {tuple(student.shape)}")
+    on.use(grad)
+    return grad.data_ptr(), _rows(grad, "grad")[2]
+
+
+def distill_topk(student, teacher_ids, teacher_logprobs, weights=None, temperature: float = 1.0,
+                 tail: int = TAIL_BUCKET, with_grad: bool = True, out=None, stream=None) -> dict:
+    """``spec_distill_topk`` on torch tensors: the distillation loss of every
+    row of student logits [..., V] (bf16 or fp32) against a teacher's top
+    log probabilities (teacher_ids int32 and teacher_logprobs float32 [...,
+    K], as token_logprobs returns them; id -1 = absent), and, with with_grad,
+    the gradient of sum(weights * loss) in the same pass.  weights float32 of
+    the leading shape or None.  Returns a dict: loss and grad, row_stats
+    [..., 8] (for distill_topk_backward), dev_error [1].  out["grad"] may be
+    the student tensor itself."""
+    lib = load()
+    dt = _dtype_code(student)
+    R, V, step = _rows(student, "student")
+    lead, dev = tuple(student.shape[:-1]), student.device
+    K = int(teacher_ids.shape[-1])
+    _check(teacher_ids, "teacher_ids", torch.int32, (*lead, K))
+    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K))
+    _check(weights, "weights", torch.float32, lead)
+    on = _On(stream, student)
+    on.use(student, teacher_ids, teacher_logprobs, weights)
+    out = {} if out is None else out
+    grad, grad_step = _grad_rows(out, student, V, on) if with_grad else (None, V)
+    st = lib.spec_distill_topk(
+        student.data_ptr(), dt, R, V, step, teacher_ids.data_ptr(), teacher_logprobs.data_ptr(), K, _data(weights),
+        float(temperature), int(tail), _out(out, "loss", torch.float32, lead, on, dev),
+        _out(out, "row_stats", torch.float32, (*lead, 8), on, dev), grad, grad_step,
+        _out(out, "dev_error", torch.int32, (1,), on, dev), on.handle)
+    if st != SPEC_OK:
+        raise SpecError("spec_distill_topk", st)
+    return out
+
+
+def distill_topk_backward(student, teacher_ids, teacher_logprobs, row_stats, grad_loss=None,
+                          temperature: float = 1.0, out=None, stream=None) -> dict:
+    """``spec_distill_topk_backward``: the gradient of sum(grad_loss * loss)
+    from the row_stats of a distill_topk call on the same student, teacher,
+    temperature and tail.  grad_loss float32 of the leading shape or None (1).
+    Returns a dict with grad (out["grad"] may be the student tensor)."""
+    lib = load()
+    dt = _dtype_code(student)
+    R, V, step = _rows(student, "student")
+    lead = tuple(student.shape[:-1])
+    K = int(teacher_ids.shape[-1])
+    _check(teacher_ids, "teacher_ids", torch.int32, (*lead, K))
+    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K))
+    _check(row_stats, "row_stats", torch.float32, (*lead, 8))
+    _check(grad_loss, "grad_loss", torch.float32, lead)
+    on = _On(stream, student)
+    on.use(student, teacher_ids, teacher_logprobs, row_stats, grad_loss)
+    out = {} if out is None else out
+    grad, grad_step = _grad_rows(out, student, V, on)
+    st = lib.spec_distill_topk_backward(
+        student.data_ptr(), dt, R, V, step, teacher_ids.data_ptr(), teacher_logprobs.data_ptr(), K,
+        row_stats.data_ptr(), _data(grad_loss), float(temperature), grad, grad_step, on.handle)
+    if st != SPEC_OK:
+        raise SpecError("spec_distill_topk_backward", st)
+    return out
+
+
+def advance_blocks(seq_lens, new_tokens, block_table, held, free_blocks, free_count, page_size: int,
+                   max_tokens: int, accepted_len=None, out=None, stream=None) -> dict:
+    """``spec_advance_blocks`` on torch tensors: seq_lens, new_tokens, held
+    and accepted_len [B] int32 (accepted_len as verify_linear returns it, or
+    None), block_table [B, max_blocks] int32 (new entries written in place),
+    free_blocks [F] int32 with free_count [1] int32 entries in use.  Returns a
+    dict: seq_lens, held, free_count (the state for the next call),
+    cu_tokens [B+1], slots [max_tokens] int64, positions [max_tokens] int32,
+    dev_error [1]."""
+    lib = load()
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must have shape [B, max_blocks], got {tuple(block_table.shape)}")
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be {torch.int32}, got {block_table.dtype}")
+    B, M, step = _rows(block_table, "block_table")
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    _check(new_tokens, "new_tokens", torch.int32, (B,))
+    _check(held, "held", torch.int32, (B,))
+    _check(accepted_len, "accepted_len", torch.int32, (B,))
+    _check(free_blocks, "free_blocks", torch.int32, (free_blocks.numel(),))
+    _check(free_count, "free_count", torch.int32, (1,))
+    dev = block_table.device
+    on = _On(stream, block_table)
+    on.use(seq_lens, new_tokens, held, accepted_len, free_blocks, free_count, block_table)
+    out = {} if out is None else out
+    T = int(max_tokens)
+    room = max(T, 0)
+    st = lib.spec_advance_blocks(
+        seq_lens.data_ptr(), _data(accepted_len), new_tokens.data_ptr(), B, int(page_size), block_table.data_ptr(),
+        M, step, held.data_ptr(), _data(free_blocks), free_blocks.numel(), free_count.data_ptr(),
+        _out(out, "seq_lens", torch.int32, (B,), on, dev), _out(out, "held", torch.int32, (B,), on, dev),
+        _out(out, "free_count", torch.int32, (1,), on, dev), _out(out, "cu_tokens", torch.int32, (B + 1,), on, dev),
+        _out(out, "slots", torch.int64, (room,), on, dev), _out(out, "positions", torch.int32, (room,), on, dev), T,
+        _out(out, "dev_error", torch.int32, (1,), on, dev), on.handle)
+    if st != SPEC_OK:
+        raise SpecError("spec_advance_blocks", st)
     return out

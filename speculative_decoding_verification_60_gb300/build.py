@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
-SOURCES = ["api.cu", "linear.cu", "rows_topp.cu", "decide.cu", "draw_stream.cu", "tree.cu", "compact.cu", "sample_rows.cu"]
+SOURCES = ["api.cu", "linear.cu", "rows_topp.cu", "decide.cu", "draw_stream.cu", "tree.cu", "compact.cu", "sample_rows.cu",
+           "logprobs.cu", "distill.cu", "blocks.cu"]
 # threads per CTA of the row-level kernels in each unit (see common.cuh)
 CTA_THREADS = {"decide.cu": 512, "tree.cu": 512, "sample_rows.cu": 512}
 # units whose CTAs hold a copy warp beside the row threads: row barriers are
