@@ -372,46 +372,46 @@ def _rows(t, name):
     return R, V, step
 
 
-class _On:
-    """Stream of a call: the given one, or the current one of the tensor's
-    device.  With a given stream, outputs are allocated on it and `use` marks
-    the caller's tensors as used there, so that the allocator does not hand
-    their memory on before the call's work is done."""
-
-    def __init__(self, stream, t):
-        self.given = stream
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-
-    def empty(self, *shape, dtype, device):
-        if self.given is None:
-            return torch.empty(*shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(*shape, dtype=dtype, device=device)
-
-    def use(self, *tensors):
-        if self.given is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.given)
-
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
+def _inputs(device, *specs):
+    """Pointers of the inputs (tensor or None, name, dtype, shape), checked."""
+    ptrs = []
+    for t, name, dtype, shape in specs:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+            _check(t, name, dtype, shape)
+            raise ValueError(f"{name} must be on cuda:{device}")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
-def _out(out, key, dtype, shape, on, device):
-    """Entry `key` of the outputs: the caller's, checked, or a new tensor."""
-    t = out.get(key)
-    if t is None:
-        t = out[key] = on.empty(*shape, dtype=dtype, device=device)
-    else:
-        _check(t, key, dtype, shape)
-        on.use(t)
-    return t.data_ptr()
+def _outputs(out, device, stream, *specs):
+    """Pointers of the outputs (name, dtype, shape): the caller's tensor in
+    out, checked, or a new one, allocated on the call's stream."""
+    ptrs = []
+    for name, dtype, shape in specs:
+        t = out.get(name)
+        if t is None:
+            with torch.cuda.stream(stream):  # no effect for None
+                t = out[name] = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
+        elif t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+            _check(t, name, dtype, shape)
+            raise ValueError(f"{name} must be on cuda:{device}")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
-def _data(t):
-    return None if t is None else t.data_ptr()
+def _handle(stream, device, *tensors):
+    """The cudaStream_t of a call: the given stream's, or that of the tensors'
+    device's current one.  A given stream is marked as a user of the tensors,
+    so that their memory is not handed on before the call's work is done."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def token_logprobs(logits, tokens=None, temperature: float = 1.0, top_k: int = 0, out=None, stream=None) -> dict:
@@ -427,32 +427,28 @@ def token_logprobs(logits, tokens=None, temperature: float = 1.0, top_k: int = 0
     lib = load()
     dt = _dtype_code(logits)
     R, V, step = _rows(logits, "logits")
-    lead, dev = tuple(logits.shape[:-1]), logits.device
-    _check(tokens, "tokens", torch.int32, lead)
-    on = _On(stream, logits)
-    on.use(logits, tokens)
-    out = {} if out is None else out
-    K = int(top_k)
+    lead, device, K = logits.shape[:-1], logits.get_device(), int(top_k)
     wide = (*lead, max(K, 0))
-    st = lib.spec_token_logprobs(
-        logits.data_ptr(), dt, R, V, step, _data(tokens), float(temperature), K,
-        _out(out, "logprob", torch.float32, lead, on, dev), _out(out, "rank", torch.int32, lead, on, dev),
-        _out(out, "entropy", torch.float32, lead, on, dev), _out(out, "top_ids", torch.int32, wide, on, dev),
-        _out(out, "top_logprobs", torch.float32, wide, on, dev), _out(out, "dev_error", torch.int32, (1,), on, dev),
-        on.handle)
+    out = {} if out is None else out
+    (tok,) = _inputs(device, (tokens, "tokens", torch.int32, lead))
+    ptrs = _outputs(out, device, stream, ("logprob", torch.float32, lead), ("rank", torch.int32, lead),
+                    ("entropy", torch.float32, lead), ("top_ids", torch.int32, wide),
+                    ("top_logprobs", torch.float32, wide), ("dev_error", torch.int32, (1,)))
+    st = lib.spec_token_logprobs(logits.data_ptr(), dt, R, V, step, tok, temperature, K, *ptrs,
+                                 _handle(stream, device, logits, tokens, *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_token_logprobs", st)
     return out
 
 
-def _grad_rows(out, student, V, on):
-    """The gradient tensor of a call: the caller's (student's own counts), checked, or a new one."""
+def _grad_rows(out, student, stream):
+    """Pointer and row stride of the gradient: the caller's tensor (student's own counts), checked, or a new one."""
     grad = out.get("grad")
     if grad is None:
-        grad = out["grad"] = on.empty(*student.shape, dtype=student.dtype, device=student.device)
-    if grad.dtype != student.dtype or grad.shape != student.shape:
-        raise ValueError(f"grad must be {student.dtype} of shape {tuple(student.shape)}")
-    on.use(grad)
+        with torch.cuda.stream(stream):
+            grad = out["grad"] = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+    if grad.dtype is not student.dtype or grad.shape != student.shape or grad.get_device() != student.get_device():
+        raise ValueError(f"grad must be {student.dtype} of shape {tuple(student.shape)} on {student.device}")
     return grad.data_ptr(), _rows(grad, "grad")[2]
 
 
@@ -469,20 +465,17 @@ def distill_topk(student, teacher_ids, teacher_logprobs, weights=None, temperatu
     lib = load()
     dt = _dtype_code(student)
     R, V, step = _rows(student, "student")
-    lead, dev = tuple(student.shape[:-1]), student.device
-    K = int(teacher_ids.shape[-1])
-    _check(teacher_ids, "teacher_ids", torch.int32, (*lead, K))
-    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K))
-    _check(weights, "weights", torch.float32, lead)
-    on = _On(stream, student)
-    on.use(student, teacher_ids, teacher_logprobs, weights)
+    lead, device, K = student.shape[:-1], student.get_device(), teacher_ids.shape[-1]
     out = {} if out is None else out
-    grad, grad_step = _grad_rows(out, student, V, on) if with_grad else (None, V)
-    st = lib.spec_distill_topk(
-        student.data_ptr(), dt, R, V, step, teacher_ids.data_ptr(), teacher_logprobs.data_ptr(), K, _data(weights),
-        float(temperature), int(tail), _out(out, "loss", torch.float32, lead, on, dev),
-        _out(out, "row_stats", torch.float32, (*lead, 8), on, dev), grad, grad_step,
-        _out(out, "dev_error", torch.int32, (1,), on, dev), on.handle)
+    ids, lps, w = _inputs(device, (teacher_ids, "teacher_ids", torch.int32, (*lead, K)),
+                          (teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K)),
+                          (weights, "weights", torch.float32, lead))
+    loss, stats, err = _outputs(out, device, stream, ("loss", torch.float32, lead),
+                                ("row_stats", torch.float32, (*lead, 8)), ("dev_error", torch.int32, (1,)))
+    grad, grad_step = _grad_rows(out, student, stream) if with_grad else (None, V)
+    st = lib.spec_distill_topk(student.data_ptr(), dt, R, V, step, ids, lps, K, w, temperature, int(tail), loss, stats,
+                               grad, grad_step, err,
+                               _handle(stream, device, student, teacher_ids, teacher_logprobs, weights, *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_distill_topk", st)
     return out
@@ -497,19 +490,16 @@ def distill_topk_backward(student, teacher_ids, teacher_logprobs, row_stats, gra
     lib = load()
     dt = _dtype_code(student)
     R, V, step = _rows(student, "student")
-    lead = tuple(student.shape[:-1])
-    K = int(teacher_ids.shape[-1])
-    _check(teacher_ids, "teacher_ids", torch.int32, (*lead, K))
-    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K))
-    _check(row_stats, "row_stats", torch.float32, (*lead, 8))
-    _check(grad_loss, "grad_loss", torch.float32, lead)
-    on = _On(stream, student)
-    on.use(student, teacher_ids, teacher_logprobs, row_stats, grad_loss)
+    lead, device, K = student.shape[:-1], student.get_device(), teacher_ids.shape[-1]
     out = {} if out is None else out
-    grad, grad_step = _grad_rows(out, student, V, on)
+    ids, lps, stats, g = _inputs(device, (teacher_ids, "teacher_ids", torch.int32, (*lead, K)),
+                                 (teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K)),
+                                 (row_stats, "row_stats", torch.float32, (*lead, 8)),
+                                 (grad_loss, "grad_loss", torch.float32, lead))
+    grad, grad_step = _grad_rows(out, student, stream)
     st = lib.spec_distill_topk_backward(
-        student.data_ptr(), dt, R, V, step, teacher_ids.data_ptr(), teacher_logprobs.data_ptr(), K,
-        row_stats.data_ptr(), _data(grad_loss), float(temperature), grad, grad_step, on.handle)
+        student.data_ptr(), dt, R, V, step, ids, lps, K, stats, g, temperature, grad, grad_step,
+        _handle(stream, device, student, teacher_ids, teacher_logprobs, row_stats, grad_loss, out["grad"]))
     if st != SPEC_OK:
         raise SpecError("spec_distill_topk_backward", st)
     return out
@@ -530,25 +520,20 @@ def advance_blocks(seq_lens, new_tokens, block_table, held, free_blocks, free_co
     if block_table.dtype != torch.int32:
         raise TypeError(f"block_table must be {torch.int32}, got {block_table.dtype}")
     B, M, step = _rows(block_table, "block_table")
-    _check(seq_lens, "seq_lens", torch.int32, (B,))
-    _check(new_tokens, "new_tokens", torch.int32, (B,))
-    _check(held, "held", torch.int32, (B,))
-    _check(accepted_len, "accepted_len", torch.int32, (B,))
-    _check(free_blocks, "free_blocks", torch.int32, (free_blocks.numel(),))
-    _check(free_count, "free_count", torch.int32, (1,))
-    dev = block_table.device
-    on = _On(stream, block_table)
-    on.use(seq_lens, new_tokens, held, accepted_len, free_blocks, free_count, block_table)
+    device, T, F = block_table.get_device(), int(max_tokens), free_blocks.numel()
     out = {} if out is None else out
-    T = int(max_tokens)
-    room = max(T, 0)
+    i32, room = torch.int32, max(T, 0)
+    lens, acc, new, have, free, count = _inputs(
+        device, (seq_lens, "seq_lens", i32, (B,)), (accepted_len, "accepted_len", i32, (B,)),
+        (new_tokens, "new_tokens", i32, (B,)), (held, "held", i32, (B,)), (free_blocks, "free_blocks", i32, (F,)),
+        (free_count, "free_count", i32, (1,)))
+    ptrs = _outputs(out, device, stream, ("seq_lens", i32, (B,)), ("held", i32, (B,)), ("free_count", i32, (1,)),
+                    ("cu_tokens", i32, (B + 1,)), ("slots", torch.int64, (room,)), ("positions", i32, (room,)),
+                    ("dev_error", i32, (1,)))
     st = lib.spec_advance_blocks(
-        seq_lens.data_ptr(), _data(accepted_len), new_tokens.data_ptr(), B, int(page_size), block_table.data_ptr(),
-        M, step, held.data_ptr(), _data(free_blocks), free_blocks.numel(), free_count.data_ptr(),
-        _out(out, "seq_lens", torch.int32, (B,), on, dev), _out(out, "held", torch.int32, (B,), on, dev),
-        _out(out, "free_count", torch.int32, (1,), on, dev), _out(out, "cu_tokens", torch.int32, (B + 1,), on, dev),
-        _out(out, "slots", torch.int64, (room,), on, dev), _out(out, "positions", torch.int32, (room,), on, dev), T,
-        _out(out, "dev_error", torch.int32, (1,), on, dev), on.handle)
+        lens, acc, new, B, int(page_size), block_table.data_ptr(), M, step, have, free, F, count, *ptrs[:6], T, ptrs[6],
+        _handle(stream, device, seq_lens, accepted_len, new_tokens, block_table, held, free_blocks, free_count,
+                *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_advance_blocks", st)
     return out

@@ -19,6 +19,95 @@ constexpr float kLn2 = 0.69314718055994531f;
 // is -inf (weight zero), where -inf minus -inf would be NaN.
 constexpr float kNoMax = -3.4028234663852886e38f;
 
+// Maximum over a warp; NaN is passed over.
+__device__ __forceinline__ float warp_max_redux(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// The next value of T below x; NaN below -inf.
+template <typename T> __device__ __forceinline__ float next_below(float x);
+template <> __device__ __forceinline__ float next_below<float>(float x) {
+    const uint32_t b = __float_as_uint(x == 0.0f ? -0.0f : x);
+    return __uint_as_float((b & 0x80000000u) ? b + 1u : b - 1u);
+}
+template <> __device__ __forceinline__ float next_below<__nv_bfloat16>(float x) {
+    const uint32_t b = __float_as_uint(x == 0.0f ? -0.0f : x);
+    return __uint_as_float((b & 0x80000000u) ? b + 0x10000u : b - 0x10000u);
+}
+
+// A 16-byte vector of T as pairs of floats, its maximum (NaN passed over),
+// the number of its elements that are not <= a bound, and the vector that
+// stands for no elements.
+template <typename T> struct RowVec;
+template <> struct RowVec<__nv_bfloat16> {
+    static constexpr int kPairs = 4;
+    __device__ static __forceinline__ __nv_bfloat162 word(const uint4& q, int i) {
+        uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+        return *reinterpret_cast<__nv_bfloat162*>(&w);
+    }
+    // pair i with values below `least` raised to it (NaN stays)
+    __device__ static __forceinline__ float2 pair_above(const uint4& q, int i, __nv_bfloat162 least) {
+        const __nv_bfloat162 h = __hmax2_nan(word(q, i), least);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+        return make_float2(bf16_lo(w), bf16_hi(w));
+    }
+    using Least = __nv_bfloat162;
+    __device__ static __forceinline__ Least least(float x) { return __float2bfloat162_rn(x); }
+    // Elements above the bound, counted in bf16 halves: exact up to 256 each.
+    using Count = __nv_bfloat162;
+    __device__ static __forceinline__ Count count_zero() { return __float2bfloat162_rn(0.0f); }
+    __device__ static __forceinline__ void count(Count& n, const uint4& q, Least bound) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) n = __hadd2(n, __hgtu2(word(q, i), bound));
+    }
+    __device__ static __forceinline__ int count_sum(Count n) { return (int)(__low2float(n) + __high2float(n)); }
+    __device__ static __forceinline__ float2 pair(const uint4& q, int i) {
+        const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+        return make_float2(bf16_lo(w), bf16_hi(w));
+    }
+    __device__ static __forceinline__ float max(const uint4& q) {
+        auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ static __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+};
+template <> struct RowVec<float> {
+    static constexpr int kPairs = 2;
+    using Least = float;
+    __device__ static __forceinline__ Least least(float x) { return x; }
+    __device__ static __forceinline__ float2 pair_above(const uint4& q, int i, float least) {
+        const float2 x = pair(q, i);
+        return make_float2(max_nan(x.x, least), max_nan(x.y, least));
+    }
+    using Count = int;
+    __device__ static __forceinline__ Count count_zero() { return 0; }
+    __device__ static __forceinline__ void count(Count& n, const uint4& q, float bound) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const float2 x = pair(q, i);
+            n += !(x.x <= bound);
+            n += !(x.y <= bound);
+        }
+    }
+    __device__ static __forceinline__ int count_sum(Count n) { return n; }
+    __device__ static __forceinline__ float2 pair(const uint4& q, int i) {
+        return i == 0 ? make_float2(__uint_as_float(q.x), __uint_as_float(q.y))
+                      : make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+    __device__ static __forceinline__ float max(const uint4& q) {
+        return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+    }
+    __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+};
+
 // (logit descending, index ascending) as one integer: larger = earlier.
 // Zero is below every entry's key.
 __device__ __forceinline__ uint64_t order_key(float x, int idx) {

@@ -156,6 +156,15 @@ def test_ties_and_sorted_rows(V, dtype, K):
     _check(x, _tokens(x, V), 1.0, K)
 
 
+def test_the_rank_of_a_token_that_is_ruled_out():
+    """Every place in the row, its unaligned ends too, among -inf entries."""
+    for V, offset in ((1003, 0), (1003, 3), (2500, 5)):
+        x = torch.full((12, V), -float("inf"), dtype=torch.bfloat16)
+        x[:, ::3] = synth.gaussian((12, len(range(0, V, 3))), 1.0, V).to(torch.bfloat16)
+        tok = np.array([1, 2, 4, 7, 8, 256, 259, 770, V - 5, V - 3, V - 2, V - 1], np.int32)
+        _check(x, tok, 1.0, 3, placed=_place(x, 0, offset))
+
+
 def test_large_magnitudes():
     x = synth.gaussian((4, 5000), 1.0, 3)
     x[0] *= 1e4
