@@ -36,4 +36,22 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float4 v) {
                  : "memory");
 }
 
+// Arrives on another CTA's mbarrier (address by cluster_map): what this
+// thread wrote before, there too, is visible to who waits for the phase.
+__device__ __forceinline__ void cluster_mbar_arrive(uint32_t bar) {
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// As mbar_test and mbar_wait for a phase completed from other CTAs.
+__device__ __forceinline__ bool cluster_mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 }  // namespace sv

@@ -25,7 +25,7 @@ struct LogprobArgs {
     int64_t stride;
     const int32_t* tokens;
     float c;
-    double inv_t;
+    float2 inv_t;  // 1 / T in two parts
     float* logprob;
     int32_t* rank;
     float* entropy;
@@ -36,70 +36,77 @@ struct LogprobArgs {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpTile = 6;   // groups of a tile: 3 KiB
+constexpr int kLpDepth = 2;  // tiles a warp has on their way
+constexpr int kLpTileBytes = kLpTile * 512;
+constexpr int kLpRing = kLpWarps * kLpDepth * kLpTileBytes;
 constexpr int kLpMaxCluster = 8;
+constexpr uint64_t kLpLimitNs = 2000000000ull;
 constexpr float kLpPlain = 1024.0f;  // |m c| below this: see LpSums
 constexpr float kLpLeastC = 1e-30f;  // so that m - kLpFar / c stays in range
 constexpr float kLpFar = 200.0f;     // 2^-200 is zero
-constexpr int kLpTile = 8;  // groups a warp has in flight: 4 KiB
 // The K-th best group need not be found exactly: any bound that leaves K to
 // K + kLpSlack groups will do.
 constexpr int kLpSlack = 36;
-constexpr int kLpGroups = 256;  // at most this many groups are read again
-constexpr int kLpHeld = kLpGroups / kLpWarps;
 constexpr int kLpCands = 8 * (kMaxTop + kLpSlack);  // the elements of that many vectors
+constexpr int kLpBins = 256;        // of the groups' keys, from the largest down
+constexpr int kLpBinShift = 17;     // two bf16 values a bin: four binades in all
+static_assert(kLpCands * 8 <= kLpRing, "the candidates take the ring's place");
 
 // What a warp makes of its groups.
-struct LpPart {
+struct __align__(16) LpPart {
     float m, z, e;
     int before;
 };
-static_assert(sizeof(LpPart) == 16, "sent to the leader as one 16-byte store");
-
-struct LpSmem {
-    LpPart part[kLpMaxCluster * kLpWarps];
-    uint64_t cand[kLpCands];
-    int group[kLpGroups];  // the groups that hold the alternatives, in index order
-    int ties[kLpGroups];   // elements equal to tau in each, then how many come before it
-    int count[2][kLpWarps];
-    int n_group, n_cand;
-    uint32_t tau;          // order key: elements above it are candidates
-    uint32_t top;          // the largest key
-    float m, ln_z_hi, ln_z_lo;
-    int valid;
-};
+static_assert(sizeof(LpPart) == 16 && alignof(LpPart) == 16, "sent to the leader as one 16-byte store");
 
 // The groups of a row: 0 is its head, 1 .. nb the vectors, nb + 1 its tail.
 template <typename T>
 struct LpRow : RowView<T> {
     int nb;
     __device__ __forceinline__ LpRow(const T* r, int v) : RowView<T>(r, v), nb((this->nvec + 31) / 32) {}
-    // This lane's elements of group g: values, index of the first, how many.
-    __device__ __forceinline__ int load(int g, float* x, int& idx) const {
-        constexpr int VEC = ElemT<T>::VEC;
+    // This lane's element of the head and of the tail (-inf: none).
+    __device__ __forceinline__ float2 ends() const {
         const int lane = threadIdx.x & 31;
+        float2 e = make_float2(-INFINITY, -INFINITY);
+        if (lane < this->head) e.x = ElemT<T>::load(this->row + lane);
+        if (lane < this->tail) e.y = ElemT<T>::load(this->row + this->head + this->nvec * ElemT<T>::VEC + lane);
+        return e;
+    }
+    // This lane's elements of group g: a vector (an end's single element
+    // first, the rest -inf), how many there are, the index of the first.
+    __device__ __forceinline__ uint4 vector(int g) const {
+        const int lane = threadIdx.x & 31;
+        uint4 q = RowVec<T>::none();
         if (g >= 1 && g <= nb) {
             const int v = (g - 1) * 32 + lane;
-            idx = this->head + v * VEC;
-            if (v >= this->nvec) return 0;
-            ElemT<T>::unpack(__ldg(this->vec() + v), x);
-            return VEC;
+            if (v < this->nvec) q = __ldg(this->vec() + v);
+        } else if (lane < (g == 0 ? this->head : this->tail)) {
+            q.x = RowVec<T>::single(ElemT<T>::load(this->row + index(g)));
         }
-        const int n = g == 0 ? this->head : this->tail;
-        idx = (g == 0 ? 0 : this->head + this->nvec * VEC) + lane;
-        if (lane >= n) return 0;
-        x[0] = ElemT<T>::load(this->row + idx);
-        return 1;
+        return q;
+    }
+    __device__ __forceinline__ int count(int g) const {
+        const int lane = threadIdx.x & 31;
+        if (g >= 1 && g <= nb) return (g - 1) * 32 + lane < this->nvec ? ElemT<T>::VEC : 0;
+        return lane < (g == 0 ? this->head : this->tail) ? 1 : 0;
+    }
+    __device__ __forceinline__ int index(int g) const {
+        const int lane = threadIdx.x & 31;
+        if (g >= 1 && g <= nb) return this->head + ((g - 1) * 32 + lane) * ElemT<T>::VEC;
+        return (g == 0 ? 0 : this->head + this->nvec * ElemT<T>::VEC) + lane;
     }
 };
 
-// A row that gets no result: skipped, or refused (logprob -inf).
-__device__ __forceinline__ void lp_no_result(const LogprobArgs& a, int r, float logprob) {
-    if (threadIdx.x == 0) {
+// A row that gets no result: skipped, or refused (logprob -inf).  Thread
+// tid of n.
+__device__ __forceinline__ void lp_no_result(const LogprobArgs& a, int r, float logprob, int tid, int n) {
+    if (tid == 0) {
         if (a.logprob) a.logprob[r] = logprob;
         if (a.rank) a.rank[r] = -1;
         if (a.entropy) a.entropy[r] = 0.0f;
     }
-    for (int j = threadIdx.x; j < a.top_k; j += blockDim.x) {
+    for (int j = tid; j < a.top_k; j += n) {
         a.top_ids[(size_t)r * a.top_k + j] = -1;
         a.top_logprobs[(size_t)r * a.top_k + j] = -INFINITY;
     }
@@ -150,18 +157,22 @@ struct LpSums {
     }
 };
 
-// A bound above which K .. K + slack keys lie, found by halving the range of
-// the keys, or, where many keys are equal, the K-th largest key itself (then
-// fewer than K lie above it).  count(b) is the number of keys >= b; K or
-// more are >= lo (or there are fewer than K), none is above hi.
+// A bound above which K .. K + slack keys lie, or, where many keys are
+// equal, the K-th largest key itself (then fewer than K lie above it).
+// count(b) is the number of keys >= b; K or more are >= lo (or there are
+// fewer than K), fewer than K are above hi.  Steps of growing width down from hi (the
+// first is half a binade), then halves.
+__device__ __forceinline__ int lp_slack(int K) { return min(kLpSlack, 4 + K / 4); }
 template <typename F>
 __device__ __forceinline__ uint32_t lp_bound(uint32_t lo, uint32_t hi, int K, F&& count) {
-    const int slack = min(kLpSlack, 4 + K / 4);
+    const int slack = lp_slack(K);
+    uint32_t step = 1u << 22;
     while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        const uint32_t mid = hi - lo > 2 * step ? hi - step : lo + (hi - lo) / 2 + 1;
         const int n = count(mid);
         if (n < K) {
             hi = mid - 1;
+            step = step < (1u << 29) ? 4 * step : step;
         } else if (n <= K + slack) {
             return mid - 1;
         } else {
@@ -171,287 +182,355 @@ __device__ __forceinline__ uint32_t lp_bound(uint32_t lo, uint32_t hi, int K, F&
     return lo;
 }
 
-template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a) {
-    constexpr int VEC = ElemT<T>::VEC;
-    __shared__ LpSmem s;
-    extern __shared__ float group_max[];  // [nb + 2], in the leading CTA
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
-    const int r = CLUSTER ? blockIdx.x / S : blockIdx.x;
-    const int tok = a.tokens ? a.tokens[r] : 0;
-    if (tok < 0 || tok >= a.V) {
-        if (part == 0) {
-            if (tok != -1 && tid == 0 && a.dev_error) atomicOr(a.dev_error, kDevErrToken);
-            lp_no_result(a, r, tok == -1 ? 0.0f : -INFINITY);
-        }
-        return;
+// What decides an element's place before the token: above xt, or equal to it
+// and of a lower index.  In the groups before the token's own that is one
+// comparison with the next value below xt.
+template <typename T>
+struct LpToken {
+    float x;
+    int tok, group;  // the token's group
+    typename RowVec<T>::Least above, reach;
+    __device__ __forceinline__ LpToken(const LpRow<T>& row, int t, float xt) : x(xt), tok(t) {
+        constexpr int VEC = ElemT<T>::VEC;
+        group = t < row.head ? 0 : t < row.head + row.nvec * VEC ? 1 + (t - row.head) / (32 * VEC) : row.nb + 1;
+        above = RowVec<T>::least(xt);
+        reach = RowVec<T>::least(next_below<T>(xt));
     }
-    if (CLUSTER) cluster_arrive();  // awaited before the first store into the leader
-    const LpRow<T> row(static_cast<const T*>(a.logits) + (size_t)r * a.stride, a.V);
-    const float xt = ElemT<T>::load(row.row + tok);
+    __device__ __forceinline__ int before(float v, int idx) const { return v > x || (v == x && idx < tok); }
+};
 
-    // ------------------------------------------------------- the one read
+// A tile of groups g0 .. g0 + kLpTile - 1: this lane's vector of each.
+template <typename T>
+struct LpTile {
     using Vec = RowVec<T>;
-    const uint4* vecs = row.vec();
-    const float2 cc = make_float2(a.c, a.c);
-    const float far = kLpFar / a.c;
-    LpSums sum;
-    // Elements before the token: above xt, and equal to it in the groups
-    // before the token's own, where the bound is the next value below.
-    int before = 0;
-    const int tok_group = tok < row.head                    ? 0
-                          : tok < row.head + row.nvec * VEC ? 1 + (tok - row.head) / (32 * VEC)
-                                                            : row.nb + 1;
-    const typename Vec::Least above = Vec::least(xt), reach = Vec::least(next_below<T>(xt));
-    bool awaited = false;
-    auto put_max = [&](int g, float v) {
-        if (CLUSTER)
-            cluster_store(cluster_map(group_max + g, 0), v);
-        else
-            group_max[g] = v;
-    };
-    auto count_before = [&](float x, int idx) { before += x > xt || (x == xt && idx < tok); };
-    if (part == 0 && warp == 0) {  // head and tail: one element a lane
-#pragma unroll
-        for (int end = 0; end < 2; ++end) {
-            float x = -INFINITY;
-            int idx;
-            const int n = row.load(end ? row.nb + 1 : 0, &x, idx);
-            const float m = warp_max_redux(x);
-            if (m > sum.m) sum.raise(m, a.c);
-            sum.exact(a.c);
-            if (n) {
-                count_before(x, idx);
-                sum.add_any(make_float2(x, -INFINITY), cc);
-            }
-            if (CLUSTER && !awaited) {
-                cluster_wait();
-                awaited = true;
-            }
-            if (lane == 0) put_max(end ? row.nb + 1 : 0, m);
-        }
-        sum.settle(a.c);
-    }
-    // A warp's tiles; a vector's register takes its successor of the next
-    // tile as soon as it has been used, so 4 KiB stay on their way.
-    const int step = S * kLpWarps * kLpTile;
-    auto load = [&](int g) {
-        const int v = g * 32 + lane;
-        return v < row.nvec ? __ldg(vecs + v) : Vec::none();
-    };
-    int g0 = (part * kLpWarps + warp) * kLpTile;
     uint4 q[kLpTile];
-#pragma unroll
-    for (int j = 0; j < kLpTile; ++j) q[j] = load(g0 + j);
-    for (; g0 < row.nb; g0 += step) {
-        float mine = 0.0f, most = -INFINITY;
-        uint32_t some = 0;  // bit j: group j holds an element that reaches xt
+    float mine;  // lane j: the maximum of group j
+    float most;
+    __device__ __forceinline__ void maxima() {
+        mine = most = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kLpTile; ++j) {
             const float gm = warp_max_redux(Vec::max(q[j]));
             most = fmaxf(most, gm);
-            if (lane == j) mine = gm;
-            some |= gm >= xt ? 1u << j : 0u;
+            if ((threadIdx.x & 31) == j) mine = gm;
         }
-        if (most > sum.m) sum.raise(most, a.c);
-        if (CLUSTER && !awaited) {
-            cluster_wait();
-            awaited = true;
+    }
+    // Elements before the token.
+    __device__ __forceinline__ int before(const LpToken<T>& tk, const LpRow<T>& row, int g0) const {
+        if (most < tk.x) return 0;
+        const int at = tk.group - g0;  // the token's group among the tile's
+        if (at < 0 || at >= kLpTile) {
+            const typename Vec::Least bound = at < 0 ? tk.above : tk.reach;
+            typename Vec::Count n = Vec::count_zero();
+#pragma unroll
+            for (int j = 0; j < kLpTile; ++j) Vec::count(n, q[j], bound);
+            return Vec::count_sum(n);
         }
-        if (lane < kLpTile && g0 + lane < row.nb) put_max(g0 + lane + 1, mine);
-        const float2 nmc = make_float2(-sum.mc, -sum.mc);
-        const typename Vec::Least least = Vec::least(sum.m - far);
-        typename Vec::Count n = Vec::count_zero();
-        const int at = tok_group - 1 - g0;  // the token's place among the tile's groups
-        auto count = [&](int j) {
-            if (!((some >> j) & 1u)) return;
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kLpTile; ++j) {
             if (j != at) {
-                Vec::count(n, q[j], j < at ? reach : above);
+                typename Vec::Count k = Vec::count_zero();
+                Vec::count(k, q[j], j < at ? tk.reach : tk.above);
+                n += Vec::count_sum(k);
             } else {
-                const int v = (g0 + j) * 32 + lane, idx = row.head + v * VEC;
+                const int idx = row.head + ((g0 - 1 + j) * 32 + (threadIdx.x & 31)) * ElemT<T>::VEC;
 #pragma unroll
                 for (int i = 0; i < Vec::kPairs; ++i) {
                     const float2 x = Vec::pair(q[j], i);
-                    count_before(x.x, idx + 2 * i);
-                    count_before(x.y, idx + 2 * i + 1);
+                    n += tk.before(x.x, idx + 2 * i) + tk.before(x.y, idx + 2 * i + 1);
                 }
             }
-        };
+        }
+        return n;
+    }
+    __device__ __forceinline__ void add(LpSums& sum, float c, float far) const {
+        const float2 cc = make_float2(c, c), nmc = make_float2(-sum.mc, -sum.mc);
+        const typename Vec::Least least = Vec::least(sum.m - far);
         if (sum.plain) {
 #pragma unroll
             for (int j = 0; j < kLpTile; ++j) {
 #pragma unroll
                 for (int i = 0; i < Vec::kPairs; ++i) sum.add_plain(Vec::pair_above(q[j], i, least), cc, nmc);
-                count(j);
-                q[j] = load(g0 + step + j);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < kLpTile; ++j) {
 #pragma unroll
                 for (int i = 0; i < Vec::kPairs; ++i) sum.add_any(Vec::pair(q[j], i), cc);
-                count(j);
-                q[j] = load(g0 + step + j);
             }
         }
-        before += Vec::count_sum(n);
     }
-    sum.exact(a.c);
-    {
-        LpPart p;
-        p.m = sum.m;
-        p.z = sum.z.x + sum.z.y;
-        p.e = sum.e.x + sum.e.y;
+};
+
+// A warp's part of a row.
+__device__ __forceinline__ LpPart lp_part(LpSums& sum, int before, float c) {
+    sum.exact(c);
+    LpPart p;
+    p.m = sum.m;
+    p.z = sum.z.x + sum.z.y;
+    p.e = sum.e.x + sum.e.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
-            p.e += __shfl_xor_sync(0xffffffffu, p.e, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
+        p.e += __shfl_xor_sync(0xffffffffu, p.e, o);
+    }
+    p.before = __reduce_add_sync(0xffffffffu, before);
+    return p;
+}
+
+// Shared memory of the CTA that finishes a row.
+struct LpFinish {
+    static constexpr int kGroups = 256;               // at most this many groups are read again
+    static constexpr int kHeld = kGroups / kLpWarps;  // vectors a lane compares of them
+    int group[kGroups];  // the groups that hold the alternatives
+    int ties[kGroups];   // elements equal to tau in each, then how many come before it
+    int bin[kLpBins];
+    int count[2][kLpWarps];
+    int n_group, n_cand;
+    uint32_t tau;  // order key: elements above it are candidates
+    float m;
+    float2 ln_z;  // in two parts
+    int valid;
+};
+
+// d / T - ln z: with both constants in two parts, one rounding.
+__device__ __forceinline__ float lp_log(const LogprobArgs& a, float d, float2 ln_z) {
+    const float lp = fmaf(d, a.inv_t.x, -ln_z.x);
+    return lp > -INFINITY ? lp + fmaf(d, a.inv_t.y, -ln_z.y) : lp;
+}
+
+// One warp: the row's sums from its parts and its ends, and the results that
+// need no alternatives.
+template <typename T>
+__device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRow<T>& row, int tok, float xt,
+                                         float2 ends, LpFinish& s, const LpPart* parts, int n_parts) {
+    constexpr int VEC = ElemT<T>::VEC;
+    const int lane = threadIdx.x & 31;
+    LpPart p[2];
+    float m = fmaxf(ends.x, ends.y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        p[k] = lane + 32 * k < n_parts ? parts[lane + 32 * k] : LpPart{kNoMax, 0.0f, 0.0f, 0};
+        m = fmaxf(m, p[k].m);
+    }
+    m = warp_max_redux(m);
+    float z = 0.0f, e = 0.0f;
+    int before = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float d = fmaxf((p[k].m - m) * a.c, -1000.0f), f = ex2(d);
+        z += p[k].z * f;
+        e += (p[k].e + p[k].z * d) * f;
+        before += p[k].before;
+    }
+    auto end = [&](float x, int idx) {
+        const float t = (x - m) * a.c, w = ex2(t);
+        z += w;
+        e = fmaf(w, fmaxf(t, -1000.0f), e);
+        before += x > xt || (x == xt && idx < tok);
+    };
+    if (lane < row.head) end(ends.x, lane);
+    if (lane < row.tail) end(ends.y, row.head + row.nvec * VEC + lane);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+        e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    // nothing is below -inf: every place of the groups before the token's
+    // was counted, the empty ones of the last group too
+    if (xt == -INFINITY && tok >= row.head + row.nvec * VEC) before -= (row.nb * 32 - row.nvec) * VEC;
+    const bool valid = z > 0.0f && z < INFINITY;  // no NaN, no +inf, something finite
+    if (lane == 0) {
+        const float2 ln_z = ln_parts(z);
+        s.m = m;
+        s.ln_z = ln_z;
+        s.valid = valid;
+        if (valid) {
+            if (a.logprob) a.logprob[r] = a.tokens ? lp_log(a, xt - m, ln_z) : 0.0f;
+            if (a.rank) a.rank[r] = a.tokens ? before + 1 : -1;
+            if (a.entropy) a.entropy[r] = fmaf(-kLn2, e / z, ln_z.x) + ln_z.y;
+        } else if (a.dev_error) {
+            atomicOr(a.dev_error, kDevErrNonfinite);
         }
-        p.before = __reduce_add_sync(0xffffffffu, before);
-        if (CLUSTER) {
-            if (!awaited) cluster_wait();
-            if (lane == 0)
-                cluster_store(cluster_map(&s.part[part * kLpWarps + warp], 0),
-                              make_float4(p.m, p.z, p.e, __int_as_float(p.before)));
-            cluster_arrive();
-            cluster_wait();
-            if (part != 0) return;
-        } else {
-            if (lane == 0) s.part[warp] = p;
+    }
+}
+
+// The row's results, from n_parts <= 64 parts and the order keys of the
+// maxima of its groups (group_key[g], 1 <= g <= nb; room for 0 and nb + 1).
+// ends: this lane's element of the head and of the tail.
+template <typename T>
+__device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpRow<T>& row, int tok, float xt,
+                                          float2 ends, LpFinish& s, uint64_t* cand, uint32_t* group_key,
+                                          const LpPart* parts, int n_parts) {
+    using Vec = RowVec<T>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_groups = row.nb + 2;
+    const bool all = n_groups <= LpFinish::kGroups;
+    uint32_t top;  // the largest key
+    {
+        const float head_max = warp_max_redux(ends.x), tail_max = warp_max_redux(ends.y);
+        float m = fmaxf(head_max, tail_max);
+        for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, parts[k].m);
+        top = okey32(warp_max_redux(m));
+        if (warp == 0 && lane == 0) {  // an empty head or tail has no key (-inf has one)
+            group_key[0] = row.head ? okey32(head_max) : 0u;
+            group_key[row.nb + 1] = row.tail ? okey32(tail_max) : 0u;
+        }
+        if (a.top_k > 0) {
+            for (int i = tid; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
             __syncthreads();
         }
     }
-
-    // ------------------------------------------- the leader: merged results
-    const int n_groups = row.nb + 2;
-    if (warp == 1) {
-        LpPart p[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            p[k] = lane + 32 * k < S * kLpWarps ? s.part[lane + 32 * k] : LpPart{kNoMax, 0.0f, 0.0f, 0};
-        const float m = warp_max_redux(fmaxf(p[0].m, p[1].m));
-        float z = 0.0f, e = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float d = fmaxf((p[k].m - m) * a.c, -1000.0f), f = ex2(d);
-            z += p[k].z * f;
-            e += (p[k].e + p[k].z * d) * f;
+    if (a.top_k > 0) {
+        // Where the K-th best group lies: the groups' keys counted in bins
+        // from the largest down.  Few groups: all of them, and the bound is
+        // found among their vectors.
+        if (!all) {
+            for (int g = tid; g < n_groups; g += kLpThreads) {
+                const uint32_t k = group_key[g], bin = (top - k) >> kLpBinShift;
+                if (k != 0u && bin < kLpBins) atomicAdd(&s.bin[bin], 1);
+            }
+            __syncthreads();
         }
+        if (all) {
+            for (int g = tid; g < n_groups; g += kLpThreads) s.group[g] = g;
+            if (tid == 0) {
+                s.tau = 0u;
+                s.n_group = n_groups;
+                s.n_cand = 0;
+            }
+        } else if (warp == 0) {
+            uint32_t tau;
+            int n_above = 0;
+            {
+                auto count = [&](uint32_t b) {
+                    int n = 0;
+                    for (int g = lane; g < n_groups; g += 32) n += group_key[g] >= b;
+                    return __reduce_add_sync(0xffffffffu, n);
+                };
+                constexpr int kEach = kLpBins / 32;
+                int n[kEach], sum = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-            e += __shfl_xor_sync(0xffffffffu, e, o);
-        }
-        before = __reduce_add_sync(0xffffffffu, p[0].before + p[1].before);
-        // nothing is below -inf: every place of the groups before the token's
-        // was counted, the empty ones of the last group too
-        if (xt == -INFINITY && tok_group == row.nb + 1) before -= (row.nb * 32 - row.nvec) * VEC;
-        const bool valid = z > 0.0f && z < INFINITY;  // no NaN, no +inf, something finite
-        const double ln_z = ln_of(z);
-        if (lane == 0) {
-            s.m = m;
-            s.ln_z_hi = (float)ln_z;
-            s.ln_z_lo = (float)(ln_z - (double)(float)ln_z);
-            s.valid = valid;
-            if (valid) {
-                if (a.logprob) a.logprob[r] = a.tokens ? (float)((double)(xt - m) * a.inv_t - ln_z) : 0.0f;
-                if (a.rank) a.rank[r] = a.tokens ? before + 1 : -1;
-                if (a.entropy) a.entropy[r] = (float)(ln_z - (double)(e / z * kLn2));
-            } else if (a.dev_error) {
-                atomicOr(a.dev_error, kDevErrNonfinite);
+                for (int i = 0; i < kEach; ++i) sum += n[i] = s.bin[lane * kEach + i];
+                const int incl = warp_inclusive_scan_i(sum);
+                int at = incl - sum, bin = kLpBins;  // the first bin by whose end K groups are counted
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    if (at < a.top_k && at + n[i] >= a.top_k) {
+                        bin = lane * kEach + i;
+                        n_above = at + n[i];
+                    }
+                    at += n[i];
+                }
+                bin = warp_min_i(bin);
+                n_above = __reduce_max_sync(0xffffffffu, n_above);
+                const uint32_t hi = top - ((uint32_t)min(bin, kLpBins - 1) << kLpBinShift);
+                if (bin == kLpBins)  // below the bins
+                    tau = lp_bound(0u, hi, a.top_k, count);
+                else if (n_above > a.top_k + lp_slack(a.top_k))  // many in that bin
+                    tau = lp_bound(hi - ((1u << kLpBinShift) - 1u), hi, a.top_k, count);
+                else
+                    tau = hi - (1u << kLpBinShift);
+                if (bin == kLpBins || n_above > a.top_k + lp_slack(a.top_k)) n_above = count(tau + 1);
+                // fewer than K above tau: also the first that reach it
+                if (n_above < a.top_k) {
+                    int n_list = 0, equal = a.top_k - n_above;
+                    const uint32_t lower = (1u << lane) - 1u;
+                    for (int g0 = 0; g0 < n_groups; g0 += 32) {
+                        const uint32_t k = g0 + lane < n_groups ? group_key[g0 + lane] : 0u;
+                        const uint32_t same = __ballot_sync(0xffffffffu, k == tau);
+                        const uint32_t taken =
+                            __ballot_sync(0xffffffffu, k > tau || (k == tau && __popc(same & lower) < equal));
+                        equal -= __popc(same);
+                        const int place = n_list + __popc(taken & lower);
+                        if (((taken >> lane) & 1u) && place < LpFinish::kGroups) s.group[place] = g0 + lane;
+                        n_list += __popc(taken);
+                    }
+                    n_above = -n_list;  // the list is made
+                }
+            }
+            if (lane == 0) {
+                s.tau = tau;
+                s.n_group = n_above < 0 ? -n_above : 0;
+                s.n_cand = 0;
             }
         }
-    } else if (warp == 0 && a.top_k > 0 && n_groups <= kLpGroups) {
-        float m = -INFINITY;
-        for (int g = lane; g < n_groups; g += 32) {
-            s.group[g] = g;
-            m = fmaxf(m, group_max[g]);
-        }
-        m = warp_max_redux(m);
-        if (lane == 0) {
-            s.top = okey32(m);
-            s.tau = 0u;
-            s.n_group = n_groups;
-            s.n_cand = 0;
-        }
-    } else if (warp == 0 && a.top_k > 0) {
-        constexpr int kKeys = 16;  // keys a lane holds; longer rows are read from shared memory
-        // an empty head or tail has no key (-inf has one)
-        auto key = [&](int g) {
-            const bool some = g < n_groups && !(g == 0 && row.head == 0) && !(g == row.nb + 1 && row.tail == 0);
-            return some ? okey32(group_max[g]) : 0u;
-        };
-        uint32_t held[kKeys], top = 0;
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-            held[i] = key(i * 32 + lane);
-            top = max(top, held[i]);
-        }
-        for (int g = kKeys * 32 + lane; g < n_groups; g += 32) top = max(top, key(g));
-        top = __reduce_max_sync(0xffffffffu, top);
-        auto count = [&](uint32_t b) {
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) n += held[i] >= b;
-            for (int g = kKeys * 32 + lane; g < n_groups; g += 32) n += key(g) >= b;
-            return __reduce_add_sync(0xffffffffu, n);
-        };
-        const uint32_t tau = lp_bound(0u, top, a.top_k, count);
-        // every group above tau and, if they are fewer than K, the first that reach it
-        int n = 0, equal = a.top_k - count(tau + 1);
-        for (int g0 = 0; g0 < n_groups; g0 += 32) {
-            const uint32_t k = key(g0 + lane);
-            const uint32_t same = __ballot_sync(0xffffffffu, k == tau), lower = (1u << lane) - 1u;
-            const bool take = k > tau || (k == tau && __popc(same & lower) < equal);
-            const uint32_t taken = __ballot_sync(0xffffffffu, take);
-            if (take) s.group[n + __popc(taken & lower)] = g0 + lane;
-            n += __popc(taken);
-            equal -= __popc(same);
-        }
-        if (lane == 0) {
-            s.top = top;
-            s.tau = tau;
-            s.n_group = n;
-            s.n_cand = 0;
+    }
+    if (warp == 1) lp_merge<T>(a, r, row, tok, xt, ends, s, parts, n_parts);
+    if (a.top_k > 0 && !all) {
+        __syncthreads();
+        if (s.n_group == 0) {  // every group above tau
+            const uint32_t tau = s.tau;
+            __syncthreads();  // all have seen the empty list
+            for (int g = tid; g < n_groups; g += kLpThreads)
+                if (group_key[g] > tau) {
+                    const int at = atomicAdd(&s.n_group, 1);
+                    if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
+                }
         }
     }
     __syncthreads();
     if (!s.valid) {
-        lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f);
+        lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
         return;
     }
     if (a.top_k == 0) return;
 
     // --------------------------- the alternatives, from the chosen groups
     const int n_group = s.n_group;
-    float x[VEC];
-    int idx;
+    // f(i) for the vectors of the chosen groups whose maximum is such that
+    // hit(maximum): read many at a time (under load a read takes 1 to 2 us),
+    // and the few hits once more, in code that is not repeated per vector
+    // (what a row runs once has to be fetched, too).
+    constexpr int kAhead = 8;
+    auto for_hits = [&](auto&& hit, auto&& f) {
+        for (int i0 = warp; i0 < n_group; i0 += kAhead * kLpWarps) {
+            uint4 q[kAhead];
+            uint32_t hits = 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kLpWarps;
+                q[k] = i < n_group ? row.vector(s.group[i]) : Vec::none();
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * kLpWarps < n_group && hit(Vec::max(q[k]))) hits |= 1u << k;
+            while (hits) {
+                const int i = i0 + (__ffs(hits) - 1) * kLpWarps;
+                hits &= hits - 1;
+                f(i);
+            }
+        }
+    };
     // The bound of the groups leaves little more than K elements, unless the
     // row has few groups or its best elements share some (a sorted row).
     // Then the bound is raised to one that leaves about K vectors.
-    bool raise = n_groups <= kLpGroups;
+    bool raise = all;
+    float bound;
     for (;;) {
         if (raise) {
-            uint32_t held[kLpHeld];  // this lane's vectors: their maxima
+            uint32_t held[LpFinish::kHeld];  // this lane's vectors: their maxima
 #pragma unroll
-            for (int k = 0; k < kLpHeld; ++k) {
-                held[k] = 0u;
-                const int i = warp + k * kLpWarps;
-                if (i < n_group) {
-                    const int n = row.load(s.group[i], x, idx);
-                    float m = x[0];
+            for (int k0 = 0; k0 < LpFinish::kHeld; k0 += 4) {
+                uint4 q[4];
 #pragma unroll
-                    for (int j = 1; j < VEC; ++j)
-                        if (j < n) m = fmaxf(m, x[j]);
-                    held[k] = n ? okey32(m) : 0u;
+                for (int k = 0; k < 4; ++k) {
+                    const int i = warp + (k0 + k) * kLpWarps;
+                    q[k] = i < n_group ? row.vector(s.group[i]) : Vec::none();
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = warp + (k0 + k) * kLpWarps;
+                    held[k0 + k] = i < n_group && row.count(s.group[i]) ? okey32(Vec::max(q[k])) : 0u;
                 }
             }
             int turn = 0;
-            const uint32_t tau = lp_bound(s.tau, s.top, a.top_k, [&](uint32_t b) {
+            const uint32_t tau = lp_bound(s.tau, top, a.top_k, [&](uint32_t b) {
                 int n = 0;
 #pragma unroll
-                for (int k = 0; k < kLpHeld; ++k) n += held[k] >= b;
+                for (int k = 0; k < LpFinish::kHeld; ++k) n += held[k] >= b;
                 n = __reduce_add_sync(0xffffffffu, n);
                 turn ^= 1;  // the other half: its readers have passed a barrier since
                 if (lane == 0) s.count[turn][warp] = n;
@@ -468,69 +547,188 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
             }
             __syncthreads();
         }
-        const uint32_t tau = s.tau;
-        for (int i = warp; i < n_group; i += kLpWarps) {
-            const int n = row.load(s.group[i], x, idx);
-            int ties = 0;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                if (j < n) {
-                    const uint32_t k = okey32(x[j]);
-                    ties += k == tau;
-                    if (k > tau) {
-                        const int at = atomicAdd(&s.n_cand, 1);
-                        if (at < kLpCands) s.cand[at] = order_key(x[j], idx + j);
-                    }
-                }
-            ties = __reduce_add_sync(0xffffffffu, ties);
-            if (lane == 0) s.ties[i] = ties;
-        }
+        // As a float: the key below zero's is -0, which compares equal to
+        // zero; key 0 is a NaN, which nothing is <= to.
+        bound = s.tau == 0x7fffffffu ? __uint_as_float(0x80000001u) : okey32_to_float(s.tau);
+        for_hits([&](float m) { return !(m <= bound); },
+                 [&](int i) {
+                     const int g = s.group[i], n = row.count(g), idx = row.index(g);
+#pragma unroll 1
+                     for (int j = 0; j < n; ++j) {
+                         const float x = ElemT<T>::load(row.row + idx + j);
+                         if (x <= bound) continue;
+                         const int at = atomicAdd(&s.n_cand, 1);
+                         if (at < kLpCands) cand[at] = order_key(x, idx + j);
+                     }
+                 });
         __syncthreads();
         if (s.n_cand <= kLpCands || raise) break;
         raise = true;
     }
     int n_cand = s.n_cand;
-    if (n_cand < a.top_k) {  // and the first elements equal to tau
+    if (n_cand < a.top_k) {  // and the first elements equal to tau, in the order of their groups
         const int need = a.top_k - n_cand;
-        if (warp == 0) {
-            int sum_before = 0;
-            for (int i0 = 0; i0 < n_group; i0 += 32) {
-                const int t = i0 + lane < n_group ? s.ties[i0 + lane] : 0;
-                const int incl = warp_inclusive_scan_i(t);
-                if (i0 + lane < n_group) s.ties[i0 + lane] = t > 0 ? sum_before + incl - t : need;
-                sum_before += __shfl_sync(0xffffffffu, incl, 31);
-            }
+        auto ties_of = [&](int g) {
+            const int n = row.count(g), idx = row.index(g);
+            int ties = 0;
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) ties += ElemT<T>::load(row.row + idx + j) == bound;
+            return ties;
+        };
+#pragma unroll 1
+        for (int i = warp; i < n_group; i += kLpWarps) {
+            const int ties = __reduce_add_sync(0xffffffffu, ties_of(s.group[i]));
+            if (lane == 0) s.ties[i] = ties;
         }
         __syncthreads();
-        const uint32_t tau = s.tau;
+        int earlier = 0, mine = 0;
+        if (tid < n_group) {
+            mine = s.ties[tid];
+            for (int j = 0; j < n_group; ++j) earlier += s.group[j] < s.group[tid] ? s.ties[j] : 0;
+        }
+        __syncthreads();
+        if (tid < n_group) s.ties[tid] = mine > 0 ? earlier : need;
+        __syncthreads();
         for (int i = warp; i < n_group; i += kLpWarps) {
             if (s.ties[i] >= need) continue;  // none here, or none still wanted
-            const int n = row.load(s.group[i], x, idx);
-            int ties = 0;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) ties += j < n && okey32(x[j]) == tau;
+            const int g = s.group[i], n = row.count(g), idx = row.index(g), ties = ties_of(g);
             int at = s.ties[i] + warp_inclusive_scan_i(ties) - ties;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                if (j < n && okey32(x[j]) == tau) {
-                    if (at < need) s.cand[n_cand + at] = order_key(x[j], idx + j);
-                    ++at;
-                }
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const float x = ElemT<T>::load(row.row + idx + j);
+                if (x != bound) continue;
+                if (at < need) cand[n_cand + at] = order_key(x, idx + j);
+                ++at;
+            }
         }
         __syncthreads();
         n_cand = a.top_k;
     }
     // a candidate's place is the number of candidates before it
-    const double ln_z = (double)s.ln_z_hi + (double)s.ln_z_lo;
     for (int i = tid; i < n_cand; i += kLpThreads) {
-        const uint64_t k = s.cand[i];
+        const uint64_t k = cand[i];
         int place = 0;
-        for (int j = 0; j < n_cand; ++j) place += s.cand[j] > k;
+#pragma unroll 4
+        for (int j = 0; j < n_cand; ++j) place += cand[j] > k;
         if (place < a.top_k) {
             a.top_ids[(size_t)r * a.top_k + place] = key_index(k);
-            a.top_logprobs[(size_t)r * a.top_k + place] = (float)((double)(key_value(k) - s.m) * a.inv_t - ln_z);
+            a.top_logprobs[(size_t)r * a.top_k + place] = lp_log(a, key_value(k) - s.m, s.ln_z);
         }
     }
+}
+
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a) {
+    __shared__ LpFinish s;
+    __shared__ LpPart parts[kLpMaxCluster * kLpWarps];
+    __shared__ uint64_t full[kLpWarps][kLpDepth];
+    extern __shared__ __align__(128) uint8_t lp_raw[];
+    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + kLpRing);  // [nb + 2]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
+    const int r = blockIdx.x / S;
+    const int tok = a.tokens ? a.tokens[r] : 0;
+    if (tok < 0 || tok >= a.V) {
+        if (part == 0) {
+            if (tok != -1 && tid == 0 && a.dev_error) atomicOr(a.dev_error, kDevErrToken);
+            lp_no_result(a, r, tok == -1 ? 0.0f : -INFINITY, tid, kLpThreads);
+        }
+        return;
+    }
+    if (CLUSTER) cluster_arrive();  // awaited before the first store into the leader
+    const LpRow<T> row(static_cast<const T*>(a.logits) + (size_t)r * a.stride, a.V);
+
+    // This warp's tiles, kLpDepth of them on their way through its part of
+    // the ring: what is in flight does not take registers, and is enough
+    // when another CTA of the SM is at its row's end.
+    uint4* ring = reinterpret_cast<uint4*>(lp_raw) + warp * (kLpRing / 16 / kLpWarps);
+    uint64_t* bars = full[warp];
+    const uint4* vecs = row.vec();
+    const int step = S * kLpWarps * kLpTile;
+    int g0 = (part * kLpWarps + warp) * kLpTile;
+    auto copy = [&](int g, int slot) {  // lane 0
+        const uint32_t bytes = (uint32_t)min(kLpTile * 32, row.nvec - g * 32) * 16;
+        mbar_arrive_expect_tx(&bars[slot], bytes);
+        bulk_load(ring + slot * (kLpTileBytes / 16), vecs + (size_t)g * 32, bytes, &bars[slot]);
+    };
+    if (lane == 0) {
+        for (int i = 0; i < kLpDepth; ++i) mbar_init(&bars[i], 1);
+        mbar_fence_init();
+        for (int i = 0; i < kLpDepth; ++i)
+            if (g0 + i * step < row.nb) copy(g0 + i * step, i);
+    }
+    __syncwarp();
+    const float xt = ElemT<T>::load(row.row + tok);
+    const float2 ends = row.ends();
+    const LpToken<T> tk(row, tok, xt);
+    const float far = kLpFar / a.c;
+    LpSums sum;
+    LpTile<T> tile;
+    int before = 0, slot = 0;
+    uint32_t parity = 0;
+    bool awaited = false, ok = true;
+    for (; g0 < row.nb; g0 += step) {
+        ok = mbar_wait(&bars[slot], parity, kLpLimitNs);
+        if (!ok) break;
+        const uint4* at = ring + slot * (kLpTileBytes / 16) + lane;
+        if ((g0 + kLpTile) * 32 <= row.nvec) {
+#pragma unroll
+            for (int j = 0; j < kLpTile; ++j) tile.q[j] = at[j * 32];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLpTile; ++j)
+                tile.q[j] = (g0 + j) * 32 + lane < row.nvec ? at[j * 32] : RowVec<T>::none();
+        }
+        __syncwarp();  // every lane has its vectors: the slot takes the next tile
+        if (lane == 0 && g0 + kLpDepth * step < row.nb) copy(g0 + kLpDepth * step, slot);
+        if (++slot == kLpDepth) {
+            slot = 0;
+            parity ^= 1;
+        }
+        tile.maxima();
+        if (tile.most > sum.m) sum.raise(tile.most, a.c);
+        if (CLUSTER && !awaited) {
+            cluster_wait();
+            awaited = true;
+        }
+        if (lane < kLpTile && g0 + lane < row.nb) {
+            const uint32_t k = okey32(tile.mine);
+            if (CLUSTER)
+                cluster_store(cluster_map(group_key + g0 + lane + 1, 0), __uint_as_float(k));
+            else
+                group_key[g0 + lane + 1] = k;
+        }
+        before += tile.before(tk, row, g0 + 1);
+        tile.add(sum, a.c, far);
+    }
+    LpPart p = lp_part(sum, before, a.c);
+    if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
+        p.z = NAN;
+        if (lane == 0) {
+            if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+            for (int i = 0; i < kLpDepth && g0 + i * step < row.nb; ++i) {
+                mbar_wait(&bars[slot], parity, kLpLimitNs);
+                if (++slot == kLpDepth) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+    }
+    if (CLUSTER) {
+        if (!awaited) cluster_wait();
+        if (lane == 0)
+            cluster_store(cluster_map(&parts[part * kLpWarps + warp], 0),
+                          make_float4(p.m, p.z, p.e, __int_as_float(p.before)));
+        cluster_arrive();
+        cluster_wait();
+        if (part != 0) return;
+    } else {
+        if (lane == 0) parts[warp] = p;
+        __syncthreads();
+    }
+    lp_finish<T>(a, r, row, tok, xt, ends, s, reinterpret_cast<uint64_t*>(lp_raw), group_key, parts, S * kLpWarps);
 }
 
 // CTAs that share a row: as many as keep every SM busy when rows are few,
@@ -538,12 +736,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
 template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;
-    int sms = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    const size_t dyn = kLpRing + (size_t)(groups + 2) * sizeof(uint32_t);
+    constexpr int kMostGroups = (int)((kRowsMaxVocab / 4 + 31) / 32);
+    constexpr size_t kMost = kLpRing + (kMostGroups + 2) * sizeof(uint32_t);
+    LaunchShape shape;
+    if (!launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, false>), kMost, kLpThreads, &shape) ||
+        !launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, true>), kMost, kLpThreads, &shape))
         return cudaErrorUnknown;
     int S = 1;
-    while (S < kLpMaxCluster && (long long)a.R * S < 2 * sms && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
-    const size_t dyn = (size_t)(groups + 2) * sizeof(float);
+    while (S < kLpMaxCluster && (long long)a.R * S < 2 * shape.sms && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
     if (S == 1) {
         k_token_logprobs<T, false><<<a.R, kLpThreads, dyn, st>>>(a);
         return cudaGetLastError();
@@ -584,8 +785,11 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dev_error && cudaMemsetAsync(dev_error, 0, sizeof(int32_t), st) != cudaSuccess) return SPEC_ERR_CUDA;
     if (R == 0) return SPEC_OK;
+    const double inv_t = 1.0 / (double)temperature;
+    const float inv_hi = (float)inv_t;
     LogprobArgs a{logits, R, V, top_k, row_stride, tokens, (float)(kLog2e / (double)temperature),
-                  1.0 / (double)temperature, logprob, rank, entropy, top_ids, top_logprobs, dev_error};
+                  make_float2(inv_hi, (float)(inv_t - (double)inv_hi)), logprob, rank, entropy, top_ids, top_logprobs,
+                  dev_error};
     return (dtype == SPEC_BF16 ? launch_logprobs<__nv_bfloat16>(a, st) : launch_logprobs<float>(a, st)) == cudaSuccess
                ? SPEC_OK
                : SPEC_ERR_CUDA;

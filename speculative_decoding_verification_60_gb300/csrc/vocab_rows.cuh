@@ -77,6 +77,8 @@ template <> struct RowVec<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
         return fmaxf(__low2float(m), __high2float(m));
     }
+    // word 0 of a vector whose first element is x, the other -inf
+    __device__ static __forceinline__ uint32_t single(float x) { return 0xff800000u | (__float_as_uint(x) >> 16); }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
 template <> struct RowVec<float> {
@@ -105,6 +107,7 @@ template <> struct RowVec<float> {
     __device__ static __forceinline__ float max(const uint4& q) {
         return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
+    __device__ static __forceinline__ uint32_t single(float x) { return __float_as_uint(x); }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
@@ -116,13 +119,20 @@ __device__ __forceinline__ uint64_t order_key(float x, int idx) {
 __device__ __forceinline__ int key_index(uint64_t k) { return 0x7fffffff - (int)(uint32_t)k; }
 __device__ __forceinline__ float key_value(uint64_t k) { return okey32_to_float((uint32_t)(k >> 32)); }
 
-// ln z for z > 0, as a double of about 25 good bits near zero and better
-// above: the exponent's part is exact, only the mantissa's logarithm is
-// rounded to 32 bits.
-__device__ __forceinline__ double ln_of(float z) {
+// ln z for z > 0 in two parts, x + y: the exponent's part is exact (ln 2 to
+// 16 bits, and the rest of it), only the mantissa's logarithm is rounded to
+// 32 bits.
+__device__ __forceinline__ float2 ln_parts(float z) {
     int e;
     const float f = frexpf(z, &e);
-    return (double)e * 0.69314718055994531 + (double)logf(f);
+    const float hi = (float)e * 0.693145751953125f, lo = fmaf((float)e, 1.4286068203e-6f, logf(f));
+    const float x = hi + lo;
+    const float b = x - hi;  // hi and lo of any size: a two-sum
+    return make_float2(x, (hi - (x - b)) + (lo - b));
+}
+__device__ __forceinline__ double ln_of(float z) {
+    const float2 p = ln_parts(z);
+    return (double)p.x + (double)p.y;
 }
 
 // Arguments that every call over rows checks the same way.
