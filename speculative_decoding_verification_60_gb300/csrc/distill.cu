@@ -7,6 +7,8 @@
 // the K listed ones.  The tail's mass q_T is then a sum of its own terms,
 // where 1 - sum q_j would cancel, and the gradient of every tail token is
 // one coefficient times 2^((s - m_T) c).
+#include <stdlib.h>
+#include "cluster.cuh"
 #include "vocab_rows.cuh"
 
 namespace sv {
@@ -18,8 +20,9 @@ struct DistillArgs {
     const int32_t* ids;
     const float* teacher;
     const float* weights;  // forward: row weights; backward: upstream gradients
-    float c;
-    double inv_t;
+    float c;       // log2(e) / T
+    double inv_t;  // c ln 2: 1 / T for the same rounded c
+
     bool bucket;
     float* loss;
     float* stats;
@@ -41,19 +44,30 @@ struct DistillStat {
 };
 static_assert(sizeof(DistillStat) == 32, "row_stats is [R, 8] float");
 
-constexpr int kDsThreads = 256;
+constexpr int kDsWarps = 8;                          // that take tiles
+constexpr int kDsThreads = (kDsWarps + 1) * 32;      // and one for the teacher and the loss
+constexpr int kDsTile = 4;                           // vectors a lane takes of a tile: 2 KiB a warp
+constexpr int kDsTileBytes = kDsTile * 512;
+constexpr int kDsMaxCluster = 16;
+constexpr int kDsMaxTiles = 12;                      // of a warp, when the row stays on the chip
+constexpr int kDsRing = 3;                           // tiles of a warp on their way, when it does not
+constexpr int kDsIds = kMaxTop / 32;                 // listed tokens a lane looks after
+constexpr uint64_t kDsLimitNs = 2000000000ull;
+constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x c - m c in one operation
 // Where the student gives the tail nothing, this much teacher mass outside
 // the listed tokens is the rounding of their log probabilities: the loss
 // would be +inf for it.
 constexpr float kTailRounding = 1.0f / 65536.0f;
 
 struct DsSmem {
-    float m[kDsThreads], z[kDsThreads];
-    float s[kMaxTop], l[kMaxTop];  // student logits and teacher values of the listed tokens
+    float2 part[kDsMaxCluster * kDsWarps];  // every warp's maximum and sum of the tail
+    float s[kMaxTop], l[kMaxTop], t[kMaxTop];  // listed tokens: student logit, teacher's value and probability
     int id[kMaxTop];
-    DistillStat st;
-    float loss;
-    int bad;
+    uint64_t full[kDsWarps][kDsMaxTiles];
+    double mass;   // sum of t_j
+    double ln_t;   // subtracted from the teacher's values
+    float t_tail;  // 1 - mass (BUCKET)
+    int bad, dead;  // error bits of the teacher; no teacher mass at all
 };
 
 __device__ __forceinline__ float warp_sum_f(float v) {
@@ -67,191 +81,542 @@ __device__ __forceinline__ double warp_sum_d(double v) {
     return v;
 }
 
-// One warp: the row's statistics and loss from the tail's maximum and sum
-// and the K listed tokens.  The differences log t - log q cancel where the
-// student is near the teacher, and 1 - sum t where the listed tokens hold
-// nearly all of the teacher, so both are taken in double (K per row).
-__device__ __forceinline__ void distill_finish(const DistillArgs& a, float m_tail, float z_tail, const float* s,
-                                               const float* l, const int* id, DistillStat* out, float* loss, int* bad) {
-    const int lane = threadIdx.x & 31;
-    float lmax = kNoMax, smax = kNoMax;
-    int err = 0;
-    for (int j = lane; j < a.K; j += 32)
-        if (id[j] >= 0) {
-            lmax = fmaxf(lmax, l[j]);
-            smax = fmaxf(smax, s[j]);
-            if (isnan(l[j]) || l[j] == INFINITY || isnan(s[j]) || s[j] == INFINITY) err = kDevErrNonfinite;
-        }
-    lmax = warp_max(lmax);
-    const float m = fmaxf(m_tail, warp_max(smax));
-    float z = 0.0f;
-    double tsum = 0.0;
-    const float lref = a.bucket ? 0.0f : lmax;
-    for (int j = lane; j < a.K; j += 32)
-        if (id[j] >= 0) {
-            z += ex2((s[j] - m) * a.c);
-            tsum += exp((double)l[j] - (double)lref);
-        }
-    tsum = warp_sum_d(tsum);
-    const float zt = z_tail * ex2(fmaxf((m_tail - m) * a.c, -1000.0f));
-    z = warp_sum_f(z) + zt;
-    if (!(z > 0.0f && z < INFINITY) || !(tsum < (double)INFINITY)) err = kDevErrNonfinite;
-    err = __reduce_or_sync(0xffffffffu, err);
-    DistillStat st{};
-    double sum = 0.0;
-    if (!err && (a.bucket || tsum > 0.0)) {
-        const double ln_z = ln_of(z);
-        const double ln_t = a.bucket ? 0.0 : (double)lref + ln_of((float)tsum);
-        float t_tail = a.bucket ? (float)fmax(1.0 - tsum, 0.0) : 0.0f;
-        if (z_tail == 0.0f && t_tail <= kTailRounding) t_tail = 0.0f;
-        const float q_tail = zt / z;
-        for (int j = lane; j < a.K; j += 32)
-            if (id[j] >= 0 && l[j] > -INFINITY) {
-                const double lt = (double)l[j] - ln_t;
-                const float t = expf((float)lt);
-                const double lq = (double)(s[j] - m) * a.inv_t - ln_z;
-                if (t > 0.0f) sum += (double)t * (lt - lq);
-            }
-        sum = warp_sum_d(sum);
-        if (t_tail > 0.0f)
-            sum = z_tail > 0.0f
-                      ? sum + (double)t_tail * (ln_of(t_tail) - ((double)(m_tail - m) * a.inv_t + ln_of(z_tail) - ln_z))
-                      : (double)INFINITY;
-        st.m_tail = m_tail;
-        st.m = m;
-        st.inv_z = 1.0f / z;
-        st.mass = a.bucket ? (float)(tsum + (double)t_tail) : 1.0f;
-        st.ln_t = (float)ln_t;
-        st.coef = z_tail > 0.0f ? (st.mass * q_tail - t_tail) * (float)a.inv_t / z_tail : 0.0f;
-        st.live = 1.0f;
+// A lane's sum of 2^t, t = (x - m) c, against its warp's reference m; mc is
+// m c rounded, and what it is off by is taken out at the end (exact()).
+struct DsSum {
+    float m = kNoMax, mc = 0.0f;
+    bool plain = false;
+    float2 z = make_float2(0.0f, 0.0f);
+    __device__ __forceinline__ void shift(float d) {
+        const float f = ex2(fmaxf(d, -1000.0f));
+        z = make_float2(z.x * f, z.y * f);
     }
+    __device__ __forceinline__ void exact(float c) {
+        if (plain) shift(fmaf(-m, c, mc));
+        plain = false;
+    }
+    __device__ __forceinline__ void raise(float m2, float c) {
+        exact(c);
+        shift((m - m2) * c);
+        m = m2;
+        mc = m * c;
+        plain = fabsf(mc) < kDsPlain;
+        if (plain) shift(fmaf(m, c, -mc));
+    }
+    template <typename T, int N>
+    __device__ __forceinline__ void add(const uint4* q, float c) {
+        const float2 cc = make_float2(c, c);
+        if (plain) {
+            const float2 nmc = make_float2(-mc, -mc);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+                    const float2 t = __ffma2_rn(RowVec<T>::pair(q[j], i), cc, nmc);
+                    z = __fadd2_rn(z, make_float2(ex2(t.x), ex2(t.y)));
+                }
+        } else {
+            const float2 nm = make_float2(-m, -m);  // x - m first: m c may not be finite
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+                    const float2 t = __fmul2_rn(__fadd2_rn(RowVec<T>::pair(q[j], i), nm), cc);
+                    z = __fadd2_rn(z, make_float2(ex2(t.x), ex2(t.y)));
+                }
+        }
+    }
+};
+
+// The teacher's side of a row, by one warp, while the row is on its way:
+// checks, student logits of the listed tokens, t_j and their sum (in double:
+// 1 - sum t cancels where the listed tokens hold nearly all of the teacher).
+template <typename T>
+__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsSmem& sm) {
+    const int lane = threadIdx.x & 31;
+    float lmax = kNoMax;
+    int err = 0;
+    for (int j = lane; j < a.K; j += 32) {
+        int v = a.ids[(size_t)r * a.K + j];
+        const float l = a.teacher[(size_t)r * a.K + j];
+        if (v != -1 && (v < 0 || v >= a.V)) {
+            err |= kDevErrToken;
+            v = -1;
+        }
+        sm.id[j] = v;
+        sm.l[j] = l;
+        if (v >= 0) {
+            sm.s[j] = ElemT<T>::load(row + v);
+            lmax = fmaxf(lmax, l);
+            if (isnan(l) || l == INFINITY) err |= kDevErrNonfinite;
+        }
+    }
+    lmax = warp_max(lmax);
+    __syncwarp();
+    for (int j = lane; j < a.K; j += 32)
+        for (int i = 0; i < j; ++i)
+            if (sm.id[j] >= 0 && sm.id[i] == sm.id[j]) err |= kDevErrToken;
+    const double ref = a.bucket ? 0.0 : (double)lmax;
+    double mass = 0.0;
+    for (int j = lane; j < a.K; j += 32)
+        if (sm.id[j] >= 0) mass += exp((double)sm.l[j] - ref);
+    mass = warp_sum_d(mass);
+    if (!(mass < (double)INFINITY)) err |= kDevErrNonfinite;
+    err = __reduce_or_sync(0xffffffffu, err);
+    const double ln_t = a.bucket ? 0.0 : ref + log(mass);
+    for (int j = lane; j < a.K; j += 32) sm.t[j] = sm.id[j] >= 0 ? expf((float)((double)sm.l[j] - ln_t)) : 0.0f;
     if (lane == 0) {
-        *out = st;
-        *loss = (float)sum;
-        *bad = err;
+        sm.mass = a.bucket ? mass : 1.0;
+        sm.t_tail = a.bucket ? (float)fmax(1.0 - mass, 0.0) : 0.0f;
+        sm.ln_t = ln_t;
+        sm.bad = err;
+        sm.dead = !a.bucket && !(mass > 0.0);
     }
 }
 
-// Gradient of listed token j.
-__device__ __forceinline__ float distill_listed_grad(const DistillStat& st, float s, float l, float c, float inv_t,
+// The row's statistics from every warp's part and the listed tokens, by each
+// warp for itself.
+struct DsSums {
+    float z, z_tail;  // relative to m and to m_tail
+    float t_tail;
+    int err;          // error bits
+};
+__device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsSmem& sm, int n_parts, DsSums* sums) {
+    const int lane = threadIdx.x & 31;
+    DistillStat st{};
+    float mt = kNoMax, ms = kNoMax;
+    for (int k = lane; k < n_parts; k += 32) mt = fmaxf(mt, sm.part[k].x);
+    for (int j = lane; j < a.K; j += 32)
+        if (sm.id[j] >= 0) ms = fmaxf(ms, sm.s[j]);
+    mt = warp_max_redux(mt);
+    const float m = fmaxf(mt, warp_max_redux(ms));
+    float zt = 0.0f, zs = 0.0f;
+    for (int k = lane; k < n_parts; k += 32) zt += sm.part[k].y * ex2(fmaxf((sm.part[k].x - mt) * a.c, -1000.0f));
+    for (int j = lane; j < a.K; j += 32)
+        if (sm.id[j] >= 0) zs += ex2((sm.s[j] - m) * a.c);
+    zt = warp_sum_f(zt);
+    const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f)), z = warp_sum_f(zs) + in_tail;
+    const float t_tail = zt == 0.0f && sm.t_tail <= kTailRounding ? 0.0f : sm.t_tail;
+    *sums = DsSums{z, zt, t_tail, sm.bad};
+    if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
+    if (sums->err || sm.dead) return st;
+    st.m_tail = mt;
+    st.m = m;
+    st.inv_z = 1.0f / z;
+    st.mass = (float)(sm.mass + (double)t_tail);
+    st.ln_t = (float)sm.ln_t;
+    st.coef = zt > 0.0f ? (st.mass * (in_tail / z) - t_tail) * (float)a.inv_t / zt : 0.0f;
+    st.live = 1.0f;
+    return st;
+}
+
+// The loss, by one warp.  log t - log q cancels where the student is near
+// the teacher: in double, and with the same c that the sums were made with.
+__device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsSmem& sm, const DistillStat& st,
+                                              const DsSums& sums) {
+    const int lane = threadIdx.x & 31;
+    const double ln_z = ln_of(sums.z);
+    double sum = 0.0;
+    for (int j = lane; j < a.K; j += 32)
+        if (sm.t[j] > 0.0f)
+            sum += (double)sm.t[j] * (((double)sm.l[j] - sm.ln_t) - ((double)(sm.s[j] - st.m) * a.inv_t - ln_z));
+    sum = warp_sum_d(sum);
+    if (sums.t_tail > 0.0f)
+        sum = sums.z_tail > 0.0f
+                  ? sum + (double)sums.t_tail *
+                              (ln_of(sums.t_tail) - ((double)(st.m_tail - st.m) * a.inv_t + ln_of(sums.z_tail) - ln_z))
+                  : (double)INFINITY;
+    return (float)sum;
+}
+
+// Gradient of a listed token.
+__device__ __forceinline__ float distill_listed_grad(const DistillStat& st, float s, float t, float c, float inv_t,
                                                      float w) {
     const float q = ex2((s - st.m) * c) * st.inv_z;
-    return w * (st.mass * q - expf(l - st.ln_t)) * inv_t;
+    return w * (st.mass * q - t) * inv_t;
 }
 
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
-
-template <typename T>
-__device__ __forceinline__ void distill_zero_grad(const DistillArgs& a, int r) {
-    if (!a.grad) return;
-    T* g = static_cast<T*>(a.grad) + (size_t)r * a.grad_stride;
-    for (int i = threadIdx.x; i < a.V; i += kDsThreads) store_elem(g + i, 0.0f);
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack(const float2* x, __nv_bfloat16) {
+    return make_uint4(bf16x2_bits(x[0].x, x[0].y), bf16x2_bits(x[1].x, x[1].y), bf16x2_bits(x[2].x, x[2].y),
+                      bf16x2_bits(x[3].x, x[3].y));
+}
+__device__ __forceinline__ uint4 pack(const float2* x, float) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
 }
 
-// The gradient of a row from its statistics; the listed tokens' values are
-// in sm (loaded before any write: grad may be the student's buffer).
+// A vector's gradient as tail tokens, stored at g (aligned: 16 bytes at once).
 template <typename T>
-__device__ __forceinline__ void distill_write_grad(const DistillArgs& a, int r, const DistillStat& st, float w,
-                                                   const DsSmem& sm) {
-    const T* row = static_cast<const T*>(a.student) + (size_t)r * a.stride;
-    T* g = static_cast<T*>(a.grad) + (size_t)r * a.grad_stride;
-    for (int i = threadIdx.x; i < a.V; i += kDsThreads)
-        store_elem(g + i, w * st.coef * ex2((ElemT<T>::load(row + i) - st.m_tail) * a.c));
-    __syncthreads();  // the listed tokens overwrite what the sweep wrote there
-    for (int j = threadIdx.x; j < a.K; j += kDsThreads)
-        if (sm.id[j] >= 0) store_elem(g + sm.id[j], distill_listed_grad(st, sm.s[j], sm.l[j], a.c, (float)a.inv_t, w));
+__device__ __forceinline__ void distill_store(T* g, const uint4& q, float coef, float m_tail, float c, bool aligned) {
+    float2 y[RowVec<T>::kPairs];
+    const float2 cc = make_float2(c, c), nm = make_float2(-m_tail, -m_tail), kk = make_float2(coef, coef);
+#pragma unroll
+    for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+        const float2 t = __fmul2_rn(__fadd2_rn(RowVec<T>::pair(q, i), nm), cc);
+        y[i] = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), kk);
+    }
+    if (aligned) {
+        *reinterpret_cast<uint4*>(g) = pack(y, T{});
+    } else {
+#pragma unroll
+        for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+            store_elem(g + 2 * i, y[i].x);
+            store_elem(g + 2 * i + 1, y[i].y);
+        }
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kDsThreads) k_distill(DistillArgs a) {
-    extern __shared__ uint32_t listed[];  // one bit per token
+__device__ __forceinline__ bool same_alignment(const RowView<T>& row, const T* g) {
+    return ((reinterpret_cast<uintptr_t>(row.row) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0;
+}
+
+// Zero gradient of tiles first, first + step, ... of a row and, in the thread
+// group that has tile 0, of its ends.  One warp.
+template <typename T>
+__device__ __forceinline__ void distill_zero(const RowView<T>& row, T* g, int first, int step) {
+    const int lane = threadIdx.x & 31;
+    const bool aligned = same_alignment(row, g);
+    for (int v0 = first * kDsTile * 32; v0 < row.nvec; v0 += step * kDsTile * 32)
+#pragma unroll
+        for (int j = 0; j < kDsTile; ++j) {
+            const int v = v0 + j * 32 + lane;
+            T* at = g + row.head + (size_t)v * ElemT<T>::VEC;
+            if (v >= row.nvec) continue;
+            if (aligned) {
+                *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < ElemT<T>::VEC; ++i) store_elem(at + i, 0.0f);
+            }
+        }
+    if (first == 0) {
+        if (lane < row.head) store_elem(g + lane, 0.0f);
+        if (lane < row.tail) store_elem(g + row.head + row.nvec * ElemT<T>::VEC + lane, 0.0f);
+    }
+}
+
+// Loss and, with GRAD, gradient of a row, by a CTA or a cluster of S.
+//
+// Each warp has every (8 S)-th tile of the row.  It sets the listed tokens of
+// a tile to -inf in shared memory, so that what it sums is the tail.  With
+// GRAD all of its tiles stay there: the sums are exchanged (every CTA of the
+// cluster gets every warp's), and the gradient is written from the same copy
+// of the row, which is read once from memory.  Bound by memory: an element's
+// 2 bytes (bf16) in and 2 out.
+template <typename T, bool CLUSTER, bool GRAD>
+__global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArgs a, int n_buf) {
+    constexpr int VEC = ElemT<T>::VEC;
+    extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps][n_buf] tiles
     __shared__ DsSmem sm;
-    const int r = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
+    const int r = blockIdx.x / S;
+    const int unit = part * kDsWarps + warp, units = S * kDsWarps;
     const float w = a.weights ? a.weights[r] : 1.0f;
+    const RowView<T> row(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V);
+    T* g = GRAD ? static_cast<T*>(a.grad) + (size_t)r * a.grad_stride : nullptr;
     if (w == 0.0f) {
-        if (tid == 0) {
+        if (part == 0 && tid == 0) {
             a.loss[r] = 0.0f;
             if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = DistillStat{};
         }
-        distill_zero_grad<T>(a, r);
+        if (GRAD && warp < kDsWarps) distill_zero(row, g, unit, units);
         return;
     }
-    const T* row = static_cast<const T*>(a.student) + (size_t)r * a.stride;
-    for (int i = tid; i < (a.V + 31) / 32; i += kDsThreads) listed[i] = 0u;
-    if (tid == 0) sm.bad = 0;
-    __syncthreads();
-    for (int j = tid; j < a.K; j += kDsThreads) {
-        const int v = a.ids[(size_t)r * a.K + j];
-        sm.l[j] = a.teacher[(size_t)r * a.K + j];
-        sm.id[j] = v;
-        if (v == -1) continue;
-        if (v < 0 || v >= a.V || ((atomicOr(&listed[v >> 5], 1u << (v & 31)) >> (v & 31)) & 1u)) {
-            sm.bad = kDevErrToken;
-            sm.id[j] = -1;
-        } else {
-            sm.s[j] = ElemT<T>::load(row + v);
+    if (CLUSTER) cluster_arrive();  // awaited before the first store into another CTA
+
+    const int tiles = (row.nvec + kDsTile * 32 - 1) / (kDsTile * 32);
+    const uint4* vecs = row.vec();
+    uint4* ring = reinterpret_cast<uint4*>(ds_raw) + (size_t)warp * n_buf * (kDsTileBytes / 16);
+    int ids[kDsIds];
+    float2 ends = make_float2(-INFINITY, -INFINITY);  // this lane's element of the head and of the tail
+    const int tail0 = row.head + row.nvec * VEC;
+    // Listed tokens of elements [e0, e0 + n): f(k, offset) for this lane's
+    auto listed_in = [&](int e0, int n, auto&& f) {
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k)
+            if ((unsigned)(ids[k] - e0) < (unsigned)n) {
+                f(k, ids[k] - e0);
+                any = true;
+            }
+        return any;
+    };
+    if (warp < kDsWarps) {
+        uint64_t* bars = sm.full[warp];
+        auto copy = [&](int t, int b) {  // lane 0
+            const int v0 = t * kDsTile * 32;
+            const uint32_t bytes = (uint32_t)min(kDsTile * 32, row.nvec - v0) * 16;
+            mbar_arrive_expect_tx(&bars[b], bytes);
+            bulk_load(ring + b * (kDsTileBytes / 16), vecs + v0, bytes, &bars[b]);
+        };
+        if (lane == 0) {
+            for (int b = 0; b < n_buf; ++b) mbar_init(&bars[b], 1);
+            mbar_fence_init();
+            for (int b = 0; b < n_buf && unit + b * units < tiles; ++b) copy(unit + b * units, b);
         }
-    }
-    __syncthreads();
-    const int bad_id = sm.bad;
-    float m = kNoMax, z = 0.0f;
-    for (int i = tid; i < a.V; i += kDsThreads) {
-        if ((listed[i >> 5] >> (i & 31)) & 1u) continue;
-        const float x = ElemT<T>::load(row + i);
-        if (x > m) {
-            z *= ex2(fmaxf((m - x) * a.c, -1000.0f));
-            m = x;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k) {
+            const int j = lane + 32 * k;
+            ids[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
         }
-        z += ex2((x - m) * a.c);
+        DsSum sum;
+        if (unit == 0) {
+            if (lane < row.head) ends.x = ElemT<T>::load(row.row + lane);
+            if (lane < row.tail) ends.y = ElemT<T>::load(row.row + tail0 + lane);
+            uint32_t in_head = 0, in_tail = 0;
+            listed_in(0, row.head, [&](int, int o) { in_head |= 1u << o; });
+            listed_in(tail0, row.tail, [&](int, int o) { in_tail |= 1u << o; });
+            in_head = __reduce_or_sync(0xffffffffu, in_head);
+            in_tail = __reduce_or_sync(0xffffffffu, in_tail);
+            if ((in_head >> lane) & 1u) ends.x = -INFINITY;
+            if ((in_tail >> lane) & 1u) ends.y = -INFINITY;
+            const float m = warp_max_redux(fmaxf(ends.x, ends.y));
+            if (m > sum.m) sum.raise(m, a.c);
+            sum.exact(a.c);
+            sum.z.x += ex2((ends.x - sum.m) * a.c);
+            sum.z.y += ex2((ends.y - sum.m) * a.c);
+            if (sum.m > kNoMax) sum.raise(sum.m, a.c);  // back to one operation per pair
+        }
+        bool ok = true;
+        int b = 0;
+        uint32_t parity = 0;
+        for (int t = unit; t < tiles; t += units) {
+            ok = mbar_wait(&bars[b], parity, kDsLimitNs);
+            if (!ok) break;
+            uint4* at = ring + b * (kDsTileBytes / 16);
+            const int v0 = t * kDsTile * 32, nv = min(kDsTile * 32, row.nvec - v0);
+            const bool any = listed_in(row.head + v0 * VEC, nv * VEC,
+                                       [&](int, int o) { reinterpret_cast<T*>(at)[o] = T(-INFINITY); });
+            if (__any_sync(0xffffffffu, any) && !GRAD) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            uint4 q[kDsTile];
+            if (nv == kDsTile * 32) {
+#pragma unroll
+                for (int j = 0; j < kDsTile; ++j) q[j] = at[j * 32 + lane];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kDsTile; ++j) q[j] = j * 32 + lane < nv ? at[j * 32 + lane] : RowVec<T>::none();
+            }
+            if (!GRAD) {  // every lane has its vectors: the buffer takes the next tile
+                __syncwarp();
+                if (lane == 0 && t + n_buf * units < tiles) copy(t + n_buf * units, b);
+            }
+            const float m = tile_max<T, kDsTile>(q);
+            if (m > sum.m) sum.raise(m, a.c);
+            sum.add<T, kDsTile>(q, a.c);
+            if (++b == n_buf) {
+                b = 0;
+                parity ^= 1;
+            }
+        }
+        if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
+            if (lane == 0) {
+                if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+                for (int i = 0; i < n_buf; ++i) {
+                    mbar_wait(&bars[b], parity, kDsLimitNs);
+                    if (++b == n_buf) {
+                        b = 0;
+                        parity ^= 1;
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        sum.exact(a.c);
+        const float2 p = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);
+        if (CLUSTER) {
+            cluster_wait();
+            if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), p);
+        } else if (lane == 0) {
+            sm.part[unit] = p;
+        }
+    } else {
+        distill_teacher<T>(a, r, row.row, sm);
+        __syncwarp();
+        if (CLUSTER) cluster_wait();
     }
-    sm.m[tid] = m;
-    sm.z[tid] = z;
-    for (int o = kDsThreads / 2; o > 0; o >>= 1) {
+    if (CLUSTER) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
-        if (tid < o) {
-            const float m2 = fmaxf(sm.m[tid], sm.m[tid + o]);
-            sm.z[tid] = sm.z[tid] * ex2(fmaxf((sm.m[tid] - m2) * a.c, -1000.0f)) +
-                        sm.z[tid + o] * ex2(fmaxf((sm.m[tid + o] - m2) * a.c, -1000.0f));
-            sm.m[tid] = m2;
+    }
+
+    if (warp == kDsWarps ? part != 0 : !GRAD) return;
+    DsSums sums;
+    const DistillStat st = distill_stat(a, sm, units, &sums);
+    if (warp == kDsWarps) {
+        const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums) : 0.0f;
+        if (lane == 0) {
+            a.loss[r] = loss;
+            if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
+            if (sums.err && a.dev_error) atomicOr(a.dev_error, sums.err);
         }
+        return;
     }
-    __syncthreads();
-    if (tid < 32) distill_finish(a, sm.m[0], sm.z[0], sm.s, sm.l, sm.id, &sm.st, &sm.loss, &sm.bad);
-    __syncthreads();
-    const int bad = sm.bad | bad_id;
-    const DistillStat st = bad ? DistillStat{} : sm.st;
-    if (tid == 0) {
-        a.loss[r] = bad ? 0.0f : sm.loss;
-        if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
-        if (bad && a.dev_error) atomicOr(a.dev_error, bad);
+    if (st.live == 0.0f) {
+        distill_zero(row, g, unit, units);
+        return;
     }
-    if (!a.grad) return;
-    if (st.live == 0.0f)
-        distill_zero_grad<T>(a, r);
-    else
-        distill_write_grad<T>(a, r, st, w, sm);
+    const bool aligned = same_alignment(row, g);
+    const float coef = w * st.coef;
+    auto listed = [&](T* g0, int e0, int n) {  // overwrites what was stored for them as tail tokens
+        __syncwarp();
+        listed_in(e0, n, [&](int k, int o) {
+            const int j = lane + 32 * k;
+            store_elem(g0 + o, distill_listed_grad(st, sm.s[j], sm.t[j], a.c, (float)a.inv_t, w));
+        });
+    };
+    if (unit == 0) {
+        if (lane < row.head) store_elem(g + lane, coef * ex2((ends.x - st.m_tail) * a.c));
+        if (lane < row.tail) store_elem(g + tail0 + lane, coef * ex2((ends.y - st.m_tail) * a.c));
+        listed(g, 0, row.head);
+        listed(g + tail0, tail0, row.tail);
+    }
+    int b = 0;
+    for (int t = unit; t < tiles; t += units, ++b) {
+        const uint4* at = ring + b * (kDsTileBytes / 16);
+        const int v0 = t * kDsTile * 32;
+        T* g0 = g + row.head + (size_t)v0 * VEC;
+#pragma unroll
+        for (int j = 0; j < kDsTile; ++j) {
+            const int v = j * 32 + lane;
+            if (v0 + v < row.nvec) distill_store(g0 + v * VEC, at[v], coef, st.m_tail, a.c, aligned);
+        }
+        listed(g0, row.head + v0 * VEC, min(kDsTile * 32, row.nvec - v0) * VEC);
+    }
 }
 
+// The gradient alone, from a row's statistics: a warp per tile, a CTA per
+// stretch of a row.  Reads and writes an element once.
+constexpr int kDbThreads = 256;
+constexpr int kDbTiles = 4;  // tiles a warp takes
+
 template <typename T>
-__global__ void __launch_bounds__(kDsThreads) k_distill_backward(DistillArgs a) {
-    __shared__ DsSmem sm;
-    const int r = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, int stretches) {
+    constexpr int VEC = ElemT<T>::VEC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.x / stretches, stretch = blockIdx.x - r * stretches;
+    const int unit = stretch * (kDbThreads / 32) + warp, units = stretches * (kDbThreads / 32);
+    const RowView<T> row(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V);
+    T* g = static_cast<T*>(a.grad) + (size_t)r * a.grad_stride;
     const float w = a.weights ? a.weights[r] : 1.0f;
     const DistillStat st = reinterpret_cast<const DistillStat*>(a.stats)[r];
     if (w == 0.0f || st.live == 0.0f) {
-        distill_zero_grad<T>(a, r);
+        distill_zero(row, g, unit, units);
         return;
     }
-    const T* row = static_cast<const T*>(a.student) + (size_t)r * a.stride;
-    for (int j = tid; j < a.K; j += kDsThreads) {
-        const int v = a.ids[(size_t)r * a.K + j];
-        sm.id[j] = v < a.V ? v : -1;
-        sm.l[j] = a.teacher[(size_t)r * a.K + j];
-        if (v >= 0 && v < a.V) sm.s[j] = ElemT<T>::load(row + v);
+    int ids[kDsIds];
+#pragma unroll
+    for (int k = 0; k < kDsIds; ++k) {
+        const int j = lane + 32 * k;
+        ids[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
     }
-    __syncthreads();
-    distill_write_grad<T>(a, r, st, w, sm);
+    const bool aligned = same_alignment(row, g);
+    const float coef = w * st.coef;
+    // The listed tokens of a piece of the row: their gradients are taken
+    // from the logits before put() stores over the piece (grad may be the
+    // student's buffer), and stored after it.
+    auto with_listed = [&](int e0, int n, auto&& put) {
+        float y[kDsIds];
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k)
+            if ((unsigned)(ids[k] - e0) < (unsigned)n) {
+                const size_t j = (size_t)r * a.K + lane + 32 * k;
+                const float t = expf(a.teacher[j] - st.ln_t);
+                y[k] = distill_listed_grad(st, ElemT<T>::load(row.row + ids[k]), t, a.c, (float)a.inv_t, w);
+            }
+        __syncwarp();
+        put();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k)
+            if ((unsigned)(ids[k] - e0) < (unsigned)n) store_elem(g + ids[k], y[k]);
+    };
+    if (unit == 0) {
+        const int tail0 = row.head + row.nvec * VEC;
+        with_listed(0, row.head, [&] {
+            if (lane < row.head) store_elem(g + lane, coef * ex2((ElemT<T>::load(row.row + lane) - st.m_tail) * a.c));
+        });
+        with_listed(tail0, row.tail, [&] {
+            if (lane < row.tail)
+                store_elem(g + tail0 + lane, coef * ex2((ElemT<T>::load(row.row + tail0 + lane) - st.m_tail) * a.c));
+        });
+    }
+    for (int t = unit; t * kDsTile * 32 < row.nvec; t += units) {
+        const int v0 = t * kDsTile * 32, nv = min(kDsTile * 32, row.nvec - v0);
+        uint4 q[kDsTile];
+#pragma unroll
+        for (int j = 0; j < kDsTile; ++j)
+            q[j] = j * 32 + lane < nv ? *(row.vec() + v0 + j * 32 + lane) : RowVec<T>::none();
+        with_listed(row.head + v0 * VEC, nv * VEC, [&] {
+#pragma unroll
+            for (int j = 0; j < kDsTile; ++j)
+                if (j * 32 + lane < nv)
+                    distill_store(g + row.head + (size_t)(v0 + j * 32 + lane) * VEC, q[j], coef, st.m_tail, a.c, aligned);
+        });
+    }
+}
+
+template <typename T, bool GRAD>
+static cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st) {
+    const int tiles = (a.V / ElemT<T>::VEC + kDsTile * 32 - 1) / (kDsTile * 32);
+    LaunchShape shape;
+    const size_t most = (size_t)kDsWarps * kDsTileBytes * (GRAD ? kDsMaxTiles : kDsRing);
+    if (!launch_shape(reinterpret_cast<const void*>(k_distill<T, false, GRAD>), most, kDsThreads, &shape) ||
+        !launch_shape(reinterpret_cast<const void*>(k_distill<T, true, GRAD>), most, kDsThreads, &shape))
+        return cudaErrorUnknown;
+    // CTAs that share a row.  With the gradient: enough that three rows' parts
+    // fit on an SM (four tiles a warp), so that one CTA's exchange hides behind
+    // the others' copies.  And, where rows are few, enough for every SM.
+    int S = 1;
+    if (GRAD)
+        while (S < kDsMaxCluster && tiles > 4 * S * kDsWarps) S *= 2;
+    if (GRAD && S > 8 && tiles <= kDsMaxTiles * 8 * kDsWarps) S = 8;  // 16 only where 8 do not hold the row
+    while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
+    if (getenv("DS_S")) S = atoi(getenv("DS_S"));
+    const int each = (tiles + S * kDsWarps - 1) / (S * kDsWarps);  // tiles of a warp
+    const int n_buf = GRAD ? (each > 0 ? each : 1) : kDsRing;
+    const size_t dyn = (size_t)kDsWarps * kDsTileBytes * n_buf;
+    if (S == 1) {
+        k_distill<T, false, GRAD><<<a.R, kDsThreads, dyn, st>>>(a, n_buf);
+        return cudaGetLastError();
+    }
+    auto* kern = k_distill<T, true, GRAD>;
+    if (S > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.R * S);
+    cfg.blockDim = dim3(kDsThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, n_buf);
+}
+
+template <typename T>
+static cudaError_t launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
+    const int tiles = (a.V / ElemT<T>::VEC + kDsTile * 32 - 1) / (kDsTile * 32);
+    const int per = (kDbThreads / 32) * kDbTiles, stretches = tiles > per ? (tiles + per - 1) / per : 1;
+    k_distill_backward<T><<<(unsigned)a.R * stretches, kDbThreads, 0, st>>>(a, stretches);
+    return cudaGetLastError();
 }
 
 static spec_status check_distill(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,
@@ -287,14 +652,14 @@ extern "C" spec_status spec_distill_topk(const void* student, spec_dtype dtype, 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dev_error && cudaMemsetAsync(dev_error, 0, sizeof(int32_t), st) != cudaSuccess) return SPEC_ERR_CUDA;
     if (R == 0) return SPEC_OK;
+    const float c = (float)(kLog2e / (double)temperature);
     DistillArgs a{student, R, V, K, row_stride, teacher_ids, teacher_logprobs, weights,
-                  (float)(kLog2e / (double)temperature), 1.0 / (double)temperature, tail == SPEC_TAIL_BUCKET,
+                  c, (double)c * 0.69314718055994531, tail == SPEC_TAIL_BUCKET,
                   loss, row_stats, grad, grad_stride, dev_error};
-    const size_t dyn = (size_t)((V + 31) / 32) * 4;
-    auto* kern = dtype == SPEC_BF16 ? k_distill<__nv_bfloat16> : k_distill<float>;
-    if (!set_dyn_smem(kern, (size_t)((kRowsMaxVocab + 31) / 32) * 4, kDsThreads)) return SPEC_ERR_CUDA;
-    kern<<<R, kDsThreads, dyn, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    const bool bf16 = dtype == SPEC_BF16;
+    const cudaError_t e = grad ? (bf16 ? launch_distill<__nv_bfloat16, true>(a, st) : launch_distill<float, true>(a, st))
+                               : (bf16 ? launch_distill<__nv_bfloat16, false>(a, st) : launch_distill<float, false>(a, st));
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 extern "C" spec_status spec_distill_topk_backward(const void* student, spec_dtype dtype, int R, int V,
@@ -310,12 +675,12 @@ extern "C" spec_status spec_distill_topk_backward(const void* student, spec_dtyp
     if (!row_stats || !grad) return SPEC_ERR_INVALID_ARG;
     if (!select_device_of(student)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const float c = (float)(kLog2e / (double)temperature);
     DistillArgs a{student, R, V, K, row_stride, teacher_ids, teacher_logprobs, grad_loss,
-                  (float)(kLog2e / (double)temperature), 1.0 / (double)temperature, false, nullptr,
+                  c, (double)c * 0.69314718055994531, false, nullptr,
                   const_cast<float*>(row_stats), grad, grad_stride, nullptr};
-    if (dtype == SPEC_BF16)
-        k_distill_backward<__nv_bfloat16><<<R, kDsThreads, 0, st>>>(a);
-    else
-        k_distill_backward<float><<<R, kDsThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return (dtype == SPEC_BF16 ? launch_distill_backward<__nv_bfloat16>(a, st)
+                               : launch_distill_backward<float>(a, st)) == cudaSuccess
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }

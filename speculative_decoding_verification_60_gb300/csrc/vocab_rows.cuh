@@ -111,6 +111,15 @@ template <> struct RowVec<float> {
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
+// Maximum over a warp's tile of N vectors a lane.
+template <typename T, int N>
+__device__ __forceinline__ float tile_max(const uint4* q) {
+    float m = RowVec<T>::max(q[0]);
+#pragma unroll
+    for (int j = 1; j < N; ++j) m = fmaxf(m, RowVec<T>::max(q[j]));
+    return warp_max_redux(m);
+}
+
 // (logit descending, index ascending) as one integer: larger = earlier.
 // Zero is below every entry's key.
 __device__ __forceinline__ uint64_t order_key(float x, int idx) {
