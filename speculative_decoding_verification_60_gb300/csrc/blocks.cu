@@ -8,7 +8,7 @@
 namespace sv {
 
 constexpr int kDevErrCapacity = 32;
-constexpr int kBlThreads = 1024;
+constexpr int kBlTokens = 4;  // consecutive tokens of a thread
 constexpr int kBlMaxRequests = 16384;
 
 struct BlocksArgs {
@@ -31,6 +31,7 @@ struct BlocksArgs {
     int32_t* positions;
     int max_tokens;
     int32_t* dev_error;
+    bool aligned;  // slots and positions on 16 bytes
 };
 
 // One request's step before the free list is looked at.
@@ -64,28 +65,35 @@ __device__ __forceinline__ BlocksRequest blocks_request(const BlocksArgs& a, int
     return q;
 }
 
-// Inclusive prefix sums of x and y over the CTA's threads in thread order.
-__device__ __forceinline__ void block_scan2(int& x, int& y, int2* part) {
+// Exclusive prefix sums of x and y over the CTA's threads in thread order;
+// *total receives the sums.
+template <int NT>
+__device__ __forceinline__ int2 block_scan2(int x, int y, int2* part, int2* total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    x = warp_inclusive_scan_i(x);
-    y = warp_inclusive_scan_i(y);
-    __syncthreads();
-    if (lane == 31) part[w] = make_int2(x, y);
+    const int ix = warp_inclusive_scan_i(x), iy = warp_inclusive_scan_i(y);
+    if (lane == 31) part[w] = make_int2(ix, iy);
     __syncthreads();
     if (w == 0) {
-        int2 p = part[lane];
+        int2 p = lane < NT / 32 ? part[lane] : make_int2(0, 0);
         p.x = warp_inclusive_scan_i(p.x);
         p.y = warp_inclusive_scan_i(p.y);
         part[lane] = p;
     }
     __syncthreads();
-    if (w > 0) {
-        x += part[w - 1].x;
-        y += part[w - 1].y;
-    }
+    *total = part[NT / 32 - 1];
+    const int2 before = w > 0 ? part[w - 1] : make_int2(0, 0);
+    return make_int2(before.x + ix - x, before.y + iy - y);
 }
 
-__global__ void __launch_bounds__(kBlThreads) k_advance_blocks(BlocksArgs a) {
+// Every CTA sums the requests for itself (they are few and in L2; a second
+// launch, or a wait for another CTA's sums, would cost more), keeps where
+// each one's tokens and new blocks begin in shared memory, and then takes its
+// share of the tokens and of the table entries.  The block of a new entry
+// comes from the free list, not from the table, so no CTA reads what another
+// writes.  CTA 0 writes the per-request outputs.  Bound by launch latency for
+// a decoding step, by the 12 bytes written per token for long prompts.
+template <int NT>
+__global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
     __shared__ int2 part[32];
     __shared__ int sh_err, sh_taken;
     extern __shared__ int sh_mem[];
@@ -95,63 +103,114 @@ __global__ void __launch_bounds__(kBlThreads) k_advance_blocks(BlocksArgs a) {
     const int free_count = count >= 0 && count <= a.free_capacity ? count : 0;
     if (tid == 0) {
         sh_err = count == free_count ? 0 : kDevErrLength;
-        sh_taken = cu[0] = 0;
+        sh_taken = 0;
     }
-    __syncthreads();
-    int tokens = 0, lacking = 0;  // of the requests before this round's
-    for (int b0 = 0; b0 < a.B; b0 += kBlThreads) {
-        const int b = b0 + tid;
-        BlocksRequest q{};
-        if (b < a.B) q = blocks_request(a, b);
-        int x = q.n, y = q.lacks;
-        block_scan2(x, y, part);
-        if (b < a.B) {
-            const int end = lacking + y;
-            const bool served = !q.err && (q.lacks == 0 || end <= free_count);
-            cu[b + 1] = tokens + x;
-            first[b] = served ? end - q.lacks : -1;
-            if (!served) atomicOr(&sh_err, q.err ? q.err : kDevErrCapacity);
-            if (served && q.lacks) atomicMax(&sh_taken, end);
+    const int each = (a.B + NT - 1) / NT, b0 = tid * each, b1 = min(b0 + each, a.B);
+    int x = 0, y = 0;
+    for (int b = b0; b < b1; ++b) {
+        const BlocksRequest q = blocks_request(a, b);
+        x += q.n;
+        y += q.lacks;
+    }
+    int2 total;
+    int2 at = block_scan2<NT>(x, y, part, &total);
+    const int tokens = total.x;
+    int err = 0, taken = 0;
+    for (int b = b0; b < b1; ++b) {
+        const BlocksRequest q = blocks_request(a, b);
+        const bool served = !q.err && (q.lacks == 0 || at.y + q.lacks <= free_count);
+        cu[b] = at.x;
+        first[b] = served ? at.y : -1;
+        at.x += q.n;
+        at.y += q.lacks;
+        if (!served) err |= q.err ? q.err : kDevErrCapacity;
+        if (served && q.lacks) taken = at.y;
+        if (blockIdx.x == 0) {
+            a.cu_tokens[b] = cu[b];
             a.out_lens[b] = q.len;
             a.out_held[b] = q.held + (served ? q.lacks : 0);
-            if (served)
-                for (int j = 0; j < q.lacks; ++j)
-                    a.table[b * a.table_stride + q.held + j] = a.free_blocks[free_count - 1 - (end - q.lacks + j)];
         }
-        tokens += part[31].x;
-        lacking += part[31].y;
-        __syncthreads();
     }
-    for (int b = tid; b <= a.B; b += kBlThreads) a.cu_tokens[b] = cu[b];
-    if (tid == 0) {
+    if (blockIdx.x == 0) {
+        err = __reduce_or_sync(0xffffffffu, err);
+        taken = __reduce_max_sync(0xffffffffu, taken);
+        if ((tid & 31) == 0 && err) atomicOr(&sh_err, err);
+        if ((tid & 31) == 0 && taken) atomicMax(&sh_taken, taken);
+    }
+    if (tid == 0) cu[a.B] = tokens;
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) {
+        a.cu_tokens[a.B] = tokens;
         *a.out_free = free_count - sh_taken;
         if (a.dev_error) *a.dev_error = sh_err | (tokens > a.max_tokens ? kDevErrLength : 0);
     }
-    for (int i = tid; i < a.max_tokens; i += kBlThreads) {
-        int64_t slot = -1;
-        int position = 0;
-        if (i < tokens) {
-            int lo = 0, hi = a.B - 1;  // the last request that starts at or before i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (cu[mid] <= i) lo = mid;
+    // new table entries: a warp per request
+    for (int b = blockIdx.x * (NT / 32) + (tid >> 5); b < a.B; b += gridDim.x * (NT / 32)) {
+        if (first[b] < 0) continue;
+        const BlocksRequest q = blocks_request(a, b);
+        for (int j = tid & 31; j < q.lacks; j += 32)
+            a.table[b * a.table_stride + q.held + j] = a.free_blocks[free_count - 1 - (first[b] + j)];
+    }
+    // slots: consecutive tokens of a thread, mostly of one request
+    for (int i0 = (blockIdx.x * NT + tid) * kBlTokens; i0 < a.max_tokens; i0 += gridDim.x * NT * kBlTokens) {
+        int b = 0;
+        if (i0 < tokens) {  // the last request that starts at or before i0
+            int hi = a.B - 1;
+            while (b < hi) {
+                const int mid = (b + hi + 1) >> 1;
+                if (cu[mid] <= i0) b = mid;
                 else hi = mid - 1;
             }
-            const BlocksRequest q = blocks_request(a, lo);
-            const int at = i - cu[lo];
-            if (q.err != kDevErrLength && at >= 0 && at < q.n) {
-                position = q.len + at;
-                if (first[lo] >= 0) {
-                    const int j = position / a.page;
-                    const int block = j < q.held ? a.table[lo * a.table_stride + j]
-                                                 : a.free_blocks[free_count - 1 - (first[lo] + j - q.held)];
-                    slot = (int64_t)block * a.page + (position - j * a.page);
-                }
-            }
         }
-        a.slots[i] = slot;
-        if (a.positions) a.positions[i] = position;
+        BlocksRequest q = blocks_request(a, b);
+        int64_t slot[kBlTokens];
+        int position[kBlTokens];
+#pragma unroll
+        for (int k = 0; k < kBlTokens; ++k) {
+            const int i = i0 + k;
+            slot[k] = -1;
+            position[k] = 0;
+            if (i >= tokens) continue;
+            if (i >= cu[b + 1]) {
+                while (i >= cu[b + 1] && b < a.B - 1) ++b;
+                q = blocks_request(a, b);
+            }
+            const int in = i - cu[b];
+            if (q.err == kDevErrLength || in < 0 || in >= q.n) continue;
+            position[k] = q.len + in;
+            if (first[b] < 0) continue;
+            const int j = position[k] / a.page;
+            const int block = j < q.held ? a.table[b * a.table_stride + j]
+                                         : a.free_blocks[free_count - 1 - (first[b] + j - q.held)];
+            slot[k] = (int64_t)block * a.page + (position[k] - j * a.page);
+        }
+        if (a.aligned && i0 + kBlTokens <= a.max_tokens) {
+            longlong2* s = reinterpret_cast<longlong2*>(a.slots + i0);
+            s[0] = make_longlong2(slot[0], slot[1]);
+            s[1] = make_longlong2(slot[2], slot[3]);
+            if (a.positions)
+                *reinterpret_cast<int4*>(a.positions + i0) = make_int4(position[0], position[1], position[2], position[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kBlTokens; ++k)
+                if (i0 + k < a.max_tokens) {
+                    a.slots[i0 + k] = slot[k];
+                    if (a.positions) a.positions[i0 + k] = position[k];
+                }
+        }
     }
+}
+
+template <int NT>
+static cudaError_t launch_blocks(const BlocksArgs& a, cudaStream_t st) {
+    LaunchShape shape;
+    if (!launch_shape(reinterpret_cast<const void*>(k_advance_blocks<NT>), (size_t)(2 * kBlMaxRequests + 1) * 4, NT, &shape))
+        return cudaErrorUnknown;
+    // a CTA per NT * kBlTokens tokens, at most one an SM
+    const long long want = ((long long)a.max_tokens + NT * kBlTokens - 1) / (NT * kBlTokens);
+    const int grid = (int)(want < 1 ? 1 : want < shape.sms ? want : shape.sms);
+    k_advance_blocks<NT><<<grid, NT, (size_t)(2 * a.B + 1) * 4, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace sv
@@ -177,9 +236,10 @@ extern "C" spec_status spec_advance_blocks(const int32_t* seq_lens, const int32_
     if (!select_device_of(seq_lens)) return SPEC_ERR_INVALID_ARG;
     BlocksArgs a{seq_lens, accepted_len, new_tokens, B, page_size, block_table, max_blocks, table_stride, held,
                  free_blocks, free_capacity, free_count, out_seq_lens, out_held, out_free_count, cu_tokens, slots, positions,
-                 max_tokens, dev_error};
-    const size_t dyn = (size_t)(2 * B + 1) * 4;
-    if (!set_dyn_smem(k_advance_blocks, (size_t)(2 * kBlMaxRequests + 1) * 4, kBlThreads)) return SPEC_ERR_CUDA;
-    k_advance_blocks<<<1, kBlThreads, dyn, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+                 max_tokens, dev_error,
+                 ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 15u) == 0};
+    // Few requests and tokens: smaller CTAs start and meet faster.
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool few = B <= 1024 && max_tokens <= 65536;
+    return (few ? launch_blocks<256>(a, st) : launch_blocks<1024>(a, st)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -7,7 +7,6 @@
 // the K listed ones.  The tail's mass q_T is then a sum of its own terms,
 // where 1 - sum q_j would cancel, and the gradient of every tail token is
 // one coefficient times 2^((s - m_T) c).
-#include <stdlib.h>
 #include "cluster.cuh"
 #include "vocab_rows.cuh"
 
@@ -46,11 +45,11 @@ static_assert(sizeof(DistillStat) == 32, "row_stats is [R, 8] float");
 
 constexpr int kDsWarps = 8;                          // that take tiles
 constexpr int kDsThreads = (kDsWarps + 1) * 32;      // and one for the teacher and the loss
-constexpr int kDsTile = 4;                           // vectors a lane takes of a tile: 2 KiB a warp
+constexpr int kDsTile = 8;                           // vectors a lane takes of a tile: 4 KiB a warp
 constexpr int kDsTileBytes = kDsTile * 512;
 constexpr int kDsMaxCluster = 16;
-constexpr int kDsMaxTiles = 12;                      // of a warp, when the row stays on the chip
-constexpr int kDsRing = 3;                           // tiles of a warp on their way, when it does not
+constexpr int kDsMaxTiles = 6;                       // of a warp, when the row stays on the chip
+constexpr int kDsRing = 1;                           // tiles of a warp on their way, when it does not
 constexpr int kDsIds = kMaxTop / 32;                 // listed tokens a lane looks after
 constexpr uint64_t kDsLimitNs = 2000000000ull;
 constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x c - m c in one operation
@@ -61,13 +60,16 @@ constexpr float kTailRounding = 1.0f / 65536.0f;
 
 struct DsSmem {
     float2 part[kDsMaxCluster * kDsWarps];  // every warp's maximum and sum of the tail
-    float s[kMaxTop], l[kMaxTop], t[kMaxTop];  // listed tokens: student logit, teacher's value and probability
-    int id[kMaxTop];
+    float s[kMaxTop], l[kMaxTop];  // listed tokens: student logit, teacher's value
+    alignas(16) int id[kMaxTop];
     uint64_t full[kDsWarps][kDsMaxTiles];
+    float4 teacher;             // from the first CTA: see DsTeacher
+    float bad[kDsMaxCluster];   // from every CTA: error bits of its share of the checks
+};
+// What the first CTA's extra warp finds about the teacher, as it is sent.
+struct DsTeacher {
     double mass;   // sum of t_j
-    double ln_t;   // subtracted from the teacher's values
-    float t_tail;  // 1 - mass (BUCKET)
-    int bad, dead;  // error bits of the teacher; no teacher mass at all
+    double ln_t;   // subtracted from the teacher's values; +inf: no teacher mass at all
 };
 
 __device__ __forceinline__ float warp_sum_f(float v) {
@@ -128,17 +130,19 @@ struct DsSum {
     }
 };
 
-// The teacher's side of a row, by one warp, while the row is on its way:
-// checks, student logits of the listed tokens, t_j and their sum (in double:
-// 1 - sum t cancels where the listed tokens hold nearly all of the teacher).
+// The teacher's side of a row, by one warp of each of the S CTAs while the
+// row is on its way: student logits of the listed tokens, checks (each CTA a
+// share of the search for doubles), and in the first CTA the sum of t_j (in
+// double: 1 - sum t cancels where the listed tokens hold nearly all of it).
 template <typename T>
-__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsSmem& sm) {
+__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsSmem& sm, int part, int S,
+                                                DsTeacher* out, int* err_out) {
     const int lane = threadIdx.x & 31;
     float lmax = kNoMax;
     int err = 0;
-    for (int j = lane; j < a.K; j += 32) {
-        int v = a.ids[(size_t)r * a.K + j];
-        const float l = a.teacher[(size_t)r * a.K + j];
+    for (int j = lane; j < kMaxTop; j += 32) {
+        int v = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
+        const float l = j < a.K ? a.teacher[(size_t)r * a.K + j] : 0.0f;
         if (v != -1 && (v < 0 || v >= a.V)) {
             err |= kDevErrToken;
             v = -1;
@@ -153,36 +157,40 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, con
     }
     lmax = warp_max(lmax);
     __syncwarp();
-    for (int j = lane; j < a.K; j += 32)
-        for (int i = 0; i < j; ++i)
-            if (sm.id[j] >= 0 && sm.id[i] == sm.id[j]) err |= kDevErrToken;
-    const double ref = a.bucket ? 0.0 : (double)lmax;
-    double mass = 0.0;
-    for (int j = lane; j < a.K; j += 32)
-        if (sm.id[j] >= 0) mass += exp((double)sm.l[j] - ref);
-    mass = warp_sum_d(mass);
-    if (!(mass < (double)INFINITY)) err |= kDevErrNonfinite;
-    err = __reduce_or_sync(0xffffffffu, err);
-    const double ln_t = a.bucket ? 0.0 : ref + log(mass);
-    for (int j = lane; j < a.K; j += 32) sm.t[j] = sm.id[j] >= 0 ? expf((float)((double)sm.l[j] - ln_t)) : 0.0f;
-    if (lane == 0) {
-        sm.mass = a.bucket ? mass : 1.0;
-        sm.t_tail = a.bucket ? (float)fmax(1.0 - mass, 0.0) : 0.0f;
-        sm.ln_t = ln_t;
-        sm.bad = err;
-        sm.dead = !a.bucket && !(mass > 0.0);
+    for (int j0 = 32 * part; j0 < a.K; j0 += 32 * S) {  // each id of 32 against all before it
+        const int v = sm.id[j0 + lane];
+        bool twice = false;
+#pragma unroll 4
+        for (int i = 0; i < j0 + 32; i += 4) {
+            const int4 u = *reinterpret_cast<const int4*>(sm.id + i);
+            const int at = j0 + lane - i;  // own place in u, if 0 .. 3
+            twice |= (u.x == v && at != 0) | (u.y == v && at != 1) | (u.z == v && at != 2) | (u.w == v && at != 3);
+        }
+        if (twice && v >= 0) err |= kDevErrToken;
     }
+    if (part == 0) {
+        const double ref = a.bucket ? 0.0 : (double)lmax;
+        double mass = 0.0;
+        for (int j = lane; j < a.K; j += 32)
+            if (sm.id[j] >= 0) mass += exp((double)sm.l[j] - ref);
+        mass = warp_sum_d(mass);
+        if (!(mass < (double)INFINITY)) err |= kDevErrNonfinite;
+        out->mass = a.bucket ? mass : 1.0;
+        out->ln_t = a.bucket ? 0.0 : mass > 0.0 ? ref + ln_of((float)mass) : (double)INFINITY;
+    }
+    *err_out = __reduce_or_sync(0xffffffffu, err);
 }
 
 // The row's statistics from every warp's part and the listed tokens, by each
 // warp for itself.
 struct DsSums {
     float z, z_tail;  // relative to m and to m_tail
-    float t_tail;
+    float t_tail;     // 1 - sum t_j (BUCKET)
     int err;          // error bits
 };
-__device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsSmem& sm, int n_parts, DsSums* sums) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsSmem& sm, int S, DsSums* sums) {
+    const int lane = threadIdx.x & 31, n_parts = S * kDsWarps;
+    const DsTeacher& te = reinterpret_cast<const DsTeacher&>(sm.teacher);
     DistillStat st{};
     float mt = kNoMax, ms = kNoMax;
     for (int k = lane; k < n_parts; k += 32) mt = fmaxf(mt, sm.part[k].x);
@@ -194,17 +202,22 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     for (int k = lane; k < n_parts; k += 32) zt += sm.part[k].y * ex2(fmaxf((sm.part[k].x - mt) * a.c, -1000.0f));
     for (int j = lane; j < a.K; j += 32)
         if (sm.id[j] >= 0) zs += ex2((sm.s[j] - m) * a.c);
-    zt = warp_sum_f(zt);
-    const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f)), z = warp_sum_f(zs) + in_tail;
-    const float t_tail = zt == 0.0f && sm.t_tail <= kTailRounding ? 0.0f : sm.t_tail;
-    *sums = DsSums{z, zt, t_tail, sm.bad};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        zt += __shfl_xor_sync(0xffffffffu, zt, o);
+        zs += __shfl_xor_sync(0xffffffffu, zs, o);
+    }
+    const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f)), z = zs + in_tail;
+    float t_tail = a.bucket ? (float)fmax(1.0 - te.mass, 0.0) : 0.0f;
+    if (zt == 0.0f && t_tail <= kTailRounding) t_tail = 0.0f;
+    *sums = DsSums{z, zt, t_tail, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
     if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
-    if (sums->err || sm.dead) return st;
+    if (sums->err || te.ln_t == (double)INFINITY) return st;
     st.m_tail = mt;
     st.m = m;
     st.inv_z = 1.0f / z;
-    st.mass = (float)(sm.mass + (double)t_tail);
-    st.ln_t = (float)sm.ln_t;
+    st.mass = (float)(te.mass + (double)t_tail);
+    st.ln_t = (float)te.ln_t;
     st.coef = zt > 0.0f ? (st.mass * (in_tail / z) - t_tail) * (float)a.inv_t / zt : 0.0f;
     st.live = 1.0f;
     return st;
@@ -215,11 +228,14 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
 __device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsSmem& sm, const DistillStat& st,
                                               const DsSums& sums) {
     const int lane = threadIdx.x & 31;
-    const double ln_z = ln_of(sums.z);
+    const double ln_z = ln_of(sums.z), ln_t = reinterpret_cast<const DsTeacher&>(sm.teacher).ln_t;
     double sum = 0.0;
-    for (int j = lane; j < a.K; j += 32)
-        if (sm.t[j] > 0.0f)
-            sum += (double)sm.t[j] * (((double)sm.l[j] - sm.ln_t) - ((double)(sm.s[j] - st.m) * a.inv_t - ln_z));
+    for (int j = lane; j < a.K; j += 32) {
+        if (sm.id[j] < 0) continue;
+        const double lt = (double)sm.l[j] - ln_t;
+        const float t = expf((float)lt);
+        if (t > 0.0f) sum += (double)t * (lt - ((double)(sm.s[j] - st.m) * a.inv_t - ln_z));
+    }
     sum = warp_sum_d(sum);
     if (sums.t_tail > 0.0f)
         sum = sums.z_tail > 0.0f
@@ -440,9 +456,21 @@ __global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArg
             sm.part[unit] = p;
         }
     } else {
-        distill_teacher<T>(a, r, row.row, sm);
+        DsTeacher te{};
+        int bad;
+        distill_teacher<T>(a, r, row.row, sm, part, S, &te, &bad);
+        const float4 message = *reinterpret_cast<const float4*>(&te);
         __syncwarp();
-        if (CLUSTER) cluster_wait();
+        if (CLUSTER) {
+            cluster_wait();
+            if (lane < S) {
+                cluster_store(cluster_map(&sm.bad[part], lane), __int_as_float(bad));
+                if (part == 0) cluster_store(cluster_map(&sm.teacher, lane), message);
+            }
+        } else if (lane == 0) {
+            sm.bad[0] = __int_as_float(bad);
+            sm.teacher = message;
+        }
     }
     if (CLUSTER) {
         cluster_arrive();
@@ -453,7 +481,7 @@ __global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArg
 
     if (warp == kDsWarps ? part != 0 : !GRAD) return;
     DsSums sums;
-    const DistillStat st = distill_stat(a, sm, units, &sums);
+    const DistillStat st = distill_stat(a, sm, S, &sums);
     if (warp == kDsWarps) {
         const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums) : 0.0f;
         if (lane == 0) {
@@ -473,7 +501,7 @@ __global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArg
         __syncwarp();
         listed_in(e0, n, [&](int k, int o) {
             const int j = lane + 32 * k;
-            store_elem(g0 + o, distill_listed_grad(st, sm.s[j], sm.t[j], a.c, (float)a.inv_t, w));
+            store_elem(g0 + o, distill_listed_grad(st, sm.s[j], expf(sm.l[j] - st.ln_t), a.c, (float)a.inv_t, w));
         });
     };
     if (unit == 0) {
@@ -576,14 +604,13 @@ static cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st) {
         !launch_shape(reinterpret_cast<const void*>(k_distill<T, true, GRAD>), most, kDsThreads, &shape))
         return cudaErrorUnknown;
     // CTAs that share a row.  With the gradient: enough that three rows' parts
-    // fit on an SM (four tiles a warp), so that one CTA's exchange hides behind
+    // fit on an SM (two tiles a warp), so that one CTA's exchange hides behind
     // the others' copies.  And, where rows are few, enough for every SM.
     int S = 1;
     if (GRAD)
-        while (S < kDsMaxCluster && tiles > 4 * S * kDsWarps) S *= 2;
+        while (S < kDsMaxCluster && tiles > 2 * S * kDsWarps) S *= 2;
     if (GRAD && S > 8 && tiles <= kDsMaxTiles * 8 * kDsWarps) S = 8;  // 16 only where 8 do not hold the row
     while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
-    if (getenv("DS_S")) S = atoi(getenv("DS_S"));
     const int each = (tiles + S * kDsWarps - 1) / (S * kDsWarps);  // tiles of a warp
     const int n_buf = GRAD ? (each > 0 ? each : 1) : kDsRing;
     const size_t dyn = (size_t)kDsWarps * kDsTileBytes * n_buf;
