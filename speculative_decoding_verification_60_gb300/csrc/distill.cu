@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArg
             }
             const float m = tile_max<T, kDsTile>(q);
             if (m > sum.m) sum.raise(m, a.c);
-            sum.add<T, kDsTile>(q, a.c);
+            if (m != -INFINITY) sum.add<T, kDsTile>(q, a.c);  // not all of it ruled out
             if (++b == n_buf) {
                 b = 0;
                 parity ^= 1;

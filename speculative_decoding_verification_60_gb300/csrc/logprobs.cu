@@ -37,7 +37,7 @@ struct LogprobArgs {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpTile = 6;   // groups of a tile: 3 KiB
-constexpr int kLpDepth = 2;  // tiles a warp has on their way
+constexpr int kLpDepth = 1;  // tiles a warp has on their way, beside the one in its registers
 constexpr int kLpTileBytes = kLpTile * 512;
 constexpr int kLpRing = kLpWarps * kLpDepth * kLpTileBytes;
 constexpr int kLpMaxCluster = 8;
@@ -48,9 +48,10 @@ constexpr float kLpFar = 200.0f;     // 2^-200 is zero
 // The K-th best group need not be found exactly: any bound that leaves K to
 // K + kLpSlack groups will do.
 constexpr int kLpSlack = 36;
-constexpr int kLpCands = 8 * (kMaxTop + kLpSlack);  // the elements of that many vectors
-constexpr int kLpBins = 256;        // of the groups' keys, from the largest down
-constexpr int kLpBinShift = 17;     // two bf16 values a bin: four binades in all
+constexpr int kLpCands = 8 * (kMaxTop + kLpSlack) + 16;  // the elements of that many vectors, and the ends
+constexpr int kLpBins = 256;
+constexpr uint32_t kLpNoneKey = 0x007fffffu;  // the order key of -inf
+constexpr int kLpBinShift = 17;  // keys a bin at first: two bf16 values, so four binades in all
 static_assert(kLpCands * 8 <= kLpRing, "the candidates take the ring's place");
 
 // What a warp makes of its groups.
@@ -73,28 +74,22 @@ struct LpRow : RowView<T> {
         if (lane < this->tail) e.y = ElemT<T>::load(this->row + this->head + this->nvec * ElemT<T>::VEC + lane);
         return e;
     }
-    // This lane's elements of group g: a vector (an end's single element
-    // first, the rest -inf), how many there are, the index of the first.
+    // This lane's vector of group g (1 .. nb), and whether it has one.
+    __device__ __forceinline__ bool has(int g) const { return (g - 1) * 32 + (int)(threadIdx.x & 31) < this->nvec; }
     __device__ __forceinline__ uint4 vector(int g) const {
-        const int lane = threadIdx.x & 31;
-        uint4 q = RowVec<T>::none();
-        if (g >= 1 && g <= nb) {
-            const int v = (g - 1) * 32 + lane;
-            if (v < this->nvec) q = __ldg(this->vec() + v);
-        } else if (lane < (g == 0 ? this->head : this->tail)) {
-            q.x = RowVec<T>::single(ElemT<T>::load(this->row + index(g)));
-        }
-        return q;
+        return has(g) ? __ldg(this->vec() + (g - 1) * 32 + (threadIdx.x & 31)) : RowVec<T>::none();
     }
-    __device__ __forceinline__ int count(int g) const {
-        const int lane = threadIdx.x & 31;
-        if (g >= 1 && g <= nb) return (g - 1) * 32 + lane < this->nvec ? ElemT<T>::VEC : 0;
-        return lane < (g == 0 ? this->head : this->tail) ? 1 : 0;
-    }
+    // Index of this lane's first element of group g, the ends' too.
     __device__ __forceinline__ int index(int g) const {
         const int lane = threadIdx.x & 31;
-        if (g >= 1 && g <= nb) return this->head + ((g - 1) * 32 + lane) * ElemT<T>::VEC;
-        return (g == 0 ? 0 : this->head + this->nvec * ElemT<T>::VEC) + lane;
+        return g == 0   ? lane
+               : g > nb ? this->head + this->nvec * ElemT<T>::VEC + lane
+                        : this->head + ((g - 1) * 32 + lane) * ElemT<T>::VEC;
+    }
+    // How many elements this lane has of group g, the ends' too.
+    __device__ __forceinline__ int count(int g) const {
+        if (g >= 1 && g <= nb) return has(g) ? ElemT<T>::VEC : 0;
+        return (int)(threadIdx.x & 31) < (g == 0 ? this->head : this->tail) ? 1 : 0;
     }
 };
 
@@ -106,6 +101,7 @@ __device__ __forceinline__ void lp_no_result(const LogprobArgs& a, int r, float 
         if (a.rank) a.rank[r] = -1;
         if (a.entropy) a.entropy[r] = 0.0f;
     }
+#pragma unroll 1
     for (int j = tid; j < a.top_k; j += n) {
         a.top_ids[(size_t)r * a.top_k + j] = -1;
         a.top_logprobs[(size_t)r * a.top_k + j] = -INFINITY;
@@ -157,34 +153,12 @@ struct LpSums {
     }
 };
 
-// A bound above which K .. K + slack keys lie, or, where many keys are
-// equal, the K-th largest key itself (then fewer than K lie above it).
-// count(b) is the number of keys >= b; K or more are >= lo (or there are
-// fewer than K), fewer than K are above hi.  Steps of growing width down from hi (the
-// first is half a binade), then halves.
 __device__ __forceinline__ int lp_slack(int K) { return min(kLpSlack, 4 + K / 4); }
-template <typename F>
-__device__ __forceinline__ uint32_t lp_bound(uint32_t lo, uint32_t hi, int K, F&& count) {
-    const int slack = lp_slack(K);
-    uint32_t step = 1u << 22;
-    while (lo < hi) {
-        const uint32_t mid = hi - lo > 2 * step ? hi - step : lo + (hi - lo) / 2 + 1;
-        const int n = count(mid);
-        if (n < K) {
-            hi = mid - 1;
-            step = step < (1u << 29) ? 4 * step : step;
-        } else if (n <= K + slack) {
-            return mid - 1;
-        } else {
-            lo = mid;
-        }
-    }
-    return lo;
-}
 
 // What decides an element's place before the token: above xt, or equal to it
 // and of a lower index.  In the groups before the token's own that is one
-// comparison with the next value below xt.
+// comparison with the next value below xt; in its own, the elements equal to
+// it are counted apart.
 template <typename T>
 struct LpToken {
     float x;
@@ -196,7 +170,6 @@ struct LpToken {
         above = RowVec<T>::least(xt);
         reach = RowVec<T>::least(next_below<T>(xt));
     }
-    __device__ __forceinline__ int before(float v, int idx) const { return v > x || (v == x && idx < tok); }
 };
 
 // A tile of groups g0 .. g0 + kLpTile - 1: this lane's vector of each.
@@ -210,39 +183,25 @@ struct LpTile {
         mine = most = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kLpTile; ++j) {
-            const float gm = warp_max_redux(Vec::max(q[j]));
-            most = fmaxf(most, gm);
+            const float gm = warp_max_redux_nan(Vec::max(q[j]));
+            most = max_nan(most, gm);
             if ((threadIdx.x & 31) == j) mine = gm;
         }
     }
-    // Elements before the token.
-    __device__ __forceinline__ int before(const LpToken<T>& tk, const LpRow<T>& row, int g0) const {
+    // Elements before the token (those equal to it in its own group apart).
+    __device__ __forceinline__ int before(const LpToken<T>& tk, int g0) const {
         if (most < tk.x) return 0;
+        typename Vec::Count n = Vec::count_zero();
         const int at = tk.group - g0;  // the token's group among the tile's
-        if (at < 0 || at >= kLpTile) {
-            const typename Vec::Least bound = at < 0 ? tk.above : tk.reach;
-            typename Vec::Count n = Vec::count_zero();
+        if (at > 0 && at < kLpTile) {
+#pragma unroll
+            for (int j = 0; j < kLpTile; ++j) Vec::count(n, q[j], j < at ? tk.reach : tk.above);
+        } else {
+            const typename Vec::Least bound = at > 0 ? tk.reach : tk.above;
 #pragma unroll
             for (int j = 0; j < kLpTile; ++j) Vec::count(n, q[j], bound);
-            return Vec::count_sum(n);
         }
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < kLpTile; ++j) {
-            if (j != at) {
-                typename Vec::Count k = Vec::count_zero();
-                Vec::count(k, q[j], j < at ? tk.reach : tk.above);
-                n += Vec::count_sum(k);
-            } else {
-                const int idx = row.head + ((g0 - 1 + j) * 32 + (threadIdx.x & 31)) * ElemT<T>::VEC;
-#pragma unroll
-                for (int i = 0; i < Vec::kPairs; ++i) {
-                    const float2 x = Vec::pair(q[j], i);
-                    n += tk.before(x.x, idx + 2 * i) + tk.before(x.y, idx + 2 * i + 1);
-                }
-            }
-        }
-        return n;
+        return Vec::count_sum(n);
     }
     __device__ __forceinline__ void add(LpSums& sum, float c, float far) const {
         const float2 cc = make_float2(c, c), nmc = make_float2(-sum.mc, -sum.mc);
@@ -281,18 +240,82 @@ __device__ __forceinline__ LpPart lp_part(LpSums& sum, int before, float c) {
 
 // Shared memory of the CTA that finishes a row.
 struct LpFinish {
-    static constexpr int kGroups = 256;               // at most this many groups are read again
-    static constexpr int kHeld = kGroups / kLpWarps;  // vectors a lane compares of them
-    int group[kGroups];  // the groups that hold the alternatives
-    int ties[kGroups];   // elements equal to tau in each, then how many come before it
+    static constexpr int kGroups = 256;  // at most this many groups are read again
+    int group[kGroups];      // the groups that hold the alternatives
+    int ties[kGroups + 2];   // elements equal to tau in each and in the ends, then how many come before
     int bin[kLpBins];
-    int count[2][kLpWarps];
+    int found, at, in;       // of a round of lp_select: the K-th key's bin, keys before it, keys in it
     int n_group, n_cand;
-    uint32_t tau;  // order key: elements above it are candidates
     float m;
     float2 ln_z;  // in two parts
     int valid;
 };
+
+// A bound tau such that K .. K + slack keys lie above it, or, where many keys
+// are equal, the K-th largest key itself (then fewer than K lie above); -inf's
+// key if fewer than K keys lie above that.  Keys are counted in bins down from `top`,
+// then the K-th one's bin in finer ones.  each(f) calls f(key) for the keys,
+// shared among the CTA's threads.  *above: keys above tau.
+template <typename F>
+__device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, int* above, F&& each) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t hi = top;
+    int shift = kLpBinShift, n = 0;  // n keys lie above hi
+    for (;;) {
+        __syncthreads();
+        for (int i = tid; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
+        if (tid == 0) s.found = kLpBins;
+        __syncthreads();
+        each([&](uint32_t k) {
+            const uint32_t bin = (hi - k) >> shift;
+            if (k <= hi && bin < kLpBins) atomicAdd(&s.bin[bin], 1);
+        });
+        __syncthreads();
+        if (tid < 32) {
+            constexpr int kEach = kLpBins / 32;
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) sum += s.bin[lane * kEach + i];
+            int at = n + warp_inclusive_scan_i(sum) - sum;
+            if (at < K && at + sum >= K)  // in one of this lane's bins
+                for (int i = lane * kEach;; ++i) {
+                    if (at + s.bin[i] >= K) {
+                        s.found = i;
+                        s.at = at;
+                        s.in = s.bin[i];
+                        break;
+                    }
+                    at += s.bin[i];
+                }
+        }
+        __syncthreads();
+        const uint32_t bin = (uint32_t)s.found;
+        if (bin == kLpBins) {  // further down: among -inf (or past the last key), or in the whole range
+            if (tid == 0) s.in = 0;
+            __syncthreads();
+            each([&](uint32_t k) {
+                if (k > kLpNoneKey) atomicAdd(&s.in, 1);
+            });
+            __syncthreads();
+            if (s.in < K) {
+                *above = s.in;
+                return kLpNoneKey;
+            }
+            shift = 24;
+            continue;
+        }
+        n = s.at;
+        hi -= bin << shift;
+        const uint64_t below = 1ull << shift;
+        if (n + s.in <= K + lp_slack(K)) {
+            *above = n + s.in;
+            return hi >= below ? hi - (uint32_t)below : 0u;
+        }
+        *above = n;
+        if (shift == 0) return hi;
+        shift = max(shift - 8, 0);
+    }
+}
 
 // d / T - ln z: with both constants in two parts, one rounding.
 __device__ __forceinline__ float lp_log(const LogprobArgs& a, float d, float2 ln_z) {
@@ -357,118 +380,135 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
     }
 }
 
+// The first `need` elements equal to `bound`, in index order, among the
+// chosen groups and the ends: candidates n_cand, n_cand + 1, ...  A function of
+// its own: few rows need it, and the code that all rows run stays together.
+template <typename T>
+__device__ __noinline__ void lp_ties(const T* logits, int V, LpFinish* fin, uint64_t* cand, int n_group, int n_cand,
+                                     int need, float bound) {
+    using Vec = RowVec<T>;
+    LpFinish& s = *fin;
+    const LpRow<T> row(logits, V);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = row.nb;
+    auto group_of = [&](int i) { return i < n_group ? s.group[i] : i == n_group ? 0 : nb + 1; };
+    auto ties_of = [&](int g) {
+        const int n = row.count(g), idx = row.index(g);
+        int ties = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) ties += ElemT<T>::load(row.row + idx + j) == bound;
+        return ties;
+    };
+    constexpr int kAhead = 4;
+#pragma unroll 1
+    for (int i0 = warp; i0 < n_group; i0 += kAhead * kLpWarps) {
+        uint4 q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            q[k] = i0 + k * kLpWarps < n_group ? row.vector(s.group[i0 + k * kLpWarps]) : Vec::none();
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * kLpWarps;
+            if (i >= n_group) break;
+            int ties = 0;
+            if (row.has(s.group[i])) {
+#pragma unroll
+                for (int p = 0; p < Vec::kPairs; ++p) {
+                    const float2 x = Vec::pair(q[k], p);
+                    ties += (x.x == bound) + (x.y == bound);
+                }
+            }
+            ties = __reduce_add_sync(0xffffffffu, ties);
+            if (lane == 0) s.ties[i] = ties;
+        }
+    }
+    if (warp < 2) {
+        const int ties = __reduce_add_sync(0xffffffffu, ties_of(group_of(n_group + warp)));
+        if (lane == 0) s.ties[n_group + warp] = ties;
+    }
+    __syncthreads();
+    int before[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        before[h] = need;
+        const int i = tid + h * kLpThreads;
+        if (i >= n_group + 2 || s.ties[i] == 0) continue;
+        const int g = group_of(i);
+        int n = 0;
+#pragma unroll 1
+        for (int j = 0; j < n_group + 2; ++j) n += group_of(j) < g ? s.ties[j] : 0;
+        before[h] = n;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (tid + h * kLpThreads < n_group + 2) s.ties[tid + h * kLpThreads] = before[h];
+    __syncthreads();
+#pragma unroll 1
+    for (int i = warp; i < n_group + 2; i += kLpWarps) {
+        if (s.ties[i] >= need) continue;  // none here, or none still wanted
+        const int g = group_of(i), n = row.count(g), idx = row.index(g), ties = ties_of(g);
+        int at = s.ties[i] + warp_inclusive_scan_i(ties) - ties;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            if (ElemT<T>::load(row.row + idx + j) != bound) continue;
+            if (at < need) cand[n_cand + at] = order_key(bound, idx + j);
+            ++at;
+        }
+    }
+    __syncthreads();
+}
+
 // The row's results, from n_parts <= 64 parts and the order keys of the
-// maxima of its groups (group_key[g], 1 <= g <= nb; room for 0 and nb + 1).
-// ends: this lane's element of the head and of the tail.
+// maxima of its groups (group_key[g], 1 <= g <= nb).  ends: this lane's
+// element of the head and of the tail.  Loops that run once a row are not
+// unrolled: their instructions have to be fetched, too.
 template <typename T>
 __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpRow<T>& row, int tok, float xt,
-                                          float2 ends, LpFinish& s, uint64_t* cand, uint32_t* group_key,
+                                          float2 ends, LpFinish& s, uint64_t* cand, const uint32_t* group_key,
                                           const LpPart* parts, int n_parts) {
     using Vec = RowVec<T>;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_groups = row.nb + 2;
-    const bool all = n_groups <= LpFinish::kGroups;
-    uint32_t top;  // the largest key
-    {
-        const float head_max = warp_max_redux(ends.x), tail_max = warp_max_redux(ends.y);
-        float m = fmaxf(head_max, tail_max);
-        for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, parts[k].m);
-        top = okey32(warp_max_redux(m));
-        if (warp == 0 && lane == 0) {  // an empty head or tail has no key (-inf has one)
-            group_key[0] = row.head ? okey32(head_max) : 0u;
-            group_key[row.nb + 1] = row.tail ? okey32(tail_max) : 0u;
-        }
-        if (a.top_k > 0) {
-            for (int i = tid; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
-            __syncthreads();
-        }
-    }
-    if (a.top_k > 0) {
-        // Where the K-th best group lies: the groups' keys counted in bins
-        // from the largest down.  Few groups: all of them, and the bound is
-        // found among their vectors.
-        if (!all) {
-            for (int g = tid; g < n_groups; g += kLpThreads) {
-                const uint32_t k = group_key[g], bin = (top - k) >> kLpBinShift;
-                if (k != 0u && bin < kLpBins) atomicAdd(&s.bin[bin], 1);
-            }
-            __syncthreads();
-        }
-        if (all) {
-            for (int g = tid; g < n_groups; g += kLpThreads) s.group[g] = g;
-            if (tid == 0) {
-                s.tau = 0u;
-                s.n_group = n_groups;
-                s.n_cand = 0;
-            }
-        } else if (warp == 0) {
-            uint32_t tau;
-            int n_above = 0;
-            {
-                auto count = [&](uint32_t b) {
-                    int n = 0;
-                    for (int g = lane; g < n_groups; g += 32) n += group_key[g] >= b;
-                    return __reduce_add_sync(0xffffffffu, n);
-                };
-                constexpr int kEach = kLpBins / 32;
-                int n[kEach], sum = 0;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) sum += n[i] = s.bin[lane * kEach + i];
-                const int incl = warp_inclusive_scan_i(sum);
-                int at = incl - sum, bin = kLpBins;  // the first bin by whose end K groups are counted
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    if (at < a.top_k && at + n[i] >= a.top_k) {
-                        bin = lane * kEach + i;
-                        n_above = at + n[i];
-                    }
-                    at += n[i];
-                }
-                bin = warp_min_i(bin);
-                n_above = __reduce_max_sync(0xffffffffu, n_above);
-                const uint32_t hi = top - ((uint32_t)min(bin, kLpBins - 1) << kLpBinShift);
-                if (bin == kLpBins)  // below the bins
-                    tau = lp_bound(0u, hi, a.top_k, count);
-                else if (n_above > a.top_k + lp_slack(a.top_k))  // many in that bin
-                    tau = lp_bound(hi - ((1u << kLpBinShift) - 1u), hi, a.top_k, count);
-                else
-                    tau = hi - (1u << kLpBinShift);
-                if (bin == kLpBins || n_above > a.top_k + lp_slack(a.top_k)) n_above = count(tau + 1);
-                // fewer than K above tau: also the first that reach it
-                if (n_above < a.top_k) {
-                    int n_list = 0, equal = a.top_k - n_above;
-                    const uint32_t lower = (1u << lane) - 1u;
-                    for (int g0 = 0; g0 < n_groups; g0 += 32) {
-                        const uint32_t k = g0 + lane < n_groups ? group_key[g0 + lane] : 0u;
-                        const uint32_t same = __ballot_sync(0xffffffffu, k == tau);
-                        const uint32_t taken =
-                            __ballot_sync(0xffffffffu, k > tau || (k == tau && __popc(same & lower) < equal));
-                        equal -= __popc(same);
-                        const int place = n_list + __popc(taken & lower);
-                        if (((taken >> lane) & 1u) && place < LpFinish::kGroups) s.group[place] = g0 + lane;
-                        n_list += __popc(taken);
-                    }
-                    n_above = -n_list;  // the list is made
-                }
-            }
-            if (lane == 0) {
-                s.tau = tau;
-                s.n_group = n_above < 0 ? -n_above : 0;
-                s.n_cand = 0;
-            }
-        }
-    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = row.nb, K = a.top_k;
     if (warp == 1) lp_merge<T>(a, r, row, tok, xt, ends, s, parts, n_parts);
-    if (a.top_k > 0 && !all) {
+    if (K == 0) {
         __syncthreads();
-        if (s.n_group == 0) {  // every group above tau
-            const uint32_t tau = s.tau;
-            __syncthreads();  // all have seen the empty list
-            for (int g = tid; g < n_groups; g += kLpThreads)
-                if (group_key[g] > tau) {
-                    const int at = atomicAdd(&s.n_group, 1);
-                    if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
-                }
+        if (!s.valid) lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
+        return;
+    }
+    float m = -INFINITY;
+    for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, parts[k].m);
+    const uint32_t top = okey32(warp_max_redux(m));
+
+    // ---------------------- the groups that can hold the K best, and a bound
+    uint32_t tau = 0u;
+    int above = 0;
+    const bool all = nb <= LpFinish::kGroups;
+    if (tid == 0) {
+        s.n_group = all ? nb : 0;
+        s.n_cand = 0;
+    }
+    if (all) {  // few groups: all of them, and the bound is found among their vectors
+        for (int g = tid; g < nb; g += kLpThreads) s.group[g] = g + 1;
+        __syncthreads();
+    } else {
+        tau = lp_select(s, top, K, &above, [&](auto&& f) {
+#pragma unroll 1
+            for (int g = 1 + tid; g <= nb; g += kLpThreads) f(group_key[g]);
+        });
+        const int equal = K - above;  // if above tau lie fewer than K: also the first that reach it
+#pragma unroll 1
+        for (int g = 1 + tid; g <= nb; g += kLpThreads) {
+            const uint32_t k = group_key[g];
+            bool take = k > tau;
+            if (k == tau && equal > 0) {
+                int before = 0;
+#pragma unroll 1
+                for (int i = 1; i < g && before < equal; ++i) before += group_key[i] == tau;
+                take = before < equal;
+            }
+            if (take) {
+                const int at = atomicAdd(&s.n_group, 1);
+                if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
+            }
         }
     }
     __syncthreads();
@@ -476,32 +516,18 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
         lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
         return;
     }
-    if (a.top_k == 0) return;
-
-    // --------------------------- the alternatives, from the chosen groups
     const int n_group = s.n_group;
-    // f(i) for the vectors of the chosen groups whose maximum is such that
-    // hit(maximum): read many at a time (under load a read takes 1 to 2 us),
-    // and the few hits once more, in code that is not repeated per vector
-    // (what a row runs once has to be fetched, too).
-    constexpr int kAhead = 8;
-    auto for_hits = [&](auto&& hit, auto&& f) {
+
+    // --------------------------- the elements above the bound, from them
+    constexpr int kAhead = 6;  // groups a warp reads at a time: under load a read takes 1 to 2 us
+    auto for_vectors = [&](auto&& f) {  // f(i, bits) per lane: bit k for group i + k * kLpWarps, from use(vector)
+#pragma unroll 1
         for (int i0 = warp; i0 < n_group; i0 += kAhead * kLpWarps) {
             uint4 q[kAhead];
-            uint32_t hits = 0;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + k * kLpWarps;
-                q[k] = i < n_group ? row.vector(s.group[i]) : Vec::none();
-            }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (i0 + k * kLpWarps < n_group && hit(Vec::max(q[k]))) hits |= 1u << k;
-            while (hits) {
-                const int i = i0 + (__ffs(hits) - 1) * kLpWarps;
-                hits &= hits - 1;
-                f(i);
-            }
+                q[k] = i0 + k * kLpWarps < n_group ? row.vector(s.group[i0 + k * kLpWarps]) : Vec::none();
+            f(i0, q);
         }
     };
     // The bound of the groups leaves little more than K elements, unless the
@@ -511,98 +537,55 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     float bound;
     for (;;) {
         if (raise) {
-            uint32_t held[LpFinish::kHeld];  // this lane's vectors: their maxima
+            tau = lp_select(s, top, K, &above, [&](auto&& count) {
+                for_vectors([&](int i0, const uint4* q) {
 #pragma unroll
-            for (int k0 = 0; k0 < LpFinish::kHeld; k0 += 4) {
-                uint4 q[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = warp + (k0 + k) * kLpWarps;
-                    q[k] = i < n_group ? row.vector(s.group[i]) : Vec::none();
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = warp + (k0 + k) * kLpWarps;
-                    held[k0 + k] = i < n_group && row.count(s.group[i]) ? okey32(Vec::max(q[k])) : 0u;
-                }
-            }
-            int turn = 0;
-            const uint32_t tau = lp_bound(s.tau, top, a.top_k, [&](uint32_t b) {
-                int n = 0;
-#pragma unroll
-                for (int k = 0; k < LpFinish::kHeld; ++k) n += held[k] >= b;
-                n = __reduce_add_sync(0xffffffffu, n);
-                turn ^= 1;  // the other half: its readers have passed a barrier since
-                if (lane == 0) s.count[turn][warp] = n;
-                __syncthreads();
-                n = 0;
-#pragma unroll
-                for (int w = 0; w < kLpWarps; ++w) n += s.count[turn][w];
-                return n;
+                    for (int k = 0; k < kAhead; ++k)
+                        if (i0 + k * kLpWarps < n_group && row.has(s.group[i0 + k * kLpWarps]))
+                            count(okey32(Vec::max(q[k])));
+                });
             });
-            __syncthreads();
-            if (tid == 0) {
-                s.tau = tau;
-                s.n_cand = 0;
-            }
+            if (tid == 0) s.n_cand = 0;
             __syncthreads();
         }
-        // As a float: the key below zero's is -0, which compares equal to
-        // zero; key 0 is a NaN, which nothing is <= to.
-        bound = s.tau == 0x7fffffffu ? __uint_as_float(0x80000001u) : okey32_to_float(s.tau);
-        for_hits([&](float m) { return !(m <= bound); },
-                 [&](int i) {
-                     const int g = s.group[i], n = row.count(g), idx = row.index(g);
+        // As a float: the key below zero's is -0, which compares equal to zero.
+        bound = tau == 0x7fffffffu ? __uint_as_float(0x80000001u) : okey32_to_float(tau);
+        auto push = [&](float x, int idx) {
+            if (x <= bound) return;
+            const int at = atomicAdd(&s.n_cand, 1);
+            if (at < kLpCands) cand[at] = order_key(x, idx);
+        };
+        for_vectors([&](int i0, const uint4* q) {
+            uint32_t hits = 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * kLpWarps < n_group && !(Vec::max(q[k]) <= bound)) hits |= 1u << k;
 #pragma unroll 1
-                     for (int j = 0; j < n; ++j) {
-                         const float x = ElemT<T>::load(row.row + idx + j);
-                         if (x <= bound) continue;
-                         const int at = atomicAdd(&s.n_cand, 1);
-                         if (at < kLpCands) cand[at] = order_key(x, idx + j);
-                     }
-                 });
+            for (; hits; hits &= hits - 1) {  // few: once more, in code that is not repeated per vector
+                const int g = s.group[i0 + (__ffs(hits) - 1) * kLpWarps], idx = row.index(g);
+                if (!row.has(g)) continue;
+                const uint4 v = row.vector(g);
+#pragma unroll
+                for (int p = 0; p < Vec::kPairs; ++p) {
+                    const float2 x = Vec::pair(v, p);
+                    push(x.x, idx + 2 * p);
+                    push(x.y, idx + 2 * p + 1);
+                }
+            }
+        });
+        if (warp == 0) {
+            if (lane < row.head) push(ends.x, row.index(0));
+            if (lane < row.tail) push(ends.y, row.index(nb + 1));
+        }
         __syncthreads();
         if (s.n_cand <= kLpCands || raise) break;
         raise = true;
+        __syncthreads();  // all have seen the count
     }
     int n_cand = s.n_cand;
-    if (n_cand < a.top_k) {  // and the first elements equal to tau, in the order of their groups
-        const int need = a.top_k - n_cand;
-        auto ties_of = [&](int g) {
-            const int n = row.count(g), idx = row.index(g);
-            int ties = 0;
-#pragma unroll 1
-            for (int j = 0; j < n; ++j) ties += ElemT<T>::load(row.row + idx + j) == bound;
-            return ties;
-        };
-#pragma unroll 1
-        for (int i = warp; i < n_group; i += kLpWarps) {
-            const int ties = __reduce_add_sync(0xffffffffu, ties_of(s.group[i]));
-            if (lane == 0) s.ties[i] = ties;
-        }
-        __syncthreads();
-        int earlier = 0, mine = 0;
-        if (tid < n_group) {
-            mine = s.ties[tid];
-            for (int j = 0; j < n_group; ++j) earlier += s.group[j] < s.group[tid] ? s.ties[j] : 0;
-        }
-        __syncthreads();
-        if (tid < n_group) s.ties[tid] = mine > 0 ? earlier : need;
-        __syncthreads();
-        for (int i = warp; i < n_group; i += kLpWarps) {
-            if (s.ties[i] >= need) continue;  // none here, or none still wanted
-            const int g = s.group[i], n = row.count(g), idx = row.index(g), ties = ties_of(g);
-            int at = s.ties[i] + warp_inclusive_scan_i(ties) - ties;
-#pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                const float x = ElemT<T>::load(row.row + idx + j);
-                if (x != bound) continue;
-                if (at < need) cand[n_cand + at] = order_key(x, idx + j);
-                ++at;
-            }
-        }
-        __syncthreads();
-        n_cand = a.top_k;
+    if (n_cand < K) {
+        lp_ties<T>(row.row, a.V, &s, cand, n_group, n_cand, K - n_cand, bound);
+        n_cand = K;
     }
     // a candidate's place is the number of candidates before it
     for (int i = tid; i < n_cand; i += kLpThreads) {
@@ -610,9 +593,9 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
         int place = 0;
 #pragma unroll 4
         for (int j = 0; j < n_cand; ++j) place += cand[j] > k;
-        if (place < a.top_k) {
-            a.top_ids[(size_t)r * a.top_k + place] = key_index(k);
-            a.top_logprobs[(size_t)r * a.top_k + place] = lp_log(a, key_value(k) - s.m, s.ln_z);
+        if (place < K) {
+            a.top_ids[(size_t)r * K + place] = key_index(k);
+            a.top_logprobs[(size_t)r * K + place] = lp_log(a, key_value(k) - s.m, s.ln_z);
         }
     }
 }
@@ -623,7 +606,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     __shared__ LpPart parts[kLpMaxCluster * kLpWarps];
     __shared__ uint64_t full[kLpWarps][kLpDepth];
     extern __shared__ __align__(128) uint8_t lp_raw[];
-    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + kLpRing);  // [nb + 2]
+    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + kLpRing);  // [nb + 1]; group 0 has none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
@@ -662,11 +645,20 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     const float2 ends = row.ends();
     const LpToken<T> tk(row, tok, xt);
     const float far = kLpFar / a.c;
+    int before = 0, slot = 0;
+    if (part == 0 && warp == 0 && tk.group >= 1 && tk.group <= row.nb) {  // equal to the token, in its own group
+        const uint4 q = row.vector(tk.group);
+        const int idx = row.index(tk.group);
+#pragma unroll
+        for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+            const float2 x = RowVec<T>::pair(q, i);
+            before += (x.x == xt && idx + 2 * i < tok) + (x.y == xt && idx + 2 * i + 1 < tok);
+        }
+    }
     LpSums sum;
     LpTile<T> tile;
-    int before = 0, slot = 0;
     uint32_t parity = 0;
-    bool awaited = false, ok = true;
+    bool awaited = false, ok = true, refused = false;
     for (; g0 < row.nb; g0 += step) {
         ok = mbar_wait(&bars[slot], parity, kLpLimitNs);
         if (!ok) break;
@@ -687,6 +679,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
         }
         tile.maxima();
         if (tile.most > sum.m) sum.raise(tile.most, a.c);
+        refused = refused || !(tile.most < INFINITY);  // a NaN or +inf
         if (CLUSTER && !awaited) {
             cluster_wait();
             awaited = true;
@@ -698,10 +691,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
             else
                 group_key[g0 + lane + 1] = k;
         }
-        before += tile.before(tk, row, g0 + 1);
-        tile.add(sum, a.c, far);
+        before += tile.before(tk, g0 + 1);
+        if (tile.most > -INFINITY) tile.add(sum, a.c, far);  // not all of it ruled out
     }
     LpPart p = lp_part(sum, before, a.c);
+    if (refused) p.z = NAN;
     if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
         p.z = NAN;
         if (lane == 0) {
@@ -736,9 +730,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
 template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;
-    const size_t dyn = kLpRing + (size_t)(groups + 2) * sizeof(uint32_t);
+    const size_t dyn = kLpRing + (size_t)(groups + 1) * sizeof(uint32_t);
     constexpr int kMostGroups = (int)((kRowsMaxVocab / 4 + 31) / 32);
-    constexpr size_t kMost = kLpRing + (kMostGroups + 2) * sizeof(uint32_t);
+    constexpr size_t kMost = kLpRing + (kMostGroups + 1) * sizeof(uint32_t);
     LaunchShape shape;
     if (!launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, false>), kMost, kLpThreads, &shape) ||
         !launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, true>), kMost, kLpThreads, &shape))

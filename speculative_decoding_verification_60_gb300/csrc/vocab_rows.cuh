@@ -19,10 +19,15 @@ constexpr float kLn2 = 0.69314718055994531f;
 // is -inf (weight zero), where -inf minus -inf would be NaN.
 constexpr float kNoMax = -3.4028234663852886e38f;
 
-// Maximum over a warp; NaN is passed over.
+// Maximum over a warp: NaN is passed over, or (nan) makes it NaN.
 __device__ __forceinline__ float warp_max_redux(float v) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_max_redux_nan(float v) {
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 
@@ -42,7 +47,7 @@ template <> __device__ __forceinline__ float next_below<__nv_bfloat16>(float x) 
     return __uint_as_float((b & 0x80000000u) ? b + 0x10000u : b - 0x10000u);
 }
 
-// A 16-byte vector of T as pairs of floats, its maximum (NaN passed over),
+// A 16-byte vector of T as pairs of floats, its maximum (NaN if there is one),
 // the number of its elements that are not <= a bound, and the vector that
 // stands for no elements.
 template <typename T> struct RowVec;
@@ -74,8 +79,8 @@ template <> struct RowVec<__nv_bfloat16> {
     }
     __device__ static __forceinline__ float max(const uint4& q) {
         auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
-        const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
-        return fmaxf(__low2float(m), __high2float(m));
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(q.x), h(q.y)), __hmax2_nan(h(q.z), h(q.w)));
+        return max_nan(__low2float(m), __high2float(m));
     }
     // word 0 of a vector whose first element is x, the other -inf
     __device__ static __forceinline__ uint32_t single(float x) { return 0xff800000u | (__float_as_uint(x) >> 16); }
@@ -105,19 +110,20 @@ template <> struct RowVec<float> {
                       : make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
     }
     __device__ static __forceinline__ float max(const uint4& q) {
-        return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+        return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
+                       max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
     __device__ static __forceinline__ uint32_t single(float x) { return __float_as_uint(x); }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
-// Maximum over a warp's tile of N vectors a lane.
+// Maximum over a warp's tile of N vectors a lane (NaN if there is one).
 template <typename T, int N>
 __device__ __forceinline__ float tile_max(const uint4* q) {
     float m = RowVec<T>::max(q[0]);
 #pragma unroll
-    for (int j = 1; j < N; ++j) m = fmaxf(m, RowVec<T>::max(q[j]));
-    return warp_max_redux(m);
+    for (int j = 1; j < N; ++j) m = max_nan(m, RowVec<T>::max(q[j]));
+    return warp_max_redux_nan(m);
 }
 
 // (logit descending, index ascending) as one integer: larger = earlier.
