@@ -352,6 +352,8 @@ def _rows(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and stride[1] == 1 and stride[0] >= shape[1]:
+        return shape[0], shape[1], stride[0]
     if len(shape) < 2:
         raise ValueError(f"{name} must have shape [..., V], got {tuple(shape)}")
     V = shape[-1]
@@ -372,46 +374,42 @@ def _rows(t, name):
     return R, V, step
 
 
-def _inputs(device, *specs):
-    """Pointers of the inputs (tensor or None, name, dtype, shape), checked."""
-    ptrs = []
-    for t, name, dtype, shape in specs:
-        if t is None:
-            ptrs.append(None)
-            continue
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-            _check(t, name, dtype, shape)
-            raise ValueError(f"{name} must be on cuda:{device}")
-        ptrs.append(t.data_ptr())
-    return ptrs
+def _at(t, name, dtype, shape, device):
+    """Pointer of a tensor that must be as described, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on cuda:{device}")
+    return t.data_ptr()
 
 
-def _outputs(out, device, stream, *specs):
-    """Pointers of the outputs (name, dtype, shape): the caller's tensor in
-    out, checked, or a new one, allocated on the call's stream."""
-    ptrs = []
-    for name, dtype, shape in specs:
-        t = out.get(name)
-        if t is None:
-            with torch.cuda.stream(stream):  # no effect for None
-                t = out[name] = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
-        elif t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-            _check(t, name, dtype, shape)
-            raise ValueError(f"{name} must be on cuda:{device}")
-        ptrs.append(t.data_ptr())
-    return ptrs
+def _to(out, name, dtype, shape, device, stream):
+    """Pointer of output `name`: the caller's tensor in out, checked, or a new
+    one, allocated on the call's stream."""
+    t = out.get(name)
+    if t is None:
+        with torch.cuda.stream(stream):  # no effect for None
+            t = out[name] = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
+    elif t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on cuda:{device}")
+    return t.data_ptr()
 
 
 def _handle(stream, device, *tensors):
-    """The cudaStream_t of a call: the given stream's, or that of the tensors'
-    device's current one.  A given stream is marked as a user of the tensors,
-    so that their memory is not handed on before the call's work is done."""
+    """The cudaStream_t of a call with a given stream, which is marked as a
+    user of the tensors, so that their memory is not handed on before the
+    call's work is done; or of the device's current stream."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
+
+
+_I32, _F32, _ONE = torch.int32, torch.float32, torch.Size((1,))
 
 
 def token_logprobs(logits, tokens=None, temperature: float = 1.0, top_k: int = 0, out=None, stream=None) -> dict:
@@ -430,12 +428,12 @@ def token_logprobs(logits, tokens=None, temperature: float = 1.0, top_k: int = 0
     lead, device, K = logits.shape[:-1], logits.get_device(), int(top_k)
     wide = (*lead, max(K, 0))
     out = {} if out is None else out
-    (tok,) = _inputs(device, (tokens, "tokens", torch.int32, lead))
-    ptrs = _outputs(out, device, stream, ("logprob", torch.float32, lead), ("rank", torch.int32, lead),
-                    ("entropy", torch.float32, lead), ("top_ids", torch.int32, wide),
-                    ("top_logprobs", torch.float32, wide), ("dev_error", torch.int32, (1,)))
-    st = lib.spec_token_logprobs(logits.data_ptr(), dt, R, V, step, tok, temperature, K, *ptrs,
-                                 _handle(stream, device, logits, tokens, *out.values()))
+    st = lib.spec_token_logprobs(
+        logits.data_ptr(), dt, R, V, step, _at(tokens, "tokens", _I32, lead, device), temperature, K,
+        _to(out, "logprob", _F32, lead, device, stream), _to(out, "rank", _I32, lead, device, stream),
+        _to(out, "entropy", _F32, lead, device, stream), _to(out, "top_ids", _I32, wide, device, stream),
+        _to(out, "top_logprobs", _F32, wide, device, stream), _to(out, "dev_error", _I32, _ONE, device, stream),
+        _handle(stream, device, logits, tokens, *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_token_logprobs", st)
     return out
@@ -467,15 +465,15 @@ def distill_topk(student, teacher_ids, teacher_logprobs, weights=None, temperatu
     R, V, step = _rows(student, "student")
     lead, device, K = student.shape[:-1], student.get_device(), teacher_ids.shape[-1]
     out = {} if out is None else out
-    ids, lps, w = _inputs(device, (teacher_ids, "teacher_ids", torch.int32, (*lead, K)),
-                          (teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K)),
-                          (weights, "weights", torch.float32, lead))
-    loss, stats, err = _outputs(out, device, stream, ("loss", torch.float32, lead),
-                                ("row_stats", torch.float32, (*lead, 8)), ("dev_error", torch.int32, (1,)))
+    wide = (*lead, K)
     grad, grad_step = _grad_rows(out, student, stream) if with_grad else (None, V)
-    st = lib.spec_distill_topk(student.data_ptr(), dt, R, V, step, ids, lps, K, w, temperature, int(tail), loss, stats,
-                               grad, grad_step, err,
-                               _handle(stream, device, student, teacher_ids, teacher_logprobs, weights, *out.values()))
+    st = lib.spec_distill_topk(
+        student.data_ptr(), dt, R, V, step, _at(teacher_ids, "teacher_ids", _I32, wide, device),
+        _at(teacher_logprobs, "teacher_logprobs", _F32, wide, device), K, _at(weights, "weights", _F32, lead, device),
+        temperature, tail, _to(out, "loss", _F32, lead, device, stream),
+        _to(out, "row_stats", _F32, (*lead, 8), device, stream), grad, grad_step,
+        _to(out, "dev_error", _I32, _ONE, device, stream),
+        _handle(stream, device, student, teacher_ids, teacher_logprobs, weights, *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_distill_topk", st)
     return out
@@ -492,13 +490,13 @@ def distill_topk_backward(student, teacher_ids, teacher_logprobs, row_stats, gra
     R, V, step = _rows(student, "student")
     lead, device, K = student.shape[:-1], student.get_device(), teacher_ids.shape[-1]
     out = {} if out is None else out
-    ids, lps, stats, g = _inputs(device, (teacher_ids, "teacher_ids", torch.int32, (*lead, K)),
-                                 (teacher_logprobs, "teacher_logprobs", torch.float32, (*lead, K)),
-                                 (row_stats, "row_stats", torch.float32, (*lead, 8)),
-                                 (grad_loss, "grad_loss", torch.float32, lead))
+    wide = (*lead, K)
     grad, grad_step = _grad_rows(out, student, stream)
     st = lib.spec_distill_topk_backward(
-        student.data_ptr(), dt, R, V, step, ids, lps, K, stats, g, temperature, grad, grad_step,
+        student.data_ptr(), dt, R, V, step, _at(teacher_ids, "teacher_ids", _I32, wide, device),
+        _at(teacher_logprobs, "teacher_logprobs", _F32, wide, device), K,
+        _at(row_stats, "row_stats", _F32, (*lead, 8), device), _at(grad_loss, "grad_loss", _F32, lead, device),
+        temperature, grad, grad_step,
         _handle(stream, device, student, teacher_ids, teacher_logprobs, row_stats, grad_loss, out["grad"]))
     if st != SPEC_OK:
         raise SpecError("spec_distill_topk_backward", st)
@@ -520,18 +518,17 @@ def advance_blocks(seq_lens, new_tokens, block_table, held, free_blocks, free_co
     if block_table.dtype != torch.int32:
         raise TypeError(f"block_table must be {torch.int32}, got {block_table.dtype}")
     B, M, step = _rows(block_table, "block_table")
-    device, T, F = block_table.get_device(), int(max_tokens), free_blocks.numel()
+    device, T, F = block_table.get_device(), int(max_tokens), free_blocks.shape[0]
     out = {} if out is None else out
-    i32, room = torch.int32, max(T, 0)
-    lens, acc, new, have, free, count = _inputs(
-        device, (seq_lens, "seq_lens", i32, (B,)), (accepted_len, "accepted_len", i32, (B,)),
-        (new_tokens, "new_tokens", i32, (B,)), (held, "held", i32, (B,)), (free_blocks, "free_blocks", i32, (F,)),
-        (free_count, "free_count", i32, (1,)))
-    ptrs = _outputs(out, device, stream, ("seq_lens", i32, (B,)), ("held", i32, (B,)), ("free_count", i32, (1,)),
-                    ("cu_tokens", i32, (B + 1,)), ("slots", torch.int64, (room,)), ("positions", i32, (room,)),
-                    ("dev_error", i32, (1,)))
+    each, room = (B,), (max(T, 0),)
     st = lib.spec_advance_blocks(
-        lens, acc, new, B, int(page_size), block_table.data_ptr(), M, step, have, free, F, count, *ptrs[:6], T, ptrs[6],
+        _at(seq_lens, "seq_lens", _I32, each, device), _at(accepted_len, "accepted_len", _I32, each, device),
+        _at(new_tokens, "new_tokens", _I32, each, device), B, page_size, block_table.data_ptr(), M, step,
+        _at(held, "held", _I32, each, device), _at(free_blocks, "free_blocks", _I32, (F,), device), F,
+        _at(free_count, "free_count", _I32, _ONE, device), _to(out, "seq_lens", _I32, each, device, stream),
+        _to(out, "held", _I32, each, device, stream), _to(out, "free_count", _I32, _ONE, device, stream),
+        _to(out, "cu_tokens", _I32, (B + 1,), device, stream), _to(out, "slots", torch.int64, room, device, stream),
+        _to(out, "positions", _I32, room, device, stream), T, _to(out, "dev_error", _I32, _ONE, device, stream),
         _handle(stream, device, seq_lens, accepted_len, new_tokens, block_table, held, free_blocks, free_count,
                 *out.values()))
     if st != SPEC_OK:
