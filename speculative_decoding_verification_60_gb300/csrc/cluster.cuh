@@ -1,8 +1,11 @@
-// Thread-block clusters for sm_103a as inline PTX: rank and size, the
-// cluster barrier, and stores into another CTA's shared memory.
+// Thread-block clusters for sm_103a: rank and size, the cluster barrier and
+// stores into another CTA's shared memory as inline PTX, and their launches.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "bulk.cuh"
 
@@ -55,6 +58,67 @@ __device__ __forceinline__ bool cluster_mbar_test(uint64_t* bar, uint32_t parity
         : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// Clusters of S CTAs of this shape that run at the same time on the current
+// device (a GPC holds whole clusters only, so this is less than its CTAs over
+// S).  The first call per (device, kernel, S, shared memory) asks, later ones
+// read the table.
+inline bool clusters_at_once(const void* kernel, int S, int block, size_t dyn_smem, int* out) {
+    struct Entry {
+        const void* fn;
+        int dev, S, block;
+        size_t dyn;
+        int n;
+    };
+    constexpr int kEntries = 128;
+    static std::mutex mu;
+    static Entry table[kEntries];
+    static int used = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (table[i].fn == kernel && table[i].dev == dev && table[i].S == S && table[i].block == block &&
+            table[i].dyn == dyn_smem) {
+            *out = table[i].n;
+            return true;
+        }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)S);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = dyn_smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return false;
+    if (used < kEntries) table[used++] = Entry{kernel, dev, S, block, dyn_smem, n};
+    *out = n;
+    return true;
+}
+
+// A launch of `clusters` clusters of S CTAs.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), long long clusters, int S, int block, size_t dyn_smem,
+                                   cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * S));
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = dyn_smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 }  // namespace sv

@@ -49,7 +49,6 @@ constexpr int kDsTile = 8;                           // vectors a lane takes of 
 constexpr int kDsTileBytes = kDsTile * 512;
 constexpr int kDsMaxCluster = 16;
 constexpr int kDsMaxTiles = 6;                       // of a warp, when the row stays on the chip
-constexpr int kDsRing = 1;                           // tiles of a warp on their way, when it does not
 constexpr int kDsIds = kMaxTop / 32;                 // listed tokens a lane looks after
 constexpr uint64_t kDsLimitNs = 2000000000ull;
 constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x c - m c in one operation
@@ -58,11 +57,12 @@ constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x 
 // would be +inf for it.
 constexpr float kTailRounding = 1.0f / 65536.0f;
 
-struct DsSmem {
+// What the CTAs of a row exchange about it, and its listed tokens.
+struct DsRow {
     float2 part[kDsMaxCluster * kDsWarps];  // every warp's maximum and sum of the tail
     float s[kMaxTop], l[kMaxTop];  // listed tokens: student logit, teacher's value
+    float m_listed, z_listed;      // their maximum, and sum of 2^((s - m_listed) c)
     alignas(16) int id[kMaxTop];
-    uint64_t full[kDsWarps][kDsMaxTiles];
     float4 teacher;             // from the first CTA: see DsTeacher
     float bad[kDsMaxCluster];   // from every CTA: error bits of its share of the checks
 };
@@ -135,11 +135,12 @@ struct DsSum {
 // share of the search for doubles), and in the first CTA the sum of t_j (in
 // double: 1 - sum t cancels where the listed tokens hold nearly all of it).
 template <typename T>
-__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsSmem& sm, int part, int S,
+__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsRow& sm, int part, int S,
                                                 DsTeacher* out, int* err_out) {
     const int lane = threadIdx.x & 31;
-    float lmax = kNoMax;
+    float lmax = kNoMax, smax = kNoMax;
     int err = 0;
+#pragma unroll
     for (int j = lane; j < kMaxTop; j += 32) {
         int v = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
         const float l = j < a.K ? a.teacher[(size_t)r * a.K + j] : 0.0f;
@@ -150,13 +151,24 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, con
         sm.id[j] = v;
         sm.l[j] = l;
         if (v >= 0) {
-            sm.s[j] = ElemT<T>::load(row + v);
+            const float x = ElemT<T>::load(row + v);
+            sm.s[j] = x;
+            smax = fmaxf(smax, x);
             lmax = fmaxf(lmax, l);
             if (isnan(l) || l == INFINITY) err |= kDevErrNonfinite;
         }
     }
-    lmax = warp_max(lmax);
+    lmax = warp_max_redux(lmax);
+    smax = warp_max_redux(smax);
     __syncwarp();
+    float z = 0.0f;
+    for (int j = lane; j < a.K; j += 32)
+        if (sm.id[j] >= 0) z += ex2((sm.s[j] - smax) * a.c);
+    z = warp_sum_f(z);
+    if (lane == 0) {
+        sm.m_listed = smax;
+        sm.z_listed = z;
+    }
     for (int j0 = 32 * part; j0 < a.K; j0 += 32 * S) {  // each id of 32 against all before it
         const int v = sm.id[j0 + lane];
         bool twice = false;
@@ -188,26 +200,19 @@ struct DsSums {
     float t_tail;     // 1 - sum t_j (BUCKET)
     int err;          // error bits
 };
-__device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsSmem& sm, int S, DsSums* sums) {
+__device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsRow& sm, int S, DsSums* sums) {
     const int lane = threadIdx.x & 31, n_parts = S * kDsWarps;
     const DsTeacher& te = reinterpret_cast<const DsTeacher&>(sm.teacher);
     DistillStat st{};
-    float mt = kNoMax, ms = kNoMax;
+    float mt = kNoMax;
     for (int k = lane; k < n_parts; k += 32) mt = fmaxf(mt, sm.part[k].x);
-    for (int j = lane; j < a.K; j += 32)
-        if (sm.id[j] >= 0) ms = fmaxf(ms, sm.s[j]);
     mt = warp_max_redux(mt);
-    const float m = fmaxf(mt, warp_max_redux(ms));
-    float zt = 0.0f, zs = 0.0f;
+    float zt = 0.0f;
     for (int k = lane; k < n_parts; k += 32) zt += sm.part[k].y * ex2(fmaxf((sm.part[k].x - mt) * a.c, -1000.0f));
-    for (int j = lane; j < a.K; j += 32)
-        if (sm.id[j] >= 0) zs += ex2((sm.s[j] - m) * a.c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        zt += __shfl_xor_sync(0xffffffffu, zt, o);
-        zs += __shfl_xor_sync(0xffffffffu, zs, o);
-    }
-    const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f)), z = zs + in_tail;
+    zt = warp_sum_f(zt);
+    const float ms = sm.m_listed, m = fmaxf(mt, ms);
+    const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f));
+    const float z = sm.z_listed * ex2(fmaxf((ms - m) * a.c, -1000.0f)) + in_tail;
     float t_tail = a.bucket ? (float)fmax(1.0 - te.mass, 0.0) : 0.0f;
     if (zt == 0.0f && t_tail <= kTailRounding) t_tail = 0.0f;
     *sums = DsSums{z, zt, t_tail, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
@@ -225,7 +230,7 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
 
 // The loss, by one warp.  log t - log q cancels where the student is near
 // the teacher: in double, and with the same c that the sums were made with.
-__device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsSmem& sm, const DistillStat& st,
+__device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsRow& sm, const DistillStat& st,
                                               const DsSums& sums) {
     const int lane = threadIdx.x & 31;
     const double ln_z = ln_of(sums.z), ln_t = reinterpret_cast<const DsTeacher&>(sm.teacher).ln_t;
@@ -267,26 +272,41 @@ __device__ __forceinline__ uint4 pack(const float2* x, float) {
                       __float_as_uint(x[1].y));
 }
 
-// A vector's gradient as tail tokens, stored at g (aligned: 16 bytes at once).
-template <typename T>
-__device__ __forceinline__ void distill_store(T* g, const uint4& q, float coef, float m_tail, float c, bool aligned) {
-    float2 y[RowVec<T>::kPairs];
-    const float2 cc = make_float2(c, c), nm = make_float2(-m_tail, -m_tail), kk = make_float2(coef, coef);
-#pragma unroll
-    for (int i = 0; i < RowVec<T>::kPairs; ++i) {
-        const float2 t = __fmul2_rn(__fadd2_rn(RowVec<T>::pair(q, i), nm), cc);
-        y[i] = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), kk);
+// The gradient of tail tokens: coef 2^((x - m_tail) c), for a row.  As in
+// DsSum, t = x c - m_tail c in one operation where that is of ordinary size;
+// what the product's rounding is off by goes into the coefficient.
+struct DsTail {
+    float2 cc, nm, kk;  // c; -m_tail or -m_tail c; the coefficient
+    bool plain;
+    __device__ __forceinline__ DsTail(float coef, float m_tail, float c) {
+        const float mc = m_tail * c;
+        plain = fabsf(mc) < kDsPlain;
+        const float k = plain ? coef * ex2(fmaf(-m_tail, c, mc)) : coef, n = plain ? -mc : -m_tail;
+        cc = make_float2(c, c);
+        nm = make_float2(n, n);
+        kk = make_float2(k, k);
     }
-    if (aligned) {
-        *reinterpret_cast<uint4*>(g) = pack(y, T{});
-    } else {
+    __device__ __forceinline__ float2 operator()(float2 x) const {
+        const float2 t = plain ? __ffma2_rn(x, cc, nm) : __fmul2_rn(__fadd2_rn(x, nm), cc);
+        return __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), kk);
+    }
+    // a vector's, stored at g: 16 bytes at once, or element by element
+    template <bool ALIGNED, typename T>
+    __device__ __forceinline__ void store(T* g, const uint4& q) const {
+        float2 y[RowVec<T>::kPairs];
 #pragma unroll
-        for (int i = 0; i < RowVec<T>::kPairs; ++i) {
-            store_elem(g + 2 * i, y[i].x);
-            store_elem(g + 2 * i + 1, y[i].y);
+        for (int i = 0; i < RowVec<T>::kPairs; ++i) y[i] = (*this)(RowVec<T>::pair(q, i));
+        if (ALIGNED) {
+            *reinterpret_cast<uint4*>(g) = pack(y, T{});
+        } else {
+#pragma unroll
+            for (int i = 0; i < RowVec<T>::kPairs; ++i) {
+                store_elem(g + 2 * i, y[i].x);
+                store_elem(g + 2 * i + 1, y[i].y);
+            }
         }
     }
-}
+};
 
 template <typename T>
 __device__ __forceinline__ bool same_alignment(const RowView<T>& row, const T* g) {
@@ -318,210 +338,367 @@ __device__ __forceinline__ void distill_zero(const RowView<T>& row, T* g, int fi
     }
 }
 
-// Loss and, with GRAD, gradient of a row, by a CTA or a cluster of S.
-//
-// Each warp has every (8 S)-th tile of the row.  It sets the listed tokens of
-// a tile to -inf in shared memory, so that what it sums is the tail.  With
-// GRAD all of its tiles stay there: the sums are exchanged (every CTA of the
-// cluster gets every warp's), and the gradient is written from the same copy
-// of the row, which is read once from memory.  Bound by memory: an element's
-// 2 bytes (bf16) in and 2 out.
-template <typename T, bool CLUSTER, bool GRAD>
-__global__ void __launch_bounds__(kDsThreads, GRAD ? 3 : 4) k_distill(DistillArgs a, int n_buf) {
-    constexpr int VEC = ElemT<T>::VEC;
-    extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps][n_buf] tiles
-    __shared__ DsSmem sm;
+// The listed tokens among elements [e0, e0 + n) of a row: f(k, offset) for
+// each that this lane looks after (entry lane + 32 k).
+template <typename F>
+__device__ __forceinline__ bool listed_in(const int* ids, int e0, int n, F&& f) {
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < kDsIds; ++k)
+        if ((unsigned)(ids[k] - e0) < (unsigned)n) {
+            f(k, ids[k] - e0);
+            any = true;
+        }
+    return any;
+}
+__device__ __forceinline__ void load_ids(const DistillArgs& a, int r, int* ids) {
+#pragma unroll
+    for (int k = 0; k < kDsIds; ++k) {
+        const int j = (threadIdx.x & 31) + 32 * k;
+        ids[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
+    }
+}
+
+// This lane's element of the head and of the tail (-inf: none, or listed),
+// and their part of the sums.
+template <typename T>
+__device__ __forceinline__ float2 distill_ends(const RowView<T>& row, const int* ids, DsSum& sum, float c) {
+    const int lane = threadIdx.x & 31, tail0 = row.head + row.nvec * ElemT<T>::VEC;
+    float2 ends = make_float2(-INFINITY, -INFINITY);
+    if (lane < row.head) ends.x = ElemT<T>::load(row.row + lane);
+    if (lane < row.tail) ends.y = ElemT<T>::load(row.row + tail0 + lane);
+    uint32_t in_head = 0, in_tail = 0;
+    listed_in(ids, 0, row.head, [&](int, int o) { in_head |= 1u << o; });
+    listed_in(ids, tail0, row.tail, [&](int, int o) { in_tail |= 1u << o; });
+    if ((__reduce_or_sync(0xffffffffu, in_head) >> lane) & 1u) ends.x = -INFINITY;
+    if ((__reduce_or_sync(0xffffffffu, in_tail) >> lane) & 1u) ends.y = -INFINITY;
+    const float m = warp_max_redux(fmaxf(ends.x, ends.y));
+    if (m > sum.m) sum.raise(m, c);
+    sum.exact(c);
+    sum.z.x += ex2((ends.x - sum.m) * c);
+    sum.z.y += ex2((ends.y - sum.m) * c);
+    if (sum.m > kNoMax) sum.raise(sum.m, c);  // back to one operation per pair
+    return ends;
+}
+
+// A tile in shared memory, its listed tokens set to -inf there, added to the
+// sum; free() is called once every lane has its vectors.
+template <typename T, typename F>
+__device__ __forceinline__ void distill_tile(const RowView<T>& row, int t, uint4* at, const int* ids, DsSum& sum, float c,
+                                             F&& free) {
+    const int lane = threadIdx.x & 31, v0 = t * kDsTile * 32, nv = min(kDsTile * 32, row.nvec - v0);
+    const bool any = listed_in(ids, row.head + v0 * ElemT<T>::VEC, nv * ElemT<T>::VEC,
+                               [&](int, int o) { reinterpret_cast<T*>(at)[o] = T(-INFINITY); });
+    // before a later copy into the same place
+    if (__any_sync(0xffffffffu, any)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    uint4 q[kDsTile];
+    if (nv == kDsTile * 32) {
+#pragma unroll
+        for (int j = 0; j < kDsTile; ++j) q[j] = at[j * 32 + lane];
+    } else {
+#pragma unroll
+        for (int j = 0; j < kDsTile; ++j) q[j] = j * 32 + lane < nv ? at[j * 32 + lane] : RowVec<T>::none();
+    }
+    free();
+    const float m = tile_max<T, kDsTile>(q);
+    if (m > sum.m) sum.raise(m, c);
+    if (m != -INFINITY) sum.add<T, kDsTile>(q, c);  // not all of it ruled out
+}
+
+// A warp's tiles of a row through its part of shared memory: buffer b, an
+// mbarrier each.
+template <typename T>
+struct DsBuffers {
+    uint4* ring;
+    uint64_t* bars;
+    __device__ __forceinline__ uint4* at(int b) const { return ring + b * (kDsTileBytes / 16); }
+    __device__ __forceinline__ void copy(const RowView<T>& row, int t, int b) const {  // one lane
+        const int v0 = t * kDsTile * 32;
+        const uint32_t bytes = (uint32_t)min(kDsTile * 32, row.nvec - v0) * 16;
+        mbar_arrive_expect_tx(&bars[b], bytes);
+        bulk_load(at(b), row.vec() + v0, bytes, &bars[b]);
+    }
+};
+template <typename T>
+__device__ __forceinline__ int tiles_of(const RowView<T>& row) {
+    return (row.nvec + kDsTile * 32 - 1) / (kDsTile * 32);
+}
+__device__ __forceinline__ void distill_no_row(const DistillArgs& a, int r) {  // one thread
+    a.loss[r] = 0.0f;
+    if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = DistillStat{};
+}
+
+// What the extra warp does for a row: the teacher, sent to every CTA of the
+// row (ready() is called before that), then sync(), then in the first CTA the
+// loss and the row's statistics.
+template <typename T, bool CLUSTER, typename R, typename W>
+__device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const T* logits, DsRow& sm, int part, int S,
+                                              R&& ready, W&& sync) {
+    const int lane = threadIdx.x & 31;
+    DsTeacher te{};
+    int bad;
+    distill_teacher<T>(a, r, logits, sm, part, S, &te, &bad);
+    const float4 message = *reinterpret_cast<const float4*>(&te);
+    __syncwarp();
+    ready();
+    if (CLUSTER) {
+        if (lane < S) {
+            cluster_store(cluster_map(&sm.bad[part], lane), __int_as_float(bad));
+            if (part == 0) cluster_store(cluster_map(&sm.teacher, lane), message);
+        }
+    } else if (lane == 0) {
+        sm.bad[0] = __int_as_float(bad);
+        sm.teacher = message;
+    }
+    sync();
+    if (part != 0) return;
+    DsSums sums;
+    const DistillStat st = distill_stat(a, sm, S, &sums);
+    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums) : 0.0f;
+    if (lane == 0) {
+        a.loss[r] = loss;
+        if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
+        if (sums.err && a.dev_error) atomicOr(a.dev_error, sums.err);
+    }
+}
+
+// The loss of a row, by a CTA or a cluster of S: each warp has every (8 S)-th
+// tile, one on its way while it works on the one in its registers.  Bound by
+// memory, one read of the row: 1024 rows of 129280 bf16 in 53 us, 0.74 of the
+// measured copy bandwidth (two waves of CTAs, the second two thirds full).
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
+    extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps] tiles
+    __shared__ DsRow sm;
+    __shared__ uint64_t full[kDsWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
-    const int unit = part * kDsWarps + warp, units = S * kDsWarps;
-    const float w = a.weights ? a.weights[r] : 1.0f;
-    const RowView<T> row(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V);
-    T* g = GRAD ? static_cast<T*>(a.grad) + (size_t)r * a.grad_stride : nullptr;
-    if (w == 0.0f) {
-        if (part == 0 && tid == 0) {
-            a.loss[r] = 0.0f;
-            if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = DistillStat{};
-        }
-        if (GRAD && warp < kDsWarps) distill_zero(row, g, unit, units);
+    if (a.weights && a.weights[r] == 0.0f) {
+        if (part == 0 && tid == 0) distill_no_row(a, r);
         return;
     }
     if (CLUSTER) cluster_arrive();  // awaited before the first store into another CTA
-
-    const int tiles = (row.nvec + kDsTile * 32 - 1) / (kDsTile * 32);
-    const uint4* vecs = row.vec();
-    uint4* ring = reinterpret_cast<uint4*>(ds_raw) + (size_t)warp * n_buf * (kDsTileBytes / 16);
-    int ids[kDsIds];
-    float2 ends = make_float2(-INFINITY, -INFINITY);  // this lane's element of the head and of the tail
-    const int tail0 = row.head + row.nvec * VEC;
-    // Listed tokens of elements [e0, e0 + n): f(k, offset) for this lane's
-    auto listed_in = [&](int e0, int n, auto&& f) {
-        bool any = false;
-#pragma unroll
-        for (int k = 0; k < kDsIds; ++k)
-            if ((unsigned)(ids[k] - e0) < (unsigned)n) {
-                f(k, ids[k] - e0);
-                any = true;
-            }
-        return any;
-    };
-    if (warp < kDsWarps) {
-        uint64_t* bars = sm.full[warp];
-        auto copy = [&](int t, int b) {  // lane 0
-            const int v0 = t * kDsTile * 32;
-            const uint32_t bytes = (uint32_t)min(kDsTile * 32, row.nvec - v0) * 16;
-            mbar_arrive_expect_tx(&bars[b], bytes);
-            bulk_load(ring + b * (kDsTileBytes / 16), vecs + v0, bytes, &bars[b]);
-        };
-        if (lane == 0) {
-            for (int b = 0; b < n_buf; ++b) mbar_init(&bars[b], 1);
-            mbar_fence_init();
-            for (int b = 0; b < n_buf && unit + b * units < tiles; ++b) copy(unit + b * units, b);
-        }
+    auto sync = [] {
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < kDsIds; ++k) {
-            const int j = lane + 32 * k;
-            ids[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
+        if (CLUSTER) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
         }
+    };
+    auto ready = [] {
+        __syncwarp();
+        if (CLUSTER) cluster_wait();
+    };
+    const RowView<T> row(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V);
+    if (warp == kDsWarps) {
+        distill_extra<T, CLUSTER>(a, r, row.row, sm, part, S, ready, sync);
+        return;
+    }
+    const int unit = part * kDsWarps + warp, units = S * kDsWarps, tiles = tiles_of(row);
+    const DsBuffers<T> buf{reinterpret_cast<uint4*>(ds_raw) + warp * (kDsTileBytes / 16), &full[warp]};
+    if (lane == 0) {
+        mbar_init(&full[warp], 1);
+        mbar_fence_init();
+        if (unit < tiles) buf.copy(row, unit, 0);
+    }
+    __syncwarp();
+    int ids[kDsIds];
+    load_ids(a, r, ids);
+    DsSum sum;
+    if (unit == 0) distill_ends(row, ids, sum, a.c);
+    bool ok = true;
+    uint32_t parity = 0;
+    for (int t = unit; t < tiles && ok; t += units, parity ^= 1) {
+        ok = mbar_wait(&full[warp], parity, kDsLimitNs);
+        if (!ok) break;
+        distill_tile(row, t, buf.at(0), ids, sum, a.c, [&] {
+            __syncwarp();
+            if (lane == 0 && t + units < tiles) buf.copy(row, t + units, 0);
+        });
+    }
+    if (!ok && lane == 0) {  // the row is refused; the copy still on its way lands before the CTA ends
+        if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+        mbar_wait(&full[warp], parity, kDsLimitNs);
+    }
+    __syncwarp();
+    sum.exact(a.c);
+    const float2 p = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);
+    ready();
+    if (CLUSTER) {
+        if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), p);
+    } else if (lane == 0) {
+        sm.part[unit] = p;
+    }
+    sync();
+}
+
+// Loss and gradient, by persistent CTAs or clusters of S that take rows in
+// turn.  All tiles of a row stay in shared memory (n_buf a warp) while the
+// sums are exchanged, every CTA of the cluster getting every warp's; the
+// gradient is written from there, and each tile's place takes the next row's
+// as soon as it has been written.  So a row is read once and written once:
+// 2 + 2 bytes an element (bf16), the bound.  What the CTAs of a row exchange
+// is there twice, for this row and the next.
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, int n_buf) {
+    constexpr int VEC = ElemT<T>::VEC;
+    extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps][n_buf] tiles
+    __shared__ DsRow rows[2];
+    __shared__ uint64_t full[kDsWarps][kDsMaxTiles];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
+    const int step = gridDim.x / S, unit = part * kDsWarps + warp, units = S * kDsWarps;
+    auto sync = [] {
+        __syncwarp();
+        if (CLUSTER) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+    };
+    bool waited = !CLUSTER;
+    auto ready = [&] {  // every CTA of the cluster has started
+        __syncwarp();
+        if (!waited) cluster_wait();
+        waited = true;
+    };
+    if (CLUSTER) cluster_arrive();
+    auto row_of = [&](int r) { return RowView<T>(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V); };
+    auto grad_of = [&](int r) { return static_cast<T*>(a.grad) + (size_t)r * a.grad_stride; };
+    float w = 0.0f;  // weight of the row that next_row found
+    auto next_row = [&](int r) {  // from r on, rows of weight zero done on the way
+        for (; r < a.R; r += step) {
+            w = a.weights ? a.weights[r] : 1.0f;
+            if (w != 0.0f) break;
+            if (warp < kDsWarps)
+                distill_zero(row_of(r), grad_of(r), unit, units);
+            else if (part == 0 && lane == 0)
+                distill_no_row(a, r);
+        }
+        return r;
+    };
+    int p = 0;
+    if (warp == kDsWarps) {
+        for (int r = next_row(blockIdx.x / S); r < a.R; r = next_row(r + step), p ^= 1)
+            distill_extra<T, CLUSTER>(a, r, row_of(r).row, rows[p], part, S, ready, sync);
+        ready();
+        return;
+    }
+    const DsBuffers<T> buf{reinterpret_cast<uint4*>(ds_raw) + (size_t)warp * n_buf * (kDsTileBytes / 16), full[warp]};
+    int next = next_row(blockIdx.x / S);
+    uint32_t phase = 0, pending = 0;  // of each buffer; pending: a copy was started and not awaited
+    if (lane == 0) {
+        for (int b = 0; b < n_buf; ++b) mbar_init(&full[warp][b], 1);
+        mbar_fence_init();
+    }
+    __syncwarp();
+    auto fill = [&](int r, int b) {  // buffer b with row r's tile
+        if (r >= a.R) return;
+        const RowView<T> row = row_of(r);
+        const int t = unit + b * units;
+        if (t >= tiles_of(row)) return;
+        if (lane == 0) buf.copy(row, t, b);
+        pending |= 1u << b;
+    };
+    for (int b = 0; b < n_buf; ++b) fill(next, b);
+    int ids_next[kDsIds];
+    if (next < a.R) load_ids(a, next, ids_next);
+    bool ok = true;
+    while (next < a.R) {
+        const int r = next;
+        const float w_row = w;
+        int ids[kDsIds];
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k) ids[k] = ids_next[k];
+        next = next_row(r + step);
+        if (next < a.R) load_ids(a, next, ids_next);  // needed a row later
+        const RowView<T> row = row_of(r);
+        T* g = grad_of(r);
+        DsRow& sm = rows[p];
+        p ^= 1;
+        const int tiles = tiles_of(row), tail0 = row.head + row.nvec * VEC;
         DsSum sum;
-        if (unit == 0) {
-            if (lane < row.head) ends.x = ElemT<T>::load(row.row + lane);
-            if (lane < row.tail) ends.y = ElemT<T>::load(row.row + tail0 + lane);
-            uint32_t in_head = 0, in_tail = 0;
-            listed_in(0, row.head, [&](int, int o) { in_head |= 1u << o; });
-            listed_in(tail0, row.tail, [&](int, int o) { in_tail |= 1u << o; });
-            in_head = __reduce_or_sync(0xffffffffu, in_head);
-            in_tail = __reduce_or_sync(0xffffffffu, in_tail);
-            if ((in_head >> lane) & 1u) ends.x = -INFINITY;
-            if ((in_tail >> lane) & 1u) ends.y = -INFINITY;
-            const float m = warp_max_redux(fmaxf(ends.x, ends.y));
-            if (m > sum.m) sum.raise(m, a.c);
-            sum.exact(a.c);
-            sum.z.x += ex2((ends.x - sum.m) * a.c);
-            sum.z.y += ex2((ends.y - sum.m) * a.c);
-            if (sum.m > kNoMax) sum.raise(sum.m, a.c);  // back to one operation per pair
-        }
-        bool ok = true;
-        int b = 0;
-        uint32_t parity = 0;
-        for (int t = unit; t < tiles; t += units) {
-            ok = mbar_wait(&bars[b], parity, kDsLimitNs);
-            if (!ok) break;
-            uint4* at = ring + b * (kDsTileBytes / 16);
-            const int v0 = t * kDsTile * 32, nv = min(kDsTile * 32, row.nvec - v0);
-            const bool any = listed_in(row.head + v0 * VEC, nv * VEC,
-                                       [&](int, int o) { reinterpret_cast<T*>(at)[o] = T(-INFINITY); });
-            if (__any_sync(0xffffffffu, any) && !GRAD) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            uint4 q[kDsTile];
-            if (nv == kDsTile * 32) {
-#pragma unroll
-                for (int j = 0; j < kDsTile; ++j) q[j] = at[j * 32 + lane];
-            } else {
-#pragma unroll
-                for (int j = 0; j < kDsTile; ++j) q[j] = j * 32 + lane < nv ? at[j * 32 + lane] : RowVec<T>::none();
+        float2 ends = make_float2(-INFINITY, -INFINITY);
+        if (unit == 0) ends = distill_ends(row, ids, sum, a.c);
+        for (int b = 0; b < n_buf && ok; ++b) {
+            if (!((pending >> b) & 1u)) continue;
+            ok = mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
+            if (!ok) {
+                if (lane == 0 && a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+                break;
             }
-            if (!GRAD) {  // every lane has its vectors: the buffer takes the next tile
-                __syncwarp();
-                if (lane == 0 && t + n_buf * units < tiles) copy(t + n_buf * units, b);
-            }
-            const float m = tile_max<T, kDsTile>(q);
-            if (m > sum.m) sum.raise(m, a.c);
-            if (m != -INFINITY) sum.add<T, kDsTile>(q, a.c);  // not all of it ruled out
-            if (++b == n_buf) {
-                b = 0;
-                parity ^= 1;
-            }
-        }
-        if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
-            if (lane == 0) {
-                if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
-                for (int i = 0; i < n_buf; ++i) {
-                    mbar_wait(&bars[b], parity, kDsLimitNs);
-                    if (++b == n_buf) {
-                        b = 0;
-                        parity ^= 1;
-                    }
-                }
-            }
-            __syncwarp();
+            pending &= ~(1u << b);
+            phase ^= 1u << b;
+            distill_tile(row, unit + b * units, buf.at(b), ids, sum, a.c, [] {});
         }
         sum.exact(a.c);
-        const float2 p = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);
+        const float2 mine = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);  // a wait ran out: refused
+        ready();
         if (CLUSTER) {
-            cluster_wait();
-            if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), p);
+            if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), mine);
         } else if (lane == 0) {
-            sm.part[unit] = p;
+            sm.part[unit] = mine;
         }
-    } else {
-        DsTeacher te{};
-        int bad;
-        distill_teacher<T>(a, r, row.row, sm, part, S, &te, &bad);
-        const float4 message = *reinterpret_cast<const float4*>(&te);
-        __syncwarp();
-        if (CLUSTER) {
-            cluster_wait();
-            if (lane < S) {
-                cluster_store(cluster_map(&sm.bad[part], lane), __int_as_float(bad));
-                if (part == 0) cluster_store(cluster_map(&sm.teacher, lane), message);
+        sync();
+        DsSums sums;
+        const DistillStat st = distill_stat(a, sm, S, &sums);
+        if (st.live == 0.0f) distill_zero(row, g, unit, units);
+        const bool aligned = same_alignment(row, g);
+        const DsTail tail(w_row * st.coef, st.m_tail, a.c);
+        auto listed = [&](T* g0, int e0, int n) {  // overwrites what was stored for them as tail tokens
+            __syncwarp();
+            listed_in(ids, e0, n, [&](int k, int o) {
+                const int j = lane + 32 * k;
+                store_elem(g0 + o, distill_listed_grad(st, sm.s[j], expf(sm.l[j] - st.ln_t), a.c, (float)a.inv_t, w_row));
+            });
+        };
+        if (st.live != 0.0f && unit == 0) {
+            const float2 y = tail(ends);
+            if (lane < row.head) store_elem(g + lane, y.x);
+            if (lane < row.tail) store_elem(g + tail0 + lane, y.y);
+            listed(g, 0, row.head);
+            listed(g + tail0, tail0, row.tail);
+        }
+        for (int b = 0; b < n_buf; ++b) {
+            const int t = unit + b * units;
+            if (st.live != 0.0f && t < tiles) {
+                const uint4* at = buf.at(b);
+                const int v0 = t * kDsTile * 32;
+                T* g0 = g + row.head + (size_t)v0 * VEC;
+                if (aligned && v0 + kDsTile * 32 <= row.nvec) {
+                    if (tail.plain) {
+                        DsTail t1 = tail;
+                        t1.plain = true;
+#pragma unroll 4
+                        for (int j = 0; j < kDsTile; ++j) t1.store<true>(g0 + (j * 32 + lane) * VEC, at[j * 32 + lane]);
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < kDsTile; ++j) tail.store<true>(g0 + (j * 32 + lane) * VEC, at[j * 32 + lane]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int v = lane; v < row.nvec - v0 && v < kDsTile * 32; v += 32) {
+                        if (aligned)
+                            tail.store<true>(g0 + v * VEC, at[v]);
+                        else
+                            tail.store<false>(g0 + v * VEC, at[v]);
+                    }
+                }
+                listed(g0, row.head + v0 * VEC, min(kDsTile * 32, row.nvec - v0) * VEC);
             }
-        } else if (lane == 0) {
-            sm.bad[0] = __int_as_float(bad);
-            sm.teacher = message;
+            __syncwarp();  // every lane has read it
+            if (ok) fill(next, b);
         }
     }
-    if (CLUSTER) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-
-    if (warp == kDsWarps ? part != 0 : !GRAD) return;
-    DsSums sums;
-    const DistillStat st = distill_stat(a, sm, S, &sums);
-    if (warp == kDsWarps) {
-        const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums) : 0.0f;
-        if (lane == 0) {
-            a.loss[r] = loss;
-            if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
-            if (sums.err && a.dev_error) atomicOr(a.dev_error, sums.err);
-        }
-        return;
-    }
-    if (st.live == 0.0f) {
-        distill_zero(row, g, unit, units);
-        return;
-    }
-    const bool aligned = same_alignment(row, g);
-    const float coef = w * st.coef;
-    auto listed = [&](T* g0, int e0, int n) {  // overwrites what was stored for them as tail tokens
-        __syncwarp();
-        listed_in(e0, n, [&](int k, int o) {
-            const int j = lane + 32 * k;
-            store_elem(g0 + o, distill_listed_grad(st, sm.s[j], expf(sm.l[j] - st.ln_t), a.c, (float)a.inv_t, w));
-        });
-    };
-    if (unit == 0) {
-        if (lane < row.head) store_elem(g + lane, coef * ex2((ends.x - st.m_tail) * a.c));
-        if (lane < row.tail) store_elem(g + tail0 + lane, coef * ex2((ends.y - st.m_tail) * a.c));
-        listed(g, 0, row.head);
-        listed(g + tail0, tail0, row.tail);
-    }
-    int b = 0;
-    for (int t = unit; t < tiles; t += units, ++b) {
-        const uint4* at = ring + b * (kDsTileBytes / 16);
-        const int v0 = t * kDsTile * 32;
-        T* g0 = g + row.head + (size_t)v0 * VEC;
-#pragma unroll
-        for (int j = 0; j < kDsTile; ++j) {
-            const int v = j * 32 + lane;
-            if (v0 + v < row.nvec) distill_store(g0 + v * VEC, at[v], coef, st.m_tail, a.c, aligned);
-        }
-        listed(g0, row.head + v0 * VEC, min(kDsTile * 32, row.nvec - v0) * VEC);
-    }
+    ready();
+    if (!ok && lane == 0)  // the copies still on their way land before the CTA ends
+        for (int b = 0; b < n_buf; ++b)
+            if ((pending >> b) & 1u) mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
 }
 
 // The gradient alone, from a row's statistics: a warp per tile, a CTA per
@@ -544,13 +721,9 @@ __global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, 
         return;
     }
     int ids[kDsIds];
-#pragma unroll
-    for (int k = 0; k < kDsIds; ++k) {
-        const int j = lane + 32 * k;
-        ids[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
-    }
+    load_ids(a, r, ids);
     const bool aligned = same_alignment(row, g);
-    const float coef = w * st.coef;
+    const DsTail tail(w * st.coef, st.m_tail, a.c);
     // The listed tokens of a piece of the row: their gradients are taken
     // from the logits before put() stores over the piece (grad may be the
     // student's buffer), and stored after it.
@@ -573,11 +746,11 @@ __global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, 
     if (unit == 0) {
         const int tail0 = row.head + row.nvec * VEC;
         with_listed(0, row.head, [&] {
-            if (lane < row.head) store_elem(g + lane, coef * ex2((ElemT<T>::load(row.row + lane) - st.m_tail) * a.c));
+            if (lane < row.head) store_elem(g + lane, tail(make_float2(ElemT<T>::load(row.row + lane), 0.0f)).x);
         });
         with_listed(tail0, row.tail, [&] {
             if (lane < row.tail)
-                store_elem(g + tail0 + lane, coef * ex2((ElemT<T>::load(row.row + tail0 + lane) - st.m_tail) * a.c));
+                store_elem(g + tail0 + lane, tail(make_float2(ElemT<T>::load(row.row + tail0 + lane), 0.0f)).x);
         });
     }
     for (int t = unit; t * kDsTile * 32 < row.nvec; t += units) {
@@ -589,53 +762,64 @@ __global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, 
         with_listed(row.head + v0 * VEC, nv * VEC, [&] {
 #pragma unroll
             for (int j = 0; j < kDsTile; ++j)
-                if (j * 32 + lane < nv)
-                    distill_store(g + row.head + (size_t)(v0 + j * 32 + lane) * VEC, q[j], coef, st.m_tail, a.c, aligned);
+                if (j * 32 + lane < nv) {
+                    T* at = g + row.head + (size_t)(v0 + j * 32 + lane) * VEC;
+                    if (aligned)
+                        tail.store<true>(at, q[j]);
+                    else
+                        tail.store<false>(at, q[j]);
+                }
         });
     }
 }
 
-template <typename T, bool GRAD>
-static cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st) {
+template <typename T>
+static cudaError_t launch_distill_loss(const DistillArgs& a, cudaStream_t st) {
+    const int tiles = (a.V / ElemT<T>::VEC + kDsTile * 32 - 1) / (kDsTile * 32);
+    const size_t dyn = (size_t)kDsWarps * kDsTileBytes;
+    LaunchShape shape;
+    if (!launch_shape(reinterpret_cast<const void*>(k_distill_loss<T, false>), dyn, kDsThreads, &shape) ||
+        !launch_shape(reinterpret_cast<const void*>(k_distill_loss<T, true>), dyn, kDsThreads, &shape))
+        return cudaErrorUnknown;
+    // CTAs that share a row: more than one where rows are too few for every SM
+    int S = 1;
+    while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
+    if (S > 1) return launch_clusters(k_distill_loss<T, true>, a.R, S, kDsThreads, dyn, st, a);
+    k_distill_loss<T, false><<<a.R, kDsThreads, dyn, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t st) {
     const int tiles = (a.V / ElemT<T>::VEC + kDsTile * 32 - 1) / (kDsTile * 32);
     LaunchShape shape;
-    const size_t most = (size_t)kDsWarps * kDsTileBytes * (GRAD ? kDsMaxTiles : kDsRing);
-    if (!launch_shape(reinterpret_cast<const void*>(k_distill<T, false, GRAD>), most, kDsThreads, &shape) ||
-        !launch_shape(reinterpret_cast<const void*>(k_distill<T, true, GRAD>), most, kDsThreads, &shape))
+    const size_t most = (size_t)kDsWarps * kDsTileBytes * kDsMaxTiles;
+    if (!launch_shape(reinterpret_cast<const void*>(k_distill_grad<T, false>), most, kDsThreads, &shape) ||
+        !launch_shape(reinterpret_cast<const void*>(k_distill_grad<T, true>), most, kDsThreads, &shape))
         return cudaErrorUnknown;
-    // CTAs that share a row.  With the gradient: enough that three rows' parts
-    // fit on an SM (two tiles a warp), so that one CTA's exchange hides behind
-    // the others' copies.  And, where rows are few, enough for every SM.
+    // CTAs that share a row: enough that three rows' parts fit on an SM (two
+    // tiles a warp), so that one CTA's exchange hides behind the others'
+    // copies; 16 only where 8 do not hold the row; more where rows are few.
     int S = 1;
-    if (GRAD)
-        while (S < kDsMaxCluster && tiles > 2 * S * kDsWarps) S *= 2;
-    if (GRAD && S > 8 && tiles <= kDsMaxTiles * 8 * kDsWarps) S = 8;  // 16 only where 8 do not hold the row
+    while (S < kDsMaxCluster && tiles > 2 * S * kDsWarps) S *= 2;
+    if (S > 8 && tiles <= kDsMaxTiles * 8 * kDsWarps) S = 8;
     while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
     const int each = (tiles + S * kDsWarps - 1) / (S * kDsWarps);  // tiles of a warp
-    const int n_buf = GRAD ? (each > 0 ? each : 1) : kDsRing;
+    const int n_buf = each > 0 ? each : 1;
     const size_t dyn = (size_t)kDsWarps * kDsTileBytes * n_buf;
-    if (S == 1) {
-        k_distill<T, false, GRAD><<<a.R, kDsThreads, dyn, st>>>(a, n_buf);
-        return cudaGetLastError();
-    }
-    auto* kern = k_distill<T, true, GRAD>;
-    if (S > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    int clusters = 0;  // as many as run at once
+    if (S > 1) {
+        auto* kern = k_distill_grad<T, true>;
+        const cudaError_t e =
+            S > 8 ? cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
         if (e != cudaSuccess) return e;
+        if (!clusters_at_once(reinterpret_cast<const void*>(kern), S, kDsThreads, dyn, &clusters)) return cudaErrorUnknown;
+        return launch_clusters(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, st, a, n_buf);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.R * S);
-    cfg.blockDim = dim3(kDsThreads);
-    cfg.dynamicSmemBytes = dyn;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, n_buf);
+    const int per_sm = n_buf <= 2 ? 3 : n_buf <= 3 ? 2 : 1;  // by registers, and by shared memory
+    clusters = shape.sms * per_sm < a.R ? shape.sms * per_sm : a.R;
+    k_distill_grad<T, false><<<clusters, kDsThreads, dyn, st>>>(a, n_buf);
+    return cudaGetLastError();
 }
 
 template <typename T>
@@ -684,8 +868,8 @@ extern "C" spec_status spec_distill_topk(const void* student, spec_dtype dtype, 
                   c, (double)c * 0.69314718055994531, tail == SPEC_TAIL_BUCKET,
                   loss, row_stats, grad, grad_stride, dev_error};
     const bool bf16 = dtype == SPEC_BF16;
-    const cudaError_t e = grad ? (bf16 ? launch_distill<__nv_bfloat16, true>(a, st) : launch_distill<float, true>(a, st))
-                               : (bf16 ? launch_distill<__nv_bfloat16, false>(a, st) : launch_distill<float, false>(a, st));
+    const cudaError_t e = grad ? (bf16 ? launch_distill_grad<__nv_bfloat16>(a, st) : launch_distill_grad<float>(a, st))
+                               : (bf16 ? launch_distill_loss<__nv_bfloat16>(a, st) : launch_distill_loss<float>(a, st));
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -747,19 +747,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
         k_token_logprobs<T, false><<<a.R, kLpThreads, dyn, st>>>(a);
         return cudaGetLastError();
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.R * S);
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = dyn;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, true>, a);
+    return launch_clusters(k_token_logprobs<T, true>, a.R, S, kLpThreads, dyn, st, a);
 }
 
 }  // namespace sv
