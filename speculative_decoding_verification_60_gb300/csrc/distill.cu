@@ -63,13 +63,19 @@ struct DsRow {
     float s[kMaxTop], l[kMaxTop];  // listed tokens: student logit, teacher's value
     float m_listed, z_listed;      // their maximum, and sum of 2^((s - m_listed) c)
     alignas(16) int id[kMaxTop];
-    float4 teacher;             // from the first CTA: see DsTeacher
+    float4 teacher;             // from the first CTA: DsTeacher's message
     float bad[kDsMaxCluster];   // from every CTA: error bits of its share of the checks
 };
-// What the first CTA's extra warp finds about the teacher, as it is sent.
+// What the first CTA's extra warp finds about the teacher.  Every warp reads
+// it, so it is sent rounded to 32 bits: double operations of 27 warps at once
+// took 2 us a row.
 struct DsTeacher {
-    double mass;   // sum of t_j
-    double ln_t;   // subtracted from the teacher's values; +inf: no teacher mass at all
+    double mass;  // sum of t_j
+    double ln_t;  // subtracted from the teacher's values; +inf: no teacher mass at all
+    __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, their sum, ln_t
+        const double t_tail = bucket ? fmax(1.0 - mass, 0.0) : 0.0;
+        return make_float4((float)mass, (float)t_tail, (float)(mass + t_tail), (float)ln_t);
+    }
 };
 
 __device__ __forceinline__ float warp_sum_f(float v) {
@@ -202,7 +208,7 @@ struct DsSums {
 };
 __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsRow& sm, int S, DsSums* sums) {
     const int lane = threadIdx.x & 31, n_parts = S * kDsWarps;
-    const DsTeacher& te = reinterpret_cast<const DsTeacher&>(sm.teacher);
+    const float4 te = sm.teacher;
     DistillStat st{};
     float mt = kNoMax;
     for (int k = lane; k < n_parts; k += 32) mt = fmaxf(mt, sm.part[k].x);
@@ -213,16 +219,16 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     const float ms = sm.m_listed, m = fmaxf(mt, ms);
     const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f));
     const float z = sm.z_listed * ex2(fmaxf((ms - m) * a.c, -1000.0f)) + in_tail;
-    float t_tail = a.bucket ? (float)fmax(1.0 - te.mass, 0.0) : 0.0f;
-    if (zt == 0.0f && t_tail <= kTailRounding) t_tail = 0.0f;
+    const bool no_tail = zt == 0.0f && te.y <= kTailRounding;
+    const float t_tail = no_tail ? 0.0f : te.y;
     *sums = DsSums{z, zt, t_tail, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
     if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
-    if (sums->err || te.ln_t == (double)INFINITY) return st;
+    if (sums->err || te.w == INFINITY) return st;
     st.m_tail = mt;
     st.m = m;
     st.inv_z = 1.0f / z;
-    st.mass = (float)(te.mass + (double)t_tail);
-    st.ln_t = (float)te.ln_t;
+    st.mass = no_tail ? te.x : te.z;
+    st.ln_t = te.w;
     st.coef = zt > 0.0f ? (st.mass * (in_tail / z) - t_tail) * (float)a.inv_t / zt : 0.0f;
     st.live = 1.0f;
     return st;
@@ -231,9 +237,9 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
 // The loss, by one warp.  log t - log q cancels where the student is near
 // the teacher: in double, and with the same c that the sums were made with.
 __device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsRow& sm, const DistillStat& st,
-                                              const DsSums& sums) {
+                                              const DsSums& sums, double ln_t) {
     const int lane = threadIdx.x & 31;
-    const double ln_z = ln_of(sums.z), ln_t = reinterpret_cast<const DsTeacher&>(sm.teacher).ln_t;
+    const double ln_z = ln_of(sums.z);
     double sum = 0.0;
     for (int j = lane; j < a.K; j += 32) {
         if (sm.id[j] < 0) continue;
@@ -439,7 +445,7 @@ __device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const
     DsTeacher te{};
     int bad;
     distill_teacher<T>(a, r, logits, sm, part, S, &te, &bad);
-    const float4 message = *reinterpret_cast<const float4*>(&te);
+    const float4 message = te.message(a.bucket);
     __syncwarp();
     ready();
     if (CLUSTER) {
@@ -455,7 +461,7 @@ __device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const
     if (part != 0) return;
     DsSums sums;
     const DistillStat st = distill_stat(a, sm, S, &sums);
-    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums) : 0.0f;
+    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums, te.ln_t) : 0.0f;
     if (lane == 0) {
         a.loss[r] = loss;
         if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
