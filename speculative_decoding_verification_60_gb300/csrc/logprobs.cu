@@ -37,9 +37,12 @@ struct LogprobArgs {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpTile = 6;   // groups of a tile: 3 KiB
-constexpr int kLpDepth = 1;  // tiles a warp has on their way, beside the one in its registers
 constexpr int kLpTileBytes = kLpTile * 512;
-constexpr int kLpRing = kLpWarps * kLpDepth * kLpTileBytes;
+// Tiles a warp has on their way, beside the one in its registers: a second
+// only where few rows are shared and a warp has two tiles in all (four CTAs of
+// an SM keep enough on the way with one, and 777 fp32 rows take 3 us less).
+constexpr int lp_depth(bool cluster) { return cluster ? 2 : 1; }
+constexpr size_t lp_ring(bool cluster) { return (size_t)kLpWarps * lp_depth(cluster) * kLpTileBytes; }
 constexpr int kLpMaxCluster = 8;
 constexpr uint64_t kLpLimitNs = 2000000000ull;
 constexpr float kLpPlain = 1024.0f;  // |m c| below this: see LpSums
@@ -52,7 +55,7 @@ constexpr int kLpCands = 8 * (kMaxTop + kLpSlack) + 16;  // the elements of that
 constexpr int kLpBins = 256;
 constexpr uint32_t kLpNoneKey = 0x007fffffu;  // the order key of -inf
 constexpr int kLpBinShift = 17;  // keys a bin at first: two bf16 values, so four binades in all
-static_assert(kLpCands * 8 <= kLpRing, "the candidates take the ring's place");
+static_assert(kLpCands * 8 <= lp_ring(false), "the candidates take the ring's place");
 
 // What a warp makes of its groups.
 struct __align__(16) LpPart {
@@ -255,17 +258,24 @@ struct LpFinish {
 // are equal, the K-th largest key itself (then fewer than K lie above); -inf's
 // key if fewer than K keys lie above that.  Keys are counted in bins down from `top`,
 // then the K-th one's bin in finer ones.  each(f) calls f(key) for the keys,
-// shared among the CTA's threads.  *above: keys above tau.
+// shared among the CTA's threads.  *above: keys above tau.  cleared: the bins
+// are (lp_clear and a barrier).
+__device__ __forceinline__ void lp_clear(LpFinish& s) {
+    for (int i = threadIdx.x; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
+    if (threadIdx.x == 0) s.found = kLpBins;
+}
 template <typename F>
-__device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, int* above, F&& each) {
+__device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, int* above, bool cleared, F&& each) {
     const int tid = threadIdx.x, lane = tid & 31;
     uint32_t hi = top;
     int shift = kLpBinShift, n = 0;  // n keys lie above hi
     for (;;) {
-        __syncthreads();
-        for (int i = tid; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
-        if (tid == 0) s.found = kLpBins;
-        __syncthreads();
+        if (!cleared) {
+            __syncthreads();
+            lp_clear(s);
+            __syncthreads();
+        }
+        cleared = false;
         each([&](uint32_t k) {
             const uint32_t bin = (hi - k) >> shift;
             if (k <= hi && bin < kLpBins) atomicAdd(&s.bin[bin], 1);
@@ -482,15 +492,11 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     uint32_t tau = 0u;
     int above = 0;
     const bool all = nb <= LpFinish::kGroups;
-    if (tid == 0) {
-        s.n_group = all ? nb : 0;
-        s.n_cand = 0;
-    }
     if (all) {  // few groups: all of them, and the bound is found among their vectors
         for (int g = tid; g < nb; g += kLpThreads) s.group[g] = g + 1;
-        __syncthreads();
+        if (tid == 0) s.n_group = nb;
     } else {
-        tau = lp_select(s, top, K, &above, [&](auto&& f) {
+        tau = lp_select(s, top, K, &above, true, [&](auto&& f) {
 #pragma unroll 1
             for (int g = 1 + tid; g <= nb; g += kLpThreads) f(group_key[g]);
         });
@@ -537,7 +543,7 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     float bound;
     for (;;) {
         if (raise) {
-            tau = lp_select(s, top, K, &above, [&](auto&& count) {
+            tau = lp_select(s, top, K, &above, all, [&](auto&& count) {
                 for_vectors([&](int i0, const uint4* q) {
 #pragma unroll
                     for (int k = 0; k < kAhead; ++k)
@@ -604,9 +610,10 @@ template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a) {
     __shared__ LpFinish s;
     __shared__ LpPart parts[kLpMaxCluster * kLpWarps];
-    __shared__ uint64_t full[kLpWarps][kLpDepth];
+    constexpr int kDepth = lp_depth(CLUSTER);
+    __shared__ uint64_t full[kLpWarps][kDepth];
     extern __shared__ __align__(128) uint8_t lp_raw[];
-    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + kLpRing);  // [nb + 1]; group 0 has none
+    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + lp_ring(CLUSTER));  // [nb + 1]; group 0 has none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
@@ -621,10 +628,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     if (CLUSTER) cluster_arrive();  // awaited before the first store into the leader
     const LpRow<T> row(static_cast<const T*>(a.logits) + (size_t)r * a.stride, a.V);
 
-    // This warp's tiles, kLpDepth of them on their way through its part of
+    // This warp's tiles, kDepth of them on their way through its part of
     // the ring: what is in flight does not take registers, and is enough
     // when another CTA of the SM is at its row's end.
-    uint4* ring = reinterpret_cast<uint4*>(lp_raw) + warp * (kLpRing / 16 / kLpWarps);
+    uint4* ring = reinterpret_cast<uint4*>(lp_raw) + warp * (kDepth * kLpTileBytes / 16);
     uint64_t* bars = full[warp];
     const uint4* vecs = row.vec();
     const int step = S * kLpWarps * kLpTile;
@@ -635,12 +642,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
         bulk_load(ring + slot * (kLpTileBytes / 16), vecs + (size_t)g * 32, bytes, &bars[slot]);
     };
     if (lane == 0) {
-        for (int i = 0; i < kLpDepth; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < kDepth; ++i) mbar_init(&bars[i], 1);
         mbar_fence_init();
-        for (int i = 0; i < kLpDepth; ++i)
+        for (int i = 0; i < kDepth; ++i)
             if (g0 + i * step < row.nb) copy(g0 + i * step, i);
     }
     __syncwarp();
+    lp_clear(s);  // for the row's end
+    if (tid == 0) s.n_group = s.n_cand = 0;
     const float xt = ElemT<T>::load(row.row + tok);
     const float2 ends = row.ends();
     const LpToken<T> tk(row, tok, xt);
@@ -672,8 +681,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
                 tile.q[j] = (g0 + j) * 32 + lane < row.nvec ? at[j * 32] : RowVec<T>::none();
         }
         __syncwarp();  // every lane has its vectors: the slot takes the next tile
-        if (lane == 0 && g0 + kLpDepth * step < row.nb) copy(g0 + kLpDepth * step, slot);
-        if (++slot == kLpDepth) {
+        if (lane == 0 && g0 + kDepth * step < row.nb) copy(g0 + kDepth * step, slot);
+        if (++slot == kDepth) {
             slot = 0;
             parity ^= 1;
         }
@@ -700,9 +709,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
         p.z = NAN;
         if (lane == 0) {
             if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
-            for (int i = 0; i < kLpDepth && g0 + i * step < row.nb; ++i) {
+            for (int i = 0; i < kDepth && g0 + i * step < row.nb; ++i) {
                 mbar_wait(&bars[slot], parity, kLpLimitNs);
-                if (++slot == kLpDepth) {
+                if (++slot == kDepth) {
                     slot = 0;
                     parity ^= 1;
                 }
@@ -732,9 +741,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
 template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;
-    const size_t dyn = kLpRing + (size_t)(groups + 1) * sizeof(uint32_t);
     constexpr int kMostGroups = (int)((kRowsMaxVocab / 4 + 31) / 32);
-    constexpr size_t kMost = kLpRing + (kMostGroups + 1) * sizeof(uint32_t);
+    constexpr size_t kMost = lp_ring(true) + (kMostGroups + 1) * sizeof(uint32_t);
     LaunchShape shape;
     if (!launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, false>), kMost, kLpThreads, &shape) ||
         !launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, true>), kMost, kLpThreads, &shape))
@@ -743,6 +751,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int S_most = 5 * R <= sms ? 8 : 5 * R <= 2 * sms ? 4 : 3 * R <= 4 * sms ? 2 : 1;
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
+    const size_t dyn = lp_ring(S > 1) + (size_t)(groups + 1) * sizeof(uint32_t);
     if (S == 1) {
         k_token_logprobs<T, false><<<a.R, kLpThreads, dyn, st>>>(a);
         return cudaGetLastError();
