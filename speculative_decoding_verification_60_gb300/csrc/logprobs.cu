@@ -304,14 +304,14 @@ __device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, 
             if (tid == 0) s.in = 0;
             __syncthreads();
             each([&](uint32_t k) {
-                if (k > kLpNoneKey) atomicAdd(&s.in, 1);
+                if (k > kLpNoneKey && k <= top) atomicAdd(&s.in, 1);
             });
             __syncthreads();
-            if (s.in < K) {
+            if (s.in < K || shift == 24) {
                 *above = s.in;
                 return kLpNoneKey;
             }
-            shift = 24;
+            shift = 24;  // 256 such bins are all keys: this round finds it
             continue;
         }
         n = s.at;
@@ -485,7 +485,16 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
         return;
     }
     float m = -INFINITY;
-    for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, parts[k].m);
+    bool refused = false;  // what the ends add to that, the merge finds
+    for (int k = lane; k < n_parts; k += 32) {
+        m = fmaxf(m, parts[k].m);
+        refused = refused || isnan(parts[k].z);
+    }
+    if (__any_sync(0xffffffffu, refused)) {  // the same in every warp
+        __syncthreads();
+        lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
+        return;
+    }
     const uint32_t top = okey32(warp_max_redux(m));
 
     // ---------------------- the groups that can hold the K best, and a bound

@@ -190,6 +190,21 @@ def test_refused_rows_and_their_neighbours():
     assert _check(x, None, 1.0, 6)["dev_error"][0] == 2
 
 
+@pytest.mark.parametrize("V", [20, 700, 30000, 100000, 262144])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_full_of_what_is_refused(V, dtype, bad):
+    """All of the row, half of it, every 50th element, one run: no answer, and an end to the search for one."""
+    x = _logits(6, V, dtype, seed=V)
+    x[1] = bad
+    x[2, V // 2:] = bad
+    x[3, ::50] = bad
+    x[4, : V // 3] = -float("inf")
+    x[4, V // 3: V // 2] = bad
+    for K in (0, 7, min(V, 128)):
+        assert _check(x, _tokens(x, V), 1.0, K)["dev_error"][0] == 2
+
+
 def test_no_tokens_no_alternatives_no_rows():
     svp = _svp()
     x = _logits(5, 700, "f32", seed=11)
