@@ -202,9 +202,10 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, con
 // The row's statistics from every warp's part and the listed tokens, by each
 // warp for itself.
 struct DsSums {
-    float z, z_tail;  // relative to m and to m_tail
-    float t_tail;     // 1 - sum t_j (BUCKET)
-    int err;          // error bits
+    float z, z_tail;          // relative to m and to m_tail
+    float listed_q, tail_q;   // the two parts of z, over z
+    bool tail;                // the teacher's tail takes part
+    int err;                  // error bits
 };
 __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const DsRow& sm, int S, DsSums* sums) {
     const int lane = threadIdx.x & 31, n_parts = S * kDsWarps;
@@ -218,10 +219,10 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     zt = warp_sum_f(zt);
     const float ms = sm.m_listed, m = fmaxf(mt, ms);
     const float in_tail = zt * ex2(fmaxf((mt - m) * a.c, -1000.0f));
-    const float z = sm.z_listed * ex2(fmaxf((ms - m) * a.c, -1000.0f)) + in_tail;
+    const float listed = sm.z_listed * ex2(fmaxf((ms - m) * a.c, -1000.0f)), z = listed + in_tail;
     const bool no_tail = zt == 0.0f && te.y <= kTailRounding;
     const float t_tail = no_tail ? 0.0f : te.y;
-    *sums = DsSums{z, zt, t_tail, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
+    *sums = DsSums{z, zt, listed / z, in_tail / z, t_tail > 0.0f, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
     if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
     if (sums->err || te.w == INFINITY) return st;
     st.m_tail = mt;
@@ -229,30 +230,37 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     st.inv_z = 1.0f / z;
     st.mass = no_tail ? te.x : te.z;
     st.ln_t = te.w;
-    st.coef = zt > 0.0f ? (st.mass * (in_tail / z) - t_tail) * (float)a.inv_t / zt : 0.0f;
+    // S q_T - t_T from the smaller part: the same as sum t_j - S (1 - q_T)
+    const float d = sums->tail_q < 0.5f ? st.mass * sums->tail_q - t_tail : te.x - st.mass * sums->listed_q;
+    st.coef = zt > 0.0f ? d * (float)a.inv_t / zt : 0.0f;
     st.live = 1.0f;
     return st;
 }
 
 // The loss, by one warp.  log t - log q cancels where the student is near
 // the teacher: in double, and with the same c that the sums were made with.
+// The logarithm of a tail's mass near 1 is taken from what it lacks.
 __device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsRow& sm, const DistillStat& st,
-                                              const DsSums& sums, double ln_t) {
+                                              const DsSums& sums, const DsTeacher& te) {
     const int lane = threadIdx.x & 31;
     const double ln_z = ln_of(sums.z);
     double sum = 0.0;
     for (int j = lane; j < a.K; j += 32) {
         if (sm.id[j] < 0) continue;
-        const double lt = (double)sm.l[j] - ln_t;
+        const double lt = (double)sm.l[j] - te.ln_t;
         const float t = expf((float)lt);
         if (t > 0.0f) sum += (double)t * (lt - ((double)(sm.s[j] - st.m) * a.inv_t - ln_z));
     }
     sum = warp_sum_d(sum);
-    if (sums.t_tail > 0.0f)
-        sum = sums.z_tail > 0.0f
-                  ? sum + (double)sums.t_tail *
-                              (ln_of(sums.t_tail) - ((double)(st.m_tail - st.m) * a.inv_t + ln_of(sums.z_tail) - ln_z))
-                  : (double)INFINITY;
+    if (sums.tail && sums.z_tail > 0.0f) {
+        const double t_tail = 1.0 - te.mass;
+        const double ln_tail = te.mass < 0.5 ? (double)log1pf(-(float)te.mass) : ln_of((float)t_tail);
+        const double ln_q = sums.tail_q > 0.5f ? (double)log1pf(-sums.listed_q)
+                                               : (double)(st.m_tail - st.m) * a.inv_t + ln_of(sums.z_tail) - ln_z;
+        sum += t_tail * (ln_tail - ln_q);
+    } else if (sums.tail) {
+        sum = (double)INFINITY;
+    }
     return (float)sum;
 }
 
@@ -461,7 +469,7 @@ __device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const
     if (part != 0) return;
     DsSums sums;
     const DistillStat st = distill_stat(a, sm, S, &sums);
-    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums, te.ln_t) : 0.0f;
+    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums, te) : 0.0f;
     if (lane == 0) {
         a.loss[r] = loss;
         if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
