@@ -57,6 +57,17 @@ constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x 
 // would be +inf for it.
 constexpr float kTailRounding = 1.0f / 65536.0f;
 
+// What the first CTA's extra warp finds about the teacher: as it is to the
+// warp that has the loss, and rounded to 32 bits to every warp (double
+// operations of 27 warps at once took 2 us a row).
+struct alignas(16) DsTeacher {
+    double mass;  // sum of t_j
+    double ln_t;  // subtracted from the teacher's values; +inf: no teacher mass at all
+    __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, their sum, ln_t
+        const double t_tail = bucket ? fmax(1.0 - mass, 0.0) : 0.0;
+        return make_float4((float)mass, (float)t_tail, (float)(mass + t_tail), (float)ln_t);
+    }
+};
 // What the CTAs of a row exchange about it, and its listed tokens.
 struct DsRow {
     float2 part[kDsMaxCluster * kDsWarps];  // every warp's maximum and sum of the tail
@@ -64,18 +75,8 @@ struct DsRow {
     float m_listed, z_listed;      // their maximum, and sum of 2^((s - m_listed) c)
     alignas(16) int id[kMaxTop];
     float4 teacher;             // from the first CTA: DsTeacher's message
+    DsTeacher exact;            // in the last CTA
     float bad[kDsMaxCluster];   // from every CTA: error bits of its share of the checks
-};
-// What the first CTA's extra warp finds about the teacher.  Every warp reads
-// it, so it is sent rounded to 32 bits: double operations of 27 warps at once
-// took 2 us a row.
-struct DsTeacher {
-    double mass;  // sum of t_j
-    double ln_t;  // subtracted from the teacher's values; +inf: no teacher mass at all
-    __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, their sum, ln_t
-        const double t_tail = bucket ? fmax(1.0 - mass, 0.0) : 0.0;
-        return make_float4((float)mass, (float)t_tail, (float)(mass + t_tail), (float)ln_t);
-    }
 };
 
 __device__ __forceinline__ float warp_sum_f(float v) {
@@ -136,38 +137,56 @@ struct DsSum {
     }
 };
 
+// A row's listed tokens as a lane loads them (entries lane + 32 k).
+struct DsListed {
+    int id[kDsIds];
+    float l[kDsIds], s[kDsIds];  // teacher's value, student logit
+    __device__ __forceinline__ void load(const DistillArgs& a, int r) {
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k) {
+            const int j = (threadIdx.x & 31) + 32 * k;
+            id[k] = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
+            l[k] = j < a.K ? a.teacher[(size_t)r * a.K + j] : 0.0f;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void gather(const DistillArgs& a, const T* row) {
+#pragma unroll
+        for (int k = 0; k < kDsIds; ++k) s[k] = (unsigned)id[k] < (unsigned)a.V ? ElemT<T>::load(row + id[k]) : 0.0f;
+    }
+};
+
 // The teacher's side of a row, by one warp of each of the S CTAs while the
-// row is on its way: student logits of the listed tokens, checks (each CTA a
-// share of the search for doubles), and in the first CTA the sum of t_j (in
+// row is on its way: the listed tokens' checks (each CTA a share of the
+// search for doubles) and sums, and in the first CTA the sum of t_j (in
 // double: 1 - sum t cancels where the listed tokens hold nearly all of it).
-template <typename T>
-__device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, const T* row, DsRow& sm, int part, int S,
+__device__ __forceinline__ void distill_teacher(const DistillArgs& a, const DsListed& in, DsRow& sm, int part, int S,
                                                 DsTeacher* out, int* err_out) {
     const int lane = threadIdx.x & 31;
     float lmax = kNoMax, smax = kNoMax;
     int err = 0;
 #pragma unroll
-    for (int j = lane; j < kMaxTop; j += 32) {
-        int v = j < a.K ? a.ids[(size_t)r * a.K + j] : -1;
-        const float l = j < a.K ? a.teacher[(size_t)r * a.K + j] : 0.0f;
+    for (int k = 0; k < kDsIds; ++k) {
+        const int j = lane + 32 * k;
+        int v = in.id[k];
         if (v != -1 && (v < 0 || v >= a.V)) {
             err |= kDevErrToken;
             v = -1;
         }
         sm.id[j] = v;
-        sm.l[j] = l;
+        sm.l[j] = in.l[k];
+        sm.s[j] = in.s[k];
         if (v >= 0) {
-            const float x = ElemT<T>::load(row + v);
-            sm.s[j] = x;
-            smax = fmaxf(smax, x);
-            lmax = fmaxf(lmax, l);
-            if (isnan(l) || l == INFINITY) err |= kDevErrNonfinite;
+            smax = fmaxf(smax, in.s[k]);
+            lmax = fmaxf(lmax, in.l[k]);
+            if (isnan(in.l[k]) || in.l[k] == INFINITY) err |= kDevErrNonfinite;
         }
     }
     lmax = warp_max_redux(lmax);
     smax = warp_max_redux(smax);
     __syncwarp();
     float z = 0.0f;
+#pragma unroll 1
     for (int j = lane; j < a.K; j += 32)
         if (sm.id[j] >= 0) z += ex2((sm.s[j] - smax) * a.c);
     z = warp_sum_f(z);
@@ -175,6 +194,7 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, con
         sm.m_listed = smax;
         sm.z_listed = z;
     }
+#pragma unroll 1
     for (int j0 = 32 * part; j0 < a.K; j0 += 32 * S) {  // each id of 32 against all before it
         const int v = sm.id[j0 + lane];
         bool twice = false;
@@ -189,6 +209,7 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, int r, con
     if (part == 0) {
         const double ref = a.bucket ? 0.0 : (double)lmax;
         double mass = 0.0;
+#pragma unroll 1
         for (int j = lane; j < a.K; j += 32)
             if (sm.id[j] >= 0) mass += exp((double)sm.l[j] - ref);
         mass = warp_sum_d(mass);
@@ -212,9 +233,11 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     const float4 te = sm.teacher;
     DistillStat st{};
     float mt = kNoMax;
+#pragma unroll 1
     for (int k = lane; k < n_parts; k += 32) mt = fmaxf(mt, sm.part[k].x);
     mt = warp_max_redux(mt);
     float zt = 0.0f;
+#pragma unroll 1
     for (int k = lane; k < n_parts; k += 32) zt += sm.part[k].y * ex2(fmaxf((sm.part[k].x - mt) * a.c, -1000.0f));
     zt = warp_sum_f(zt);
     const float ms = sm.m_listed, m = fmaxf(mt, ms);
@@ -245,6 +268,7 @@ __device__ __forceinline__ float distill_loss(const DistillArgs& a, const DsRow&
     const int lane = threadIdx.x & 31;
     const double ln_z = ln_of(sums.z);
     double sum = 0.0;
+#pragma unroll 1
     for (int j = lane; j < a.K; j += 32) {
         if (sm.id[j] < 0) continue;
         const double lt = (double)sm.l[j] - te.ln_t;
@@ -333,8 +357,9 @@ template <typename T>
 __device__ __forceinline__ void distill_zero(const RowView<T>& row, T* g, int first, int step) {
     const int lane = threadIdx.x & 31;
     const bool aligned = same_alignment(row, g);
+#pragma unroll 1
     for (int v0 = first * kDsTile * 32; v0 < row.nvec; v0 += step * kDsTile * 32)
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < kDsTile; ++j) {
             const int v = v0 + j * 32 + lane;
             T* at = g + row.head + (size_t)v * ElemT<T>::VEC;
@@ -342,7 +367,7 @@ __device__ __forceinline__ void distill_zero(const RowView<T>& row, T* g, int fi
             if (aligned) {
                 *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
             } else {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < ElemT<T>::VEC; ++i) store_elem(at + i, 0.0f);
             }
         }
@@ -443,16 +468,15 @@ __device__ __forceinline__ void distill_no_row(const DistillArgs& a, int r) {  /
     if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = DistillStat{};
 }
 
-// What the extra warp does for a row: the teacher, sent to every CTA of the
-// row (ready() is called before that), then sync(), then in the first CTA the
-// loss and the row's statistics.
-template <typename T, bool CLUSTER, typename R, typename W>
-__device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const T* logits, DsRow& sm, int part, int S,
-                                              R&& ready, W&& sync) {
+// What the extra warp does for a row.  Before its sums are exchanged: the
+// teacher, sent to every CTA of the row (ready() is called before that).
+template <bool CLUSTER, typename R>
+__device__ __forceinline__ void distill_before(const DistillArgs& a, const DsListed& in, DsRow& sm, int part, int S,
+                                               R&& ready) {
     const int lane = threadIdx.x & 31;
     DsTeacher te{};
     int bad;
-    distill_teacher<T>(a, r, logits, sm, part, S, &te, &bad);
+    distill_teacher(a, in, sm, part, S, &te, &bad);
     const float4 message = te.message(a.bucket);
     __syncwarp();
     ready();
@@ -461,16 +485,22 @@ __device__ __forceinline__ void distill_extra(const DistillArgs& a, int r, const
             cluster_store(cluster_map(&sm.bad[part], lane), __int_as_float(bad));
             if (part == 0) cluster_store(cluster_map(&sm.teacher, lane), message);
         }
+        if (part == 0 && lane == S) cluster_store(cluster_map(&sm.exact, S - 1), *reinterpret_cast<const float4*>(&te));
     } else if (lane == 0) {
         sm.bad[0] = __int_as_float(bad);
         sm.teacher = message;
+        sm.exact = te;
     }
-    sync();
-    if (part != 0) return;
+    __syncwarp();
+}
+// After it, in the row's last CTA (the first one has the teacher's sums to
+// do): the loss and the row's statistics.
+__device__ __forceinline__ void distill_after(const DistillArgs& a, int r, const DsRow& sm, int part, int S) {
+    if (part != S - 1) return;
     DsSums sums;
     const DistillStat st = distill_stat(a, sm, S, &sums);
-    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums, te) : 0.0f;
-    if (lane == 0) {
+    const float loss = st.live != 0.0f ? distill_loss(a, sm, st, sums, sm.exact) : 0.0f;
+    if ((threadIdx.x & 31) == 0) {
         a.loss[r] = loss;
         if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
         if (sums.err && a.dev_error) atomicOr(a.dev_error, sums.err);
@@ -509,7 +539,12 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
     };
     const RowView<T> row(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V);
     if (warp == kDsWarps) {
-        distill_extra<T, CLUSTER>(a, r, row.row, sm, part, S, ready, sync);
+        DsListed in;
+        in.load(a, r);
+        in.gather(a, row.row);
+        distill_before<CLUSTER>(a, in, sm, part, S, ready);
+        sync();
+        distill_after(a, r, sm, part, S);
         return;
     }
     const int unit = part * kDsWarps + warp, units = S * kDsWarps, tiles = tiles_of(row);
@@ -557,6 +592,10 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
 // as soon as it has been written.  So a row is read once and written once:
 // 2 + 2 bytes an element (bf16), the bound.  What the CTAs of a row exchange
 // is there twice, for this row and the next.
+//
+// Its size matters: three CTAs' warps are in different phases of it, and with
+// the loops that run once or twice a row unrolled (101 KB of code, 74 KB
+// without) the same row took a tenth longer.
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, int n_buf) {
     constexpr int VEC = ElemT<T>::VEC;
@@ -584,29 +623,42 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
     if (CLUSTER) cluster_arrive();
     auto row_of = [&](int r) { return RowView<T>(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V); };
     auto grad_of = [&](int r) { return static_cast<T*>(a.grad) + (size_t)r * a.grad_stride; };
-    float w = 0.0f;  // weight of the row that next_row found
-    auto next_row = [&](int r) {  // from r on, rows of weight zero done on the way
-        for (; r < a.R; r += step) {
-            w = a.weights ? a.weights[r] : 1.0f;
-            if (w != 0.0f) break;
+    // The rows of this cluster in turn, those of weight zero done on the way.
+    int ahead = blockIdx.x / S;
+    float w = 0.0f;  // of the row that next_row gave
+    auto next_row = [&] {
+        for (;;) {
+            const int r = ahead;
+            ahead += step;
+            w = a.weights && r < a.R ? a.weights[r] : 1.0f;
+            if (r >= a.R || w != 0.0f) return r;
             if (warp < kDsWarps)
                 distill_zero(row_of(r), grad_of(r), unit, units);
             else if (part == 0 && lane == 0)
                 distill_no_row(a, r);
         }
-        return r;
     };
     int p = 0;
     if (warp == kDsWarps) {
-        for (int r = next_row(blockIdx.x / S); r < a.R; r = next_row(r + step), p ^= 1)
-            distill_extra<T, CLUSTER>(a, r, row_of(r).row, rows[p], part, S, ready, sync);
+#pragma unroll 1
+        for (int r = next_row(); r < a.R; p ^= 1) {
+            DsListed in;
+            in.load(a, r);
+            in.gather(a, row_of(r).row);
+            const int after = next_row();
+            distill_before<CLUSTER>(a, in, rows[p], part, S, ready);
+            sync();
+            distill_after(a, r, rows[p], part, S);
+            r = after;
+        }
         ready();
         return;
     }
     const DsBuffers<T> buf{reinterpret_cast<uint4*>(ds_raw) + (size_t)warp * n_buf * (kDsTileBytes / 16), full[warp]};
-    int next = next_row(blockIdx.x / S);
+    int next = next_row();
     uint32_t phase = 0, pending = 0;  // of each buffer; pending: a copy was started and not awaited
     if (lane == 0) {
+#pragma unroll 1
         for (int b = 0; b < n_buf; ++b) mbar_init(&full[warp][b], 1);
         mbar_fence_init();
     }
@@ -619,17 +671,19 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         if (lane == 0) buf.copy(row, t, b);
         pending |= 1u << b;
     };
+#pragma unroll 1
     for (int b = 0; b < n_buf; ++b) fill(next, b);
     int ids_next[kDsIds];
     if (next < a.R) load_ids(a, next, ids_next);
     bool ok = true;
+#pragma unroll 1
     while (next < a.R) {
         const int r = next;
         const float w_row = w;
         int ids[kDsIds];
 #pragma unroll
         for (int k = 0; k < kDsIds; ++k) ids[k] = ids_next[k];
-        next = next_row(r + step);
+        next = next_row();
         if (next < a.R) load_ids(a, next, ids_next);  // needed a row later
         const RowView<T> row = row_of(r);
         T* g = grad_of(r);
@@ -639,6 +693,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         DsSum sum;
         float2 ends = make_float2(-INFINITY, -INFINITY);
         if (unit == 0) ends = distill_ends(row, ids, sum, a.c);
+#pragma unroll 1
         for (int b = 0; b < n_buf && ok; ++b) {
             if (!((pending >> b) & 1u)) continue;
             ok = mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
@@ -678,6 +733,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
             listed(g, 0, row.head);
             listed(g + tail0, tail0, row.tail);
         }
+#pragma unroll 1
         for (int b = 0; b < n_buf; ++b) {
             const int t = unit + b * units;
             if (st.live != 0.0f && t < tiles) {
@@ -711,6 +767,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
     }
     ready();
     if (!ok && lane == 0)  // the copies still on their way land before the CTA ends
+#pragma unroll 1
         for (int b = 0; b < n_buf; ++b)
             if ((pending >> b) & 1u) mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
 }
