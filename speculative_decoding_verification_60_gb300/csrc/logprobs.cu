@@ -254,16 +254,16 @@ struct LpFinish {
     int valid;
 };
 
+__device__ __forceinline__ void lp_clear(LpFinish& s) {
+    for (int i = threadIdx.x; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
+    if (threadIdx.x == 0) s.found = kLpBins;
+}
 // A bound tau such that K .. K + slack keys lie above it, or, where many keys
 // are equal, the K-th largest key itself (then fewer than K lie above); -inf's
 // key if fewer than K keys lie above that.  Keys are counted in bins down from `top`,
 // then the K-th one's bin in finer ones.  each(f) calls f(key) for the keys,
 // shared among the CTA's threads.  *above: keys above tau.  cleared: the bins
 // are (lp_clear and a barrier).
-__device__ __forceinline__ void lp_clear(LpFinish& s) {
-    for (int i = threadIdx.x; i < kLpBins; i += kLpThreads) s.bin[i] = 0;
-    if (threadIdx.x == 0) s.found = kLpBins;
-}
 template <typename F>
 __device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, int* above, bool cleared, F&& each) {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -276,10 +276,13 @@ __device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, 
             __syncthreads();
         }
         cleared = false;
+        int finite = 0;  // keys above -inf's that this thread has seen
         each([&](uint32_t k) {
             const uint32_t bin = (hi - k) >> shift;
             if (k <= hi && bin < kLpBins) atomicAdd(&s.bin[bin], 1);
+            finite += k > kLpNoneKey && k <= top;
         });
+        if (tid == 0) s.in = 0;
         __syncthreads();
         if (tid < 32) {
             constexpr int kEach = kLpBins / 32;
@@ -301,11 +304,8 @@ __device__ __forceinline__ uint32_t lp_select(LpFinish& s, uint32_t top, int K, 
         __syncthreads();
         const uint32_t bin = (uint32_t)s.found;
         if (bin == kLpBins) {  // further down: among -inf (or past the last key), or in the whole range
-            if (tid == 0) s.in = 0;
-            __syncthreads();
-            each([&](uint32_t k) {
-                if (k > kLpNoneKey && k <= top) atomicAdd(&s.in, 1);
-            });
+            finite = __reduce_add_sync(0xffffffffu, finite);
+            if (lane == 0 && finite) atomicAdd(&s.in, finite);
             __syncthreads();
             if (s.in < K || shift == 24) {
                 *above = s.in;
@@ -497,45 +497,9 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     }
     const uint32_t top = okey32(warp_max_redux(m));
 
-    // ---------------------- the groups that can hold the K best, and a bound
-    uint32_t tau = 0u;
-    int above = 0;
-    const bool all = nb <= LpFinish::kGroups;
-    if (all) {  // few groups: all of them, and the bound is found among their vectors
-        for (int g = tid; g < nb; g += kLpThreads) s.group[g] = g + 1;
-        if (tid == 0) s.n_group = nb;
-    } else {
-        tau = lp_select(s, top, K, &above, true, [&](auto&& f) {
-#pragma unroll 1
-            for (int g = 1 + tid; g <= nb; g += kLpThreads) f(group_key[g]);
-        });
-        const int equal = K - above;  // if above tau lie fewer than K: also the first that reach it
-#pragma unroll 1
-        for (int g = 1 + tid; g <= nb; g += kLpThreads) {
-            const uint32_t k = group_key[g];
-            bool take = k > tau;
-            if (k == tau && equal > 0) {
-                int before = 0;
-#pragma unroll 1
-                for (int i = 1; i < g && before < equal; ++i) before += group_key[i] == tau;
-                take = before < equal;
-            }
-            if (take) {
-                const int at = atomicAdd(&s.n_group, 1);
-                if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
-            }
-        }
-    }
-    __syncthreads();
-    if (!s.valid) {
-        lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
-        return;
-    }
-    const int n_group = s.n_group;
-
-    // --------------------------- the elements above the bound, from them
     constexpr int kAhead = 6;  // groups a warp reads at a time: under load a read takes 1 to 2 us
-    auto for_vectors = [&](auto&& f) {  // f(i, bits) per lane: bit k for group i + k * kLpWarps, from use(vector)
+    int n_group = nb;
+    auto for_vectors = [&](auto&& f) {  // f(i, vectors) per lane: vector k of group i + k * kLpWarps
 #pragma unroll 1
         for (int i0 = warp; i0 < n_group; i0 += kAhead * kLpWarps) {
             uint4 q[kAhead];
@@ -545,24 +509,56 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
             f(i0, q);
         }
     };
-    // The bound of the groups leaves little more than K elements, unless the
-    // row has few groups or its best elements share some (a sorted row).
-    // Then the bound is raised to one that leaves about K vectors.
-    bool raise = all;
+    // A bound from the keys of the groups, the groups that reach it, and the
+    // elements above it from those.  Where the row has few groups, or the
+    // bound leaves many more than K elements (the best of a sorted row share
+    // some groups), the bound comes from the keys of the chosen groups'
+    // vectors.
+    bool vectors = nb <= LpFinish::kGroups;
+    if (vectors) {
+        for (int g = tid; g < nb; g += kLpThreads) s.group[g] = g + 1;
+        __syncthreads();
+    }
     float bound;
-    for (;;) {
-        if (raise) {
-            tau = lp_select(s, top, K, &above, all, [&](auto&& count) {
+#pragma unroll 1
+    for (bool first = true;; first = false) {
+        int above;
+        const uint32_t tau = lp_select(s, top, K, &above, first, [&](auto&& f) {
+            if (vectors) {
                 for_vectors([&](int i0, const uint4* q) {
 #pragma unroll
                     for (int k = 0; k < kAhead; ++k)
-                        if (i0 + k * kLpWarps < n_group && row.has(s.group[i0 + k * kLpWarps]))
-                            count(okey32(Vec::max(q[k])));
+                        if (i0 + k * kLpWarps < n_group && row.has(s.group[i0 + k * kLpWarps])) f(okey32(Vec::max(q[k])));
                 });
-            });
-            if (tid == 0) s.n_cand = 0;
-            __syncthreads();
+            } else {
+#pragma unroll 1
+                for (int g = 1 + tid; g <= nb; g += kLpThreads) f(group_key[g]);
+            }
+        });
+        if (!vectors) {
+            const int equal = K - above;  // if above tau lie fewer than K: also the first that reach it
+#pragma unroll 1
+            for (int g = 1 + tid; g <= nb; g += kLpThreads) {
+                const uint32_t k = group_key[g];
+                bool take = k > tau;
+                if (k == tau && equal > 0) {
+                    int before = 0;
+#pragma unroll 1
+                    for (int i = 1; i < g && before < equal; ++i) before += group_key[i] == tau;
+                    take = before < equal;
+                }
+                if (take) {
+                    const int at = atomicAdd(&s.n_group, 1);
+                    if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
+                }
+            }
         }
+        __syncthreads();
+        if (!s.valid) {
+            lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
+            return;
+        }
+        if (!vectors) n_group = s.n_group;
         // As a float: the key below zero's is -0, which compares equal to zero.
         bound = tau == 0x7fffffffu ? __uint_as_float(0x80000001u) : okey32_to_float(tau);
         auto push = [&](float x, int idx) {
@@ -593,9 +589,10 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
             if (lane < row.tail) push(ends.y, row.index(nb + 1));
         }
         __syncthreads();
-        if (s.n_cand <= kLpCands || raise) break;
-        raise = true;
+        if (s.n_cand <= kLpCands || vectors) break;
+        vectors = true;
         __syncthreads();  // all have seen the count
+        if (tid == 0) s.n_cand = 0;
     }
     int n_cand = s.n_cand;
     if (n_cand < K) {
