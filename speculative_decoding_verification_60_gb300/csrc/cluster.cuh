@@ -42,24 +42,6 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float4 v) {
                  : "memory");
 }
 
-// Arrives on another CTA's mbarrier (address by cluster_map): what this
-// thread wrote before, there too, is visible to who waits for the phase.
-__device__ __forceinline__ void cluster_mbar_arrive(uint32_t bar) {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// As mbar_test and mbar_wait for a phase completed from other CTAs.
-__device__ __forceinline__ bool cluster_mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Clusters of S CTAs of this shape that run at the same time on the current
 // device (a GPC holds whole clusters only, so this is less than its CTAs over
 // S).  The first call per (device, kernel, S, shared memory) asks, later ones
@@ -102,22 +84,30 @@ inline bool clusters_at_once(const void* kernel, int S, int block, size_t dyn_sm
     return true;
 }
 
-// A launch of `clusters` clusters of S CTAs.
+// A launch of n clusters of S CTAs (S = 1: of n CTAs), after_clear: right
+// after clear_error on this stream, and allowed to start beside it.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_clusters(void (*kernel)(KArgs...), long long clusters, int S, int block, size_t dyn_smem,
-                                   cudaStream_t st, Args... args) {
+inline cudaError_t launch_rows(void (*kernel)(KArgs...), long long n, int S, int block, size_t dyn_smem, bool after_clear,
+                               cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * S));
+    cfg.gridDim = dim3((unsigned)(n * S));
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = dyn_smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int used = 0;
+    if (after_clear) {
+        attr[used].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[used++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (S > 1) {
+        attr[used].id = cudaLaunchAttributeClusterDimension;
+        attr[used].val.clusterDim.x = S;
+        attr[used].val.clusterDim.y = 1;
+        attr[used++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = used;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 

@@ -503,7 +503,7 @@ __device__ __forceinline__ void distill_after(const DistillArgs& a, int r, const
     if ((threadIdx.x & 31) == 0) {
         a.loss[r] = loss;
         if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = st;
-        if (sums.err && a.dev_error) atomicOr(a.dev_error, sums.err);
+        if (sums.err) set_error(a.dev_error, sums.err);
     }
 }
 
@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
+    error_cleared();
     if (a.weights && a.weights[r] == 0.0f) {
         if (part == 0 && tid == 0) distill_no_row(a, r);
         return;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
         });
     }
     if (!ok && lane == 0) {  // the row is refused; the copy still on its way lands before the CTA ends
-        if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+        set_error(a.dev_error, kDevErrTimeout);
         mbar_wait(&full[warp], parity, kDsLimitNs);
     }
     __syncwarp();
@@ -620,6 +621,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         if (!waited) cluster_wait();
         waited = true;
     };
+    error_cleared();
     if (CLUSTER) cluster_arrive();
     auto row_of = [&](int r) { return RowView<T>(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V); };
     auto grad_of = [&](int r) { return static_cast<T*>(a.grad) + (size_t)r * a.grad_stride; };
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
             if (!((pending >> b) & 1u)) continue;
             ok = mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
             if (!ok) {
-                if (lane == 0 && a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+                if (lane == 0) set_error(a.dev_error, kDevErrTimeout);
                 break;
             }
             pending &= ~(1u << b);
@@ -855,9 +857,8 @@ static cudaError_t launch_distill_loss(const DistillArgs& a, cudaStream_t st) {
     // CTAs that share a row: more than one where rows are too few for every SM
     int S = 1;
     while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
-    if (S > 1) return launch_clusters(k_distill_loss<T, true>, a.R, S, kDsThreads, dyn, st, a);
-    k_distill_loss<T, false><<<a.R, kDsThreads, dyn, st>>>(a);
-    return cudaGetLastError();
+    return launch_rows(S > 1 ? k_distill_loss<T, true> : k_distill_loss<T, false>, a.R, S, kDsThreads, dyn,
+                       a.dev_error != nullptr, st, a);
 }
 
 template <typename T>
@@ -885,12 +886,12 @@ static cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t st) {
             S > 8 ? cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
         if (e != cudaSuccess) return e;
         if (!clusters_at_once(reinterpret_cast<const void*>(kern), S, kDsThreads, dyn, &clusters)) return cudaErrorUnknown;
-        return launch_clusters(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, st, a, n_buf);
+        return launch_rows(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, a.dev_error != nullptr, st, a,
+                           n_buf);
     }
     const int per_sm = n_buf <= 2 ? 3 : n_buf <= 3 ? 2 : 1;  // by registers, and by shared memory
     clusters = shape.sms * per_sm < a.R ? shape.sms * per_sm : a.R;
-    k_distill_grad<T, false><<<clusters, kDsThreads, dyn, st>>>(a, n_buf);
-    return cudaGetLastError();
+    return launch_rows(k_distill_grad<T, false>, clusters, 1, kDsThreads, dyn, a.dev_error != nullptr, st, a, n_buf);
 }
 
 template <typename T>
@@ -932,7 +933,7 @@ extern "C" spec_status spec_distill_topk(const void* student, spec_dtype dtype, 
     if (!on_device) return SPEC_OK;  // no rows and no error word: nothing to do
     if (!select_device_of(on_device)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dev_error && cudaMemsetAsync(dev_error, 0, sizeof(int32_t), st) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (!clear_error(dev_error, st)) return SPEC_ERR_CUDA;
     if (R == 0) return SPEC_OK;
     const float c = (float)(kLog2e / (double)temperature);
     DistillArgs a{student, R, V, K, row_stride, teacher_ids, teacher_logprobs, weights,

@@ -384,8 +384,8 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
             if (a.logprob) a.logprob[r] = a.tokens ? lp_log(a, xt - m, ln_z) : 0.0f;
             if (a.rank) a.rank[r] = a.tokens ? before + 1 : -1;
             if (a.entropy) a.entropy[r] = fmaf(-kLn2, e / z, ln_z.x) + ln_z.y;
-        } else if (a.dev_error) {
-            atomicOr(a.dev_error, kDevErrNonfinite);
+        } else {
+            set_error(a.dev_error, kDevErrNonfinite);
         }
     }
 }
@@ -623,10 +623,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
+    error_cleared();
     const int tok = a.tokens ? a.tokens[r] : 0;
     if (tok < 0 || tok >= a.V) {
         if (part == 0) {
-            if (tok != -1 && tid == 0 && a.dev_error) atomicOr(a.dev_error, kDevErrToken);
+            if (tok != -1 && tid == 0) set_error(a.dev_error, kDevErrToken);
             lp_no_result(a, r, tok == -1 ? 0.0f : -INFINITY, tid, kLpThreads);
         }
         return;
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
         p.z = NAN;
         if (lane == 0) {
-            if (a.dev_error) atomicOr(a.dev_error, kDevErrTimeout);
+            set_error(a.dev_error, kDevErrTimeout);
             for (int i = 0; i < kDepth && g0 + i * step < row.nb; ++i) {
                 mbar_wait(&bars[slot], parity, kLpLimitNs);
                 if (++slot == kDepth) {
@@ -758,11 +759,8 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
     const size_t dyn = lp_ring(S > 1) + (size_t)(groups + 1) * sizeof(uint32_t);
-    if (S == 1) {
-        k_token_logprobs<T, false><<<a.R, kLpThreads, dyn, st>>>(a);
-        return cudaGetLastError();
-    }
-    return launch_clusters(k_token_logprobs<T, true>, a.R, S, kLpThreads, dyn, st, a);
+    return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn,
+                       a.dev_error != nullptr, st, a);
 }
 
 }  // namespace sv
@@ -784,7 +782,7 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     if (!on_device) return SPEC_OK;  // no rows and no error word: nothing to do
     if (!select_device_of(on_device)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dev_error && cudaMemsetAsync(dev_error, 0, sizeof(int32_t), st) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (!clear_error(dev_error, st)) return SPEC_ERR_CUDA;
     if (R == 0) return SPEC_OK;
     const double inv_t = 1.0 / (double)temperature;
     const float inv_hi = (float)inv_t;
