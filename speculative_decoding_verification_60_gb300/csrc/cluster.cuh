@@ -42,6 +42,45 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float4 v) {
                  : "memory");
 }
 
+// Stores into another CTA whose bytes count on an mbarrier there: what the
+// mbarrier has counted is visible to who waits for its phase with
+// cluster_mbar_wait.  Nothing else that this thread wrote is waited for, which
+// a cluster barrier's release would.  addr and bar of the same CTA.
+__device__ __forceinline__ void cluster_send(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_int(v)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_send(uint32_t addr, float2 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "r"(__float_as_int(v.x)), "r"(__float_as_int(v.y)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_send(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     addr),
+                 "r"(__float_as_int(v.x)), "r"(__float_as_int(v.y)), "r"(__float_as_int(v.z)),
+                 "r"(__float_as_int(v.w)), "r"(bar)
+                 : "memory");
+}
+// As mbar_wait, for a phase that other CTAs complete.
+__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) return false;
+    }
+}
+
 // Clusters of S CTAs of this shape that run at the same time on the current
 // device (a GPC holds whole clusters only, so this is less than its CTAs over
 // S).  The first call per (device, kernel, S, shared memory) asks, later ones

@@ -468,11 +468,18 @@ __device__ __forceinline__ void distill_no_row(const DistillArgs& a, int r) {  /
     if (a.stats) reinterpret_cast<DistillStat*>(a.stats)[r] = DistillStat{};
 }
 
+// What the CTAs of a row send each other, in bytes to the one of rank `part`:
+// every warp's part, every CTA's error bits, the teacher.
+__device__ __forceinline__ uint32_t distill_bytes(int part, int S) {
+    return (uint32_t)(S * (kDsWarps * sizeof(float2) + sizeof(float)) + sizeof(float4) +
+                      (part == S - 1 ? sizeof(DsTeacher) : 0));
+}
 // What the extra warp does for a row.  Before its sums are exchanged: the
 // teacher, sent to every CTA of the row (ready() is called before that).
+// bar: the mbarrier that counts what is sent.
 template <bool CLUSTER, typename R>
-__device__ __forceinline__ void distill_before(const DistillArgs& a, const DsListed& in, DsRow& sm, int part, int S,
-                                               R&& ready) {
+__device__ __forceinline__ void distill_before(const DistillArgs& a, const DsListed& in, DsRow& sm, uint64_t* bar,
+                                               int part, int S, R&& ready) {
     const int lane = threadIdx.x & 31;
     DsTeacher te{};
     int bad;
@@ -481,11 +488,14 @@ __device__ __forceinline__ void distill_before(const DistillArgs& a, const DsLis
     __syncwarp();
     ready();
     if (CLUSTER) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, distill_bytes(part, S));  // sm's own entries are written, too
         if (lane < S) {
-            cluster_store(cluster_map(&sm.bad[part], lane), __int_as_float(bad));
-            if (part == 0) cluster_store(cluster_map(&sm.teacher, lane), message);
+            const uint32_t to = cluster_map(bar, lane);
+            cluster_send(cluster_map(&sm.bad[part], lane), __int_as_float(bad), to);
+            if (part == 0) cluster_send(cluster_map(&sm.teacher, lane), message, to);
         }
-        if (part == 0 && lane == S) cluster_store(cluster_map(&sm.exact, S - 1), *reinterpret_cast<const float4*>(&te));
+        if (part == 0 && lane == S)
+            cluster_send(cluster_map(&sm.exact, S - 1), *reinterpret_cast<const float4*>(&te), cluster_map(bar, S - 1));
     } else if (lane == 0) {
         sm.bad[0] = __int_as_float(bad);
         sm.teacher = message;
@@ -515,7 +525,7 @@ template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
     extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps] tiles
     __shared__ DsRow sm;
-    __shared__ uint64_t full[kDsWarps];
+    __shared__ uint64_t full[kDsWarps], sent;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
@@ -524,16 +534,14 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
         if (part == 0 && tid == 0) distill_no_row(a, r);
         return;
     }
-    if (CLUSTER) cluster_arrive();  // awaited before the first store into another CTA
-    auto sync = [] {
-        __syncwarp();
-        if (CLUSTER) {
-            cluster_arrive();
-            cluster_wait();
-        } else {
-            __syncthreads();
+    if (CLUSTER) {
+        if (tid == 0) {
+            mbar_init(&sent, 1);
+            mbar_fence_init();
         }
-    };
+        __syncwarp();
+        cluster_arrive();  // awaited before the first store into another CTA
+    }
     auto ready = [] {
         __syncwarp();
         if (CLUSTER) cluster_wait();
@@ -543,9 +551,18 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
         DsListed in;
         in.load(a, r);
         in.gather(a, row.row);
-        distill_before<CLUSTER>(a, in, sm, part, S, ready);
-        sync();
-        distill_after(a, r, sm, part, S);
+        distill_before<CLUSTER>(a, in, sm, &sent, part, S, ready);
+        if (!CLUSTER) __syncthreads();
+        if (!CLUSTER || cluster_mbar_wait(&sent, 0, kDsLimitNs)) {
+            distill_after(a, r, sm, part, S);
+        } else if (part == S - 1 && lane == 0) {
+            set_error(a.dev_error, kDevErrTimeout | kDevErrNonfinite);
+            distill_no_row(a, r);
+        }
+        if (CLUSTER) {
+            cluster_arrive();
+            cluster_wait();
+        }
         return;
     }
     const int unit = part * kDsWarps + warp, units = S * kDsWarps, tiles = tiles_of(row);
@@ -579,11 +596,13 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
     const float2 p = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);
     ready();
     if (CLUSTER) {
-        if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), p);
-    } else if (lane == 0) {
-        sm.part[unit] = p;
+        if (lane < S) cluster_send(cluster_map(&sm.part[unit], lane), p, cluster_map(&sent, lane));
+        cluster_arrive();  // no CTA ends while another may write into it
+        cluster_wait();
+    } else {
+        if (lane == 0) sm.part[unit] = p;
+        __syncthreads();
     }
-    sync();
 }
 
 // Loss and gradient, by persistent CTAs or clusters of S that take rows in
@@ -602,18 +621,20 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
     constexpr int VEC = ElemT<T>::VEC;
     extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps][n_buf] tiles
     __shared__ DsRow rows[2];
-    __shared__ uint64_t full[kDsWarps][kDsMaxTiles];
+    __shared__ uint64_t full[kDsWarps][kDsMaxTiles], sent[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int step = gridDim.x / S, unit = part * kDsWarps + warp, units = S * kDsWarps;
-    auto sync = [] {
-        __syncwarp();
-        if (CLUSTER) {
-            cluster_arrive();
-            cluster_wait();
-        } else {
+    // What this row's CTAs sent each other has arrived (once for each of the
+    // two places in turn); false if not in time.
+    uint32_t turn = 0;
+    auto arrived = [&] {
+        if (!CLUSTER) {
             __syncthreads();
+            return true;
         }
+        const uint32_t n = turn++;
+        return cluster_mbar_wait(&sent[n & 1], (n >> 1) & 1, kDsLimitNs);
     };
     bool waited = !CLUSTER;
     auto ready = [&] {  // every CTA of the cluster has started
@@ -622,7 +643,22 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         waited = true;
     };
     error_cleared();
-    if (CLUSTER) cluster_arrive();
+    if (CLUSTER) {
+        if (tid == 0) {
+            mbar_init(&sent[0], 1);
+            mbar_init(&sent[1], 1);
+            mbar_fence_init();
+        }
+        __syncwarp();
+        cluster_arrive();
+    }
+    auto leave = [&] {  // no CTA ends while another may write into it
+        ready();
+        if (CLUSTER) {
+            cluster_arrive();
+            cluster_wait();
+        }
+    };
     auto row_of = [&](int r) { return RowView<T>(static_cast<const T*>(a.student) + (size_t)r * a.stride, a.V); };
     auto grad_of = [&](int r) { return static_cast<T*>(a.grad) + (size_t)r * a.grad_stride; };
     // The rows of this cluster in turn, those of weight zero done on the way.
@@ -648,12 +684,17 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
             in.load(a, r);
             in.gather(a, row_of(r).row);
             const int after = next_row();
-            distill_before<CLUSTER>(a, in, rows[p], part, S, ready);
-            sync();
+            distill_before<CLUSTER>(a, in, rows[p], &sent[p], part, S, ready);
+            if (!arrived()) {  // this row and those left are refused
+                if (lane == 0) set_error(a.dev_error, kDevErrTimeout | kDevErrNonfinite);
+                for (; r < a.R; r += step)
+                    if (part == 0 && lane == 0) distill_no_row(a, r);
+                break;
+            }
             distill_after(a, r, rows[p], part, S);
             r = after;
         }
-        ready();
+        leave();
         return;
     }
     const DsBuffers<T> buf{reinterpret_cast<uint4*>(ds_raw) + (size_t)warp * n_buf * (kDsTileBytes / 16), full[warp]};
@@ -690,6 +731,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         const RowView<T> row = row_of(r);
         T* g = grad_of(r);
         DsRow& sm = rows[p];
+        const int at_row = p;
         p ^= 1;
         const int tiles = tiles_of(row), tail0 = row.head + row.nvec * VEC;
         DsSum sum;
@@ -711,11 +753,16 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         const float2 mine = make_float2(sum.m, ok ? warp_sum_f(sum.z.x + sum.z.y) : NAN);  // a wait ran out: refused
         ready();
         if (CLUSTER) {
-            if (lane < S) cluster_store(cluster_map(&sm.part[unit], lane), mine);
+            if (lane < S) cluster_send(cluster_map(&sm.part[unit], lane), mine, cluster_map(&sent[at_row], lane));
         } else if (lane == 0) {
             sm.part[unit] = mine;
         }
-        sync();
+        if (!arrived()) {  // as the extra warp finds, too
+            ok = false;
+#pragma unroll 1
+            for (int k = r; k < a.R; k += step) distill_zero(row_of(k), grad_of(k), unit, units);
+            break;
+        }
         DsSums sums;
         const DistillStat st = distill_stat(a, sm, S, &sums);
         if (st.live == 0.0f) distill_zero(row, g, unit, units);
@@ -767,11 +814,12 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
             if (ok) fill(next, b);
         }
     }
-    ready();
     if (!ok && lane == 0)  // the copies still on their way land before the CTA ends
 #pragma unroll 1
         for (int b = 0; b < n_buf; ++b)
             if ((pending >> b) & 1u) mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
+    __syncwarp();
+    leave();
 }
 
 // The gradient alone, from a row's statistics: a warp per tile, a CTA per
