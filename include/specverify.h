@@ -46,6 +46,13 @@
  *    ending, and waits for that kernel to complete before it reads or
  *    writes anything.  Stream order is kept; after any other stream
  *    operation (a copy, an event) they are ordinary launches.
+ *  - spec_token_logprobs and spec_distill_topk take no workspace.  Where
+ *    dev_error is given, a small kernel clears it and their own kernel may
+ *    start beside that one; both come after everything enqueued before the
+ *    call.  Ids, ranks, slots and error bits do not depend on the batch; the
+ *    floats of a row may differ in their last bits with R, because the
+ *    number of CTAs that share a row goes by it, and with the row's
+ *    alignment.  The same call gives the same bits every time.
  */
 #ifndef SPECVERIFY_H
 #define SPECVERIFY_H
@@ -99,8 +106,10 @@ typedef enum {
 #define SPEC_DEVERR_PARENT 4     /* parent[] not a tree rooted at 0 with parent[i] < i, deeper than max_depth,
                                     or a node with more than 64 children */
 #define SPEC_DEVERR_LENGTH 8     /* compaction: accepted length or source row out of range */
-#define SPEC_DEVERR_TIMEOUT 16   /* a wait for a bulk copy ran out (2 s); the rows it left were
-                                    recomputed by the two-pass route, so the results stand */
+#define SPEC_DEVERR_TIMEOUT 16   /* a wait for a bulk copy ran out (2 s).  Verification, sampling:
+                                    the rows it left were recomputed by the two-pass route, so
+                                    the results stand.  spec_token_logprobs, spec_distill_topk:
+                                    the rows are refused (SPEC_DEVERR_NONFINITE is set, too) */
 #define SPEC_DEVERR_CAPACITY 32  /* cache blocks: the free list or a request's table row ran out */
 
 typedef struct {
@@ -398,12 +407,15 @@ spec_status spec_sample_rows(const void* logits, spec_dtype dtype, int R, int V,
  *               (logit descending, index ascending) order.
  *  entropy      [R] out or NULL: -sum p log p, in nats.
  *  top_ids, top_logprobs  [R, top_k] out: the first top_k tokens in that
- *               order and log p of each (-inf where the logit is).
+ *               order and log p of each (-inf where the logit is, or where
+ *               log p is below what a float holds).
  *  A skipped row gets logprob 0, entropy 0, rank -1, top_ids -1 and
  *  top_logprobs -inf.  A token outside [0, V) other than -1
  *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it
  *  (SPEC_DEVERR_NONFINITE) gives the same, with logprob -inf.  With tokens
  *  NULL, logprob (if given) is 0 and rank -1 in every row.
+ *  The waits inside are bounded (2 s): a row whose wait runs out is refused
+ *  in the same way, with SPEC_DEVERR_TIMEOUT and SPEC_DEVERR_NONFINITE.
  *  R == 0 is valid and enqueues only the clearing of dev_error.
  *  Limits: V <= 524,280, top_k <= 128 (SPEC_ERR_UNSUPPORTED above).
  */
@@ -427,7 +439,7 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int
  *  listed:
  *    SPEC_TAIL_RENORM: t_j <- t_j / M,  t_T = 0   (M = 0: loss 0, gradient 0)
  *    SPEC_TAIL_BUCKET: t_T = max(0, 1 - M), and 0 where q_T = 0 and 1 - M
-                      <= 2^-16 (the rounding of the l_j)
+ *                      <= 2^-16 (the rounding of the l_j)
  *    loss = sum_j t_j (log t_j - log q_j) + t_T (log t_T - log q_T), terms
  *    with t = 0 being 0, and q_T summed over the tail itself, never as
  *    1 - sum q_j.
@@ -441,8 +453,10 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int
  *  An id outside [0, V) other than -1, or one listed twice
  *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it,
  *  a NaN or +inf teacher value of a listed token (SPEC_DEVERR_NONFINITE):
- *  the row has loss 0 and gradient 0.  A listed token of t_j > 0 whose
- *  student logit is -inf makes the loss +inf; the gradient stays finite.
+ *  the row has loss 0 and gradient 0; so has a row, and those that the same
+ *  CTAs would take after it, whose wait runs out (2 s: SPEC_DEVERR_TIMEOUT
+ *  and SPEC_DEVERR_NONFINITE).  A listed token of t_j > 0 whose student
+ *  logit is -inf makes the loss +inf; the gradient stays finite.
  *  R == 0 is valid.  Limits: 1 <= K <= 128, V <= 524,280.
  */
 spec_status spec_distill_topk(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,

@@ -612,6 +612,15 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     }
 }
 
+// A row by a CTA, or by a cluster whose first CTA finishes it.  Bound by
+// memory, one read of the row, while rows are many: 2048 rows of 128256 bf16
+// without alternatives take 86 us, 0.90 of the measured copy bandwidth; 3072
+// live rows of 129280 with 8 alternatives 141 us, 0.83.  The rest is the rows'
+// ends, where a CTA has nothing on its way: four CTAs an SM (57 registers, 24 KB
+// of tiles each) cover each other's.  Fewer, larger CTAs with a ring of copies
+// and teams of finishing warps took 137 and 230 us, rows split over CTAs that
+// meet in global memory 195 to 252.  Few rows are bound by one row's latency:
+// 5 rows 8.9 us, launch included.
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a) {
     __shared__ LpFinish s;
@@ -743,8 +752,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
 
 // CTAs that share a row, each with a tile for every warp: measured at
 // V = 128256 bf16 with 20 alternatives, one CTA a row against 2, 4 and 8 takes
-// 16.9 / 14.7 / 12.8 / 12.5 us for 5 rows, 18.8 / 16.5 / 16.7 / - for 76, 24.7 /
-// 23.3 / 27.9 / - for 200, and 24.9 / 27.1 / 34.7 / - for 304.
+// 15.0 / 12.8 / 10.3 / 9.6 us for 5 rows, 15.1 / 13.0 / 10.7 / 10.7 for 30,
+// 15.1 / 13.1 / 12.3 / 14.5 for 60, 15.2 / 13.3 / 14.1 / 14.7 for 76, 16.7 / 17.4 /
+// 18.8 / 23.8 for 150 and 21.5 / 25.6 / 32.0 / 38.8 for 304.
 template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;
@@ -755,7 +765,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
         !launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, true>), kMost, kLpThreads, &shape))
         return cudaErrorUnknown;
     const long long R = a.R, sms = shape.sms;
-    const int S_most = 5 * R <= sms ? 8 : 5 * R <= 2 * sms ? 4 : 3 * R <= 4 * sms ? 2 : 1;
+    const int S_most = 5 * R <= sms ? 8 : 5 * R <= 2 * sms ? 4 : 2 * R <= sms ? 2 : 1;
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
     const size_t dyn = lp_ring(S > 1) + (size_t)(groups + 1) * sizeof(uint32_t);

@@ -82,8 +82,6 @@ template <> struct RowVec<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(q.x), h(q.y)), __hmax2_nan(h(q.z), h(q.w)));
         return max_nan(__low2float(m), __high2float(m));
     }
-    // word 0 of a vector whose first element is x, the other -inf
-    __device__ static __forceinline__ uint32_t single(float x) { return 0xff800000u | (__float_as_uint(x) >> 16); }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
 template <> struct RowVec<float> {
@@ -113,7 +111,6 @@ template <> struct RowVec<float> {
         return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
                        max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
-    __device__ static __forceinline__ uint32_t single(float x) { return __float_as_uint(x); }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
