@@ -41,18 +41,18 @@
  *  - Each call makes the device that holds its logits (or hidden states)
  *    current for its own launches and puts the caller's current device
  *    back before it returns.
- *  - The linear calls and the draft-side sampler use dependent launches:
+ *  - The linear calls, the draft-side sampler and the calls around a
+ *    verification (log probabilities, distillation, cache slots) use
+ *    dependent launches:
  *    a launch may be scheduled while the kernel before it on the stream is
  *    ending, and waits for that kernel to complete before it reads or
  *    writes anything.  Stream order is kept; after any other stream
  *    operation (a copy, an event) they are ordinary launches.
- *  - spec_token_logprobs and spec_distill_topk take no workspace.  Where
- *    dev_error is given, a small kernel clears it and their own kernel may
- *    start beside that one; both come after everything enqueued before the
- *    call.  Ids, ranks, slots and error bits do not depend on the batch; the
- *    floats of a row may differ in their last bits with R, because the
- *    number of CTAs that share a row goes by it, and with the row's
- *    alignment.  The same call gives the same bits every time.
+ *  - spec_token_logprobs, spec_distill_topk and spec_advance_blocks take no
+ *    workspace.  The same call gives the same bits every time.  Ids, ranks
+ *    and error bits of a row do not depend on the other rows; its floats
+ *    may differ in their last bits with R, because the number of CTAs that
+ *    share a row goes by it, and with the row's alignment.
  */
 #ifndef SPECVERIFY_H
 #define SPECVERIFY_H

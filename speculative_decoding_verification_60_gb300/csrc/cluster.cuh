@@ -120,11 +120,11 @@ inline bool clusters_at_once(const void* kernel, int S, int block, size_t dyn_sm
     return true;
 }
 
-// A launch of n clusters of S CTAs (S = 1: of n CTAs), after_clear: right
-// after clear_error on this stream, and allowed to start beside it.
+// A launch of n clusters of S CTAs (S = 1: of n CTAs), dependent (as
+// launch_dependent) or ordinary.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_rows(void (*kernel)(KArgs...), long long n, int S, int block, size_t dyn_smem, bool after_clear,
-                               cudaStream_t st, Args... args) {
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), long long n, int S, int block, size_t dyn_smem,
+                                   bool dependent, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n * S));
     cfg.blockDim = dim3((unsigned)block);
@@ -132,7 +132,7 @@ inline cudaError_t launch_rows(void (*kernel)(KArgs...), long long n, int S, int
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int used = 0;
-    if (after_clear) {
+    if (dependent) {
         attr[used].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[used++].val.programmaticStreamSerializationAllowed = 1;
     }

@@ -50,6 +50,7 @@ static_assert(sizeof(DistillStat) == 32, "row_stats is [R, 8] float");
 
 constexpr int kDsWarps = 8;                          // that take tiles
 constexpr int kDsThreads = (kDsWarps + 1) * 32;      // and one for the teacher and the loss
+constexpr int kDsLossPerSm = 4, kDsGradPerSm = 3;     // CTAs an SM holds
 constexpr int kDsTile = 8;                           // vectors a lane takes of a tile: 4 KiB a warp
 constexpr int kDsTileBytes = kDsTile * 512;
 constexpr int kDsMaxCluster = 16;
@@ -525,18 +526,18 @@ __device__ __forceinline__ void distill_after(const DistillArgs& a, int r, const
 // The loss of a row, by a CTA or a cluster of S: each warp has every (8 S)-th
 // tile, one on its way while it works on the one in its registers.  Bound by
 // memory, one read of the row: 2432 rows of 128256 bf16 (four full waves of
-// CTAs) in 99 us, 0.93 of the measured copy bandwidth; 1024 rows in 46 us,
-// 0.84 (two waves, the second two thirds full), and 50 us with 128 listed
+// CTAs) in 98 us, 0.94 of the measured copy bandwidth; 1024 rows in 45 us,
+// 0.85 (two waves, the second two thirds full), and 49 us with 128 listed
 // tokens.
 template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
+__global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(DistillArgs a) {
     extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps] tiles
     __shared__ DsRow sm;
     __shared__ uint64_t full[kDsWarps], sent;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
-    error_cleared();
+    rows_begin();
     if (a.weights && a.weights[r] == 0.0f) {
         if (part == 0 && tid == 0) distill_no_row(a, r);
         return;
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) k_distill_loss(DistillArgs a) {
 // the loops that run once or twice a row unrolled (101 KB of code, 74 KB
 // without) the same row took a tenth longer.
 template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, int n_buf) {
+__global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(DistillArgs a, int n_buf) {
     constexpr int VEC = ElemT<T>::VEC;
     extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps][n_buf] tiles
     __shared__ DsRow rows[2];
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kDsThreads, 3) k_distill_grad(DistillArgs a, i
         if (!waited) cluster_wait();
         waited = true;
     };
-    error_cleared();
+    rows_begin();
     if (CLUSTER) {
         if (tid == 0) {
             mbar_init(&sent[0], 1);
@@ -843,6 +844,7 @@ constexpr int kDbTiles = 4;  // tiles a warp takes
 template <typename T>
 __global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, int stretches) {
     constexpr int VEC = ElemT<T>::VEC;
+    rows_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.x / stretches, stretch = blockIdx.x - r * stretches;
     const int unit = stretch * (kDbThreads / 32) + warp, units = stretches * (kDbThreads / 32);
@@ -919,7 +921,7 @@ static cudaError_t launch_distill_loss(const DistillArgs& a, cudaStream_t st) {
     int S = 1;
     while (S < 8 && (long long)a.R * S < 2 * shape.sms && tiles >= 2 * S * kDsWarps) S *= 2;
     return launch_rows(S > 1 ? k_distill_loss<T, true> : k_distill_loss<T, false>, a.R, S, kDsThreads, dyn,
-                       a.dev_error != nullptr, st, a);
+                       shape.sms, kDsLossPerSm, a.dev_error, st, a);
 }
 
 template <typename T>
@@ -940,27 +942,26 @@ static cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t st) {
     const int each = (tiles + S * kDsWarps - 1) / (S * kDsWarps);  // tiles of a warp
     const int n_buf = each > 0 ? each : 1;
     const size_t dyn = (size_t)kDsWarps * kDsTileBytes * n_buf;
-    int clusters = 0;  // as many as run at once
+    int clusters = 0;  // as many as run at once: they take rows in turn, so where each starts matters little
     if (S > 1) {
         auto* kern = k_distill_grad<T, true>;
         const cudaError_t e =
             S > 8 ? cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
         if (e != cudaSuccess) return e;
         if (!clusters_at_once(reinterpret_cast<const void*>(kern), S, kDsThreads, dyn, &clusters)) return cudaErrorUnknown;
-        return launch_rows(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, a.dev_error != nullptr, st, a,
+        return launch_rows(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, shape.sms, 0, a.dev_error, st, a,
                            n_buf);
     }
     const int per_sm = n_buf <= 2 ? 3 : n_buf <= 3 ? 2 : 1;  // by registers, and by shared memory
     clusters = shape.sms * per_sm < a.R ? shape.sms * per_sm : a.R;
-    return launch_rows(k_distill_grad<T, false>, clusters, 1, kDsThreads, dyn, a.dev_error != nullptr, st, a, n_buf);
+    return launch_rows(k_distill_grad<T, false>, clusters, 1, kDsThreads, dyn, shape.sms, 0, a.dev_error, st, a, n_buf);
 }
 
 template <typename T>
 static cudaError_t launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
     const int tiles = (a.V / ElemT<T>::VEC + kDsTile * 32 - 1) / (kDsTile * 32);
     const int per = (kDbThreads / 32) * kDbTiles, stretches = tiles > per ? (tiles + per - 1) / per : 1;
-    k_distill_backward<T><<<(unsigned)a.R * stretches, kDbThreads, 0, st>>>(a, stretches);
-    return cudaGetLastError();
+    return launch_clusters(k_distill_backward<T>, (long long)a.R * stretches, 1, kDbThreads, 0, true, st, a, stretches);
 }
 
 static spec_status check_distill(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,
@@ -994,8 +995,7 @@ extern "C" spec_status spec_distill_topk(const void* student, spec_dtype dtype, 
     if (!on_device) return SPEC_OK;  // no rows and no error word: nothing to do
     if (!select_device_of(on_device)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!clear_error(dev_error, st)) return SPEC_ERR_CUDA;
-    if (R == 0) return SPEC_OK;
+    if (R == 0) return clear_error(dev_error, st);
     const float c = (float)(kLog2e / (double)temperature);
     DistillArgs a{student, R, V, K, row_stride, teacher_ids, teacher_logprobs, weights,
                   c, (double)c * 0.69314718055994531, tail == SPEC_TAIL_BUCKET,

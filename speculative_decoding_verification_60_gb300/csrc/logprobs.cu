@@ -36,6 +36,7 @@ struct LogprobArgs {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpPerSm = 4;
 constexpr int kLpTile = 6;   // groups of a tile: 3 KiB
 constexpr int kLpTileBytes = kLpTile * 512;
 // Tiles a warp has on their way, beside the one in its registers: a second
@@ -614,15 +615,15 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
 
 // A row by a CTA, or by a cluster whose first CTA finishes it.  Bound by
 // memory, one read of the row, while rows are many: 2048 rows of 128256 bf16
-// without alternatives take 86 us, 0.90 of the measured copy bandwidth; 3072
-// live rows of 129280 with 8 alternatives 141 us, 0.83.  The rest is the rows'
+// without alternatives take 85.5 us, 0.91 of the measured copy bandwidth; 3072
+// live rows of 129280 with 8 alternatives 140 us, 0.84.  The rest is the rows'
 // ends, where a CTA has nothing on its way: four CTAs an SM (57 registers, 24 KB
 // of tiles each) cover each other's.  Fewer, larger CTAs with a ring of copies
 // and teams of finishing warps took 137 and 230 us, rows split over CTAs that
 // meet in global memory 195 to 252.  Few rows are bound by one row's latency:
-// 5 rows 8.9 us, launch included.
+// 5 rows 8.4 us, launch included.
 template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(LogprobArgs a) {
     __shared__ LpFinish s;
     __shared__ LpPart parts[kLpMaxCluster * kLpWarps];
     constexpr int kDepth = lp_depth(CLUSTER);
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
-    error_cleared();
+    rows_begin();
     const int tok = a.tokens ? a.tokens[r] : 0;
     if (tok < 0 || tok >= a.V) {
         if (part == 0) {
@@ -769,8 +770,8 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
     const size_t dyn = lp_ring(S > 1) + (size_t)(groups + 1) * sizeof(uint32_t);
-    return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn,
-                       a.dev_error != nullptr, st, a);
+    return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn, shape.sms,
+                       kLpPerSm, a.dev_error, st, a);
 }
 
 }  // namespace sv
@@ -792,8 +793,7 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     if (!on_device) return SPEC_OK;  // no rows and no error word: nothing to do
     if (!select_device_of(on_device)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!clear_error(dev_error, st)) return SPEC_ERR_CUDA;
-    if (R == 0) return SPEC_OK;
+    if (R == 0) return clear_error(dev_error, st);
     const double inv_t = 1.0 / (double)temperature;
     const float inv_hi = (float)inv_t;
     LogprobArgs a{logits, R, V, top_k, row_stride, tokens, (float)(kLog2e / (double)temperature),

@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include "../../include/specverify.h"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
 
@@ -147,28 +148,42 @@ __device__ __forceinline__ double ln_of(float z) {
     return (double)p.x + (double)p.y;
 }
 
-// The error word of a call.  It is cleared by a kernel of its own that lets
-// the call's kernel start at once (a memset in between costs 2.5 to 3.5 us a
-// call: 5 rows of 128256 bf16 take 8.8 us, not 11.2).  That kernel waits for the
-// clearing where it sets a bit, and once in any case (error_cleared): who
-// waits for it has waited for both.  What the stream did before, the clearing
-// has waited for.
-static __global__ void __launch_bounds__(32) k_clear_error(int32_t* dev_error) {
+// The launches of a call are dependent launches: scheduled while the kernel
+// before is ending, they wait for it (rows_begin) before they read anything.
+// The error word is cleared by a kernel of its own in that chain; a memset
+// there would make the next launch an ordinary one (5 rows of 128256 bf16 by
+// token_logprobs: 8.4 us, with a memset 11.2).
+__device__ __forceinline__ void rows_begin() {
     grid_dep_trigger();
+    grid_dep_wait();
+}
+static __global__ void __launch_bounds__(32) k_clear_error(int32_t* dev_error) {
+    rows_begin();
     if (threadIdx.x == 0) *dev_error = 0;
 }
-inline bool clear_error(int32_t* dev_error, cudaStream_t st) {
-    if (!dev_error) return true;
-    k_clear_error<<<1, 32, 0, st>>>(dev_error);
-    return cudaGetLastError() == cudaSuccess;
+// A call's launch, its error word (may be NULL) cleared before it: n clusters
+// of S CTAs.  A grid of one CTA to one wave of CTAs per SM is placed on an idle
+// GPU (its first launch is an ordinary one): on one that is still ending a
+// kernel, the SMs that are free first get more than their share of CTAs, and
+// nothing follows to even it out (320 rows, 192 of them live: 26.4 us, started
+// early 30.6; fewer or more CTAs are 0.5 us faster started early).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_rows(void (*kernel)(KArgs...), long long n, int S, int block, size_t dyn_smem, int sms,
+                               int per_sm, int32_t* dev_error, cudaStream_t st, Args... args) {
+    const bool early = n * S <= sms || n * S > (long long)per_sm * sms;
+    if (dev_error) {
+        const cudaError_t e = launch_clusters(k_clear_error, 1, 1, 32, 0, early, st, dev_error);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_clusters(kernel, n, S, block, dyn_smem, early || dev_error, st, args...);
 }
-__device__ __forceinline__ void error_cleared() {
-    if (blockIdx.x == 0 && threadIdx.x == blockDim.x - 1) grid_dep_wait();
+// The error word of a call without rows.
+inline spec_status clear_error(int32_t* dev_error, cudaStream_t st) {
+    if (!dev_error) return SPEC_OK;
+    return launch_clusters(k_clear_error, 1, 1, 32, 0, true, st, dev_error) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 __device__ __forceinline__ void set_error(int32_t* dev_error, int bits) {
-    if (!dev_error) return;
-    grid_dep_wait();
-    atomicOr(dev_error, bits);
+    if (dev_error) atomicOr(dev_error, bits);
 }
 
 // Arguments that every call over rows checks the same way.
