@@ -56,7 +56,8 @@ constexpr int kLpCands = 8 * (kMaxTop + kLpSlack) + 16;  // the elements of that
 constexpr int kLpBins = 256;
 constexpr uint32_t kLpNoneKey = 0x007fffffu;  // the order key of -inf
 constexpr int kLpBinShift = 17;  // keys a bin at first: two bf16 values, so four binades in all
-static_assert(kLpCands * 8 <= lp_ring(false), "the candidates take the ring's place");
+constexpr size_t kLpCandBytes = kLpCands * sizeof(uint64_t);
+static_assert(kLpCandBytes % 16 == 0, "the group keys come after the candidates");
 
 // What a warp makes of its groups.
 struct __align__(16) LpPart {
@@ -469,14 +470,44 @@ __device__ __noinline__ void lp_ties(const T* logits, int V, LpFinish* fin, uint
     __syncthreads();
 }
 
+__device__ __forceinline__ void lp_take(LpFinish& s, int g) {
+    const int at = atomicAdd(&s.n_group, 1);
+    if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused before they are read
+}
+// Takes the first n groups whose key is tau; each warp looks at a stretch of
+// the row's groups (777 fp32 rows, half of them masked, 64 alternatives: 48.6
+// us; 52 with every thread counting the groups before its own).  A function of
+// its own as lp_ties is: in line it cost rows that never get here 1 to 2 %.
+__device__ __noinline__ void lp_equal(LpFinish* fin, const uint32_t* group_key, int nb, uint32_t tau, int n) {
+    LpFinish& s = *fin;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int each = (nb + kLpThreads - 1) / kLpThreads * 32;
+    const int from = 1 + warp * each + lane, to = min(nb, warp * each + each);
+    int before = 0;
+#pragma unroll 1
+    for (int g = from; g - lane <= to; g += 32) before += __popc(__ballot_sync(0xffffffffu, g <= to && group_key[g] == tau));
+    if (lane == 0) s.ties[warp] = before;
+    __syncthreads();
+    before = 0;
+#pragma unroll 1
+    for (int w = 0; w < warp; ++w) before += s.ties[w];
+#pragma unroll 1
+    for (int g = from; g - lane <= to && before < n; g += 32) {
+        const uint32_t same = __ballot_sync(0xffffffffu, g <= to && group_key[g] == tau);
+        if (((same >> lane) & 1u) && before + __popc(same & ((1u << lane) - 1u)) < n) lp_take(s, g);
+        before += __popc(same);
+    }
+}
+
 // The row's results, from n_parts <= 64 parts and the order keys of the
 // maxima of its groups (group_key[g], 1 <= g <= nb).  ends: this lane's
-// element of the head and of the tail.  Loops that run once a row are not
+// element of the head and of the tail.  stage: the warp's part of the ring,
+// now free.  Loops that run once a row are not
 // unrolled: their instructions have to be fetched, too.
 template <typename T>
 __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpRow<T>& row, int tok, float xt,
-                                          float2 ends, LpFinish& s, uint64_t* cand, const uint32_t* group_key,
-                                          const LpPart* parts, int n_parts) {
+                                          float2 ends, LpFinish& s, uint64_t* cand, uint4* stage,
+                                          const uint32_t* group_key, const LpPart* parts, int n_parts) {
     using Vec = RowVec<T>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = row.nb, K = a.top_k;
     if (warp == 1) lp_merge<T>(a, r, row, tok, xt, ends, s, parts, n_parts);
@@ -499,6 +530,7 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     const uint32_t top = okey32(warp_max_redux(m));
 
     constexpr int kAhead = 6;  // groups a warp reads at a time: under load a read takes 1 to 2 us
+    static_assert(kAhead <= kLpTile, "staged in the warp's part of the ring");
     int n_group = nb;
     auto for_vectors = [&](auto&& f) {  // f(i, vectors) per lane: vector k of group i + k * kLpWarps
 #pragma unroll 1
@@ -537,22 +569,10 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
             }
         });
         if (!vectors) {
-            const int equal = K - above;  // if above tau lie fewer than K: also the first that reach it
 #pragma unroll 1
-            for (int g = 1 + tid; g <= nb; g += kLpThreads) {
-                const uint32_t k = group_key[g];
-                bool take = k > tau;
-                if (k == tau && equal > 0) {
-                    int before = 0;
-#pragma unroll 1
-                    for (int i = 1; i < g && before < equal; ++i) before += group_key[i] == tau;
-                    take = before < equal;
-                }
-                if (take) {
-                    const int at = atomicAdd(&s.n_group, 1);
-                    if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused below
-                }
-            }
+            for (int g = 1 + tid; g <= nb; g += kLpThreads)
+                if (group_key[g] > tau) lp_take(s, g);
+            if (above < K) lp_equal(&s, group_key, nb, tau, K - above);
         }
         __syncthreads();
         if (!s.valid) {
@@ -571,12 +591,15 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
             uint32_t hits = 0;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (i0 + k * kLpWarps < n_group && !(Vec::max(q[k]) <= bound)) hits |= 1u << k;
+                if (i0 + k * kLpWarps < n_group && !(Vec::max(q[k]) <= bound)) {
+                    hits |= 1u << k;
+                    stage[k * 32 + lane] = q[k];
+                }
 #pragma unroll 1
-            for (; hits; hits &= hits - 1) {  // few: once more, in code that is not repeated per vector
-                const int g = s.group[i0 + (__ffs(hits) - 1) * kLpWarps], idx = row.index(g);
+            for (; hits; hits &= hits - 1) {  // few: in code that is not repeated per vector
+                const int k = __ffs(hits) - 1, g = s.group[i0 + k * kLpWarps], idx = row.index(g);
                 if (!row.has(g)) continue;
-                const uint4 v = row.vector(g);
+                const uint4 v = stage[k * 32 + lane];
 #pragma unroll
                 for (int p = 0; p < Vec::kPairs; ++p) {
                     const float2 x = Vec::pair(v, p);
@@ -629,7 +652,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
     constexpr int kDepth = lp_depth(CLUSTER);
     __shared__ uint64_t full[kLpWarps][kDepth];
     extern __shared__ __align__(128) uint8_t lp_raw[];
-    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + lp_ring(CLUSTER));  // [nb + 1]; group 0 has none
+    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + lp_ring(CLUSTER) + kLpCandBytes);  // [nb + 1]; group 0 has none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
@@ -748,7 +771,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
         if (lane == 0) parts[warp] = p;
         __syncthreads();
     }
-    lp_finish<T>(a, r, row, tok, xt, ends, s, reinterpret_cast<uint64_t*>(lp_raw), group_key, parts, S * kLpWarps);
+    lp_finish<T>(a, r, row, tok, xt, ends, s, reinterpret_cast<uint64_t*>(lp_raw + lp_ring(CLUSTER)), ring, group_key, parts,
+                 S * kLpWarps);
 }
 
 // CTAs that share a row, each with a tile for every warp: measured at
@@ -760,7 +784,7 @@ template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;
     constexpr int kMostGroups = (int)((kRowsMaxVocab / 4 + 31) / 32);
-    constexpr size_t kMost = lp_ring(true) + (kMostGroups + 1) * sizeof(uint32_t);
+    constexpr size_t kMost = lp_ring(true) + kLpCandBytes + (kMostGroups + 1) * sizeof(uint32_t);
     LaunchShape shape;
     if (!launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, false>), kMost, kLpThreads, &shape) ||
         !launch_shape(reinterpret_cast<const void*>(k_token_logprobs<T, true>), kMost, kLpThreads, &shape))
@@ -769,7 +793,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int S_most = 5 * R <= sms ? 8 : 5 * R <= 2 * sms ? 4 : 2 * R <= sms ? 2 : 1;
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
-    const size_t dyn = lp_ring(S > 1) + (size_t)(groups + 1) * sizeof(uint32_t);
+    const size_t dyn = lp_ring(S > 1) + kLpCandBytes + (size_t)(groups + 1) * sizeof(uint32_t);
     return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn, shape.sms,
                        kLpPerSm, a.dev_error, st, a);
 }
