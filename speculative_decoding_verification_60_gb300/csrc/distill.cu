@@ -26,7 +26,6 @@ struct DistillArgs {
     const float* weights;  // forward: row weights; backward: upstream gradients
     float c;       // log2(e) / T
     double inv_t;  // c ln 2: 1 / T for the same rounded c
-
     bool bucket;
     float* loss;
     float* stats;
@@ -251,7 +250,8 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     const float listed = sm.z_listed * ex2(fmaxf((ms - m) * a.c, -1000.0f)), z = listed + in_tail;
     const bool no_tail = zt == 0.0f && te.y <= kTailRounding;
     const float t_tail = no_tail ? 0.0f : te.y;
-    *sums = DsSums{z, zt, listed / z, in_tail / z, t_tail > 0.0f, (int)__reduce_or_sync(0xffffffffu, lane < S ? __float_as_int(sm.bad[lane]) : 0)};
+    const uint32_t bad = __reduce_or_sync(0xffffffffu, lane < S ? __float_as_uint(sm.bad[lane]) : 0u);
+    *sums = DsSums{z, zt, listed / z, in_tail / z, t_tail > 0.0f, (int)bad};
     if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
     if (sums->err || te.w == INFINITY) return st;
     st.m_tail = mt;
@@ -429,8 +429,8 @@ __device__ __forceinline__ float2 distill_ends(const RowView<T>& row, const int*
 // A tile in shared memory, its listed tokens set to -inf there, added to the
 // sum; free() is called once every lane has its vectors.
 template <typename T, typename F>
-__device__ __forceinline__ void distill_tile(const RowView<T>& row, int t, uint4* at, const int* ids, DsSum& sum, float c,
-                                             F&& free) {
+__device__ __forceinline__ void distill_tile(const RowView<T>& row, int t, uint4* at, const int* ids, DsSum& sum,
+                                             float c, F&& free) {
     const int lane = threadIdx.x & 31, v0 = t * kDsTile * 32, nv = min(kDsTile * 32, row.nvec - v0);
     const bool any = listed_in(ids, row.head + v0 * ElemT<T>::VEC, nv * ElemT<T>::VEC,
                                [&](int, int o) { reinterpret_cast<T*>(at)[o] = T(-INFINITY); });
@@ -948,7 +948,8 @@ static cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t st) {
         const cudaError_t e =
             S > 8 ? cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
         if (e != cudaSuccess) return e;
-        if (!clusters_at_once(reinterpret_cast<const void*>(kern), S, kDsThreads, dyn, &clusters)) return cudaErrorUnknown;
+        if (!clusters_at_once(reinterpret_cast<const void*>(kern), S, kDsThreads, dyn, &clusters))
+            return cudaErrorUnknown;
         return launch_rows(kern, clusters < a.R ? clusters : a.R, S, kDsThreads, dyn, shape.sms, 0, a.dev_error, st, a,
                            n_buf);
     }

@@ -485,7 +485,8 @@ __device__ __noinline__ void lp_equal(LpFinish* fin, const uint32_t* group_key, 
     const int from = 1 + warp * each + lane, to = min(nb, warp * each + each);
     int before = 0;
 #pragma unroll 1
-    for (int g = from; g - lane <= to; g += 32) before += __popc(__ballot_sync(0xffffffffu, g <= to && group_key[g] == tau));
+    for (int g = from; g - lane <= to; g += 32)
+        before += __popc(__ballot_sync(0xffffffffu, g <= to && group_key[g] == tau));
     if (lane == 0) s.ties[warp] = before;
     __syncthreads();
     before = 0;
@@ -561,7 +562,8 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
                 for_vectors([&](int i0, const uint4* q) {
 #pragma unroll
                     for (int k = 0; k < kAhead; ++k)
-                        if (i0 + k * kLpWarps < n_group && row.has(s.group[i0 + k * kLpWarps])) f(okey32(Vec::max(q[k])));
+                        if (i0 + k * kLpWarps < n_group && row.has(s.group[i0 + k * kLpWarps]))
+                            f(okey32(Vec::max(q[k])));
                 });
             } else {
 #pragma unroll 1
@@ -652,7 +654,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
     constexpr int kDepth = lp_depth(CLUSTER);
     __shared__ uint64_t full[kLpWarps][kDepth];
     extern __shared__ __align__(128) uint8_t lp_raw[];
-    uint32_t* group_key = reinterpret_cast<uint32_t*>(lp_raw + lp_ring(CLUSTER) + kLpCandBytes);  // [nb + 1]; group 0 has none
+    uint64_t* cand = reinterpret_cast<uint64_t*>(lp_raw + lp_ring(CLUSTER));  // [kLpCands]
+    uint32_t* group_key = reinterpret_cast<uint32_t*>(cand + kLpCands);       // [nb + 1]; group 0 has none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = CLUSTER ? (int)cluster_size() : 1, part = CLUSTER ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / S;
@@ -771,8 +774,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
         if (lane == 0) parts[warp] = p;
         __syncthreads();
     }
-    lp_finish<T>(a, r, row, tok, xt, ends, s, reinterpret_cast<uint64_t*>(lp_raw + lp_ring(CLUSTER)), ring, group_key, parts,
-                 S * kLpWarps);
+    lp_finish<T>(a, r, row, tok, xt, ends, s, cand, ring, group_key, parts, S * kLpWarps);
 }
 
 // CTAs that share a row, each with a tile for every warp: measured at
@@ -794,8 +796,8 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     int S = 1;
     while (S < S_most && groups >= 2 * S * kLpWarps * kLpTile) S *= 2;
     const size_t dyn = lp_ring(S > 1) + kLpCandBytes + (size_t)(groups + 1) * sizeof(uint32_t);
-    return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn, shape.sms,
-                       kLpPerSm, a.dev_error, st, a);
+    return launch_rows(S > 1 ? k_token_logprobs<T, true> : k_token_logprobs<T, false>, a.R, S, kLpThreads, dyn,
+                       shape.sms, kLpPerSm, a.dev_error, st, a);
 }
 
 }  // namespace sv
