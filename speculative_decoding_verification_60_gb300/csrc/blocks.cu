@@ -155,8 +155,10 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
         for (int j = tid & 31; j < q.lacks; j += 32)
             a.table[b * a.table_stride + q.held + j] = a.free_blocks[free_count - 1 - (first[b] + j)];
     }
-    // slots: consecutive tokens of a thread, mostly of one request
-    for (int i0 = (blockIdx.x * NT + tid) * kBlTokens; i0 < a.max_tokens; i0 += gridDim.x * NT * kBlTokens) {
+    // slots: consecutive tokens of a thread, mostly of one request; their
+    // index passes 2^31 - 1 in the last turn of the largest max_tokens
+    const long long step = (long long)gridDim.x * NT * kBlTokens;
+    for (long long i0 = (long long)(blockIdx.x * NT + tid) * kBlTokens; i0 < a.max_tokens; i0 += step) {
         int b = 0;
         if (i0 < tokens) {  // the last request that starts at or before i0
             int hi = a.B - 1;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
         int position[kBlTokens];
 #pragma unroll
         for (int k = 0; k < kBlTokens; ++k) {
-            const int i = i0 + k;
+            const long long i = i0 + k;
             slot[k] = -1;
             position[k] = 0;
             if (i >= tokens) continue;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
                 while (i >= cu[b + 1] && b < a.B - 1) ++b;
                 q = blocks_request(a, b);
             }
-            const int in = i - cu[b];
+            const int in = (int)(i - cu[b]);
             if (q.err == kDevErrLength || in < 0 || in >= q.n) continue;
             position[k] = q.len + in;
             if (first[b] < 0) continue;
