@@ -155,16 +155,17 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
         for (int j = tid & 31; j < q.lacks; j += 32)
             a.table[b * a.table_stride + q.held + j] = a.free_blocks[free_count - 1 - (first[b] + j)];
     }
-    // slots: consecutive tokens of a thread, mostly of one request; their
-    // index passes 2^31 - 1 in the last turn of the largest max_tokens
-    const long long step = (long long)gridDim.x * NT * kBlTokens;
-    for (long long i0 = (long long)(blockIdx.x * NT + tid) * kBlTokens; i0 < a.max_tokens; i0 += step) {
+    // slots: consecutive tokens of a thread, mostly of one request.  Their
+    // index passes 2^31 - 1 in the last turn of the largest max_tokens, by at
+    // most a step (SMs * NT * kBlTokens): unsigned 32 bits hold it.
+    const uint32_t most = (uint32_t)a.max_tokens, live = (uint32_t)max(tokens, 0);
+    for (uint32_t i0 = (blockIdx.x * NT + tid) * kBlTokens; i0 < most; i0 += gridDim.x * NT * kBlTokens) {
         int b = 0;
-        if (i0 < tokens) {  // the last request that starts at or before i0
+        if (i0 < live) {  // the last request that starts at or before i0
             int hi = a.B - 1;
             while (b < hi) {
                 const int mid = (b + hi + 1) >> 1;
-                if (cu[mid] <= i0) b = mid;
+                if ((uint32_t)cu[mid] <= i0) b = mid;
                 else hi = mid - 1;
             }
         }
@@ -173,15 +174,15 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
         int position[kBlTokens];
 #pragma unroll
         for (int k = 0; k < kBlTokens; ++k) {
-            const long long i = i0 + k;
             slot[k] = -1;
             position[k] = 0;
-            if (i >= tokens) continue;
+            if (i0 + k >= live) continue;
+            const int i = (int)(i0 + k);
             if (i >= cu[b + 1]) {
                 while (i >= cu[b + 1] && b < a.B - 1) ++b;
                 q = blocks_request(a, b);
             }
-            const int in = (int)(i - cu[b]);
+            const int in = i - cu[b];
             if (q.err == kDevErrLength || in < 0 || in >= q.n) continue;
             position[k] = q.len + in;
             if (first[b] < 0) continue;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
                                          : a.free_blocks[free_count - 1 - (first[b] + j - q.held)];
             slot[k] = (int64_t)block * a.page + (position[k] - j * a.page);
         }
-        if (a.aligned && i0 + kBlTokens <= a.max_tokens) {
+        if (a.aligned && i0 + kBlTokens <= most) {
             longlong2* s = reinterpret_cast<longlong2*>(a.slots + i0);
             s[0] = make_longlong2(slot[0], slot[1]);
             s[1] = make_longlong2(slot[2], slot[3]);
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
         } else {
 #pragma unroll
             for (int k = 0; k < kBlTokens; ++k)
-                if (i0 + k < a.max_tokens) {
+                if (i0 + k < most) {
                     a.slots[i0 + k] = slot[k];
                     if (a.positions) a.positions[i0 + k] = position[k];
                 }
