@@ -419,7 +419,8 @@ spec_status spec_sample_rows(const void* logits, spec_dtype dtype, int R, int V,
  *  The waits inside are bounded (2 s): a row whose wait runs out is refused
  *  in the same way, with SPEC_DEVERR_TIMEOUT and SPEC_DEVERR_NONFINITE.
  *  R == 0 is valid and enqueues only the clearing of dev_error.
- *  Limits: V <= 524,280, top_k <= 128 (SPEC_ERR_UNSUPPORTED above).
+ *  Limits: V <= 524,280, top_k <= 128, T >= 2^-126 (SPEC_ERR_UNSUPPORTED
+ *  otherwise).
  */
 spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int V, int64_t row_stride,
                                 const int32_t* tokens, float temperature, int top_k, float* logprob, int32_t* rank,
@@ -459,7 +460,7 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int
  *  CTAs would take after it, whose wait runs out (2 s: SPEC_DEVERR_TIMEOUT
  *  and SPEC_DEVERR_NONFINITE).  A listed token of t_j > 0 whose student
  *  logit is -inf makes the loss +inf; the gradient stays finite.
- *  R == 0 is valid.  Limits: 1 <= K <= 128, V <= 524,280.
+ *  R == 0 is valid.  Limits: 1 <= K <= 128, V <= 524,280, T >= 2^-126.
  */
 spec_status spec_distill_topk(const void* student, spec_dtype dtype, int R, int V, int64_t row_stride,
                               const int32_t* teacher_ids, const float* teacher_logprobs, int K, const float* weights,

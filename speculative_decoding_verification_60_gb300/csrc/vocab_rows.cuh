@@ -14,6 +14,8 @@ namespace sv {
 
 constexpr long long kRowsMaxVocab = 524280;  // as the verification calls
 constexpr int kMaxTop = 128;                 // alternatives or teacher entries of a row
+// Below it log2(e) / T leaves the range of 32 bits, and 0 times it is no number.
+constexpr float kMinTemperature = 1.17549435e-38f;  // 2^-126
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLn2 = 0.69314718055994531f;
 // The reference of a running maximum before any finite entry: -inf minus it
@@ -191,7 +193,7 @@ inline spec_status check_rows(spec_dtype dtype, int R, int V, int64_t row_stride
     if (dtype != SPEC_BF16 && dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
     if (R < 0 || V < 1 || row_stride < V) return SPEC_ERR_INVALID_ARG;
     if (!(temperature > 0.0f) || !(temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
-    if ((int64_t)V > kRowsMaxVocab) return SPEC_ERR_UNSUPPORTED;
+    if ((int64_t)V > kRowsMaxVocab || temperature < kMinTemperature) return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
 
