@@ -7,9 +7,16 @@
 // time: 32 vectors side by side are a group (256 bf16 or 128 fp32 elements),
 // and the unaligned head and tail of a row are the first and the last group.
 // Per group a warp takes the maximum (one reduction instruction) and, against
-// its own running maximum m, z = sum 2^t and e = sum t 2^t of t = (x - m) c,
-// c = log2(e) / T.  From the merged sums
+// a reference r near its own running maximum m, z = sum 2^t and e = sum t 2^t
+// of t = x c - r, c = log2(e) / T.  From the merged sums, now against m,
 //     log p(v) = (x_v - m) / T - ln z,    entropy = ln z - ln 2 * e / z.
+// Exactness: r is a whole number, so a new one scales the sums by a power of
+// two; a maximum that may hold most of the row is counted, not summed, so that
+// ln z = ln(1 + rest) keeps every digit of the rest; and what c is off by,
+// rounded to 32 bits, is put right in ln z: d ln z / d ln c is ln 2 * e / z.
+// (Largest errors over 200 rows of 128256: log p 1.3e-7 to 6e-7, and 2e-7 to
+// 4e-7 of the value where it is near 0; that costs 1.5 % of the time of many
+// rows and 0.6 us of few.)
 // The group maxima are what makes the alternatives cheap: groups are
 // contiguous, so in the order (logit descending, index ascending) every
 // element of a group comes after that group's first maximum, and the K best
@@ -24,7 +31,9 @@ struct LogprobArgs {
     int R, V, top_k;
     int64_t stride;
     const int32_t* tokens;
-    float c;
+    float c;       // log2(e) / T
+    float c_off;   // (log2(e) / T / c - 1) ln 2
+    float beside;  // T ln 8: how far below another of an eighth of its weight is
     float2 inv_t;  // 1 / T in two parts
     float* logprob;
     int32_t* rank;
@@ -46,7 +55,7 @@ constexpr int lp_depth(bool cluster) { return cluster ? 2 : 1; }
 constexpr size_t lp_ring(bool cluster) { return (size_t)kLpWarps * lp_depth(cluster) * kLpTileBytes; }
 constexpr int kLpMaxCluster = 8;
 constexpr uint64_t kLpLimitNs = 2000000000ull;
-constexpr float kLpPlain = 1024.0f;  // |m c| below this: see LpSums
+constexpr float kLpPlain = 4096.0f;  // |m c| below this: see LpSums
 constexpr float kLpLeastC = 1e-30f;  // so that m - kLpFar / c stays in range
 constexpr float kLpFar = 200.0f;     // 2^-200 is zero
 // The K-th best group need not be found exactly: any bound that leaves K to
@@ -59,12 +68,12 @@ constexpr int kLpBinShift = 17;  // keys a bin at first: two bf16 values, so fou
 constexpr size_t kLpCandBytes = kLpCands * sizeof(uint64_t);
 static_assert(kLpCandBytes % 16 == 0, "the group keys come after the candidates");
 
-// What a warp makes of its groups.
+// What a warp makes of its groups (see LpSums).
 struct __align__(16) LpPart {
-    float m, z, e;
-    int before;
+    float m, ref, z, e;
+    int n, before, pad[2];
 };
-static_assert(sizeof(LpPart) == 16 && alignof(LpPart) == 16, "sent to the leader as one 16-byte store");
+static_assert(sizeof(LpPart) == 32 && alignof(LpPart) == 16, "sent to the leader as two 16-byte stores");
 
 // The groups of a row: 0 is its head, 1 .. nb the vectors, nb + 1 its tail.
 template <typename T>
@@ -113,48 +122,57 @@ __device__ __forceinline__ void lp_no_result(const LogprobArgs& a, int r, float 
     }
 }
 
-// Running sums of a lane against the warp's reference m.  Where m c is of
-// ordinary size (a masked row's lowest values, a huge or tiny temperature
-// are not) t = x c - mc is one fused operation, mc = m c rounded: every term
-// has the same reference, and what mc is off by is taken out at the end.
+// 2^d for a whole number d <= 0.
+__device__ __forceinline__ float lp_pow2(float d) { return __int_as_float(((int)fmaxf(d, -127.0f) + 127) << 23); }
+
+// Running sums of a lane; m is the warp's largest value so far.  Where m c is
+// of ordinary size (a masked row's lowest values, a huge or tiny temperature
+// are not) t = x c - ref is one operation, ref = m c rounded up to a whole
+// number; otherwise t = (x - m) c.
 struct LpSums {
-    float m = kNoMax, mc = 0.0f;
-    bool plain = false;  // t = x c - mc; otherwise t = (x - m) c
+    static constexpr float kNone = INFINITY;  // ref where t = (x - m) c
+    float m = -INFINITY, ref = kNone;
+    bool counted = false;  // n of this lane's elements, equal to m, are not in the sums
+    int n = 0;
     float2 z = make_float2(0.0f, 0.0f), e = make_float2(0.0f, 0.0f);
-    __device__ __forceinline__ void shift(float d) {  // every t moves by d
-        d = fmaxf(d, -1000.0f);  // any distance whose weight is zero
-        const float f = ex2(d);
-        e = make_float2((e.x + z.x * d) * f, (e.y + z.y * d) * f);
-        z = make_float2(z.x * f, z.y * f);
+    __device__ __forceinline__ bool plain() const { return ref != kNone; }
+    __device__ static __forceinline__ float ref_of(float m, float c) {
+        const float mc = m * c;
+        return fabsf(mc) < kLpPlain && c > kLpLeastC ? ceilf(mc) : kNone;
     }
-    __device__ __forceinline__ void raise(float m2, float c) {  // to a higher reference
-        exact(c);
-        shift((m - m2) * c);
+    // How far the reference lies above m's own place.
+    __device__ static __forceinline__ float above(float m, float ref, float c) {
+        return ref != kNone ? fmaf(-m, c, ref) : 0.0f;
+    }
+    // By how much places fall when (m, ref) gives way to (m2, ref2); *f: 2^ that.
+    __device__ static __forceinline__ float change(float m, float ref, float m2, float ref2, float c, float* f) {
+        if (ref != kNone && ref2 != kNone) {
+            *f = lp_pow2(ref - ref2);
+            return ref - ref2;
+        }
+        const float d = fmaxf((m - m2) * c + above(m, ref, c) - above(m2, ref2, c), -1000.0f);
+        *f = ex2(d);  // 0 for any distance whose weight is
+        return d;
+    }
+    __device__ __forceinline__ void raise(float m2, float c) {  // to a larger value
+        const float ref2 = ref_of(m2, c);
+        if (m > -INFINITY) {
+            if (counted) {  // joins the sums
+                const float t = -above(m, ref, c), w = (float)n * ex2(t);
+                z.x += w;
+                e.x = fmaf(w, t, e.x);
+            }
+            if (ref2 != ref || ref2 == kNone) {
+                float f;
+                const float d = change(m, ref, m2, ref2, c, &f);
+                e = make_float2((e.x + z.x * d) * f, (e.y + z.y * d) * f);
+                z = make_float2(z.x * f, z.y * f);
+            }
+        }
+        counted = false;
+        n = 0;
         m = m2;
-        settle(c);
-    }
-    __device__ __forceinline__ void settle(float c) {
-        mc = m * c;
-        plain = fabsf(mc) < kLpPlain && c > kLpLeastC;
-        if (plain) shift(fmaf(m, c, -mc));
-    }
-    __device__ __forceinline__ void exact(float c) {  // back to the reference m itself
-        if (plain) shift(fmaf(-m, c, mc));
-        plain = false;
-    }
-    __device__ __forceinline__ void add(float2 t, float2 t_e) {
-        const float2 w = make_float2(ex2(t.x), ex2(t.y));
-        z = __fadd2_rn(z, w);
-        e = __ffma2_rn(w, t_e, e);
-    }
-    // values at least kLpFar / c below m add nothing, and -inf has no product with 0
-    __device__ __forceinline__ void add_plain(float2 x, float2 cc, float2 nmc) {
-        const float2 t = __ffma2_rn(x, cc, nmc);
-        add(t, t);
-    }
-    __device__ __forceinline__ void add_any(float2 x, float2 cc) {
-        const float2 t = __fmul2_rn(__fadd2_rn(x, make_float2(-m, -m)), cc);
-        add(t, make_float2(fmaxf(t.x, -1000.0f), fmaxf(t.y, -1000.0f)));  // a NaN still shows in z
+        ref = ref2;
     }
 };
 
@@ -208,30 +226,72 @@ struct LpTile {
         }
         return Vec::count_sum(n);
     }
+    // The tile's maximum is the warp's new one.  Where neither the old one nor
+    // another group of the tile has an eighth of its weight, it may hold
+    // most of the row, and is taken out (where one has, ln z is at least 0.1,
+    // and the maximum may as well be summed).  Rare in rows without such a
+    // token: taking out whatever has nothing of half its weight beside it
+    // cost 4096 rows 1.5 us.
+    __device__ __forceinline__ void raise(LpSums& sum, float c, float beside, uint4* spare) {
+        const float near = most - beside;
+        const bool far = sum.m < near;
+        sum.raise(most, c);
+        if (!far) return;
+        const uint32_t groups = __ballot_sync(0xffffffffu, mine >= near && mine > -INFINITY);
+        if (groups & (groups - 1)) return;
+        sum.counted = true;
+        // by way of shared memory: the code for one group, not for each
+#pragma unroll
+        for (int j = 0; j < kLpTile; ++j)
+            if (groups == 1u << j) *spare = q[j];
+        sum.n = Vec::take_out(*spare, most);
+#pragma unroll
+        for (int j = 0; j < kLpTile; ++j)
+            if (groups == 1u << j) q[j] = *spare;
+    }
+    // z is summed by vectors, tiles and then the row: 24 to 85 adds one after
+    // another would be off by as many roundings where all weights are alike.
     __device__ __forceinline__ void add(LpSums& sum, float c, float far) const {
-        const float2 cc = make_float2(c, c), nmc = make_float2(-sum.mc, -sum.mc);
-        const typename Vec::Least least = Vec::least(sum.m - far);
-        if (sum.plain) {
+        const float2 cc = make_float2(c, c);
+        float2 z;
+        if (sum.plain()) {
+            // values at least kLpFar / c below m add nothing, and -inf has no product with 0
+            const float2 nr = make_float2(-sum.ref, -sum.ref);
+            const typename Vec::Least least = Vec::least(sum.m - far);
 #pragma unroll
             for (int j = 0; j < kLpTile; ++j) {
+                float2 w[Vec::kPairs];
 #pragma unroll
-                for (int i = 0; i < Vec::kPairs; ++i) sum.add_plain(Vec::pair_above(q[j], i, least), cc, nmc);
+                for (int i = 0; i < Vec::kPairs; ++i) {
+                    const float2 t = __ffma2_rn(Vec::pair_above(q[j], i, least), cc, nr);
+                    w[i] = make_float2(ex2(t.x), ex2(t.y));
+                    sum.e = __ffma2_rn(w[i], t, sum.e);
+                }
+                z = j == 0 ? Vec::sum(w) : __fadd2_rn(z, Vec::sum(w));
             }
         } else {
+            const float2 nm = make_float2(-sum.m, -sum.m);
 #pragma unroll
             for (int j = 0; j < kLpTile; ++j) {
+                float2 w[Vec::kPairs];
 #pragma unroll
-                for (int i = 0; i < Vec::kPairs; ++i) sum.add_any(Vec::pair(q[j], i), cc);
+                for (int i = 0; i < Vec::kPairs; ++i) {
+                    const float2 t = __fmul2_rn(__fadd2_rn(Vec::pair(q[j], i), nm), cc);
+                    w[i] = make_float2(ex2(t.x), ex2(t.y));  // a NaN still shows in z
+                    sum.e = __ffma2_rn(w[i], make_float2(fmaxf(t.x, -1000.0f), fmaxf(t.y, -1000.0f)), sum.e);
+                }
+                z = j == 0 ? Vec::sum(w) : __fadd2_rn(z, Vec::sum(w));
             }
         }
+        sum.z = __fadd2_rn(sum.z, z);
     }
 };
 
 // A warp's part of a row.
-__device__ __forceinline__ LpPart lp_part(LpSums& sum, int before, float c) {
-    sum.exact(c);
+__device__ __forceinline__ LpPart lp_part(const LpSums& sum, int before) {
     LpPart p;
     p.m = sum.m;
+    p.ref = sum.ref;
     p.z = sum.z.x + sum.z.y;
     p.e = sum.e.x + sum.e.y;
 #pragma unroll
@@ -239,6 +299,7 @@ __device__ __forceinline__ LpPart lp_part(LpSums& sum, int before, float c) {
         p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
         p.e += __shfl_xor_sync(0xffffffffu, p.e, o);
     }
+    p.n = __reduce_add_sync(0xffffffffu, sum.n);
     p.before = __reduce_add_sync(0xffffffffu, before);
     return p;
 }
@@ -346,23 +407,33 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
     float m = fmaxf(ends.x, ends.y);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        p[k] = lane + 32 * k < n_parts ? parts[lane + 32 * k] : LpPart{kNoMax, 0.0f, 0.0f, 0};
+        p[k] = lane + 32 * k < n_parts ? parts[lane + 32 * k] : LpPart{-INFINITY, LpSums::kNone, 0.0f, 0.0f, 0, 0};
         m = fmaxf(m, p[k].m);
     }
     m = warp_max_redux(m);
+    const float ref = LpSums::ref_of(m, a.c), g = LpSums::above(m, ref, a.c);
     float z = 0.0f, e = 0.0f;
-    int before = 0;
+    int n = 0, before = 0;  // n: elements equal to m that are not in the sums
+    auto add = [&](float x, int count) {
+        if (x == m) {
+            n += count;
+            return;
+        }
+        const float t = ref != LpSums::kNone ? fmaf(x, a.c, -ref) : (x - m) * a.c, w = (float)count * ex2(t);
+        z += w;
+        e = fmaf(w, fmaxf(t, -1000.0f), e);
+    };
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const float d = fmaxf((p[k].m - m) * a.c, -1000.0f), f = ex2(d);
+        float f;
+        const float d = LpSums::change(p[k].m, p[k].ref, m, ref, a.c, &f);
         z += p[k].z * f;
         e += (p[k].e + p[k].z * d) * f;
         before += p[k].before;
+        add(p[k].m, p[k].n);
     }
     auto end = [&](float x, int idx) {
-        const float t = (x - m) * a.c, w = ex2(t);
-        z += w;
-        e = fmaf(w, fmaxf(t, -1000.0f), e);
+        add(x, 1);
         before += x > xt || (x == xt && idx < tok);
     };
     if (lane < row.head) end(ends.x, lane);
@@ -372,20 +443,36 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
         z += __shfl_xor_sync(0xffffffffu, z, o);
         e += __shfl_xor_sync(0xffffffffu, e, o);
     }
+    n = __reduce_add_sync(0xffffffffu, n);
     before = __reduce_add_sync(0xffffffffu, before);
     // nothing is below -inf: every place of the groups before the token's
     // was counted, the empty ones of the last group too
     if (xt == -INFINITY && tok >= row.head + row.nvec * VEC) before -= (row.nb * 32 - row.nvec) * VEC;
-    const bool valid = z > 0.0f && z < INFINITY;  // no NaN, no +inf, something finite
+    // no NaN, no +inf, something finite
+    const bool valid = m > -INFINITY && m < INFINITY && z >= 0.0f && z < INFINITY;
     if (lane == 0) {
-        const float2 ln_z = ln_parts(z);
+        // The maximum holds most of the row: z is 1 + rest against m itself.
+        // Otherwise z is taken against its reference, g above m.
+        const float up = ex2(g), w = (float)n * ex2(-g);
+        const bool most = n == 1 && z * up < 1.0f;
+        const float rest = most ? z * up : w + z, all = most ? 1.0f + rest : rest;
+        const float at = (most ? fmaf(g, z, e) * up : fmaf(w, -g, e)) / all;
+        const float mean = most ? at : at + g;  // of (x - m) c
+        int exp2 = 0;
+        const float f = most ? rest : fmaf(2.0f, frexpf(rest, &exp2), -1.0f);  // in [0, 1): ln z = ln(1 + f) + ...
+        const float whole = most ? 0.0f : (float)(exp2 - 1);
+        float2 ln_z = make_float2(whole * kLn2Hi, fmaf(whole, kLn2Lo, log1pf(f)));
+        ln_z = add_parts(make_float2(ln_z.x, 0.0f), ln_z.y);
+        const float entropy = fmaf(-kLn2, at, ln_z.x) + ln_z.y;
+        if (!most) ln_z = add_parts(ln_z, g * kLn2);
+        ln_z = add_parts(ln_z, a.c_off * mean);
         s.m = m;
         s.ln_z = ln_z;
         s.valid = valid;
         if (valid) {
             if (a.logprob) a.logprob[r] = a.tokens ? lp_log(a, xt - m, ln_z) : 0.0f;
             if (a.rank) a.rank[r] = a.tokens ? before + 1 : -1;
-            if (a.entropy) a.entropy[r] = fmaf(-kLn2, e / z, ln_z.x) + ln_z.y;
+            if (a.entropy) a.entropy[r] = entropy;
         } else {
             set_error(a.dev_error, kDevErrNonfinite);
         }
@@ -528,7 +615,7 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
         lp_no_result(a, r, a.tokens ? -INFINITY : 0.0f, tid, kLpThreads);
         return;
     }
-    const uint32_t top = okey32(warp_max_redux(m));
+    const uint32_t top = okey32(fmaxf(warp_max_redux(m), kNoMax));
 
     constexpr int kAhead = 6;  // groups a warp reads at a time: under load a read takes 1 to 2 us
     static_assert(kAhead <= kLpTile, "staged in the warp's part of the ring");
@@ -709,6 +796,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
     }
     LpSums sum;
     LpTile<T> tile;
+    uint4* spare = reinterpret_cast<uint4*>(cand) + tid;  // this lane's; the candidates come after the last tile
+    static_assert(kLpThreads * sizeof(uint4) <= kLpCandBytes, "a vector each");
     uint32_t parity = 0;
     bool awaited = false, ok = true, refused = false;
     for (; g0 < row.nb; g0 += step) {
@@ -730,7 +819,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
             parity ^= 1;
         }
         tile.maxima();
-        if (tile.most > sum.m) sum.raise(tile.most, a.c);
         refused = refused || !(tile.most < INFINITY);  // a NaN or +inf
         if (CLUSTER && !awaited) {
             cluster_wait();
@@ -744,9 +832,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
                 group_key[g0 + lane + 1] = k;
         }
         before += tile.before(tk, g0 + 1);
+        if (tile.most > sum.m) tile.raise(sum, a.c, a.beside, spare);
         if (tile.most > -INFINITY) tile.add(sum, a.c, far);  // not all of it ruled out
     }
-    LpPart p = lp_part(sum, before, a.c);
+    LpPart p = lp_part(sum, before);
     if (refused) p.z = NAN;
     if (!ok) {  // the row is refused; the copies still on their way land before the CTA ends
         p.z = NAN;
@@ -764,9 +853,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
     }
     if (CLUSTER) {
         if (!awaited) cluster_wait();
-        if (lane == 0)
-            cluster_store(cluster_map(&parts[part * kLpWarps + warp], 0),
-                          make_float4(p.m, p.z, p.e, __int_as_float(p.before)));
+        if (lane == 0) {
+            LpPart* to = &parts[part * kLpWarps + warp];
+            cluster_store(cluster_map(to, 0), make_float4(p.m, p.ref, p.z, p.e));
+            cluster_store(cluster_map(&to->n, 0),
+                          make_float4(__int_as_float(p.n), __int_as_float(p.before), 0.0f, 0.0f));
+        }
         cluster_arrive();
         cluster_wait();
         if (part != 0) return;
@@ -821,8 +913,10 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (R == 0) return clear_error(dev_error, st);
     const double inv_t = 1.0 / (double)temperature;
-    const float inv_hi = (float)inv_t;
-    LogprobArgs a{logits, R, V, top_k, row_stride, tokens, (float)(kLog2e / (double)temperature),
+    const float inv_hi = (float)inv_t, c = (float)(kLog2e / (double)temperature);
+    LogprobArgs a{logits, R, V, top_k, row_stride, tokens, c,
+                  (float)((kLog2e / (double)temperature / (double)c - 1.0) * 0.69314718055994531),
+                  (float)((double)temperature * 2.0794415416798359),
                   make_float2(inv_hi, (float)(inv_t - (double)inv_hi)), logprob, rank, entropy, top_ids, top_logprobs,
                   dev_error};
     return (dtype == SPEC_BF16 ? launch_logprobs<__nv_bfloat16>(a, st) : launch_logprobs<float>(a, st)) == cudaSuccess

@@ -18,6 +18,7 @@ constexpr int kMaxTop = 128;                 // alternatives or teacher entries 
 constexpr float kMinTemperature = 1.17549435e-38f;  // 2^-126
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLn2Hi = 0.693145751953125f, kLn2Lo = 1.4286068203e-6f;  // ln 2: its first 16 bits, and the rest
 // The reference of a running maximum before any finite entry: -inf minus it
 // is -inf (weight zero), where -inf minus -inf would be NaN.
 constexpr float kNoMax = -3.4028234663852886e38f;
@@ -85,6 +86,24 @@ template <> struct RowVec<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(q.x), h(q.y)), __hmax2_nan(h(q.z), h(q.w)));
         return max_nan(__low2float(m), __high2float(m));
     }
+    __device__ static __forceinline__ float2 sum(const float2* w) {
+        return __fadd2_rn(__fadd2_rn(w[0], w[1]), __fadd2_rn(w[2], w[3]));
+    }
+    // Elements equal to x become -inf; how many there were.
+    __device__ static __forceinline__ int take_out(uint4& q, float x) {
+        const __nv_bfloat162 xx = __float2bfloat162_rn(x);
+        int n = 0;
+        auto one = [&](uint32_t& w) {
+            const uint32_t same = __heq2_mask(*reinterpret_cast<__nv_bfloat162*>(&w), xx);
+            n += __popc(same) >> 4;
+            w = (w & ~same) | (0xff80ff80u & same);
+        };
+        one(q.x);
+        one(q.y);
+        one(q.z);
+        one(q.w);
+        return n;
+    }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
 template <> struct RowVec<float> {
@@ -114,6 +133,20 @@ template <> struct RowVec<float> {
         return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
                        max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
+    __device__ static __forceinline__ float2 sum(const float2* w) { return __fadd2_rn(w[0], w[1]); }
+    __device__ static __forceinline__ int take_out(uint4& q, float x) {
+        int n = 0;
+        auto one = [&](uint32_t& w) {
+            const bool same = __uint_as_float(w) == x;
+            n += same;
+            if (same) w = 0xff800000u;
+        };
+        one(q.x);
+        one(q.y);
+        one(q.z);
+        one(q.w);
+        return n;
+    }
     __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
@@ -140,10 +173,15 @@ __device__ __forceinline__ float key_value(uint64_t k) { return okey32_to_float(
 __device__ __forceinline__ float2 ln_parts(float z) {
     int e;
     const float f = frexpf(z, &e);
-    const float hi = (float)e * 0.693145751953125f, lo = fmaf((float)e, 1.4286068203e-6f, logf(f));
+    const float hi = (float)e * kLn2Hi, lo = fmaf((float)e, kLn2Lo, logf(f));
     const float x = hi + lo;
     const float b = x - hi;  // hi and lo of any size: a two-sum
     return make_float2(x, (hi - (x - b)) + (lo - b));
+}
+// a + v, in two parts as a is.
+__device__ __forceinline__ float2 add_parts(float2 a, float v) {
+    const float s = a.x + v, b = s - a.x;
+    return make_float2(s, ((a.x - (s - b)) + (v - b)) + a.y);
 }
 __device__ __forceinline__ double ln_of(float z) {
     const float2 p = ln_parts(z);
