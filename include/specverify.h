@@ -108,8 +108,9 @@ typedef enum {
 #define SPEC_DEVERR_LENGTH 8     /* compaction: accepted length or source row out of range */
 #define SPEC_DEVERR_TIMEOUT 16   /* a wait for a bulk copy ran out (2 s).  Verification, sampling:
                                     the rows it left were recomputed by the two-pass route, so
-                                    the results stand.  spec_token_logprobs, spec_distill_topk:
-                                    the rows are refused (SPEC_DEVERR_NONFINITE is set, too) */
+                                    the results stand.  spec_token_logprobs: the rows are
+                                    refused (SPEC_DEVERR_NONFINITE is set, too).
+                                    spec_distill_topk: the call's results are not to be used */
 #define SPEC_DEVERR_CAPACITY 32  /* cache blocks: the free list or a request's table row ran out */
 
 typedef struct {
@@ -458,9 +459,11 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int
  *  An id outside [0, V) other than -1, or one listed twice
  *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it,
  *  a NaN or +inf teacher value of a listed token (SPEC_DEVERR_NONFINITE):
- *  the row has loss 0 and gradient 0; so has a row, and those that the same
- *  CTAs would take after it, whose wait runs out (2 s: SPEC_DEVERR_TIMEOUT
- *  and SPEC_DEVERR_NONFINITE).  A listed token of t_j > 0 whose student
+ *  the row has loss 0 and gradient 0.  The waits inside are bounded (2 s):
+ *  after one that ran out (SPEC_DEVERR_TIMEOUT and SPEC_DEVERR_NONFINITE)
+ *  the row that it was for, and those that the same CTAs would take after
+ *  it, may be refused in part only: the losses and gradients of such a call
+ *  are not to be used.  A listed token of t_j > 0 whose student
  *  logit is -inf makes the loss +inf; the gradient stays finite.
  *  R == 0 is valid.  Limits: 1 <= K <= 128, V <= 524,280, T >= 2^-126.
  */

@@ -55,7 +55,6 @@ constexpr int kDsTileBytes = kDsTile * 512;
 constexpr int kDsMaxCluster = 16;
 constexpr int kDsMaxTiles = 6;                       // of a warp, when the row stays on the chip
 constexpr int kDsIds = kMaxTop / 32;                 // listed tokens a lane looks after
-constexpr uint64_t kDsLimitNs = 2000000000ull;
 constexpr float kDsPlain = 1024.0f;                  // |m c| below this: t = x c - m c in one operation
 // Where the student gives the tail nothing, this much teacher mass outside
 // the listed tokens is the rounding of their log probabilities: the loss
@@ -561,7 +560,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(Disti
         in.gather(a, row.row);
         distill_before<CLUSTER>(a, in, sm, &sent, part, S, ready);
         if (!CLUSTER) __syncthreads();
-        if (!CLUSTER || cluster_mbar_wait(&sent, 0, kDsLimitNs)) {
+        if (!CLUSTER || warp_cluster_wait(&sent, 0, kClusterWaitNs)) {
             distill_after(a, r, sm, part, S);
         } else if (part == S - 1 && lane == 0) {
             set_error(a.dev_error, kDevErrTimeout | kDevErrNonfinite);
@@ -588,7 +587,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(Disti
     bool ok = true;
     uint32_t parity = 0;
     for (int t = unit; t < tiles && ok; t += units, parity ^= 1) {
-        ok = mbar_wait(&full[warp], parity, kDsLimitNs);
+        ok = warp_mbar_wait(&full[warp], parity, kCopyWaitNs);
         if (!ok) break;
         distill_tile(row, t, buf.at(0), ids, sum, a.c, [&] {
             __syncwarp();
@@ -597,7 +596,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(Disti
     }
     if (!ok && lane == 0) {  // the row is refused; the copy still on its way lands before the CTA ends
         set_error(a.dev_error, kDevErrTimeout);
-        mbar_wait(&full[warp], parity, kDsLimitNs);
+        mbar_wait(&full[warp], parity, kDrainNs);
     }
     __syncwarp();
     sum.exact(a.c);
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
             return true;
         }
         const uint32_t n = turn++;
-        return cluster_mbar_wait(&sent[n & 1], (n >> 1) & 1, kDsLimitNs);
+        return warp_cluster_wait(&sent[n & 1], (n >> 1) & 1, kClusterWaitNs);
     };
     bool waited = !CLUSTER;
     auto ready = [&] {  // every CTA of the cluster has started
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
             if (!arrived()) {  // this row and those left are refused
                 if (lane == 0) set_error(a.dev_error, kDevErrTimeout | kDevErrNonfinite);
                 for (; r < a.R; r += step)
-                    if (part == 0 && lane == 0) distill_no_row(a, r);
+                    if (part == S - 1 && lane == 0) distill_no_row(a, r);  // by who has the loss
                 break;
             }
             distill_after(a, r, rows[p], part, S);
@@ -753,7 +752,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
 #pragma unroll 1
         for (int b = 0; b < n_buf && ok; ++b) {
             if (!((pending >> b) & 1u)) continue;
-            ok = mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
+            ok = warp_mbar_wait(&full[warp][b], (phase >> b) & 1u, kCopyWaitNs);
             if (!ok) {
                 if (lane == 0) set_error(a.dev_error, kDevErrTimeout);
                 break;
@@ -770,7 +769,8 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
         } else if (lane == 0) {
             sm.part[unit] = mine;
         }
-        if (!arrived()) {  // as the extra warp finds, too
+        if (!arrived()) {  // this warp's part of this row and those left is refused
+            if (lane == 0) set_error(a.dev_error, kDevErrTimeout | kDevErrNonfinite);
             ok = false;
 #pragma unroll 1
             for (int k = r; k < a.R; k += step) distill_zero(row_of(k), grad_of(k), unit, units);
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
     if (!ok && lane == 0)  // the copies still on their way land before the CTA ends
 #pragma unroll 1
         for (int b = 0; b < n_buf; ++b)
-            if ((pending >> b) & 1u) mbar_wait(&full[warp][b], (phase >> b) & 1u, kDsLimitNs);
+            if ((pending >> b) & 1u) mbar_wait(&full[warp][b], (phase >> b) & 1u, kDrainNs);
     __syncwarp();
     leave();
 }

@@ -54,7 +54,6 @@ constexpr int kLpTileBytes = kLpTile * 512;
 constexpr int lp_depth(bool cluster) { return cluster ? 2 : 1; }
 constexpr size_t lp_ring(bool cluster) { return (size_t)kLpWarps * lp_depth(cluster) * kLpTileBytes; }
 constexpr int kLpMaxCluster = 8;
-constexpr uint64_t kLpLimitNs = 2000000000ull;
 constexpr float kLpPlain = 4096.0f;  // |m c| below this: see LpSums
 constexpr float kLpLeastC = 1e-30f;  // so that m - kLpFar / c stays in range
 constexpr float kLpFar = 200.0f;     // 2^-200 is zero
@@ -801,7 +800,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
     uint32_t parity = 0;
     bool awaited = false, ok = true, refused = false;
     for (; g0 < row.nb; g0 += step) {
-        ok = mbar_wait(&bars[slot], parity, kLpLimitNs);
+        ok = warp_mbar_wait(&bars[slot], parity, kCopyWaitNs);
         if (!ok) break;
         const uint4* at = ring + slot * (kLpTileBytes / 16) + lane;
         if ((g0 + kLpTile) * 32 <= row.nvec) {
@@ -842,7 +841,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
         if (lane == 0) {
             set_error(a.dev_error, kDevErrTimeout);
             for (int i = 0; i < kDepth && g0 + i * step < row.nb; ++i) {
-                mbar_wait(&bars[slot], parity, kLpLimitNs);
+                mbar_wait(&bars[slot], parity, kDrainNs);
                 if (++slot == kDepth) {
                     slot = 0;
                     parity ^= 1;

@@ -17,11 +17,31 @@ constexpr int kMaxTop = 128;                 // alternatives or teacher entries 
 // Below it log2(e) / T leaves the range of 32 bits, and 0 times it is no number.
 constexpr float kMinTemperature = 1.17549435e-38f;  // 2^-126
 constexpr double kLog2e = 1.4426950408889634;
+// Limits of the waits for bulk copies, for what the CTAs of a cluster send each
+// other, and for copies in flight before a CTA may end.
+constexpr uint64_t kCopyWaitNs = 2000000000ull, kClusterWaitNs = 2000000000ull, kDrainNs = 2000000000ull;
+// Conditions on a thread under which its wait counts as run out; a test sets
+// them for a library of its own.
+#ifndef SV_LATE_COPY
+#define SV_LATE_COPY false
+#endif
+#ifndef SV_LATE_CLUSTER
+#define SV_LATE_CLUSTER false
+#endif
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLn2Hi = 0.693145751953125f, kLn2Lo = 1.4286068203e-6f;  // ln 2: its first 16 bits, and the rest
 // The reference of a running maximum before any finite entry: -inf minus it
 // is -inf (weight zero), where -inf minus -inf would be NaN.
 constexpr float kNoMax = -3.4028234663852886e38f;
+
+// A whole warp's wait, with one answer: lanes that met the limit at different
+// times would go different ways.
+__device__ __forceinline__ bool warp_mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns) && !(SV_LATE_COPY));
+}
+__device__ __forceinline__ bool warp_cluster_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, cluster_mbar_wait(bar, parity, limit_ns) && !(SV_LATE_CLUSTER));
+}
 
 // Maximum over a warp: NaN is passed over, or (nan) makes it NaN.
 __device__ __forceinline__ float warp_max_redux(float v) {
