@@ -41,9 +41,10 @@ struct DistillStat {
     float m;       // maximum of the row
     float inv_z;   // 1 / sum of 2^((s - m) c) over the row
     float mass;    // S = sum t_j + t_T
-    float ln_t;    // subtracted from the teacher's values: t_j = exp(l_j - ln_t)
+    float ln_t;    // subtracted from the teacher's values in two parts (a constant of any
+    float ln_t2;   // size may be in them): t_j = exp(l_j - ln_t - ln_t2)
     float live;    // 0: the row has loss 0 and gradient 0
-    float pad;
+    __device__ __forceinline__ float t(float l) const { return expf(l - ln_t - ln_t2); }
 };
 static_assert(sizeof(DistillStat) == 32, "row_stats is [R, 8] float");
 
@@ -67,9 +68,10 @@ constexpr float kTailRounding = 1.0f / 65536.0f;
 struct alignas(16) DsTeacher {
     double mass;  // sum of t_j
     double ln_t;  // subtracted from the teacher's values; +inf: no teacher mass at all
-    __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, their sum, ln_t
-        const double t_tail = bucket ? fmax(1.0 - mass, 0.0) : 0.0;
-        return make_float4((float)mass, (float)t_tail, (float)(mass + t_tail), (float)ln_t);
+    __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, ln_t in two parts
+        const float hi = (float)ln_t;
+        return make_float4((float)mass, bucket ? (float)fmax(1.0 - mass, 0.0) : 0.0f, hi,
+                           hi < INFINITY ? (float)(ln_t - (double)hi) : 0.0f);
     }
 };
 // What the CTAs of a row exchange about it, and its listed tokens.
@@ -252,12 +254,13 @@ __device__ __forceinline__ DistillStat distill_stat(const DistillArgs& a, const 
     const uint32_t bad = __reduce_or_sync(0xffffffffu, lane < S ? __float_as_uint(sm.bad[lane]) : 0u);
     *sums = DsSums{z, zt, listed / z, in_tail / z, t_tail > 0.0f, (int)bad};
     if (!(z > 0.0f && z < INFINITY)) sums->err |= kDevErrNonfinite;  // NaN, +inf, or nothing finite
-    if (sums->err || te.w == INFINITY) return st;
+    if (sums->err || te.z == INFINITY) return st;
     st.m_tail = mt;
     st.m = m;
     st.inv_z = 1.0f / z;
-    st.mass = no_tail ? te.x : te.z;
-    st.ln_t = te.w;
+    st.mass = t_tail > 0.0f ? 1.0f : te.x;
+    st.ln_t = te.z;
+    st.ln_t2 = te.w;
     // S q_T - t_T from the smaller part: the same as sum t_j - S (1 - q_T)
     const float d = sums->tail_q < 0.5f ? st.mass * sums->tail_q - t_tail : te.x - st.mass * sums->listed_q;
     st.coef = zt > 0.0f ? d * (float)a.inv_t / zt : 0.0f;
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(Disti
             __syncwarp();
             listed_in(ids, e0, n, [&](int k, int o) {
                 const int j = lane + 32 * k;
-                store_elem(g0 + o, distill_listed_grad(st, sm.s[j], expf(sm.l[j] - st.ln_t), a.c, (float)a.inv_t, w_row));
+                store_elem(g0 + o, distill_listed_grad(st, sm.s[j], st.t(sm.l[j]), a.c, (float)a.inv_t, w_row));
             });
         };
         if (st.live != 0.0f && unit == 0) {
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kDbThreads) k_distill_backward(DistillArgs a, 
         for (int k = 0; k < kDsIds; ++k)
             if ((unsigned)(ids[k] - e0) < (unsigned)n) {
                 const size_t j = (size_t)r * a.K + lane + 32 * k;
-                const float t = expf(a.teacher[j] - st.ln_t);
+                const float t = st.t(a.teacher[j]);
                 y[k] = distill_listed_grad(st, ElemT<T>::load(row.row + ids[k]), t, a.c, (float)a.inv_t, w);
             }
         __syncwarp();
