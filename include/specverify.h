@@ -458,7 +458,8 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int R, int
  *             with S = sum t_j + t_T; may be student's own buffer.
  *  An id outside [0, V) other than -1, or one listed twice
  *  (SPEC_DEVERR_TOKEN), a NaN or +inf in the row or no finite entry in it,
- *  a NaN or +inf teacher value of a listed token (SPEC_DEVERR_NONFINITE):
+ *  a NaN or +inf teacher value of a listed token, or under
+ *  SPEC_TAIL_BUCKET an M past the range of 32 bits (SPEC_DEVERR_NONFINITE):
  *  the row has loss 0 and gradient 0.  The waits inside are bounded (2 s):
  *  after one that ran out (SPEC_DEVERR_TIMEOUT and SPEC_DEVERR_NONFINITE)
  *  the row that it was for, and those that the same CTAs would take after

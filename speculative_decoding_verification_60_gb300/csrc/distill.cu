@@ -219,7 +219,7 @@ __device__ __forceinline__ void distill_teacher(const DistillArgs& a, const DsLi
         for (int j = lane; j < a.K; j += 32)
             if (sm.id[j] >= 0) mass += exp((double)sm.l[j] - ref);
         mass = warp_sum_d(mass);
-        if (!(mass < (double)INFINITY)) err |= kDevErrNonfinite;
+        if (!(mass <= (double)-kNoMax)) err |= kDevErrNonfinite;  // as 32 bits hold it
         out->mass = a.bucket ? mass : 1.0;
         out->ln_t = a.bucket ? 0.0 : mass > 0.0 ? ref + ln_of((float)mass) : (double)INFINITY;
     }

@@ -1,5 +1,5 @@
 """Teachers' values far from log probabilities: any constant added under
-TAIL_RENORM."""
+TAIL_RENORM, masses past the range of 32 bits under TAIL_BUCKET."""
 
 import numpy as np
 import pytest
@@ -38,3 +38,23 @@ def test_a_constant_added_to_the_teacher(V, constant):
         far = float(np.abs(spread).max()) + 40.0
         for h in (grad[r], back[r]):
             _grad_ok(h, g, scale, i, lr, V, 1.0, 1.0, "f32", far)
+
+
+@pytest.mark.parametrize("V", [700, 128256])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_teacher_whose_mass_no_float_holds(V, dtype):
+    svp = _svp()
+    s, ids, l = _case(5, V, 6, dtype, seed=V)
+    l[1, 2] = 89.0
+    l[2, :] = 88.5  # none of them alone
+    l[3, 5] = 1e5
+    a = (s.cuda(), ids.cuda(), l.cuda())
+    got = svp.distill_topk(*a, tail=svp.TAIL_BUCKET)
+    alone = svp.distill_topk(*a, tail=svp.TAIL_BUCKET, with_grad=False)
+    back = svp.distill_topk_backward(*a, got["row_stats"])
+    assert int(got["dev_error"]) == int(alone["dev_error"]) == ref.DEVERR_NONFINITE
+    for r in (1, 2, 3):
+        assert float(got["loss"][r]) == 0 == float(alone["loss"][r])
+        assert not got["grad"][r].any() and not back["grad"][r].any()
+    for r in (0, 4):
+        assert float(got["loss"][r]) > 0 and got["grad"][r].any()
