@@ -69,9 +69,9 @@ struct alignas(16) DsTeacher {
     double mass;  // sum of t_j
     double ln_t;  // subtracted from the teacher's values; +inf: no teacher mass at all
     __device__ __forceinline__ float4 message(bool bucket) const {  // mass, t_T, ln_t in two parts
+        if (bucket) return make_float4((float)mass, (float)fmax(1.0 - mass, 0.0), 0.0f, 0.0f);
         const float hi = (float)ln_t;
-        return make_float4((float)mass, bucket ? (float)fmax(1.0 - mass, 0.0) : 0.0f, hi,
-                           hi < INFINITY ? (float)(ln_t - (double)hi) : 0.0f);
+        return make_float4(1.0f, 0.0f, hi, hi < INFINITY ? (float)(ln_t - (double)hi) : 0.0f);
     }
 };
 // What the CTAs of a row exchange about it, and its listed tokens.

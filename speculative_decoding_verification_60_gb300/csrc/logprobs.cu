@@ -414,11 +414,9 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
     float z = 0.0f, e = 0.0f;
     int n = 0, before = 0;  // n: elements equal to m that are not in the sums
     auto add = [&](float x, int count) {
-        if (x == m) {
-            n += count;
-            return;
-        }
-        const float t = ref != LpSums::kNone ? fmaf(x, a.c, -ref) : (x - m) * a.c, w = (float)count * ex2(t);
+        const float t = ref != LpSums::kNone ? fmaf(x, a.c, -ref) : (x - m) * a.c;
+        const float w = x == m ? 0.0f : (float)count * ex2(t);
+        n += x == m ? count : 0;
         z += w;
         e = fmaf(w, fmaxf(t, -1000.0f), e);
     };
@@ -457,9 +455,10 @@ __device__ __forceinline__ void lp_merge(const LogprobArgs& a, int r, const LpRo
         const float rest = most ? z * up : w + z, all = most ? 1.0f + rest : rest;
         const float at = (most ? fmaf(g, z, e) * up : fmaf(w, -g, e)) / all;
         const float mean = most ? at : at + g;  // of (x - m) c
-        int exp2 = 0;
-        const float f = most ? rest : fmaf(2.0f, frexpf(rest, &exp2), -1.0f);  // in [0, 1): ln z = ln(1 + f) + ...
-        const float whole = most ? 0.0f : (float)(exp2 - 1);
+        // f in [0, 1): ln z = ln(1 + f) + whole ln 2 (the sum is 1/2 or more: its exponent is in its bits)
+        const int bits = __float_as_int(rest);
+        const float f = most ? rest : __int_as_float((bits & 0x007fffff) | 0x3f800000) - 1.0f;
+        const float whole = most ? 0.0f : (float)((bits >> 23) - 127);
         float2 ln_z = make_float2(whole * kLn2Hi, fmaf(whole, kLn2Lo, log1pf(f)));
         ln_z = add_parts(make_float2(ln_z.x, 0.0f), ln_z.y);
         const float entropy = fmaf(-kLn2, at, ln_z.x) + ln_z.y;
