@@ -406,7 +406,7 @@ spec_status spec_sample_rows(const void* logits, spec_dtype dtype, int R, int V,
  *  logprob      [R] out: log p(token).  Over rows of many kinds it was off
  *               by 8e-7 at most (1.5e-6 at V = 524,280 where all weights
  *               are alike) or, if that is more, by its rounding; where the
- *               token holds nearly all of the row, by 4e-7 of its value.
+ *               token holds nearly all of the row, by 1.2e-6 of its value.
  *               NULL only when tokens is NULL.
  *  rank         [R] out or NULL: 1 + the number of v before the token in
  *               (logit descending, index ascending) order.

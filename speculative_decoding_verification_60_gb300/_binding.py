@@ -459,7 +459,10 @@ def distill_topk(student, teacher_ids, teacher_logprobs, weights=None, temperatu
     the gradient of sum(weights * loss) in the same pass.  weights float32 of
     the leading shape or None.  Returns a dict: loss and grad, row_stats
     [..., 8] (for distill_topk_backward), dev_error [1].  out["grad"] may be
-    the student tensor itself."""
+    the student tensor itself.  The teacher's tensors are contiguous (a slice
+    of token_logprobs' outputs along the drafts is not).  The loss is not part
+    of an autograd graph, whether or not student requires gradients: hand grad
+    to the model's backward pass, student.backward(grad)."""
     lib = load()
     dt = _dtype_code(student)
     R, V, step = _rows(student, "student")

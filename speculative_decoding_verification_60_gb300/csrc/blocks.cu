@@ -93,7 +93,7 @@ __device__ __forceinline__ int2 block_scan2(int x, int y, int2* part, int2* tota
 // writes.  CTA 0 writes the per-request outputs.  Bound by latency (the reads
 // of a request's state, two scans, the search, the table): 64 requests of 5
 // tokens take 8.3 us on the device back to back, launch included; 1024 requests,
-// 128 of them with prompts of up to 4096 tokens (3.3 MB), 8.8 us.
+// 128 of them with prompts of up to 4096 tokens (3.3 MB), 8.9 us.
 template <int NT>
 __global__ void __launch_bounds__(NT) k_advance_blocks(BlocksArgs a) {
     __shared__ int2 part[32];

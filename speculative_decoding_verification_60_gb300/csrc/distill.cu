@@ -530,7 +530,7 @@ __device__ __forceinline__ void distill_after(const DistillArgs& a, int r, const
 // memory, one read of the row: 2432 rows of 128256 bf16 (four full waves of
 // CTAs) in 98 us, 0.94 of the measured copy bandwidth; 1024 rows in 45 us,
 // 0.85 (two waves, the second two thirds full), and 49 us with 128 listed
-// tokens.
+// tokens.  Held to 56 registers, which spills 4 to 8 bytes a thread.
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(DistillArgs a) {
     extern __shared__ __align__(128) uint8_t ds_raw[];  // [kDsWarps] tiles
@@ -630,7 +630,8 @@ __global__ void __launch_bounds__(kDsThreads, kDsLossPerSm) k_distill_loss(Disti
 //
 // Its size matters: three CTAs' warps are in different phases of it, and with
 // the loops that run once or twice a row unrolled (101 KB of code, 74 KB
-// without) the same row took a tenth longer.
+// without) the same row took a tenth longer.  It is held to 72 registers, which
+// spills up to 28 bytes a thread.
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kDsThreads, kDsGradPerSm) k_distill_grad(DistillArgs a, int n_buf) {
     constexpr int VEC = ElemT<T>::VEC;

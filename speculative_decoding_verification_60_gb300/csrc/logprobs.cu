@@ -14,9 +14,10 @@
 // two; a maximum that may hold most of the row is counted, not summed, so that
 // ln z = ln(1 + rest) keeps every digit of the rest; and what c is off by,
 // rounded to 32 bits, is put right in ln z: d ln z / d ln c is ln 2 * e / z.
-// (Largest errors over 200 rows of 128256: log p 1.3e-7 to 6e-7, and 2e-7 to
-// 4e-7 of the value where it is near 0; that costs 1.5 % of the time of many
-// rows and 0.6 us of few.)
+// (Largest errors, 96 kinds of rows of 1000 to 524280: log p 1.5e-6, and 1.2e-6
+// of its value near 0, where plain sums lose all digits.  Sums that rescale by
+// exponentials and include the maximum were up to 3e-5 off and 1.5 % faster
+// over many long rows, 0.6 us over few, 5 to 8 % over thousands of short ones.)
 // The group maxima are what makes the alternatives cheap: groups are
 // contiguous, so in the order (logit descending, index ascending) every
 // element of a group comes after that group's first maximum, and the K best
@@ -229,8 +230,8 @@ struct LpTile {
     // another group of the tile has an eighth of its weight, it may hold
     // most of the row, and is taken out (where one has, ln z is at least 0.1,
     // and the maximum may as well be summed).  Rare in rows without such a
-    // token: taking out whatever has nothing of half its weight beside it
-    // cost 4096 rows 1.5 us.
+    // token: 4096 rows take 0.6 us more where only half its weight rules that
+    // out, and up to 4 us more where every new maximum is taken out.
     __device__ __forceinline__ void raise(LpSums& sum, float c, float beside, uint4* spare) {
         const float near = most - beside;
         const bool far = sum.m < near;
@@ -248,8 +249,9 @@ struct LpTile {
         for (int j = 0; j < kLpTile; ++j)
             if (groups == 1u << j) q[j] = *spare;
     }
-    // z is summed by vectors, tiles and then the row: 24 to 85 adds one after
-    // another would be off by as many roundings where all weights are alike.
+    // z is summed by vectors, tiles and then the row: 250 adds one after
+    // another (1000 in the longest rows) are off by a quarter as many roundings
+    // where all weights are alike.
     __device__ __forceinline__ void add(LpSums& sum, float c, float far) const {
         const float2 cc = make_float2(c, c);
         float2 z;
@@ -560,8 +562,8 @@ __device__ __forceinline__ void lp_take(LpFinish& s, int g) {
     if (at < LpFinish::kGroups) s.group[at] = g;  // more only in a row of NaN, refused before they are read
 }
 // Takes the first n groups whose key is tau; each warp looks at a stretch of
-// the row's groups (777 fp32 rows, half of them masked, 64 alternatives: 48.6
-// us; 52 with every thread counting the groups before its own).  A function of
+// the row's groups (777 fp32 rows, half of them masked, 64 alternatives: 3.5 us
+// of 52 less than with every thread counting the groups before its own).  A function of
 // its own as lp_ties is: in line it cost rows that never get here 1 to 2 %.
 __device__ __noinline__ void lp_equal(LpFinish* fin, const uint32_t* group_key, int nb, uint32_t tau, int n) {
     LpFinish& s = *fin;
@@ -632,7 +634,11 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
     // elements above it from those.  Where the row has few groups, or the
     // bound leaves many more than K elements (the best of a sorted row share
     // some groups), the bound comes from the keys of the chosen groups'
-    // vectors.
+    // vectors.  "Few" is what s.group holds, not what is faster: with the
+    // groups' keys wherever there are more groups than K and the slack, 4096
+    // rows of 32000 bf16 take 76 us for 5 alternatives and 104 for 64, with all
+    // vectors' keys 121 and 139; of 50257, 95 and 122 against 172 and 191; of
+    // 4096, 41 for 5 against 47, and the same where the groups are fewer.
     bool vectors = nb <= LpFinish::kGroups;
     if (vectors) {
         for (int g = tid; g < nb; g += kLpThreads) s.group[g] = g + 1;
@@ -725,13 +731,14 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
 
 // A row by a CTA, or by a cluster whose first CTA finishes it.  Bound by
 // memory, one read of the row, while rows are many: 2048 rows of 128256 bf16
-// without alternatives take 85.5 us, 0.91 of the measured copy bandwidth; 3072
-// live rows of 129280 with 8 alternatives 140 us, 0.84.  The rest is the rows'
-// ends, where a CTA has nothing on its way: four CTAs an SM (57 registers, 24 KB
+// without alternatives take 86.8 us, 0.89 of the measured copy bandwidth; 3072
+// live rows of 129280 with 8 alternatives 141 us, 0.83.  The rest is the rows'
+// ends, where a CTA has nothing on its way: four CTAs an SM (60 registers, 24 KB
 // of tiles each) cover each other's.  Fewer, larger CTAs with a ring of copies
 // and teams of finishing warps took 137 and 230 us, rows split over CTAs that
 // meet in global memory 195 to 252.  Few rows are bound by one row's latency:
-// 5 rows 8.4 us, launch included.
+// 5 rows 8.7 us, launch included; so are short ones, a CTA each: 4096 rows of
+// 1000 take 21 us, 40 with 5 alternatives, 17 and 33 times their bytes' time.
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(LogprobArgs a) {
     __shared__ LpFinish s;
@@ -869,9 +876,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) k_token_logprobs(Logprob
 
 // CTAs that share a row, each with a tile for every warp: measured at
 // V = 128256 bf16 with 20 alternatives, one CTA a row against 2, 4 and 8 takes
-// 15.0 / 12.8 / 10.3 / 9.6 us for 5 rows, 15.1 / 13.0 / 10.7 / 10.7 for 30,
-// 15.1 / 13.1 / 12.3 / 14.5 for 60, 15.2 / 13.3 / 14.1 / 14.7 for 76, 16.7 / 17.4 /
-// 18.8 / 23.8 for 150 and 21.5 / 25.6 / 32.0 / 38.8 for 304.
+// 14.9 / 12.9 / 10.4 / 9.4 us for 5 rows, 15.0 / 13.3 / 11.3 / 11.0 for 30,
+// 15.2 / 16.1 / 12.3 / 15.0 for 60, 15.1 / 13.5 / 14.4 / 16.5 for 76, 15.5 / 16.5 /
+// 14.9 / 20.2 for 100, 18.7 / 18.5 / 23.4 / 27.1 for 150 and 21.8 / 34.5 / 36.0 /
+// 45.6 for 304.  At V = 262144, at 50021 fp32 with 64 alternatives and without
+// alternatives the same sizes are best up to 76 rows and from 304; between
+// them sharing would save up to 2.5 us (100 rows by 4) and 4 (150 by 2) of the
+// 262144, and 1 without alternatives.
 template <typename T>
 static cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
     const int groups = (a.V / ElemT<T>::VEC + 31) / 32;

@@ -212,7 +212,7 @@ __device__ __forceinline__ double ln_of(float z) {
 // before is ending, they wait for it (rows_begin) before they read anything.
 // The error word is cleared by a kernel of its own in that chain; a memset
 // there would make the next launch an ordinary one (5 rows of 128256 bf16 by
-// token_logprobs: 8.4 us, with a memset 11.2).
+// token_logprobs: 8.7 us, with a memset 2.8 more).
 __device__ __forceinline__ void rows_begin() {
     grid_dep_trigger();
     grid_dep_wait();
@@ -225,8 +225,8 @@ static __global__ void __launch_bounds__(32) k_clear_error(int32_t* dev_error) {
 // of S CTAs.  A grid of one CTA to one wave of CTAs per SM is placed on an idle
 // GPU (its first launch is an ordinary one): on one that is still ending a
 // kernel, the SMs that are free first get more than their share of CTAs, and
-// nothing follows to even it out (320 rows, 192 of them live: 26.4 us, started
-// early 30.6; fewer or more CTAs are 0.5 us faster started early).
+// nothing follows to even it out (320 rows, 192 of them live: 27 us, started
+// early 4 more; fewer or more CTAs are 0.5 us faster started early).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_rows(void (*kernel)(KArgs...), long long n, int S, int block, size_t dyn_smem, int sms,
                                int per_sm, int32_t* dev_error, cudaStream_t st, Args... args) {
