@@ -75,7 +75,8 @@ typedef enum {
     SPEC_ERR_CUDA = 4          /* a CUDA call or kernel launch failed */
 } spec_status;
 
-typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1 } spec_dtype;
+/* SPEC_F16: the calls over a paged cache only. */
+typedef enum { SPEC_BF16 = 0, SPEC_F32 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* How the children of a draft-tree node were drawn from the draft model
  * (section "EAGLE": Top-K candidates per node).  The residual update after
@@ -111,7 +112,8 @@ typedef enum {
                                     the results stand.  spec_token_logprobs: the rows are
                                     refused (SPEC_DEVERR_NONFINITE is set, too).
                                     spec_distill_topk: the call's results are not to be used */
-#define SPEC_DEVERR_CAPACITY 32  /* cache blocks: the free list or a request's table row ran out */
+#define SPEC_DEVERR_CAPACITY 32  /* cache blocks: the free list or a request's table row ran out; a slot or a block
+                                    that the cache does not have */
 
 typedef struct {
     float temperature;  /* 0 => greedy (argmax, ties to the lowest index); > 0 => sampled */
@@ -535,6 +537,195 @@ spec_status spec_advance_blocks(const int32_t* seq_lens, const int32_t* accepted
                                 const int32_t* free_count, int32_t* out_seq_lens, int32_t* out_held, int32_t* out_free_count,
                                 int32_t* cu_tokens, int64_t* slots, int32_t* positions, int max_tokens,
                                 int32_t* dev_error, spec_stream_t stream);
+
+/*
+ * A paged cache of keys or of values: entry `place` of block j, head h,
+ * begins at base + j * block_stride + place * entry_stride + h * head_stride
+ * (in elements; its dim elements are contiguous), so that blocks may hold
+ * [entry, head, dim] or [head, entry, dim], and keys and values may lie in one
+ * buffer.  Position t of request b is entry t % page_size of block
+ * block_table[b, t / page_size]; slot s is entry s % page_size of block
+ * s / page_size, as spec_advance_blocks hands them out.
+ */
+typedef struct {
+    int32_t blocks, page_size, heads, dim;
+    int64_t block_stride, entry_stride, head_stride;
+} spec_cache_layout;
+
+/*
+ * New tokens on their way from a model's projections into attention: heads of
+ * queries and keys normalised (optional) and turned by their position, keys and
+ * values stored in the tokens' cache slots.
+ *
+ *  q, k, v      [T, heads, dim], token t's head h at t * *_token_stride +
+ *               h * *_head_stride elements (slices of one projection output
+ *               count).  q NULL: only keys and values.  bf16 or fp16.
+ *  q_norm, k_norm [dim] of the same type, or NULL (both or neither; k_norm
+ *               alone when q is NULL): x <- x / sqrt(mean(x^2) + eps) * norm,
+ *               over the head's dim elements, in 32 bits.
+ *  positions    [T] int32; NULL only with rot_dim 0.
+ *  inv_freq     [rot_dim / 2] fp32: pair i turns by positions[t] *
+ *               inv_freq[i], (x, y) <- (x cos - y sin, y cos + x sin).  Pair i
+ *               is elements (i, i + rot_dim / 2) of a head, or with
+ *               `interleaved` (2i, 2i + 1); elements from rot_dim on stay.
+ *               The angle is taken modulo a turn in 64-bit fixed point: exact
+ *               to 2^-33 turns at any position.  In a tree, a node's position
+ *               is its request's length plus its depth.
+ *  slots        [T] int64 cache slots; a negative one stores nothing (its
+ *               queries are still turned).  Slots are distinct: an entry named
+ *               twice holds either token's values, per 16 bytes.
+ *  out_q        [T, q_heads, dim] out, contiguous; may be q itself when that
+ *               is contiguous.
+ *  k_cache, v_cache  out: caches of one layout (heads = the kv heads).
+ *  A slot of blocks * page_size or more sets SPEC_DEVERR_CAPACITY and stores
+ *  nothing.  Norm, turn and rounding to the type happen once, in 32 bits.
+ *  T == 0 is valid.  Limits (SPEC_ERR_UNSUPPORTED otherwise): dim a multiple
+ *  of 8 up to 256, rot_dim a multiple of 8 up to dim, pointers and strides
+ *  multiples of 8 bytes.
+ */
+spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dtype dtype, int T, int q_heads,
+                           int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const void* q_norm,
+                           const void* k_norm, float eps, const int32_t* positions, const float* inv_freq, int rot_dim,
+                           int interleaved, const int64_t* slots, void* out_q, void* k_cache, void* v_cache,
+                           const spec_cache_layout* layout, int32_t* dev_error, spec_stream_t stream);
+
+/*
+ * Attention of drafted nodes over a paged cache.  Request b has seq_lens[b]
+ * entries in the cache (its sequence) and behind them the entries of this
+ * step's nodes, node i at position seq_lens[b] + i, all stored before the call.
+ * Node n's queries see the sequence and the nodes on n's path from the root, n
+ * itself included:
+ *   out[b, n, h] = sum_t softmax_t(scale * q[b, n, h] . k[t, h']) v[t, h'],
+ * h' = h / (q_heads / kv heads).  A linear draft is the chain (parent NULL);
+ * N = 1 is a decoding step.
+ *
+ *  q            [B, N, q_heads, dim], strides of request, node and head in
+ *               elements, heads contiguous; bf16 or fp16, as the caches.
+ *  k_cache, v_cache  caches of one layout; q_heads a multiple of its heads.
+ *  block_table  [B, max_blocks] int32, rows table_stride apart, as
+ *               spec_advance_blocks keeps it; only the entries of positions
+ *               below seq_lens[b] + n_b are read.
+ *  seq_lens     [B] int32 >= 0: out_seq_lens of spec_advance_blocks.
+ *  parent       NULL (node i's parent is i - 1), [N] with parent_stride 0, or
+ *               [B, N] with parent_stride >= N: as in the tree verification.
+ *  n_nodes      [B] int32 in 0 .. N, or NULL (N each).  Rows from n_b on are
+ *               neither read nor written.
+ *  scale        > 0, finite.
+ *  out          [B, N, q_heads, dim] out, contiguous; must not overlap the
+ *               inputs.
+ *  Entries that a node does not see have no influence on it, whatever they
+ *  hold.  An entry of this step's nodes whose values are not all finite makes
+ *  the whole head row of each node that sees it NaN.  Scores, softmax sums and
+ *  outputs are held in 32 bits; the weights of the products with the values are
+ *  rounded to the type.
+ *  A request with seq_lens[b] < 0, n_b outside 0 .. N or more positions than
+ *  max_blocks blocks hold (SPEC_DEVERR_LENGTH), a parent array that is not a
+ *  tree rooted at 0 with parent[i] < i (SPEC_DEVERR_PARENT), or a block outside
+ *  the cache (SPEC_DEVERR_CAPACITY) gets rows of zeros (all N rows when n_b is
+ *  out of range).  The waits inside are bounded (2 s): after one that ran out
+ *  (SPEC_DEVERR_TIMEOUT) the call's results are not to be used.
+ *  The same call gives the same bits every time; a request's floats may differ
+ *  in their last bits with the other requests of its batch.
+ *  workspace    spec_tree_attention_workspace() bytes on 256, for this call
+ *               alone until it has completed; needs no initial value.
+ *  Limits (SPEC_ERR_UNSUPPORTED): dim a multiple of 8 in 64 .. 128, N <= 1024,
+ *  B <= 65,535, strides of the caches multiples of 16 bytes, caches on 16 bytes,
+ *  q on 16 bytes with strides of multiples of 16 bytes.
+ */
+size_t spec_tree_attention_workspace(int B, int N, int q_heads, int kv_heads, int dim);
+spec_status spec_tree_attention(const void* q, spec_dtype dtype, int B, int N, int q_heads, int64_t q_request_stride,
+                                int64_t q_node_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+                                const spec_cache_layout* layout, const int32_t* block_table, int max_blocks,
+                                int64_t table_stride, const int32_t* seq_lens, const int32_t* parent,
+                                int64_t parent_stride, const int32_t* n_nodes, float scale, void* out,
+                                int32_t* dev_error, void* workspace, size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * What spec_adjust_logits does to a request's rows; every pointer is a device
+ * pointer, and each group may be NULL.
+ */
+typedef struct {
+    /* [B, history_capacity] token ids, rows history_stride apart: request b has history_lens[b] of them, the first
+     * prompt_lens[b] (NULL: none) its prompt, the others its output so far, the root's token included */
+    const int32_t* history;
+    int64_t history_stride;
+    const int32_t* history_lens;
+    const int32_t* prompt_lens;
+    int32_t history_capacity;
+    /* token of node i, 1 <= i < R, at drafted[b * drafted_stride + i - 1]: draft_tokens [B, k] of a linear
+     * verification, or node_tokens + 1 with stride N of a tree's */
+    const int32_t* drafted;
+    int64_t drafted_stride;
+    /* as in spec_tree_attention */
+    const int32_t* parent;
+    int64_t parent_stride;
+    const int32_t* n_nodes;
+    /* [B] each */
+    const float *repetition, *frequency, *presence;
+    /* [B, bias_count] ids (-1: none) and what is added to their logits; an id given twice gets both */
+    const int32_t* bias_ids;
+    const float* bias_values;
+    int32_t bias_count;
+    /* bit v % 32 of word v / 32 of a row: token v is allowed.  Rows allowed_stride words apart, in the order of the
+     * logits' rows */
+    const int32_t* allowed;
+    int64_t allowed_stride;
+} spec_adjustments;
+
+/*
+ * Target (or draft) logits before they are verified or sampled from: penalties
+ * for tokens that were said already, biases, and a grammar's mask.  Row i of
+ * request b scores what follows node i, so it counts the request's history and
+ * the drafted tokens on the path from the root to i:
+ *   seen(v): v in the history or on the path;  c(v): times v occurs in the
+ *            history from prompt_lens[b] on, and on the path
+ *   y = seen ? (x > 0 ? x / repetition : x * repetition) : x
+ *   y = y - (frequency * c + presence * [c > 0]) + sum of v's biases
+ *   y = -inf where v is not allowed (whatever x is; x is not read there).
+ * In 32 bits, rounded once.  c is held up to 2^31 - 1.
+ *
+ *  logits, out  B * R rows of V elements, row r at r * row_stride (out:
+ *               out_stride), bf16 or fp32; out may be logits itself with the
+ *               same stride.  Rows from n_nodes[b] on are left as they are.
+ *  A token id of the history, the path or the biases outside [0, V) (other
+ *  than a bias of -1) is passed over (SPEC_DEVERR_TOKEN); history_lens[b]
+ *  outside 0 .. history_capacity counts as 0, prompt_lens[b] outside
+ *  0 .. history_lens[b] as the nearer end, n_nodes[b] outside 0 .. R as R
+ *  (SPEC_DEVERR_LENGTH); a parent array that is not a tree (see above) makes
+ *  the request's paths empty (SPEC_DEVERR_PARENT).  Parameters that are no
+ *  numbers act by the formula.
+ *  B == 0 is valid.  Limits: V <= 524,280, R <= 1024, bias_count <= 1024,
+ *  B <= 65,535 (SPEC_ERR_UNSUPPORTED).
+ */
+spec_status spec_adjust_logits(const void* logits, spec_dtype dtype, int B, int R, int V, int64_t row_stride,
+                               const spec_adjustments* adjustments, void* out, int64_t out_stride,
+                               int32_t* dev_error, spec_stream_t stream);
+
+/*
+ * After a tree verification: the cache entries of the accepted path move
+ * together, so that the a_b + 1 valid entries that spec_advance_blocks counts on
+ * are consecutive.  In every plane, the entry of node path_nodes[b, i] (position
+ * seq_lens[b] + path_nodes[b, i]) moves to position seq_lens[b] + i,
+ * i = 0 .. a_b.  (Entries were turned by their depth, which is i.)  Other
+ * entries stay; a linear draft needs no such call.
+ *
+ *  planes       HOST array of n_planes device pointers, key and value caches of
+ *               all layers, of one layout; read before the call returns.
+ *  element_size 1, 2 or 4 bytes.
+ *  path_nodes   [B, W], accepted_len [B]: as the tree verification gives them,
+ *               on the block_table and seq_lens of its attention.
+ *  A request whose a_b is outside 0 .. W - 1, whose path is not increasing from
+ *  a node >= 0 or whose positions pass its table (SPEC_DEVERR_LENGTH), or that
+ *  has a block outside the cache there (SPEC_DEVERR_CAPACITY), is left as it is.
+ *  Two requests must not share blocks from seq_lens[b] on.  B == 0 and
+ *  n_planes == 0 are valid.  Limits: B <= 65,535, W <= 1024
+ *  (SPEC_ERR_UNSUPPORTED).
+ */
+spec_status spec_keep_path(void* const* planes, int n_planes, int element_size, const spec_cache_layout* layout, int B,
+                           int W, const int32_t* path_nodes, const int32_t* accepted_len, const int32_t* seq_lens,
+                           const int32_t* block_table, int max_blocks, int64_t table_stride, int32_t* dev_error,
+                           spec_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* spec_status_string(spec_status status);

@@ -20,16 +20,22 @@ from ._binding import (  # noqa: F401
     SPEC_OP_TREE,
     TAIL_BUCKET,
     TAIL_RENORM,
+    Adjustments,
+    CacheLayout,
     SamplingParams,
     SpecError,
+    adjust_logits,
     advance_blocks,
+    append_kv,
     compact_accepted,
     distill_topk,
     distill_topk_backward,
+    keep_path,
     load,
     sample_rows,
     status_string,
     token_logprobs,
+    tree_attention,
     verify_linear,
     verify_linear_compact,
     verify_tree,

@@ -17,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libspecverify.so")
 
 SPEC_OK = 0
-SPEC_BF16, SPEC_F32 = 0, 1
+SPEC_BF16, SPEC_F32, SPEC_F16 = 0, 1, 2
 SPEC_OP_LINEAR, SPEC_OP_TREE = 0, 1
 CHILD_WOR, CHILD_IID, CHILD_DETERMINISTIC = 0, 1, 2
 DEVERR_TOKEN, DEVERR_NONFINITE, DEVERR_PARENT, DEVERR_LENGTH, DEVERR_CAPACITY = 1, 2, 4, 8, 32
@@ -28,12 +28,28 @@ EXPORTS = ("spec_workspace_size", "spec_verify_linear", "spec_verify_linear_comp
            "spec_linear_draw", "spec_verify_linear_noalloc", "spec_verify_tree", "spec_verify_tree_dynamic",
            "spec_compact_accepted",
            "spec_sample_rows", "spec_token_logprobs", "spec_distill_topk", "spec_distill_topk_backward",
-           "spec_advance_blocks", "spec_status_string")
+           "spec_advance_blocks", "spec_append_kv", "spec_tree_attention_workspace", "spec_tree_attention",
+           "spec_adjust_logits", "spec_keep_path", "spec_status_string")
 
 
 class SamplingParams(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("seed", ctypes.c_uint64),
                 ("child_mode", ctypes.c_int32)]
+
+
+class CacheLayout(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("block_stride", ctypes.c_int64), ("entry_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Adjustments(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64), ("history_lens", ctypes.c_void_p),
+                ("prompt_lens", ctypes.c_void_p), ("history_capacity", ctypes.c_int32), ("drafted", ctypes.c_void_p),
+                ("drafted_stride", ctypes.c_int64), ("parent", ctypes.c_void_p), ("parent_stride", ctypes.c_int64),
+                ("n_nodes", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_count", ctypes.c_int32), ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -91,6 +107,17 @@ def load() -> ctypes.CDLL:
     lib.spec_distill_topk_backward.restype = I
     lib.spec_advance_blocks.argtypes = [P, P, P, I, I, P, I, L, P, P, I, P, P, P, P, P, P, P, I, P, P]
     lib.spec_advance_blocks.restype = I
+    layout = ctypes.POINTER(CacheLayout)
+    lib.spec_append_kv.argtypes = [P, P, P, I, I, I, L, L, L, L, L, L, P, P, F, P, P, I, I, P, P, P, P, layout, P, P]
+    lib.spec_append_kv.restype = I
+    lib.spec_tree_attention_workspace.argtypes = [I, I, I, I, I]
+    lib.spec_tree_attention_workspace.restype = Z
+    lib.spec_tree_attention.argtypes = [P, I, I, I, I, L, L, L, P, P, layout, P, I, L, P, P, L, P, F, P, P, P, Z, P]
+    lib.spec_tree_attention.restype = I
+    lib.spec_adjust_logits.argtypes = [P, I, I, I, I, L, ctypes.POINTER(Adjustments), P, L, P, P]
+    lib.spec_adjust_logits.restype = I
+    lib.spec_keep_path.argtypes = [P, I, I, layout, I, I, P, P, P, P, I, L, P, P]
+    lib.spec_keep_path.restype = I
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -536,4 +563,264 @@ def advance_blocks(seq_lens, new_tokens, block_table, held, free_blocks, free_co
                 *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_advance_blocks", st)
+    return out
+
+
+def _half_code(t, name) -> int:
+    if t.dtype is torch.bfloat16:
+        return SPEC_BF16
+    if t.dtype is torch.float16:
+        return SPEC_F16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _cache(t, name, device=None) -> CacheLayout:
+    """Layout of a cache [blocks, page_size, heads, dim] whose dim is contiguous; the other dimensions may lie in any
+    order and be parts of a wider buffer, but must not overlap."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4 or t.numel() == 0:
+        raise ValueError(f"{name} must have shape [blocks, page_size, heads, dim], got {tuple(t.shape)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}")
+    shape, stride = t.shape, t.stride()
+    if shape[3] > 1 and stride[3] != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    room = shape[3]
+    steps = [0, 0, 0]
+    for s, n, i in sorted((stride[i], shape[i], i) for i in range(3)):
+        if n > 1:
+            if s < room:
+                raise ValueError(f"{name} must have entries that do not overlap")
+            steps[i], room = s, s * (n - 1) + room
+    return CacheLayout(shape[0], shape[1], shape[2], shape[3], *steps)
+
+
+def _caches(k_cache, v_cache, device):
+    """The one layout of a key and a value cache."""
+    layout = _cache(k_cache, "k_cache", device)
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one dtype and shape")
+    other = _cache(v_cache, "v_cache", device)
+    if (layout.block_stride, layout.entry_stride, layout.head_stride) != (
+            other.block_stride, other.entry_stride, other.head_stride):
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return layout
+
+
+def _heads(t, name, dtype, shape, device):
+    """(pointer, strides) of a tensor [..., heads, dim] whose heads are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}" if t.is_cuda else f"{name} must be a CUDA tensor")
+    stride = t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    return t.data_ptr(), [s if n > 1 else 0 for s, n in zip(stride[:-1], shape[:-1])]
+
+
+def _table(block_table, B, device):
+    """(pointer, blocks of a row, row stride) of a block table [B, max_blocks]."""
+    if block_table.dtype is not _I32:
+        raise TypeError(f"block_table must be {_I32}, got {block_table.dtype}")
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.get_device() != device:
+        raise ValueError(f"block_table must have shape [{B}, max_blocks] on cuda:{device}")
+    _, M, step = _rows(block_table, "block_table")
+    return block_table.data_ptr(), M, step
+
+
+def _tree(parent, B, N, device):
+    """(pointer, row stride) of a parent array [N] or [B, N], or of none."""
+    if parent is None:
+        return None, 0
+    if parent.dim() == 1:
+        return _at(parent, "parent", _I32, torch.Size((N,)), device), 0
+    return _at(parent, "parent", _I32, torch.Size((B, N)), device), N
+
+
+def append_kv(q, k, v, positions, slots, k_cache, v_cache, inv_freq=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+              interleaved: bool = False, out=None, stream=None) -> dict:
+    """``spec_append_kv`` on torch tensors: q [T, q_heads, dim] (or None), k and v [T, heads, dim] (bf16 or fp16;
+    slices of one projection count), positions [T] int32, slots [T] int64 as advance_blocks returns them (negative:
+    nothing is stored), caches [blocks, page_size, heads, dim] of one layout, written in place.  inv_freq [rot_dim / 2]
+    float32 or None (no turn); q_norm and k_norm [dim] or None.  Returns a dict: q (turned; out["q"] may be q itself),
+    dev_error [1]."""
+    lib = load()
+    dt = _half_code(k, "k")
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q, k and v must have shape [T, heads, dim]")
+    device, (T, H, D) = k.get_device(), k.shape
+    if not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    layout = _caches(k_cache, v_cache, device)
+    if k_cache.dtype is not k.dtype or (layout.heads, layout.dim) != (H, D):
+        raise ValueError(f"caches must be {k.dtype} of {H} heads of {D}")
+    out = {} if out is None else out
+    q_heads = 0 if q is None else q.shape[1]
+    wide = torch.Size((T, q_heads, D))
+    q_ptr, (q_token, q_head) = (None, (0, 0)) if q is None else _heads(q, "q", k.dtype, wide, device)
+    k_ptr, (k_token, k_head) = _heads(k, "k", k.dtype, k.shape, device)
+    v_ptr, (v_token, v_head) = _heads(v, "v", k.dtype, k.shape, device)
+    one, each = torch.Size((D,)), torch.Size((T,))
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    if inv_freq is not None and positions is None:
+        raise ValueError("positions are required with inv_freq")
+    st = lib.spec_append_kv(
+        q_ptr, k_ptr, v_ptr, dt, T, q_heads, q_token, q_head, k_token, k_head, v_token, v_head,
+        _at(q_norm, "q_norm", k.dtype, one, device), _at(k_norm, "k_norm", k.dtype, one, device), eps,
+        _at(positions, "positions", _I32, each, device),
+        None if inv_freq is None else _at(inv_freq, "inv_freq", _F32, torch.Size((rot // 2,)), device), rot,
+        bool(interleaved), _at(slots, "slots", torch.int64, each, device),
+        None if q is None else _to(out, "q", k.dtype, wide, device, stream), k_cache.data_ptr(), v_cache.data_ptr(),
+        ctypes.byref(layout), _to(out, "dev_error", _I32, _ONE, device, stream),
+        _handle(stream, device, q, k, v, positions, slots, k_cache, v_cache, inv_freq, q_norm, k_norm, *out.values()))
+    if st != SPEC_OK:
+        raise SpecError("spec_append_kv", st)
+    return out
+
+
+def tree_attention(q, k_cache, v_cache, block_table, seq_lens, parent=None, n_nodes=None, scale=None, out=None,
+                   stream=None) -> dict:
+    """``spec_tree_attention`` on torch tensors: q [B, N, q_heads, dim] (bf16 or fp16), caches [blocks, page_size,
+    heads, dim] of one layout, block_table [B, max_blocks] and seq_lens [B] int32 (advance_blocks' state; the nodes'
+    entries lie behind seq_lens), parent None (a chain), [N] or [B, N] int32, n_nodes [B] int32 or None, scale
+    (default 1 / sqrt(dim)).  Returns a dict: out [B, N, q_heads, dim] (a new tensor has zeros behind a request's
+    nodes; a given one keeps what it has there), dev_error [1], and workspace, used again when the dict is given as
+    `out` to later calls on the same stream."""
+    lib = load()
+    dt = _half_code(q, "q")
+    if q.dim() != 4 or q.numel() == 0:
+        raise ValueError(f"q must have shape [B, N, q_heads, dim], got {tuple(q.shape)}")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    device, (B, N, H, D) = q.get_device(), q.shape
+    layout = _caches(k_cache, v_cache, device)
+    if k_cache.dtype is not q.dtype or layout.dim != D or H % layout.heads:
+        raise ValueError(f"caches must be {q.dtype} of heads that divide {H}, of {D}")
+    q_ptr, (q_request, q_node, q_head) = _heads(q, "q", q.dtype, q.shape, device)
+    table, M, step = _table(block_table, B, device)
+    tree, tree_step = _tree(parent, B, N, device)
+    out = {} if out is None else out
+    each = torch.Size((B,))
+    if "out" not in out and n_nodes is not None:
+        with torch.cuda.stream(stream):  # no effect for None
+            out["out"] = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    need = lib.spec_tree_attention_workspace(B, N, H, layout.heads, D)
+    space = out.get("workspace")
+    if space is None or space.numel() < need or space.get_device() != device:
+        with torch.cuda.stream(stream):
+            space = out["workspace"] = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.spec_tree_attention(
+        q_ptr, dt, B, N, H, q_request, q_node, q_head, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(layout),
+        table, M, step, _at(seq_lens, "seq_lens", _I32, each, device), tree, tree_step,
+        _at(n_nodes, "n_nodes", _I32, each, device), D ** -0.5 if scale is None else scale,
+        _to(out, "out", q.dtype, q.shape, device, stream), _to(out, "dev_error", _I32, _ONE, device, stream),
+        space.data_ptr(), space.numel(),
+        _handle(stream, device, q, k_cache, v_cache, block_table, seq_lens, parent, n_nodes, *out.values()))
+    if st != SPEC_OK:
+        raise SpecError("spec_tree_attention", st)
+    return out
+
+
+def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, drafted=None, parent=None, n_nodes=None,
+                  repetition=None, frequency=None, presence=None, bias_ids=None, bias_values=None, allowed=None,
+                  out=None, stream=None) -> dict:
+    """``spec_adjust_logits`` on torch tensors: logits [B, R, V] (bf16 or fp32; rows may be slices of a wider buffer);
+    history [B, L] int32 with history_lens and prompt_lens [B] int32; drafted int32 [B, R - 1] (draft_tokens of a
+    linear verification) or [B, R] (node_tokens of a tree's), parent None (a chain), [R] or [B, R], n_nodes [B] int32;
+    repetition, frequency, presence [B] float32; bias_ids int32 and bias_values float32 [B, K]; allowed [B, R, ceil(V /
+    32)] int32, a bit a token.  Returns a dict: logits (out["logits"] may be the tensor itself; by default a new one,
+    in which rows behind a request's nodes are zero), dev_error [1]."""
+    lib = load()
+    dt = _dtype_code(logits)
+    if logits.dim() != 3:
+        raise ValueError(f"logits must have shape [B, R, V], got {tuple(logits.shape)}")
+    _, V, step = _rows(logits, "logits")
+    B, R, device = logits.shape[0], logits.shape[1], logits.get_device()
+    out = {} if out is None else out
+    to = out.get("logits")
+    if to is None:
+        make = torch.empty if n_nodes is None else torch.zeros
+        with torch.cuda.stream(stream):
+            to = out["logits"] = make(logits.shape, dtype=logits.dtype, device=logits.device)
+    if to.dtype is not logits.dtype or to.shape != logits.shape or to.get_device() != device:
+        raise ValueError(f"out logits must be {logits.dtype} of shape {tuple(logits.shape)} on {logits.device}")
+    each = torch.Size((B,))
+    a = Adjustments()
+    if history is not None:
+        if history.dtype is not _I32 or history.dim() != 2 or history.shape[0] != B or history.get_device() != device:
+            raise ValueError(f"history must be {_I32} of shape [{B}, L] on cuda:{device}")
+        if history_lens is None:
+            raise ValueError("history_lens is required with history")
+        a.history_capacity = history.shape[1]
+        a.history_stride = _rows(history, "history")[2] if history.numel() else history.shape[1]
+        a.history = history.data_ptr() or None
+        a.history_lens = _at(history_lens, "history_lens", _I32, each, device)
+        a.prompt_lens = _at(prompt_lens, "prompt_lens", _I32, each, device)
+    if drafted is not None and R > 1:
+        whole = drafted.dim() == 2 and drafted.shape[1] == R
+        a.drafted = _at(drafted, "drafted", _I32, torch.Size((B, R if whole else R - 1)), device)
+        a.drafted_stride = R if whole else R - 1
+        if whole and a.drafted:
+            a.drafted += 4  # node 0's token is the last of the history
+        a.parent, a.parent_stride = _tree(parent, B, R, device)
+    a.n_nodes = _at(n_nodes, "n_nodes", _I32, each, device)
+    a.repetition = _at(repetition, "repetition", _F32, each, device)
+    a.frequency = _at(frequency, "frequency", _F32, each, device)
+    a.presence = _at(presence, "presence", _F32, each, device)
+    if bias_ids is not None:
+        wide = torch.Size((B, bias_ids.shape[-1]))
+        a.bias_ids, a.bias_count = _at(bias_ids, "bias_ids", _I32, wide, device), wide[1]
+        if bias_values is None:
+            raise ValueError("bias_values are required with bias_ids")
+        a.bias_values = _at(bias_values, "bias_values", _F32, wide, device)
+    if allowed is not None:
+        if allowed.dtype is not _I32 or allowed.shape != (B, R, (V + 31) // 32) or allowed.get_device() != device:
+            raise ValueError(f"allowed must be {_I32} of shape {(B, R, (V + 31) // 32)} on cuda:{device}")
+        a.allowed, a.allowed_stride = allowed.data_ptr(), _rows(allowed, "allowed")[2]
+    st = lib.spec_adjust_logits(
+        logits.data_ptr(), dt, B, R, V, step, ctypes.byref(a), to.data_ptr(), _rows(to, "out logits")[2],
+        _to(out, "dev_error", _I32, _ONE, device, stream),
+        _handle(stream, device, logits, history, history_lens, prompt_lens, drafted, parent, n_nodes, repetition,
+                frequency, presence, bias_ids, bias_values, allowed, *out.values()))
+    if st != SPEC_OK:
+        raise SpecError("spec_adjust_logits", st)
+    return out
+
+
+def keep_path(planes, path_nodes, accepted_len, seq_lens, block_table, out=None, stream=None) -> dict:
+    """``spec_keep_path`` on torch tensors: planes, a sequence of caches [blocks, page_size, heads, dim] of one layout
+    and dtype (keys and values of all layers), changed in place; path_nodes [B, W] and accepted_len [B] as verify_tree
+    returns them, seq_lens [B] and block_table [B, max_blocks] as the attention had them.  Returns a dict: dev_error
+    [1]."""
+    lib = load()
+    device = path_nodes.get_device()
+    if path_nodes.dim() != 2:
+        raise ValueError(f"path_nodes must have shape [B, W], got {tuple(path_nodes.shape)}")
+    if not path_nodes.is_cuda:
+        raise ValueError("path_nodes must be a CUDA tensor")
+    B, W = path_nodes.shape
+    planes = list(planes)
+    if not planes:
+        raise ValueError("planes must name at least one cache")
+    head = planes[0]
+    layout = _cache(head, "planes[0]", device)
+    shape, stride, dtype = head.shape, head.stride(), head.dtype
+    for i, t in enumerate(planes):
+        if t.shape != shape or t.stride() != stride or t.dtype is not dtype or t.get_device() != device:
+            raise ValueError(f"planes[{i}] must have the dtype, shape, strides and device of planes[0]")
+    each = torch.Size((B,))
+    table, M, step = _table(block_table, B, device)
+    out = {} if out is None else out
+    st = lib.spec_keep_path(
+        (ctypes.c_void_p * len(planes))(*[t.data_ptr() for t in planes]), len(planes), head.element_size(),
+        ctypes.byref(layout), B, W, _at(path_nodes, "path_nodes", _I32, path_nodes.shape, device),
+        _at(accepted_len, "accepted_len", _I32, each, device), _at(seq_lens, "seq_lens", _I32, each, device), table, M,
+        step, _to(out, "dev_error", _I32, _ONE, device, stream),
+        _handle(stream, device, *planes, path_nodes, accepted_len, seq_lens, block_table, *out.values()))
+    if st != SPEC_OK:
+        raise SpecError("spec_keep_path", st)
     return out
