@@ -1,31 +1,55 @@
 // Attention of drafted nodes over a paged cache (spec_tree_attention).
+#include <type_traits>
+
 #include "../../include/specverify.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace sv {
 
+constexpr int kAtTile = 128;  // cache entries of a tile; query rows of a block
 constexpr int kAtPrepNT = 256;
+constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, a copy warp, a matrix warp, a query warp, a mending warp
+constexpr int kAtMaxCtas = 160;
+constexpr int kMaxAttendHeads = 4096;
+constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
+constexpr uint64_t kAtWaitNs = 2000000000ull;
+#ifndef SV_LATE_ATTEND
+#define SV_LATE_ATTEND false
+#endif
+
+// Query rows of a request and key head h: row i * group + j is head h * group
+// + j of node i.  A CTA takes `blocks` blocks of 128 rows of them (one or two)
+// and a run of tiles.  Work is counted in units: (request, key head, chunk of
+// rows, tile) in this order, shared out evenly among `groups` groups of `share`
+// CTAs; the CTAs of a group take the chunk's row blocks, over the same tiles.
+struct AttendPlan {
+    int blocks, chunks, share, groups;
+};
 
 struct AttendArgs {
     const uint16_t* q;
     int B, N, q_heads, kv_heads, group, dim;
     int64_t q_request, q_node, q_head;
-    const uint16_t *k, *v;
-    int blocks, page;
-    int64_t block_stride, entry_stride, head_stride;
+    int cache_blocks, page, box;  // box: entries of a copy
+    int at_head, at_entry;        // which of the maps' dimensions 1 .. 3 they are (the third is the block)
     const int32_t* table;
     int64_t table_stride, capacity;  // capacity: positions that a table row holds
     const int32_t* lens;
     const int32_t* parent;
     int64_t parent_stride;
     const int32_t* n_nodes;
-    float scale;
+    float c;  // scale * log2(e)
     uint16_t* out;
     int32_t* dev_error;
+    AttendPlan plan;
     // workspace
     int32_t* err;        // [B] error bits of a request: its lengths, later its blocks
     int32_t* tree_err;   // [B], or [1] for a shared tree: error bits of the parent array
+    int32_t* first;      // [B + 1] units before a request
+    int32_t* late;       // [1] SPEC_DEVERR_TIMEOUT
     uint32_t* masks;     // [B or 1][N][mask_words]: bit m of node n's words: n sees node m
+    float* part;         // partial results: [CTA][2][part_floats]
     int mask_words;
 };
 
@@ -41,14 +65,39 @@ __device__ __forceinline__ AttendRequest attend_request(const AttendArgs& a, int
     return r;
 }
 
-// Before the attention: the requests' error words, and which nodes each node
-// of a tree sees.  CTA 0 has the requests, the others a tree each.
+__device__ __forceinline__ int attend_tiles(const AttendRequest& r) {
+    return r.err || r.n == 0 ? 0 : (int)(((int64_t)r.len + r.n + kAtTile - 1) / kAtTile);
+}
+
+// Before the attention: the requests' error words and units, and which nodes
+// each node of a tree sees.  CTA 0 has the requests, the others a tree each.
 __global__ void __launch_bounds__(kAtPrepNT) k_attend_prepare(AttendArgs a) {
     __shared__ int32_t sh_parent[kMaxDraftNodes];
+    __shared__ int sh_part[kAtPrepNT / 32];
     rows_begin();
     const int tid = threadIdx.x;
     if (blockIdx.x == 0) {
-        for (int b = tid; b < a.B; b += kAtPrepNT) a.err[b] = attend_request(a, b).err;
+        const int each = (a.B + kAtPrepNT - 1) / kAtPrepNT, b0 = min(tid * each, a.B), b1 = min(b0 + each, a.B);
+        const int times = a.kv_heads * a.plan.chunks;
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) {
+            const AttendRequest r = attend_request(a, b);
+            a.err[b] = r.err;
+            sum += attend_tiles(r) * times;
+        }
+        const int upto = warp_inclusive_scan_i(sum);
+        if ((tid & 31) == 31) sh_part[tid >> 5] = upto;
+        __syncthreads();
+        int at = upto - sum;
+        for (int w = 0; w < (tid >> 5); ++w) at += sh_part[w];
+        for (int b = b0; b < b1; ++b) {
+            a.first[b] = at;
+            at += attend_tiles(attend_request(a, b)) * times;
+        }
+        if (tid == kAtPrepNT - 1) {
+            a.first[a.B] = at;
+            *a.late = 0;
+        }
         return;
     }
     const int t = blockIdx.x - 1;
@@ -71,122 +120,794 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_prepare(AttendArgs a) {
     }
 }
 
-// One CTA per query row; a warp takes every fourth entry.
-template <typename T>
-__global__ void __launch_bounds__(128) k_attend_rows(AttendArgs a) {
-    __shared__ float sh_m[4], sh_l[4], sh_o[4][128];
-    rows_begin();
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int h = blockIdx.x % a.q_heads, n = blockIdx.x / a.q_heads % a.N, b = blockIdx.x / a.q_heads / a.N;
-    const AttendRequest r = attend_request(a, b);
-    const int tree = a.parent_stride ? b : 0;
-    if (r.err || n >= r.n || (a.parent && a.tree_err[tree])) return;
-    const uint16_t* q = a.q + b * a.q_request + n * a.q_node + h * a.q_head;
-    const uint32_t* mask = a.masks + ((int64_t)tree * a.N + n) * a.mask_words;
-    float x[4], o[4] = {}, m = -INFINITY, l = 0.0f;
-    auto get = [](uint16_t v) { return Pair<T>::get(v).x; };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < a.dim ? get(q[lane + 32 * i]) : 0.0f;
-    for (int t = w; t < r.len + r.n; t += 4) {
-        if (t >= r.len) {
-            const int node = t - r.len;
-            if (a.parent ? !((mask[node >> 5] >> (node & 31)) & 1u) : node > n) continue;
+// A run of tiles of one (request, key head, row blocks of this CTA).
+struct AttendItem {
+    int b, len, n, head;
+    int row0, rows;  // this CTA's first row, and how many of its rows there are
+    int t0, t1, tiles;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    __device__ __forceinline__ bool masked(int t) const { return (t + 1) * (int64_t)kAtTile > len; }
+};
+// Groups that have units: as many as there are units, if those are fewer.
+__device__ __forceinline__ int attend_groups(const AttendArgs& a, int64_t units) {
+    return units < a.plan.groups ? max((int)units, 1) : a.plan.groups;
+}
+// The items of a CTA, one after the other; every role walks them for itself.
+struct AttendWalk {
+    int u, u1, b, start, next, share;
+    AttendRequest r;
+    int tiles;
+    __device__ __forceinline__ void request(const AttendArgs& a) {
+        r = attend_request(a, b);
+        tiles = attend_tiles(r);
+    }
+    // b0: the request of unit u0 (any value when there are no units)
+    __device__ __forceinline__ AttendWalk(const AttendArgs& a, int u0, int end, int b0) : u(u0), u1(end), b(b0) {
+        share = blockIdx.x % a.plan.share;
+        if (u >= u1) return;
+        start = a.first[b];
+        next = a.first[b + 1];
+        request(a);
+    }
+    __device__ __forceinline__ bool item(const AttendArgs& a, AttendItem* x) {
+        while (u < u1) {
+            if (u >= next) {
+                do {
+                    ++b;
+                    start = next;
+                    next = a.first[b + 1];
+                } while (u >= next);
+                request(a);
+            }
+            const int at = u - start, i = at / tiles;
+            x->t0 = at - i * tiles;
+            x->t1 = min(tiles, x->t0 + (u1 - u));
+            u += x->t1 - x->t0;
+            x->head = i / a.plan.chunks;
+            const int rows = a.plan.blocks * kAtTile;
+            x->row0 = ((i - x->head * a.plan.chunks) * a.plan.share + share) * rows;
+            x->rows = min(r.n * a.group - x->row0, rows);
+            if (x->rows <= 0) continue;  // a request of fewer nodes than N
+            x->b = b;
+            x->len = r.len;
+            x->n = r.n;
+            x->tiles = tiles;
+            return true;
         }
-        const int block = a.table[b * a.table_stride + t / a.page];
-        if (block < 0 || block >= a.blocks) {
-            if (lane == 0) atomicOr(a.err + b, kDevErrCapacity);
+        return false;
+    }
+};
+
+template <int DT> struct AttendShape {
+    static constexpr int kTileBytes = kAtTile * DT * 2;      // 128 entries (or rows) of DT 16-bit values
+    static constexpr int kBlockBytes = kAtTile * 128;        // 64 of their columns
+    static constexpr int kStages = 5 * 128 / DT;             // 160 KiB of keys and values
+    static constexpr int kQueryBytes = 2 * kTileBytes;       // two blocks, or two turns of one
+    static constexpr int kTiles = kQueryBytes + kStages * kTileBytes;
+};
+struct AttendCtrl {
+    uint64_t full[10], empty[10], mend[10], mended[10];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], ml_full, read, drain;
+    uint32_t poison[10][4];
+    float2 ml[2][kAtTile];
+    uint32_t tmem;
+    int b0;
+    volatile int dead;
+};
+template <int DT> constexpr size_t kAttendSmem = AttendShape<DT>::kTiles + sizeof(AttendCtrl);
+static_assert(kAttendSmem<128> <= 232448 && kAttendSmem<64> <= 232448, "a CTA's shared memory");
+
+// A wait of one thread; false once it, or another of the CTA's, has run out.
+__device__ __noinline__ bool attend_wait_long(AttendCtrl* c, uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_test(bar, parity)) {
+        if (c->dead) return false;
+        if (global_ns() - t0 > kAtWaitNs) {
+            c->dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool attend_wait(AttendCtrl* c, uint64_t* bar, uint32_t parity) {
+    if (SV_LATE_ATTEND) {
+        c->dead = 1;
+        return false;
+    }
+    return mbar_test(bar, parity) || attend_wait_long(c, bar, parity);
+}
+__device__ __forceinline__ bool attend_wait_warp(AttendCtrl* c, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, attend_wait(c, bar, parity));
+}
+__device__ __forceinline__ void attend_arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bit i: whether a node sees position base + i of those behind the sequence
+// (base < 0: the sequence's own, which every node sees).
+__device__ __forceinline__ uint32_t attend_sees(const AttendArgs& a, const uint32_t* mask, int node, int base) {
+    if (base <= -32) return 0xffffffffu;
+    if (!a.parent) {
+        const int upto = node - base + 1;
+        return upto >= 32 ? 0xffffffffu : upto <= 0 ? 0u : (1u << upto) - 1u;
+    }
+    auto word = [&](int i) { return i < a.mask_words ? mask[i] : 0u; };
+    if (base < 0) return ((1u << -base) - 1u) | (word(0) << -base);
+    return __funnelshift_r(word(base >> 5), word((base >> 5) + 1), base & 31);
+}
+
+// The copy warp: keys and values of each tile into the ring, the tile's pages
+// one by one.  Blocks behind the last position are not looked up: the copy
+// reads outside the cache there, which gives zeros.
+template <int DT>
+__device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* km, const CUtensorMap* vm,
+                                            AttendWalk walk, AttendCtrl* c, uint32_t ring) {
+    using S = AttendShape<DT>;
+    const int lane = threadIdx.x & 31, boxes = kAtTile / a.box;
+    AttendItem x;
+    int issued = 0;
+    bool ok = true;
+    while (ok && walk.item(a, &x)) {
+        for (int t = x.t0; ok && t < x.t1; ++t) {
+            int block[4], entry[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = lane + 32 * k;
+                const int64_t at = (int64_t)t * kAtTile + i * a.box;
+                block[k] = a.cache_blocks;
+                entry[k] = 0;
+                if (i < boxes && at < (int64_t)x.len + x.n) {
+                    const int64_t j = at / a.page;
+                    block[k] = a.table[x.b * a.table_stride + j];
+                    entry[k] = (int)(at - j * a.page);
+                    if (block[k] < 0 || block[k] >= a.cache_blocks) {
+                        atomicOr(a.err + x.b, kDevErrCapacity);
+                        block[k] = a.cache_blocks;
+                    }
+                }
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slot = issued % S::kStages, use = issued / S::kStages;
+                if (use > 0 && !attend_wait_warp(c, &c->empty[slot], (use - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], S::kTileBytes);
+                __syncwarp();
+                const uint32_t to = ring + slot * S::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = lane + 32 * k;
+                    if (i >= boxes) continue;
+                    auto at = [&](int dim) { return dim == a.at_head ? x.head : dim == a.at_entry ? entry[k] : block[k]; };
+                    const int c1 = at(1), c2 = at(2), c3 = at(3);
+#pragma unroll
+                    for (int d = 0; d < DT / 64; ++d)
+                        tma_load_4d(to + d * S::kBlockBytes + i * a.box * 128, kv ? vm : km, d * 64, c1, c2, c3,
+                                    &c->full[slot]);
+                }
+                if (kv && lane == 0 && x.masked(t)) mbar_arrive(&c->mend[slot]);
+                ++issued;
+            }
+        }
+    }
+    // nothing is on its way into shared memory when the CTA ends
+    for (int i = max(0, issued - S::kStages); i < issued; ++i)
+        mbar_wait(&c->full[i % S::kStages], (i / S::kStages) & 1, kDrainNs);
+    __syncwarp();
+}
+
+// The matrix thread.  Stream w: the products with S, P and O of warpgroup w.
+// NB = 2: both streams take every tile, each for its own block of rows.
+// NB = 1: the streams take turns.  S of a stream's next tile follows its
+// product with the values of the tile before, so a warpgroup's softmax runs
+// beside the other stream's products.
+template <typename T, int DT, int NB>
+__device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t queries,
+                                                uint32_t ring, uint32_t tmem) {
+    using S = AttendShape<DT>;
+    constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+    constexpr uint32_t kScores = mma_shape<kBf16>(kAtTile, false), kValues = mma_shape<kBf16>(DT, true);
+    constexpr int kTurns = NB == 1 ? 2 : 1;  // query buffers
+    AttendItem x;
+    int J = 0, qi = 0;
+    uint32_t mended = 0;            // parity of each slot's next mending
+    uint32_t weights[2] = {0, 0};   // parity of p_full
+    bool ok = true;
+    // O_w (+)= P_w V of tile t, the J-th; `last` stream of the tile gives the slot back
+    auto product = [&](int w, int t, int j, bool add, bool wait_values, bool last) {
+        const int index = 2 * j + 1, slot = index % S::kStages;
+        if (wait_values) {
+            if (!attend_wait(c, &c->full[slot], (index / S::kStages) & 1)) return false;
+            if (x.masked(t)) {
+                if (!attend_wait(c, &c->mended[slot], (mended >> slot) & 1u)) return false;
+                mended ^= 1u << slot;
+            }
+        }
+        if (!attend_wait(c, &c->p_full[w], weights[w])) return false;
+        weights[w] ^= 1u;
+        tmem_fence_after();
+        const uint32_t v = ring + slot * S::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kAtTile / 16; ++k)
+            mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, mma_operand(v + k * 2048, S::kBlockBytes), kValues,
+                       add || k > 0);
+        if (last) mma_commit(&c->empty[slot]);
+        return true;
+    };
+    auto scores = [&](int w, uint32_t q, uint32_t k0) {
+#pragma unroll
+        for (int k = 0; k < DT / 16; ++k) {
+            const uint32_t at = (k / 4) * S::kBlockBytes + (k % 4) * 32;
+            mma_shared(tmem + w * 128, mma_operand(q + at, 16), mma_operand(k0 + at, 16), kScores, k > 0);
+        }
+        mma_commit(&c->s_full[w]);
+    };
+    while (ok && walk.item(a, &x)) {
+        const int turn = qi % kTurns;
+        if (!attend_wait(c, &c->q_full[turn], (qi / kTurns) & 1)) break;
+        ++qi;
+        tmem_fence_after();
+        const uint32_t q = queries + (NB == 1 ? turn * S::kTileBytes : 0);
+        const int n = x.t1 - x.t0, streams = NB == 2 && x.rows > kAtTile ? 2 : 1;
+        for (int j = 0; ok && j < n; ++j) {
+            const int index = 2 * (J + j), slot = index % S::kStages;
+            if (!attend_wait(c, &c->full[slot], (index / S::kStages) & 1)) {
+                ok = false;
+                break;
+            }
+            const uint32_t k0 = ring + slot * S::kTileBytes;
+            if (NB == 1) {
+                if (j >= 2) ok = product(j & 1, x.t0 + j - 2, J + j - 2, j >= 4, true, true);
+                if (ok) scores(j & 1, q, k0);
+            } else {
+                for (int w = 0; ok && w < streams; ++w) {
+                    if (j >= 1) ok = product(w, x.t0 + j - 1, J + j - 1, j >= 2, w == 0, w == streams - 1);
+                    if (ok) scores(w, q + w * S::kTileBytes, k0);
+                }
+            }
+            if (ok) mma_commit(&c->empty[slot]);
+        }
+        if (!ok) break;
+        mma_commit(&c->q_empty[turn]);
+        if (NB == 1) {
+            for (int j = max(0, n - 2); ok && j < n; ++j) {
+                ok = product(j & 1, x.t0 + j, J + j, j >= 2, true, true);
+                if (ok) mma_commit(&c->o_full[j & 1]);
+            }
+        } else {
+            for (int w = 0; ok && w < streams; ++w) {
+                ok = product(w, x.t1 - 1, J + n - 1, n >= 2, w == 0, w == streams - 1);
+                if (ok) mma_commit(&c->o_full[w]);
+            }
+        }
+        J += n;
+    }
+    // no product is on its way when tensor memory is freed
+    mma_commit(&c->drain);
+    mbar_wait(&c->drain, 0, kDrainNs);
+}
+
+// The query warp: rows of an item's queries, swizzled as a copy would.
+template <int DT, int NB>
+__device__ __forceinline__ void attend_queries(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t queries) {
+    using S = AttendShape<DT>;
+    constexpr int kTurns = NB == 1 ? 2 : 1, kChunks = DT / 8;
+    const int lane = threadIdx.x & 31;
+    AttendItem x;
+    for (int qi = 0; walk.item(a, &x); ++qi) {
+        const int turn = qi % kTurns, use = qi / kTurns;
+        if (use > 0 && !attend_wait_warp(c, &c->q_empty[turn], (use - 1) & 1)) break;
+        const uint32_t to = queries + (NB == 1 ? turn * S::kTileBytes : 0);
+        const uint16_t* from = a.q + x.b * a.q_request + (int64_t)x.head * a.group * a.q_head;
+        const int chunk = lane % kChunks;
+        for (int row = lane / kChunks; row < x.rows; row += 32 / kChunks) {
+            const int r = x.row0 + row, node = r / a.group;
+            const uint16_t* at = from + node * a.q_node + (r - node * a.group) * a.q_head + chunk * 8;
+            const uint32_t dst = to + (row / kAtTile) * S::kTileBytes + (chunk / 8) * S::kBlockBytes +
+                                 (row % kAtTile) * 128 + (((chunk % 8) ^ (row % 8)) * 16);
+            const int bytes = chunk * 8 < a.dim ? 16 : 0;  // columns behind the head's end are zero
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(bytes ? at : from), "r"(bytes)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_shared();
+        attend_arrive_warp(&c->q_full[turn]);
+    }
+}
+
+// The mending warp: in tiles that reach behind the sequence, values that no
+// product may meet.  A weight of zero does not hide an infinity or a NaN, so
+// entries behind the last node, and nodes' entries that are not finite, become
+// zeros; the latter's places are told to the softmax, which makes the rows
+// that see them NaN.
+template <typename T, int DT>
+__device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint8_t* ring) {
+    using S = AttendShape<DT>;
+    const int lane = threadIdx.x & 31;
+    AttendItem x;
+    int J = 0;
+    uint32_t parity = 0;  // of each slot's next tile to mend
+    while (walk.item(a, &x)) {
+        for (int t = x.t0; t < x.t1; ++t, ++J) {
+            if (!x.masked(t)) continue;
+            // This warp does not follow the ring.  Once the copy warp has named
+            // the slot, its turn cannot end before it is mended.
+            const int index = 2 * J + 1, slot = index % S::kStages;
+            if (!attend_wait_warp(c, &c->mend[slot], (parity >> slot) & 1u)) return;
+            parity ^= 1u << slot;
+            if (!attend_wait_warp(c, &c->full[slot], (index / S::kStages) & 1)) return;
+#pragma unroll 1
+            for (int k = 0; k < kAtTile / 32; ++k) {
+                const int row = k * 32 + lane;
+                const int64_t node = (int64_t)t * kAtTile + row - x.len;
+                bool bad = false;
+                uint8_t* at = ring + slot * S::kTileBytes + row * 128;
+                if (node >= 0 && node < x.n) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < DT / 8; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(at + (i / 8) * S::kBlockBytes +
+                                                                        (((i % 8) ^ (row % 8)) * 16));
+                        // 0 times an infinity or a NaN is NaN
+                        const float2 p = Pair<T>::get(v.x), q = Pair<T>::get(v.y), r = Pair<T>::get(v.z),
+                                     s = Pair<T>::get(v.w);
+                        sum += (p.x * 0.0f + p.y * 0.0f) + (q.x * 0.0f + q.y * 0.0f) + (r.x * 0.0f + r.y * 0.0f) +
+                               (s.x * 0.0f + s.y * 0.0f);
+                    }
+                    bad = sum != 0.0f;
+                }
+                if (bad || node >= x.n) {
+#pragma unroll
+                    for (int i = 0; i < DT / 8; ++i)
+                        *reinterpret_cast<uint4*>(at + (i / 8) * S::kBlockBytes + (((i % 8) ^ (row % 8)) * 16)) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                const uint32_t all = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) c->poison[slot][k] = all;
+            }
+            fence_async_shared();
+            attend_arrive_warp(&c->mended[slot]);
+        }
+    }
+}
+
+// A warpgroup of the softmax: a thread has a query row.  The scores of a tile
+// come from tensor memory, the weights go back over them in 16 bits.  The
+// reference of the exponentials follows the running maximum only when that has
+// grown by more than 8 (in powers of two), so that O is rarely scaled; sums and
+// outputs stay in 32 bits.
+template <typename T, int DT, int NB>
+__device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t tmem) {
+    using S = AttendShape<DT>;
+    const int w = threadIdx.x >> 7, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int row = quarter * 32 + lane;  // of the block
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_at = tmem + lanes + w * 128;
+    uint32_t scored = 0, done[2] = {0, 0}, met = 0, mended = 0;  // parities
+    int J = 0;
+    AttendItem x;
+    while (walk.item(a, &x)) {
+        const int n = x.t1 - x.t0, block0 = NB == 2 ? w * kAtTile : 0;
+        if (NB == 2 && x.rows <= block0) {  // the second block is empty
+            for (int t = x.t0; t < x.t1; ++t, ++J)
+                if (x.masked(t)) mended ^= 1u << ((2 * J + 1) % S::kStages);
             continue;
         }
-        const int64_t at = block * a.block_stride + (t % a.page) * a.entry_stride + (h / a.group) * a.head_stride;
-        float dot = 0.0f;
+        const bool live = quarter * 32 < x.rows - block0;  // this warp has a row
+        const int r = min(x.row0 + block0 + row, x.n * a.group - 1), node = r / a.group;
+        const uint32_t* mask =
+            a.parent ? a.masks + ((int64_t)(a.parent_stride ? x.b : 0) * a.N + node) * a.mask_words : nullptr;
+        float m = kNoMax;
+        float2 l = make_float2(0.0f, 0.0f);
+        bool begun = false;
+        for (int t = x.t0; t < x.t1; ++t, ++J) {
+            const bool masked = x.masked(t);
+            const int slot = (2 * J + 1) % S::kStages;
+            const uint32_t mend_parity = (mended >> slot) & 1u;
+            if (masked) mended ^= 1u << slot;
+            if (NB == 1 && ((t - x.t0) & 1) != w) continue;
+            if (!attend_wait_warp(c, &c->s_full[w], scored)) return;
+            scored ^= 1u;
+            tmem_fence_after();
+            if (live) {
+                float s[kAtTile];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) dot += x[i] * get(a.k[at + lane + 32 * i]);
+                for (int i = 0; i < 4; ++i) tmem_load32(s_at + i * 32, reinterpret_cast<uint32_t*>(s) + i * 32);
+                tmem_wait_load();
+                if (masked) {
+                    if (!attend_wait_warp(c, &c->mended[slot], mend_parity)) return;
 #pragma unroll
-        for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        dot *= a.scale;
-        const float top = fmaxf(m, dot);
-        const float down = top > m ? expf(m - top) : 1.0f, e = expf(dot - top);
-        m = top;
-        l = l * down + e;
-        bool bad = false;
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t base = (int64_t)t * kAtTile + i * 32 - x.len;
+                        const uint32_t sees = attend_sees(a, mask, node, base < -32 ? -32 : (int)base);
+                        if (sees & c->poison[slot][i]) l.x = NAN;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) {
-                const float v = get(a.v[at + lane + 32 * i]);
-                o[i] = o[i] * down + e * v;
-                bad = bad || !(fabsf(v) < INFINITY);
+                        for (int k = 0; k < 32; ++k) s[i * 32 + k] = (sees >> k) & 1u ? s[i * 32 + k] : -INFINITY;
+                    }
+                }
+                float top[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i] = s[i];
+#pragma unroll
+                for (int i = 4; i < kAtTile; i += 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], i + k + 4 < kAtTile ? fmaxf(s[i + k], s[i + k + 4]) : s[i + k]);
+                }
+                const float most = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+                const bool grows = (most - m) * a.c > 8.0f;
+                if (__any_sync(0xffffffffu, grows)) {
+                    const float f = grows ? exp2_fast((m - most) * a.c) : 1.0f;
+                    if (grows) m = most;
+                    l.x *= f;
+                    l.y *= f;
+                    if (begun) {
+                        const uint32_t o_at = tmem + lanes + 256 + w * DT;
+#pragma unroll 1
+                        for (int i = 0; i < DT / 32; ++i) {
+                            uint32_t o[32];
+                            tmem_load32(o_at + i * 32, o);
+                            tmem_wait_load();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_store32(o_at + i * 32, o);
+                        }
+                    }
+                }
+                // nothing seen yet: every score is -inf, and so is its exponent
+                const float off = m == kNoMax ? 0.0f : -m * a.c;
+                const float2 cc = make_float2(a.c, a.c), oo = make_float2(off, off);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float2 e = __ffma2_rn(make_float2(s[i * 32 + 2 * k], s[i * 32 + 2 * k + 1]), cc, oo);
+                        e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                        l = __fadd2_rn(l, e);
+                        p[k] = Pair<T>::put(e.x, e.y);
+                    }
+                    tmem_store16(s_at + i * 16, p);
+                }
+                tmem_wait_store();
             }
-        if (t >= r.len && __any_sync(0xffffffffu, bad)) l = NAN;  // a node's entry that is not finite
-    }
-    if (lane == 0) {
-        sh_m[w] = m;
-        sh_l[w] = l;
-    }
+            begun = true;
+            tmem_fence_before();
+            attend_arrive_warp(&c->p_full[w]);
+        }
+        // the item's end
+        float total = l.x + l.y;
+        float f0 = 1.0f, f1 = 0.0f;  // factors of the streams' outputs
+        const bool both = NB == 1 && n >= 2;
+        if (NB == 1) {
+            c->ml[w][row] = make_float2(m, total);
+            attend_arrive_warp(&c->ml_full);
+            if (!attend_wait_warp(c, &c->ml_full, met)) return;
+            const float2 p = c->ml[0][row], q = c->ml[1][row];
+            m = fmaxf(p.x, q.x);
+            f0 = exp2_fast((p.x - m) * a.c);
+            f1 = both ? exp2_fast((q.x - m) * a.c) : 0.0f;
+            total = p.y * f0 + (both ? q.y * f1 : 0.0f);
+        }
+        if (NB == 1) {
+            if (!attend_wait_warp(c, &c->o_full[0], done[0])) return;
+            done[0] ^= 1u;
+            if (both) {
+                if (!attend_wait_warp(c, &c->o_full[1], done[1])) return;
+                done[1] ^= 1u;
+            }
+        } else {
+            if (!attend_wait_warp(c, &c->o_full[w], done[0])) return;
+            done[0] ^= 1u;
+        }
+        tmem_fence_after();
+        if (live) {
+            const bool there = row < x.rows - block0;
+            constexpr int kCols = NB == 1 ? DT / 2 : DT;  // of this thread
+            const int col0 = NB == 1 ? w * kCols : 0, rows = NB * kAtTile, at_row = block0 + row;
+            const uint32_t o_at = tmem + lanes + 256 + (NB == 2 ? w * DT : 0);
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + (x.t0 == 0 ? 1 : 0)) * (rows * (DT + 2));
+            if (!x.whole() && there && (NB == 2 || w == 0))
+                reinterpret_cast<float2*>(part)[at_row] = make_float2(m, total);
+            float4* part_o = reinterpret_cast<float4*>(part + 2 * rows) + at_row;
+            const float inv = 1.0f / total;
+            uint16_t* out = a.out + (((int64_t)x.b * a.N + node) * a.q_heads + x.head * a.group + (r - node * a.group)) * a.dim;
+#pragma unroll 1
+            for (int i = 0; i < kCols / 32; ++i) {
+                const int col = col0 + i * 32;
+                float o[32];
+                tmem_load32(o_at + col, reinterpret_cast<uint32_t*>(o));
+                if (NB == 1) {
+                    float o1[32];
+                    if (both) tmem_load32(o_at + DT + col, reinterpret_cast<uint32_t*>(o1));
+                    tmem_wait_load();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sh_o[w][lane + 32 * i] = o[i];
-    __syncthreads();
-    const float top = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3]));
-    float sum = 0.0f, value = 0.0f;
-    for (int i = 0; i < 4; ++i) {
-        const float e = sh_m[i] == -INFINITY ? 0.0f : expf(sh_m[i] - top);
-        if (e == 0.0f) continue;
-        sum += e * sh_l[i];
-        value += e * sh_o[i][tid];
+                    for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + (both ? o1[k] * f1 : 0.0f);
+                } else {
+                    tmem_wait_load();
+                }
+                if (!there) continue;
+                if (x.whole()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (col + k * 8 >= a.dim) break;
+                        uint4 v;
+                        v.x = Pair<T>::put(o[k * 8] * inv, o[k * 8 + 1] * inv);
+                        v.y = Pair<T>::put(o[k * 8 + 2] * inv, o[k * 8 + 3] * inv);
+                        v.z = Pair<T>::put(o[k * 8 + 4] * inv, o[k * 8 + 5] * inv);
+                        v.w = Pair<T>::put(o[k * 8 + 6] * inv, o[k * 8 + 7] * inv);
+                        *reinterpret_cast<uint4*>(out + col + k * 8) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        part_o[(col / 4 + k) * rows] = make_float4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
+                }
+            }
+        }
+        if (NB == 1) {
+            // the other warpgroup's next weights let its O be written again
+            tmem_fence_before();
+            attend_arrive_warp(&c->read);
+            if (!attend_wait_warp(c, &c->read, met)) return;
+            met ^= 1u;
+        }
     }
-    if (tid < a.dim)
-        a.out[(((int64_t)b * a.N + n) * a.q_heads + h) * a.dim + tid] = (uint16_t)Pair<T>::put(value / sum, 0.0f);
 }
 
-// After the attention: refused requests get their zeros, and the error word
-// what was found.
-__global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(AttendArgs a) {
+template <typename T, int DT, int NB>
+__global__ void __launch_bounds__(kAtNT, 1)
+    k_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap km,
+             const __grid_constant__ CUtensorMap vm) {
+    using S = AttendShape<DT>;
+    extern __shared__ __align__(1024) uint8_t sh_attend[];
+    AttendCtrl* c = reinterpret_cast<AttendCtrl*>(sh_attend + S::kTiles);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&c->full[i], 1);
+            mbar_init(&c->empty[i], 1);
+            mbar_init(&c->mend[i], 1);
+            mbar_init(&c->mended[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->q_full[i], 1);
+            mbar_init(&c->q_empty[i], 1);
+            mbar_init(&c->s_full[i], 1);
+            mbar_init(&c->p_full[i], 4);  // warps of a warpgroup
+            mbar_init(&c->o_full[i], 1);
+        }
+        mbar_init(&c->ml_full, 8);
+        mbar_init(&c->read, 8);
+        mbar_init(&c->drain, 1);
+        c->dead = 0;
+        c->b0 = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&km);
+        tma_prefetch_map(&vm);
+    }
+    if (warp == 8) tmem_alloc_all(&c->tmem);
+    rows_begin();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = c->tmem, queries = smem_addr(sh_attend), ring = queries + S::kQueryBytes;
+    const int64_t units = a.first[a.B];
+    const int g = blockIdx.x / a.plan.share;
+    const int groups = attend_groups(a, units);
+    const int u0 = (int)(units * min(g, groups) / groups), u1 = (int)(units * min(g + 1, groups) / groups);
+    if (u0 < u1)
+        for (int b = tid; b < a.B; b += kAtNT)
+            if (a.first[b] <= u0 && u0 < a.first[b + 1]) c->b0 = b;
+    __syncthreads();
+    const AttendWalk walk(a, u0, u1, c->b0);
+    if (warp < 8) {
+        attend_softmax<T, DT, NB>(a, walk, c, tmem);
+    } else if (warp == 8) {
+        attend_copy<DT>(a, &km, &vm, walk, c, ring);
+    } else if (warp == 9) {
+        if ((tid & 31) == 0) attend_products<T, DT, NB>(a, walk, c, queries, ring, tmem);
+        __syncwarp();
+    } else if (warp == 10) {
+        attend_queries<DT, NB>(a, walk, c, queries);
+    } else {
+        attend_mend<T, DT>(a, walk, c, sh_attend + S::kQueryBytes);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (tid == 0 && c->dead) *a.late = kDevErrTimeout;
+    if (warp == 8) {
+        tmem_fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// The group that has a unit.
+__device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int groups) {
+    return (int)(((unit + 1) * groups - 1) / units);
+}
+
+// Joins the results of items that several groups shared: a CTA per request, key
+// head and block of 128 rows.
+template <typename T, int DT, int NB>
+__device__ __forceinline__ void attend_join(const AttendArgs& a, int index) {
+    const int per = a.plan.chunks * a.plan.share * NB;  // row blocks of a request's head
+    const int b = index / (a.kv_heads * per), head = index / per % a.kv_heads, block = index % per;
+    const AttendRequest r = attend_request(a, b);
+    const int tiles = attend_tiles(r), row0 = block * kAtTile, rows = min(r.n * a.group - row0, kAtTile);
+    if (tiles == 0 || rows <= 0) return;
+    const int pair = block / NB, chunk = pair / a.plan.share, share = pair % a.plan.share;
+    const int64_t units = a.first[a.B], begin = a.first[b] + (int64_t)(head * a.plan.chunks + chunk) * tiles;
+    const int groups = attend_groups(a, units);
+    const int g0 = attend_group(begin, units, groups), g1 = attend_group(begin + tiles - 1, units, groups);
+    if (g0 == g1) return;
+    constexpr int R = NB * kAtTile;
+    // the first group's part is the end of its run, the others' the beginning of theirs
+    auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.share + share) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
+    for (int i = threadIdx.x; i < rows * (a.dim / 4); i += kAtPrepNT) {
+        const int row = i % rows, d = i / rows, at = (block % NB) * kAtTile + row;
+        float m = kNoMax;
+        for (int g = g0; g <= g1; ++g) m = fmaxf(m, reinterpret_cast<const float2*>(part(g))[at].x);
+        float l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int g = g0; g <= g1; ++g) {
+            const float* p = part(g);
+            const float2 ml = reinterpret_cast<const float2*>(p)[at];
+            const float f = exp2f((ml.x - m) * a.c);
+            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + at];
+            l += f * ml.y;
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+        }
+        const int q = row0 + row, node = q / a.group;
+        uint2 v;
+        v.x = Pair<T>::put(o.x / l, o.y / l);
+        v.y = Pair<T>::put(o.z / l, o.w / l);
+        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node) * a.q_heads + head * a.group + (q - node * a.group)) * a.dim +
+                                  d * 4) = v;
+    }
+}
+
+// After the attention: joins, refused requests' zeros, and what was found.  The
+// first CTAs have a request's zeros or the error word, the others join.
+template <typename T, int DT, int NB>
+__global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_constant__ AttendArgs a) {
+    __shared__ int sh_err;
     rows_begin();
     const int tid = threadIdx.x;
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        int err = a.err[b];
-        if (a.parent) err |= a.tree_err[a.parent_stride ? b : 0];
-        if (!err) continue;
+    auto err_of = [&](int b) { return a.err[b] | (a.parent ? a.tree_err[a.parent_stride ? b : 0] : 0); };
+    if (blockIdx.x > 0) {
+        const int index = blockIdx.x - 1, b = index / (a.kv_heads * a.plan.chunks * a.plan.share * NB);
+        const int err = err_of(b);
+        if (!err) {
+            attend_join<T, DT, NB>(a, index);
+            return;
+        }
+        // the CTAs of a refused request share its zeros
         const AttendRequest r = attend_request(a, b);
-        const int n = r.n < 0 || r.n > a.N ? a.N : r.n;
-        const int64_t each = (int64_t)a.q_heads * a.dim;
-        for (int64_t i = tid; i < n * each; i += kAtPrepNT) a.out[(int64_t)b * a.N * each + i] = 0;
+        const int n = r.n < 0 || r.n > a.N ? a.N : r.n, ctas = a.kv_heads * a.plan.chunks * a.plan.share * NB;
+        const int64_t each = (int64_t)a.q_heads * a.dim / 8;
+        uint4* out = reinterpret_cast<uint4*>(a.out) + (int64_t)b * a.N * each;
+        for (int64_t i = (int64_t)(index - b * ctas) * kAtPrepNT + tid; i < n * each; i += (int64_t)ctas * kAtPrepNT)
+            out[i] = make_uint4(0, 0, 0, 0);
+        return;
     }
-    if (blockIdx.x == 0 && a.dev_error) {
-        int err = 0;
-        for (int b = tid; b < a.B; b += kAtPrepNT) err |= a.err[b];
-        if (a.parent)
-            for (int t = tid; t < (a.parent_stride ? a.B : 1); t += kAtPrepNT) err |= a.tree_err[t];
-        __shared__ int all;
-        if (tid == 0) all = 0;
-        __syncthreads();
-        if (err) atomicOr(&all, err);
-        __syncthreads();
-        if (tid == 0) *a.dev_error = all;
-    }
+    if (!a.dev_error) return;
+    if (tid == 0) sh_err = *a.late;
+    __syncthreads();
+    int err = 0;
+    for (int b = tid; b < a.B; b += kAtPrepNT) err |= err_of(b);
+    if (err) atomicOr(&sh_err, err);
+    __syncthreads();
+    if (tid == 0) *a.dev_error = sh_err;
 }
 
+static AttendPlan attend_plan(int N, int group, int ctas) {
+    AttendPlan p;
+    const int64_t rows = (int64_t)N * group;
+    p.blocks = rows > kAtTile ? 2 : 1;
+    const int parts = (int)((rows + p.blocks * kAtTile - 1) / (p.blocks * kAtTile));
+    p.chunks = (parts + kAtShare - 1) / kAtShare;
+    p.share = (parts + p.chunks - 1) / p.chunks;
+    p.groups = ctas / p.share;
+    return p;
+}
 struct AttendSpace {
-    size_t err, tree_err, masks, total;
+    size_t err, tree_err, first, late, masks, part, total;
 };
-static AttendSpace attend_space(int B, int N) {
+static AttendSpace attend_space(int B, int N, int group, int dim) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     AttendSpace s;
     s.err = 0;
     s.tree_err = up((size_t)B * 4);
-    s.masks = s.tree_err + up((size_t)B * 4);
-    s.total = s.masks + up((size_t)B * N * ((N + 31) / 32) * 4);
+    s.first = s.tree_err + up((size_t)B * 4);
+    s.late = s.first + up(((size_t)B + 1) * 4);
+    s.masks = s.late + 256;
+    s.part = s.masks + up((size_t)B * N * ((N + 31) / 32) * 4);
+    const int rows = attend_plan(N, group, kAtMaxCtas).blocks * kAtTile, cols = dim > 64 ? 128 : 64;
+    s.total = s.part + (size_t)kAtMaxCtas * 2 * rows * (cols + 2) * 4;
     return s;
 }
 
-template <typename T>
-static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+// The map of a cache: dim innermost, then heads, entries and blocks by stride;
+// boxes of 64 values of `box` entries.  false: the driver refuses it.
+struct AttendMapOrder {
+    int head, entry;
+};
+static bool attend_map(CUtensorMap* map, const void* base, bool bf16, const spec_cache_layout* l, int box,
+                       AttendMapOrder* order) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    struct Dim {
+        cuuint64_t size;
+        int64_t stride;
+        cuuint32_t box;
+        int what;
+    } d[3] = {{(cuuint64_t)l->heads, l->head_stride, 1, 0},
+              {(cuuint64_t)l->page_size, l->entry_stride, (cuuint32_t)box, 1},
+              {(cuuint64_t)l->blocks, l->block_stride, 1, 2}};
+    for (Dim& x : d)
+        if (x.size == 1) x.stride = l->dim;  // not used, but has to be one
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (d[j].stride > d[j + 1].stride) {
+                const Dim t = d[j];
+                d[j] = d[j + 1];
+                d[j + 1] = t;
+            }
+    cuuint64_t sizes[4] = {(cuuint64_t)l->dim}, strides[3];
+    cuuint32_t boxes[4] = {64}, steps[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        sizes[i + 1] = d[i].size;
+        strides[i] = (cuuint64_t)d[i].stride * 2;
+        boxes[i + 1] = d[i].box;
+        if (d[i].what == 0) order->head = i + 1;
+        if (d[i].what == 1) order->entry = i + 1;
+    }
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+                  sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DT, int NB>
+static cudaError_t launch_attend(AttendArgs a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+    LaunchShape shape;
+    if (!launch_shape(reinterpret_cast<const void*>(k_attend<T, DT, NB>), kAttendSmem<DT>, kAtNT, &shape))
+        return cudaErrorUnknown;
+    a.plan = attend_plan(a.N, a.group, shape.sms < kAtMaxCtas ? shape.sms : kAtMaxCtas);
     const int trees = !a.parent ? 0 : a.parent_stride ? a.B : 1;
     cudaError_t e = launch_dependent(k_attend_prepare, dim3(1 + trees), dim3(kAtPrepNT), 0, st, a);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(k_attend_rows<T>, dim3((unsigned)((int64_t)a.B * a.N * a.q_heads)), dim3(128), 0, st, a);
+    e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.share), dim3(kAtNT), kAttendSmem<DT>, st, a, km, vm);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_attend_finish, dim3(a.B < 128 ? a.B : 128), dim3(kAtPrepNT), 0, st, a);
+    const int64_t joins = (int64_t)a.B * a.kv_heads * a.plan.chunks * a.plan.share * NB;
+    return launch_dependent(k_attend_finish<T, DT, NB>, dim3((unsigned)(1 + joins)), dim3(kAtPrepNT), 0, st, a);
+}
+template <typename T>
+static cudaError_t launch_attend(const AttendArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+    const bool two = (int64_t)a.N * a.group > kAtTile;
+    if (a.dim > 64) return two ? launch_attend<T, 128, 2>(a, km, vm, st) : launch_attend<T, 128, 1>(a, km, vm, st);
+    return two ? launch_attend<T, 64, 2>(a, km, vm, st) : launch_attend<T, 64, 1>(a, km, vm, st);
 }
 
 }  // namespace sv
@@ -194,8 +915,8 @@ static cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
 using namespace sv;
 
 extern "C" size_t spec_tree_attention_workspace(int B, int N, int q_heads, int kv_heads, int dim) {
-    if (B < 1 || N < 1 || q_heads < 1 || kv_heads < 1 || dim < 1) return 0;
-    return attend_space(B, N).total;
+    if (B < 1 || N < 1 || q_heads < 1 || kv_heads < 1 || dim < 1 || q_heads % kv_heads) return 0;
+    return attend_space(B, N, q_heads / kv_heads, dim).total;
 }
 
 extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int B, int N, int q_heads,
@@ -212,27 +933,41 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
         q_request_stride < 0 || q_node_stride < 0 || q_head_stride < 0 ||
         (parent && parent_stride != 0 && parent_stride < N) || !(scale > 0.0f) || !(scale < INFINITY))
         return SPEC_ERR_INVALID_ARG;
+    const int group = q_heads / layout->heads;
+    const int64_t capacity = (int64_t)max_blocks * layout->page_size;
     if (B > kMaxRequests || N > kMaxDraftNodes || layout->dim % 8 || layout->dim < 64 || layout->dim > 128 ||
-        (int64_t)B * N * q_heads > 0x7fffffffLL)
+        q_heads > kMaxAttendHeads)
+        return SPEC_ERR_UNSUPPORTED;
+    const AttendPlan plan = attend_plan(N, group, kAtMaxCtas);
+    // units, and the last launch's CTAs, in 31 bits
+    const int64_t parts = (int64_t)B * layout->heads * plan.chunks, tiles = (capacity + kAtTile - 1) / kAtTile;
+    if (tiles > 0x7fffffffLL || parts * plan.share * plan.blocks > 0x7ffffffeLL || parts > 0x7fffffffLL / tiles)
         return SPEC_ERR_UNSUPPORTED;
     if ((q_request_stride | q_node_stride | q_head_stride | layout->block_stride | layout->entry_stride |
          layout->head_stride) % 8 ||
         ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
           reinterpret_cast<uintptr_t>(out)) & 15u))
         return SPEC_ERR_UNSUPPORTED;
-    const AttendSpace s = attend_space(B, N);
+    const AttendSpace s = attend_space(B, N, group, layout->dim);
     if (!workspace || workspace_bytes < s.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPEC_ERR_WORKSPACE;
     if (!select_device_of(q)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // a copy takes as many entries as lie together in every page and tile
+    int box = 1;
+    while (box < kAtTile && layout->page_size % (2 * box) == 0) box *= 2;
+    CUtensorMap km, vm;
+    AttendMapOrder order{};
+    const bool bf16 = dtype == SPEC_BF16;
+    if (!attend_map(&km, k_cache, bf16, layout, box, &order) || !attend_map(&vm, v_cache, bf16, layout, box, &order))
+        return SPEC_ERR_UNSUPPORTED;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    AttendArgs a{static_cast<const uint16_t*>(q), B, N, q_heads, layout->heads, q_heads / layout->heads, layout->dim,
-                 q_request_stride, q_node_stride, q_head_stride, static_cast<const uint16_t*>(k_cache),
-                 static_cast<const uint16_t*>(v_cache), layout->blocks, layout->page_size, layout->block_stride,
-                 layout->entry_stride, layout->head_stride, block_table, table_stride,
-                 (int64_t)max_blocks * layout->page_size, seq_lens, parent, parent_stride, n_nodes, scale,
-                 static_cast<uint16_t*>(out), dev_error, reinterpret_cast<int32_t*>(w + s.err),
-                 reinterpret_cast<int32_t*>(w + s.tree_err), reinterpret_cast<uint32_t*>(w + s.masks), (N + 31) / 32};
-    return (dtype == SPEC_BF16 ? launch_attend<__nv_bfloat16>(a, st) : launch_attend<__half>(a, st)) == cudaSuccess
+    auto at = [&](size_t offset) { return reinterpret_cast<int32_t*>(w + offset); };
+    AttendArgs a{static_cast<const uint16_t*>(q), B, N, q_heads, layout->heads, group, layout->dim, q_request_stride,
+                 q_node_stride, q_head_stride, layout->blocks, layout->page_size, box, order.head, order.entry, block_table,
+                 table_stride, capacity, seq_lens, parent, parent_stride, n_nodes, (float)((double)scale * kLog2e),
+                 static_cast<uint16_t*>(out), dev_error, plan, at(s.err), at(s.tree_err), at(s.first), at(s.late),
+                 reinterpret_cast<uint32_t*>(w + s.masks), reinterpret_cast<float*>(w + s.part), (N + 31) / 32};
+    return (bf16 ? launch_attend<__nv_bfloat16>(a, km, vm, st) : launch_attend<__half>(a, km, vm, st)) == cudaSuccess
                ? SPEC_OK
                : SPEC_ERR_CUDA;
 }
