@@ -13,7 +13,7 @@ constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, a copy warp, a m
 constexpr int kAtMaxCtas = 160;
 constexpr int kMaxAttendHeads = 4096;
 constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
-constexpr uint64_t kAtWaitNs = 2000000000ull;
+constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 #ifndef SV_LATE_ATTEND
 #define SV_LATE_ATTEND false
 #endif
@@ -199,10 +199,10 @@ static_assert(kAttendSmem<128> <= 232448 && kAttendSmem<64> <= 232448, "a CTA's 
 
 // A wait of one thread; false once it, or another of the CTA's, has run out.
 __device__ __noinline__ bool attend_wait_long(AttendCtrl* c, uint64_t* bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
+    const long long t0 = clock64();  // a read of the global timer takes longer than most waits here
     while (!mbar_test(bar, parity)) {
         if (c->dead) return false;
-        if (global_ns() - t0 > kAtWaitNs) {
+        if (clock64() - t0 > kAtWaitClocks) {
             c->dead = 1;
             return false;
         }
@@ -249,29 +249,47 @@ template <int DT>
 __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* km, const CUtensorMap* vm,
                                             AttendWalk walk, AttendCtrl* c, uint32_t ring) {
     using S = AttendShape<DT>;
-    const int lane = threadIdx.x & 31, boxes = kAtTile / a.box;
+    constexpr int kCopies = kAtTile / 32 * (DT / 64);  // of a lane, at most
+    // a lane takes every 32nd of the tile's copies, (box, 64 columns) each
+    constexpr int kWide = DT / 64;
+    const uint32_t lane = threadIdx.x & 31, boxes = kAtTile / a.box, copies = boxes * kWide, per = a.page / a.box;
     AttendItem x;
     int issued = 0;
     bool ok = true;
-    while (ok && walk.item(a, &x)) {
-        for (int t = x.t0; ok && t < x.t1; ++t) {
-            int block[4], entry[4];
+    int block[kCopies], entry[kCopies];
+    auto look_up = [&](int t) {
+        const uint32_t end = (uint32_t)x.len + x.n;  // below 2^31 + 1024
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = lane + 32 * k;
-                const int64_t at = (int64_t)t * kAtTile + i * a.box;
-                block[k] = a.cache_blocks;
-                entry[k] = 0;
-                if (i < boxes && at < (int64_t)x.len + x.n) {
-                    const int64_t j = at / a.page;
-                    block[k] = a.table[x.b * a.table_stride + j];
-                    entry[k] = (int)(at - j * a.page);
-                    if (block[k] < 0 || block[k] >= a.cache_blocks) {
-                        atomicOr(a.err + x.b, kDevErrCapacity);
-                        block[k] = a.cache_blocks;
-                    }
-                }
+        for (uint32_t k = 0; k < kCopies; ++k) {
+            if (k * 32 >= copies) break;
+            const uint32_t i = (uint32_t)t * boxes + (lane + 32 * k) / kWide;  // box of the sequence
+            block[k] = a.cache_blocks;
+            entry[k] = 0;
+            if (lane + 32 * k < copies && i * a.box < end) {
+                const uint32_t j = i / per;
+                block[k] = a.table[x.b * a.table_stride + j];
+                entry[k] = (int)((i - j * per) * a.box);
+                if ((uint32_t)block[k] >= (uint32_t)a.cache_blocks) block[k] = -1;
             }
+        }
+    };
+    while (ok && walk.item(a, &x)) {
+        look_up(x.t0);
+        for (int t = x.t0; ok && t < x.t1; ++t) {
+            int c1[kCopies], c2[kCopies], c3[kCopies];
+#pragma unroll
+            for (uint32_t k = 0; k < kCopies; ++k) {
+                if (k * 32 >= copies) break;
+                if (lane + 32 * k < copies && block[k] < 0) {
+                    atomicOr(a.err + x.b, kDevErrCapacity);
+                    block[k] = a.cache_blocks;
+                }
+                auto at = [&](int dim) { return dim == a.at_head ? x.head : dim == a.at_entry ? entry[k] : block[k]; };
+                c1[k] = at(1);
+                c2[k] = at(2);
+                c3[k] = at(3);
+            }
+            if (t + 1 < x.t1) look_up(t + 1);  // on its way while the ring is waited for
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 const int slot = issued % S::kStages, use = issued / S::kStages;
@@ -281,17 +299,13 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], S::kTileBytes);
                 __syncwarp();
-                const uint32_t to = ring + slot * S::kTileBytes;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = lane + 32 * k;
-                    if (i >= boxes) continue;
-                    auto at = [&](int dim) { return dim == a.at_head ? x.head : dim == a.at_entry ? entry[k] : block[k]; };
-                    const int c1 = at(1), c2 = at(2), c3 = at(3);
-#pragma unroll
-                    for (int d = 0; d < DT / 64; ++d)
-                        tma_load_4d(to + d * S::kBlockBytes + i * a.box * 128, kv ? vm : km, d * 64, c1, c2, c3,
-                                    &c->full[slot]);
+                for (uint32_t k = 0; k < kCopies; ++k) {
+                    if (k * 32 >= copies) break;
+                    const uint32_t i = lane + 32 * k, d = i % kWide;
+                    if (i < copies)
+                        tma_load_4d(ring + slot * S::kTileBytes + d * S::kBlockBytes + i / kWide * a.box * 128, kv ? vm : km,
+                                    d * 64, c1[k], c2[k], c3[k], &c->full[slot]);
                 }
                 if (kv && lane == 0 && x.masked(t)) mbar_arrive(&c->mend[slot]);
                 ++issued;
@@ -359,17 +373,16 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
         const int n = x.t1 - x.t0, streams = NB == 2 && x.rows > kAtTile ? 2 : 1;
         for (int j = 0; ok && j < n; ++j) {
             const int index = 2 * (J + j), slot = index % S::kStages;
-            if (!attend_wait(c, &c->full[slot], (index / S::kStages) & 1)) {
-                ok = false;
-                break;
-            }
             const uint32_t k0 = ring + slot * S::kTileBytes;
+            auto keys = [&] { return attend_wait(c, &c->full[slot], (index / S::kStages) & 1); };
+            // the values' product goes first: it gives back the slot that a coming tile waits for
             if (NB == 1) {
                 if (j >= 2) ok = product(j & 1, x.t0 + j - 2, J + j - 2, j >= 4, true, true);
-                if (ok) scores(j & 1, q, k0);
+                if ((ok = ok && keys())) scores(j & 1, q, k0);
             } else {
                 for (int w = 0; ok && w < streams; ++w) {
                     if (j >= 1) ok = product(w, x.t0 + j - 1, J + j - 1, j >= 2, w == 0, w == streams - 1);
+                    if (w == 0) ok = ok && keys();
                     if (ok) scores(w, q + w * S::kTileBytes, k0);
                 }
             }
@@ -506,7 +519,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         const uint32_t* mask =
             a.parent ? a.masks + ((int64_t)(a.parent_stride ? x.b : 0) * a.N + node) * a.mask_words : nullptr;
         float m = kNoMax;
-        float2 l = make_float2(0.0f, 0.0f);
+        float2 l = make_float2(0.0f, 0.0f);  // two sums of a row's weights
         bool begun = false;
         for (int t = x.t0; t < x.t1; ++t, ++J) {
             const bool masked = x.masked(t);
@@ -516,6 +529,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
             if (NB == 1 && ((t - x.t0) & 1) != w) continue;
             if (!attend_wait_warp(c, &c->s_full[w], scored)) return;
             scored ^= 1u;
+            if (masked && !attend_wait_warp(c, &c->mended[slot], mend_parity)) return;
             tmem_fence_after();
             if (live) {
                 float s[kAtTile];
@@ -523,7 +537,6 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                 for (int i = 0; i < 4; ++i) tmem_load32(s_at + i * 32, reinterpret_cast<uint32_t*>(s) + i * 32);
                 tmem_wait_load();
                 if (masked) {
-                    if (!attend_wait_warp(c, &c->mended[slot], mend_parity)) return;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int64_t base = (int64_t)t * kAtTile + i * 32 - x.len;
@@ -551,19 +564,20 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                     if (begun) {
                         const uint32_t o_at = tmem + lanes + 256 + w * DT;
 #pragma unroll 1
-                        for (int i = 0; i < DT / 32; ++i) {
-                            uint32_t o[32];
-                            tmem_load32(o_at + i * 32, o);
+                        for (int i = 0; i < DT / 8; ++i) {
+                            uint32_t o[8];
+                            tmem_load8(o_at + i * 8, o);
                             tmem_wait_load();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_store32(o_at + i * 32, o);
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_store8(o_at + i * 8, o);
                         }
                     }
                 }
                 // nothing seen yet: every score is -inf, and so is its exponent
                 const float off = m == kNoMax ? 0.0f : -m * a.c;
                 const float2 cc = make_float2(a.c, a.c), oo = make_float2(off, off);
+                float2 part[4] = {l, {0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t p[16];
@@ -571,11 +585,12 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                     for (int k = 0; k < 16; ++k) {
                         float2 e = __ffma2_rn(make_float2(s[i * 32 + 2 * k], s[i * 32 + 2 * k + 1]), cc, oo);
                         e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-                        l = __fadd2_rn(l, e);
+                        part[k & 3] = __fadd2_rn(part[k & 3], e);
                         p[k] = Pair<T>::put(e.x, e.y);
                     }
                     tmem_store16(s_at + i * 16, p);
                 }
+                l = __fadd2_rn(__fadd2_rn(part[0], part[1]), __fadd2_rn(part[2], part[3]));
                 tmem_wait_store();
             }
             begun = true;
@@ -620,36 +635,35 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
             const float inv = 1.0f / total;
             uint16_t* out = a.out + (((int64_t)x.b * a.N + node) * a.q_heads + x.head * a.group + (r - node * a.group)) * a.dim;
 #pragma unroll 1
-            for (int i = 0; i < kCols / 32; ++i) {
-                const int col = col0 + i * 32;
-                float o[32];
-                tmem_load32(o_at + col, reinterpret_cast<uint32_t*>(o));
+            for (int i = 0; i < kCols / 16; ++i) {
+                const int col = col0 + i * 16;
+                float o[16];
+                tmem_load16(o_at + col, reinterpret_cast<uint32_t*>(o));
                 if (NB == 1) {
-                    float o1[32];
-                    if (both) tmem_load32(o_at + DT + col, reinterpret_cast<uint32_t*>(o1));
+                    float o1[16];
+                    if (both) tmem_load16(o_at + DT + col, reinterpret_cast<uint32_t*>(o1));
                     tmem_wait_load();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + (both ? o1[k] * f1 : 0.0f);
+                    for (int k = 0; k < 16; ++k) o[k] = o[k] * f0 + (both ? o1[k] * f1 : 0.0f);
                 } else {
                     tmem_wait_load();
                 }
-                if (!there) continue;
-                if (x.whole()) {
+                if (there && x.whole()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (col + k * 8 >= a.dim) break;
+                    for (int k = 0; k < 2; ++k) {
                         uint4 v;
                         v.x = Pair<T>::put(o[k * 8] * inv, o[k * 8 + 1] * inv);
                         v.y = Pair<T>::put(o[k * 8 + 2] * inv, o[k * 8 + 3] * inv);
                         v.z = Pair<T>::put(o[k * 8 + 4] * inv, o[k * 8 + 5] * inv);
                         v.w = Pair<T>::put(o[k * 8 + 6] * inv, o[k * 8 + 7] * inv);
-                        *reinterpret_cast<uint4*>(out + col + k * 8) = v;
+                        if (col + k * 8 < a.dim) *reinterpret_cast<uint4*>(out + col + k * 8) = v;
                     }
-                } else {
+                } else if (there) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < 4; ++k)
                         part_o[(col / 4 + k) * rows] = make_float4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
                 }
+                __syncwarp();  // the next columns are loaded by the whole warp
             }
         }
         if (NB == 1) {
