@@ -609,8 +609,8 @@ spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dty
  *  seq_lens     [B] int32 >= 0: out_seq_lens of spec_advance_blocks.
  *  parent       NULL (node i's parent is i - 1), [N] with parent_stride 0, or
  *               [B, N] with parent_stride >= N: as in the tree verification.
- *  n_nodes      [B] int32 in 0 .. N, or NULL (N each).  Rows from n_b on are
- *               neither read nor written.
+ *  n_nodes      [B] int32 in 0 .. N, or NULL (N each).  Rows from n_b on have
+ *               no influence and are not written.
  *  scale        > 0, finite.
  *  out          [B, N, q_heads, dim] out, contiguous; must not overlap the
  *               inputs.
@@ -630,7 +630,7 @@ spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dty
  *  workspace    spec_tree_attention_workspace() bytes on 256, for this call
  *               alone until it has completed; needs no initial value.
  *  Limits (SPEC_ERR_UNSUPPORTED): dim a multiple of 8 in 64 .. 128, N <= 1024,
- *  B <= 65,535, strides of the caches multiples of 16 bytes, caches on 16 bytes,
+ *  q_heads / heads <= 128, B <= 65,535, strides of the caches multiples of 16 bytes, caches on 16 bytes,
  *  q on 16 bytes with strides of multiples of 16 bytes.
  */
 size_t spec_tree_attention_workspace(int B, int N, int q_heads, int kv_heads, int dim);

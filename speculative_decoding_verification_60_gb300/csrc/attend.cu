@@ -9,30 +9,28 @@ namespace sv {
 
 constexpr int kAtTile = 128;  // cache entries of a tile; query rows of a block
 constexpr int kAtPrepNT = 256;
-constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, a copy warp, a matrix warp, a query warp, a mending warp
+constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, products, values, queries and mending
 constexpr int kAtMaxCtas = 160;
-constexpr int kMaxAttendHeads = 4096;
 constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
 constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 #ifndef SV_LATE_ATTEND
 #define SV_LATE_ATTEND false
 #endif
 
-// Query rows of a request and key head h: row i * group + j is head h * group
-// + j of node i.  A CTA takes `blocks` blocks of 128 rows of them (one or two)
-// and a run of tiles.  Work is counted in units: (request, key head, chunk of
-// rows, tile) in this order, shared out evenly among `groups` groups of `share`
-// CTAs; the CTAs of a group take the chunk's row blocks, over the same tiles.
+// The query rows of a request and a key head: a block has as many whole nodes as
+// fit in 128 rows, row i * group + j being head h * group + j of its node i.  A
+// CTA takes one or two blocks (`blocks`) and a run of tiles.  Work is counted in
+// units: (request, key head, chunk of blocks, tile) in this order, shared out
+// evenly among `groups` groups of `share` CTAs; the CTAs of a group take the
+// chunk's blocks, over the same tiles.
 struct AttendPlan {
+    int nodes;  // of a block
     int blocks, chunks, share, groups;
 };
 
 struct AttendArgs {
-    const uint16_t* q;
     int B, N, q_heads, kv_heads, group, dim;
-    int64_t q_request, q_node, q_head;
     int cache_blocks, page, box;  // box: entries of a copy
-    int at_head, at_entry;        // which of the maps' dimensions 1 .. 3 they are (the third is the block)
     const int32_t* table;
     int64_t table_stride, capacity;  // capacity: positions that a table row holds
     const int32_t* lens;
@@ -123,7 +121,7 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_prepare(AttendArgs a) {
 // A run of tiles of one (request, key head, row blocks of this CTA).
 struct AttendItem {
     int b, len, n, head;
-    int row0, rows;  // this CTA's first row, and how many of its rows there are
+    int node0, nodes;  // this CTA's first node, and how many of its nodes there are
     int t0, t1, tiles;
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
     __device__ __forceinline__ bool masked(int t) const { return (t + 1) * (int64_t)kAtTile > len; }
@@ -164,10 +162,10 @@ struct AttendWalk {
             x->t1 = min(tiles, x->t0 + (u1 - u));
             u += x->t1 - x->t0;
             x->head = i / a.plan.chunks;
-            const int rows = a.plan.blocks * kAtTile;
-            x->row0 = ((i - x->head * a.plan.chunks) * a.plan.share + share) * rows;
-            x->rows = min(r.n * a.group - x->row0, rows);
-            if (x->rows <= 0) continue;  // a request of fewer nodes than N
+            const int most = a.plan.blocks * a.plan.nodes;
+            x->node0 = ((i - x->head * a.plan.chunks) * a.plan.share + share) * most;
+            x->nodes = min(r.n - x->node0, most);
+            if (x->nodes <= 0) continue;  // a request of fewer nodes than N
             x->b = b;
             x->len = r.len;
             x->n = r.n;
@@ -184,10 +182,14 @@ template <int DT> struct AttendShape {
     static constexpr int kStages = 5 * 128 / DT;             // 160 KiB of keys and values
     static constexpr int kQueryBytes = 2 * kTileBytes;       // two blocks, or two turns of one
     static constexpr int kTiles = kQueryBytes + kStages * kTileBytes;
+    // The ring's turns of the J-th tile.  Values are needed later than keys by
+    // more than a tile's time, so they come a tile later.  Turn 1 is nobody's.
+    __device__ static __forceinline__ int key_turn(int J) { return 2 * J; }
+    __device__ static __forceinline__ int value_turn(int J) { return 2 * J + 3; }
 };
 struct AttendCtrl {
     uint64_t full[10], empty[10], mend[10], mended[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], ml_full, read, drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], ml_full, read, drain;
     uint32_t poison[10][4];
     float2 ml[2][kAtTile];
     uint32_t tmem;
@@ -242,19 +244,21 @@ __device__ __forceinline__ uint32_t attend_sees(const AttendArgs& a, const uint3
     return __funnelshift_r(word(base >> 5), word((base >> 5) + 1), base & 31);
 }
 
-// The copy warp: keys and values of each tile into the ring, the tile's pages
-// one by one.  Blocks behind the last position are not looked up: the copy
-// reads outside the cache there, which gives zeros.
-template <int DT>
-__device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* km, const CUtensorMap* vm,
-                                            AttendWalk walk, AttendCtrl* c, uint32_t ring) {
+// The warps that copy keys (KV = 0) and values (1) of each tile into the ring,
+// the tile's pages one by one.  Blocks behind the last position are not looked
+// up: the copy reads outside the cache there, which gives zeros.  (One warp for
+// both took 3900 clocks a tile of eight pages, 75 a copy, and the products
+// waited.)
+template <int DT, int KV>
+__device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* map, AttendWalk walk, AttendCtrl* c,
+                                            uint32_t ring) {
     using S = AttendShape<DT>;
     constexpr int kCopies = kAtTile / 32 * (DT / 64);  // of a lane, at most
     // a lane takes every 32nd of the tile's copies, (box, 64 columns) each
     constexpr int kWide = DT / 64;
     const uint32_t lane = threadIdx.x & 31, boxes = kAtTile / a.box, copies = boxes * kWide, per = a.page / a.box;
-    AttendItem x;
-    int issued = 0;
+    AttendItem x{};
+    int J = 0;
     bool ok = true;
     int block[kCopies], entry[kCopies];
     auto look_up = [&](int t) {
@@ -276,58 +280,58 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
     while (ok && walk.item(a, &x)) {
         look_up(x.t0);
         for (int t = x.t0; ok && t < x.t1; ++t) {
-            int c1[kCopies], c2[kCopies], c3[kCopies];
+            int to_block[kCopies], to_entry[kCopies];
 #pragma unroll
             for (uint32_t k = 0; k < kCopies; ++k) {
                 if (k * 32 >= copies) break;
                 if (lane + 32 * k < copies && block[k] < 0) {
-                    atomicOr(a.err + x.b, kDevErrCapacity);
+                    if (KV == 0) atomicOr(a.err + x.b, kDevErrCapacity);
                     block[k] = a.cache_blocks;
                 }
-                auto at = [&](int dim) { return dim == a.at_head ? x.head : dim == a.at_entry ? entry[k] : block[k]; };
-                c1[k] = at(1);
-                c2[k] = at(2);
-                c3[k] = at(3);
+                to_block[k] = block[k];
+                to_entry[k] = entry[k];
             }
             if (t + 1 < x.t1) look_up(t + 1);  // on its way while the ring is waited for
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int slot = issued % S::kStages, use = issued / S::kStages;
-                if (use > 0 && !attend_wait_warp(c, &c->empty[slot], (use - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], S::kTileBytes);
-                __syncwarp();
-#pragma unroll
-                for (uint32_t k = 0; k < kCopies; ++k) {
-                    if (k * 32 >= copies) break;
-                    const uint32_t i = lane + 32 * k, d = i % kWide;
-                    if (i < copies)
-                        tma_load_4d(ring + slot * S::kTileBytes + d * S::kBlockBytes + i / kWide * a.box * 128, kv ? vm : km,
-                                    d * 64, c1[k], c2[k], c3[k], &c->full[slot]);
-                }
-                if (kv && lane == 0 && x.masked(t)) mbar_arrive(&c->mend[slot]);
-                ++issued;
+            const int turn = KV ? S::value_turn(J) : S::key_turn(J), slot = turn % S::kStages, use = turn / S::kStages;
+            if (use > 0 && !attend_wait_warp(c, &c->empty[slot], (use - 1) & 1)) {
+                ok = false;
+                break;
             }
+            if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], S::kTileBytes);
+            __syncwarp();
+#pragma unroll
+            for (uint32_t k = 0; k < kCopies; ++k) {
+                if (k * 32 >= copies) break;
+                const uint32_t i = lane + 32 * k, d = i % kWide;
+                if (i < copies)
+                    tma_load_4d(ring + slot * S::kTileBytes + d * S::kBlockBytes + i / kWide * a.box * 128, map, d * 64, x.head,
+                                to_entry[k], to_block[k], &c->full[slot]);
+            }
+            if (KV == 1 && lane == 0 && x.masked(t)) mbar_arrive(&c->mend[slot]);
+            ++J;
         }
     }
-    // nothing is on its way into shared memory when the CTA ends
-    for (int i = max(0, issued - S::kStages); i < issued; ++i)
-        mbar_wait(&c->full[i % S::kStages], (i / S::kStages) & 1, kDrainNs);
+    // Nothing is on its way into shared memory when the CTA ends: this warp's
+    // copies into slots that no later turn has had (turn + kStages).
+    constexpr int kLast = S::kStages % 2 == 0 ? S::kStages / 2 : KV ? (S::kStages + 3) / 2 : (S::kStages - 3) / 2;
+    for (int j = max(0, J - kLast); j < J; ++j) {
+        const int turn = KV ? S::value_turn(j) : S::key_turn(j);
+        mbar_wait(&c->full[turn % S::kStages], (turn / S::kStages) & 1, kDrainNs);
+    }
     __syncwarp();
 }
 
-// The matrix thread.  Stream w: the products with S, P and O of warpgroup w.
-// NB = 2: both streams take every tile, each for its own block of rows.
-// NB = 1: the streams take turns.  S of a stream's next tile follows its
-// product with the values of the tile before, so a warpgroup's softmax runs
-// beside the other stream's products.
+// The matrix warp.  Stream w: the products with S, P and O of warpgroup w.
+// NB = 2: both streams take every tile, each for its own block of rows; S of a
+// stream's next tile follows its product with the values of the tile before, so
+// a warpgroup's softmax runs beside the other stream's products.
+// NB = 1: the streams take turns, and what comes first is done first: scores as
+// soon as the keys are there, a product as soon as its weights are.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t queries,
                                                 uint32_t ring, uint32_t tmem) {
     using S = AttendShape<DT>;
-    constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+    constexpr bool kBf16 = !std::is_same<T, __half>::value;
     constexpr uint32_t kScores = mma_shape<kBf16>(kAtTile, false), kValues = mma_shape<kBf16>(DT, true);
     constexpr int kTurns = NB == 1 ? 2 : 1;  // query buffers
     AttendItem x;
@@ -337,126 +341,139 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
     bool ok = true;
     // O_w (+)= P_w V of tile t, the J-th; `last` stream of the tile gives the slot back
     auto product = [&](int w, int t, int j, bool add, bool wait_values, bool last) {
-        const int index = 2 * j + 1, slot = index % S::kStages;
+        const int slot = S::value_turn(j) % S::kStages;
         if (wait_values) {
-            if (!attend_wait(c, &c->full[slot], (index / S::kStages) & 1)) return false;
+            if (!attend_wait_warp(c, &c->full[slot], S::value_turn(j) / S::kStages & 1)) return false;
             if (x.masked(t)) {
-                if (!attend_wait(c, &c->mended[slot], (mended >> slot) & 1u)) return false;
+                if (!attend_wait_warp(c, &c->mended[slot], (mended >> slot) & 1u)) return false;
                 mended ^= 1u << slot;
             }
         }
-        if (!attend_wait(c, &c->p_full[w], weights[w])) return false;
-        weights[w] ^= 1u;
-        tmem_fence_after();
-        const uint32_t v = ring + slot * S::kTileBytes;
+        const uint32_t v = mma_operand(ring + slot * S::kTileBytes, S::kBlockBytes);
 #pragma unroll
-        for (int k = 0; k < kAtTile / 16; ++k)
-            mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, mma_operand(v + k * 2048, S::kBlockBytes), kValues,
-                       add || k > 0);
+        for (int k = 0; k < kAtTile / 16; ++k) {
+            if (k % 4 == 0) {  // the weights come in halves
+                if (!attend_wait_warp(c, &c->p_full[w][k / 4], weights[w])) return false;
+                tmem_fence_after();
+            }
+            mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, v + k * (2048 / 16), kValues, add || k > 0);
+        }
+        weights[w] ^= 1u;
         if (last) mma_commit(&c->empty[slot]);
         return true;
     };
-    auto scores = [&](int w, uint32_t q, uint32_t k0) {
+    auto scores = [&](int w, uint32_t q_at, int j) {
+        const uint32_t q = mma_operand(q_at, 16),
+                       k0 = mma_operand(ring + S::key_turn(j) % S::kStages * S::kTileBytes, 16);
 #pragma unroll
         for (int k = 0; k < DT / 16; ++k) {
-            const uint32_t at = (k / 4) * S::kBlockBytes + (k % 4) * 32;
-            mma_shared(tmem + w * 128, mma_operand(q + at, 16), mma_operand(k0 + at, 16), kScores, k > 0);
+            const uint32_t at = ((k / 4) * S::kBlockBytes + (k % 4) * 32) / 16;
+            mma_shared(tmem + w * 128, q + at, k0 + at, kScores, k > 0);
         }
         mma_commit(&c->s_full[w]);
     };
     while (ok && walk.item(a, &x)) {
         const int turn = qi % kTurns;
-        if (!attend_wait(c, &c->q_full[turn], (qi / kTurns) & 1)) break;
+        if (!attend_wait_warp(c, &c->q_full[turn], (qi / kTurns) & 1)) break;
         ++qi;
         tmem_fence_after();
         const uint32_t q = queries + (NB == 1 ? turn * S::kTileBytes : 0);
-        const int n = x.t1 - x.t0, streams = NB == 2 && x.rows > kAtTile ? 2 : 1;
-        for (int j = 0; ok && j < n; ++j) {
-            const int index = 2 * (J + j), slot = index % S::kStages;
-            const uint32_t k0 = ring + slot * S::kTileBytes;
-            auto keys = [&] { return attend_wait(c, &c->full[slot], (index / S::kStages) & 1); };
-            // the values' product goes first: it gives back the slot that a coming tile waits for
-            if (NB == 1) {
-                if (j >= 2) ok = product(j & 1, x.t0 + j - 2, J + j - 2, j >= 4, true, true);
-                if ((ok = ok && keys())) scores(j & 1, q, k0);
-            } else {
-                for (int w = 0; ok && w < streams; ++w) {
-                    if (j >= 1) ok = product(w, x.t0 + j - 1, J + j - 1, j >= 2, w == 0, w == streams - 1);
-                    if (w == 0) ok = ok && keys();
-                    if (ok) scores(w, q + w * S::kTileBytes, k0);
-                }
-            }
-            if (ok) mma_commit(&c->empty[slot]);
-        }
-        if (!ok) break;
-        mma_commit(&c->q_empty[turn]);
+        const int n = x.t1 - x.t0, streams = NB == 2 && x.nodes > a.plan.nodes ? 2 : 1;
+        auto keys = [&](int j) { return &c->full[S::key_turn(J + j) % S::kStages]; };
+        auto keys_parity = [&](int j) { return (uint32_t)(S::key_turn(J + j) / S::kStages & 1); };
+        auto keys_done = [&](int j) {
+            mma_commit(&c->empty[S::key_turn(J + j) % S::kStages]);
+            if (j == n - 1) mma_commit(&c->q_empty[turn]);
+        };
         if (NB == 1) {
-            for (int j = max(0, n - 2); ok && j < n; ++j) {
-                ok = product(j & 1, x.t0 + j, J + j, j >= 2, true, true);
-                if (ok) mma_commit(&c->o_full[j & 1]);
+            long long since = clock64();
+            for (int s = 0, p = 0; ok && p < n;) {
+                if (p < s && __all_sync(0xffffffffu, mbar_test(&c->p_full[p & 1][0], weights[p & 1]))) {
+                    ok = product(p & 1, x.t0 + p, J + p, p >= 2, true, true);
+                    if (p >= n - 2) mma_commit(&c->o_full[p & 1]);
+                    ++p;
+                } else if (s < n && s < p + 2 && __all_sync(0xffffffffu, mbar_test(keys(s), keys_parity(s)))) {
+                    scores(s & 1, q, J + s);
+                    keys_done(s);
+                    ++s;
+                } else {
+                    if (__any_sync(0xffffffffu, c->dead != 0 || clock64() - since > kAtWaitClocks)) {
+                        c->dead = 1;
+                        ok = false;
+                    }
+                    continue;
+                }
+                since = clock64();
             }
         } else {
-            for (int w = 0; ok && w < streams; ++w) {
-                ok = product(w, x.t1 - 1, J + n - 1, n >= 2, w == 0, w == streams - 1);
-                if (ok) mma_commit(&c->o_full[w]);
-            }
+            for (int j = 0; ok && j <= n; ++j)
+                for (int w = 0; ok && w < streams; ++w) {
+                    // the values' product goes first: it gives back the slot that a coming tile waits for
+                    if (j >= 1) ok = product(w, x.t0 + j - 1, J + j - 1, j >= 2, w == 0, w == streams - 1);
+                    if (j == n) {
+                        if (ok) mma_commit(&c->o_full[w]);
+                        continue;
+                    }
+                    if (w == 0) ok = ok && attend_wait_warp(c, keys(j), keys_parity(j));
+                    if (!ok) break;
+                    scores(w, q + w * S::kTileBytes, J + j);
+                    if (w == streams - 1) keys_done(j);
+                }
         }
         J += n;
     }
     // no product is on its way when tensor memory is freed
     mma_commit(&c->drain);
     mbar_wait(&c->drain, 0, kDrainNs);
+    __syncwarp();
 }
 
-// The query warp: rows of an item's queries, swizzled as a copy would.
-template <int DT, int NB>
-__device__ __forceinline__ void attend_queries(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t queries) {
+// The warp that copies queries and mends values.  An item's queries are one box
+// of its block's nodes and heads for every 64 columns; nodes behind the last
+// read as zeros or as rows that nothing is written for.
+//
+// Mending: in tiles that reach behind the sequence, values that no product may
+// meet.  A weight of zero does not hide an infinity or a NaN, so entries behind
+// the last node, and nodes' entries that are not finite, become zeros; the
+// latter's places are told to the softmax, which makes the rows that see them
+// NaN.
+template <typename T, int DT, int NB>
+__device__ __forceinline__ void attend_mend(const AttendArgs& a, const CUtensorMap* map, AttendWalk walk, AttendCtrl* c,
+                                            uint8_t* queries, uint8_t* ring) {
     using S = AttendShape<DT>;
-    constexpr int kTurns = NB == 1 ? 2 : 1, kChunks = DT / 8;
+    constexpr int kTurns = NB == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31;
-    AttendItem x;
-    for (int qi = 0; walk.item(a, &x); ++qi) {
+    auto copy = [&](const AttendItem& x, int qi) {
         const int turn = qi % kTurns, use = qi / kTurns;
-        if (use > 0 && !attend_wait_warp(c, &c->q_empty[turn], (use - 1) & 1)) break;
-        const uint32_t to = queries + (NB == 1 ? turn * S::kTileBytes : 0);
-        const uint16_t* from = a.q + x.b * a.q_request + (int64_t)x.head * a.group * a.q_head;
-        const int chunk = lane % kChunks;
-        for (int row = lane / kChunks; row < x.rows; row += 32 / kChunks) {
-            const int r = x.row0 + row, node = r / a.group;
-            const uint16_t* at = from + node * a.q_node + (r - node * a.group) * a.q_head + chunk * 8;
-            const uint32_t dst = to + (row / kAtTile) * S::kTileBytes + (chunk / 8) * S::kBlockBytes +
-                                 (row % kAtTile) * 128 + (((chunk % 8) ^ (row % 8)) * 16);
-            const int bytes = chunk * 8 < a.dim ? 16 : 0;  // columns behind the head's end are zero
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(bytes ? at : from), "r"(bytes)
-                         : "memory");
+        if (use > 0 && !attend_wait_warp(c, &c->q_empty[turn], (use - 1) & 1)) return false;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&c->q_full[turn], NB * (DT / 64) * a.plan.nodes * a.group * 128);
+            for (int w = 0; w < NB; ++w)
+                for (int d = 0; d < DT / 64; ++d)
+                    tma_load_4d(smem_addr(queries) + (turn + w) * S::kTileBytes + d * S::kBlockBytes, map, d * 64,
+                                x.head * a.group, x.node0 + w * a.plan.nodes, x.b, &c->q_full[turn]);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_shared();
-        attend_arrive_warp(&c->q_full[turn]);
-    }
-}
-
-// The mending warp: in tiles that reach behind the sequence, values that no
-// product may meet.  A weight of zero does not hide an infinity or a NaN, so
-// entries behind the last node, and nodes' entries that are not finite, become
-// zeros; the latter's places are told to the softmax, which makes the rows
-// that see them NaN.
-template <typename T, int DT>
-__device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint8_t* ring) {
-    using S = AttendShape<DT>;
-    const int lane = threadIdx.x & 31;
-    AttendItem x;
-    int J = 0;
+        return true;
+    };
+    AttendItem x, ahead;
+    int J = 0, qi = 0;
     uint32_t parity = 0;  // of each slot's next tile to mend
-    while (walk.item(a, &x)) {
-        for (int t = x.t0; t < x.t1; ++t, ++J) {
+    bool more = walk.item(a, &ahead), ok = !more || NB == 2 || copy(ahead, qi++);
+    while (ok && more) {
+        x = ahead;
+        more = walk.item(a, &ahead);
+        // with two turns the next item's queries are on their way during this one; with one they wait for its end
+        if (NB == 2) ok = copy(x, qi++);
+        else if (more) ok = copy(ahead, qi++);
+        for (int t = x.t0; ok && t < x.t1; ++t, ++J) {
             if (!x.masked(t)) continue;
             // This warp does not follow the ring.  Once the copy warp has named
             // the slot, its turn cannot end before it is mended.
-            const int index = 2 * J + 1, slot = index % S::kStages;
-            if (!attend_wait_warp(c, &c->mend[slot], (parity >> slot) & 1u)) return;
+            const int index = S::value_turn(J), slot = index % S::kStages;
+            ok = attend_wait_warp(c, &c->mend[slot], (parity >> slot) & 1u) &&
+                 attend_wait_warp(c, &c->full[slot], (index / S::kStages) & 1);
+            if (!ok) break;
             parity ^= 1u << slot;
-            if (!attend_wait_warp(c, &c->full[slot], (index / S::kStages) & 1)) return;
 #pragma unroll 1
             for (int k = 0; k < kAtTile / 32; ++k) {
                 const int row = k * 32 + lane;
@@ -490,6 +507,9 @@ __device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk
             attend_arrive_warp(&c->mended[slot]);
         }
     }
+    // no queries are on their way either
+    for (int i = max(0, qi - kTurns); i < qi; ++i) mbar_wait(&c->q_full[i % kTurns], (i / kTurns) & 1, kDrainNs);
+    __syncwarp();
 }
 
 // A warpgroup of the softmax: a thread has a query row.  The scores of a tile
@@ -508,14 +528,15 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
     int J = 0;
     AttendItem x;
     while (walk.item(a, &x)) {
-        const int n = x.t1 - x.t0, block0 = NB == 2 ? w * kAtTile : 0;
-        if (NB == 2 && x.rows <= block0) {  // the second block is empty
+        const int n = x.t1 - x.t0, first = NB == 2 ? w * a.plan.nodes : 0;  // the block's first node in the item
+        const int live_rows = min(x.nodes - first, a.plan.nodes) * a.group;
+        if (NB == 2 && live_rows <= 0) {  // the second block is empty
             for (int t = x.t0; t < x.t1; ++t, ++J)
-                if (x.masked(t)) mended ^= 1u << ((2 * J + 1) % S::kStages);
+                if (x.masked(t)) mended ^= 1u << (S::value_turn(J) % S::kStages);
             continue;
         }
-        const bool live = quarter * 32 < x.rows - block0;  // this warp has a row
-        const int r = min(x.row0 + block0 + row, x.n * a.group - 1), node = r / a.group;
+        const bool live = quarter * 32 < live_rows;  // this warp has a row
+        const int at_node = min(row, live_rows - 1) / a.group, node = x.node0 + first + at_node;
         const uint32_t* mask =
             a.parent ? a.masks + ((int64_t)(a.parent_stride ? x.b : 0) * a.N + node) * a.mask_words : nullptr;
         float m = kNoMax;
@@ -523,7 +544,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         bool begun = false;
         for (int t = x.t0; t < x.t1; ++t, ++J) {
             const bool masked = x.masked(t);
-            const int slot = (2 * J + 1) % S::kStages;
+            const int slot = S::value_turn(J) % S::kStages;
             const uint32_t mend_parity = (mended >> slot) & 1u;
             if (masked) mended ^= 1u << slot;
             if (NB == 1 && ((t - x.t0) & 1) != w) continue;
@@ -589,13 +610,20 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                         p[k] = Pair<T>::put(e.x, e.y);
                     }
                     tmem_store16(s_at + i * 16, p);
+                    if (i == 1) {  // the product with the tile's first 64 values may begin
+                        tmem_wait_store();
+                        tmem_fence_before();
+                        attend_arrive_warp(&c->p_full[w][0]);
+                    }
                 }
                 l = __fadd2_rn(__fadd2_rn(part[0], part[1]), __fadd2_rn(part[2], part[3]));
                 tmem_wait_store();
+            } else {
+                attend_arrive_warp(&c->p_full[w][0]);
             }
             begun = true;
             tmem_fence_before();
-            attend_arrive_warp(&c->p_full[w]);
+            attend_arrive_warp(&c->p_full[w][1]);
         }
         // the item's end
         float total = l.x + l.y;
@@ -624,16 +652,16 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         }
         tmem_fence_after();
         if (live) {
-            const bool there = row < x.rows - block0;
+            const bool there = row < live_rows;
             constexpr int kCols = NB == 1 ? DT / 2 : DT;  // of this thread
-            const int col0 = NB == 1 ? w * kCols : 0, rows = NB * kAtTile, at_row = block0 + row;
+            const int col0 = NB == 1 ? w * kCols : 0, rows = NB * kAtTile, at_row = (NB == 2 ? w * kAtTile : 0) + row;
             const uint32_t o_at = tmem + lanes + 256 + (NB == 2 ? w * DT : 0);
             float* part = a.part + ((int64_t)blockIdx.x * 2 + (x.t0 == 0 ? 1 : 0)) * (rows * (DT + 2));
             if (!x.whole() && there && (NB == 2 || w == 0))
                 reinterpret_cast<float2*>(part)[at_row] = make_float2(m, total);
             float4* part_o = reinterpret_cast<float4*>(part + 2 * rows) + at_row;
             const float inv = 1.0f / total;
-            uint16_t* out = a.out + (((int64_t)x.b * a.N + node) * a.q_heads + x.head * a.group + (r - node * a.group)) * a.dim;
+            uint16_t* out = a.out + (((int64_t)x.b * a.N + node) * a.q_heads + x.head * a.group + (row - at_node * a.group)) * a.dim;
 #pragma unroll 1
             for (int i = 0; i < kCols / 16; ++i) {
                 const int col = col0 + i * 16;
@@ -678,8 +706,8 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
 
 template <typename T, int DT, int NB>
 __global__ void __launch_bounds__(kAtNT, 1)
-    k_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap km,
-             const __grid_constant__ CUtensorMap vm) {
+    k_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qm,
+             const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
     using S = AttendShape<DT>;
     extern __shared__ __align__(1024) uint8_t sh_attend[];
     AttendCtrl* c = reinterpret_cast<AttendCtrl*>(sh_attend + S::kTiles);
@@ -695,7 +723,8 @@ __global__ void __launch_bounds__(kAtNT, 1)
             mbar_init(&c->q_full[i], 1);
             mbar_init(&c->q_empty[i], 1);
             mbar_init(&c->s_full[i], 1);
-            mbar_init(&c->p_full[i], 4);  // warps of a warpgroup
+            mbar_init(&c->p_full[i][0], 4);  // warps of a warpgroup
+            mbar_init(&c->p_full[i][1], 4);
             mbar_init(&c->o_full[i], 1);
         }
         mbar_init(&c->ml_full, 8);
@@ -704,6 +733,9 @@ __global__ void __launch_bounds__(kAtNT, 1)
         c->dead = 0;
         c->b0 = 0;
         mbar_fence_init();
+        mbar_arrive(&c->full[1]);  // turn 1 is over
+        mbar_arrive(&c->empty[1]);
+        tma_prefetch_map(&qm);
         tma_prefetch_map(&km);
         tma_prefetch_map(&vm);
     }
@@ -725,14 +757,13 @@ __global__ void __launch_bounds__(kAtNT, 1)
     if (warp < 8) {
         attend_softmax<T, DT, NB>(a, walk, c, tmem);
     } else if (warp == 8) {
-        attend_copy<DT>(a, &km, &vm, walk, c, ring);
+        attend_copy<DT, 0>(a, &km, walk, c, ring);
     } else if (warp == 9) {
-        if ((tid & 31) == 0) attend_products<T, DT, NB>(a, walk, c, queries, ring, tmem);
-        __syncwarp();
+        attend_products<T, DT, NB>(a, walk, c, queries, ring, tmem);
     } else if (warp == 10) {
-        attend_queries<DT, NB>(a, walk, c, queries);
+        attend_copy<DT, 1>(a, &vm, walk, c, ring);
     } else {
-        attend_mend<T, DT>(a, walk, c, sh_attend + S::kQueryBytes);
+        attend_mend<T, DT, NB>(a, &qm, walk, c, sh_attend, sh_attend + S::kQueryBytes);
     }
     tmem_fence_before();
     __syncthreads();
@@ -749,13 +780,15 @@ __device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int gro
 }
 
 // Joins the results of items that several groups shared: a CTA per request, key
-// head and block of 128 rows.
+// head and block.  A warp finds a row's reference and sum over the parts, then
+// every thread adds up four columns of a row, with the parts' loads in flight.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_join(const AttendArgs& a, int index) {
-    const int per = a.plan.chunks * a.plan.share * NB;  // row blocks of a request's head
+    __shared__ float2 sh_row[kAtTile];  // reference, 1 / sum
+    const int per = a.plan.chunks * a.plan.share * NB;  // blocks of a request's head
     const int b = index / (a.kv_heads * per), head = index / per % a.kv_heads, block = index % per;
     const AttendRequest r = attend_request(a, b);
-    const int tiles = attend_tiles(r), row0 = block * kAtTile, rows = min(r.n * a.group - row0, kAtTile);
+    const int tiles = attend_tiles(r), node0 = block * a.plan.nodes, rows = min(r.n - node0, a.plan.nodes) * a.group;
     if (tiles == 0 || rows <= 0) return;
     const int pair = block / NB, chunk = pair / a.plan.share, share = pair % a.plan.share;
     const int64_t units = a.first[a.B], begin = a.first[b] + (int64_t)(head * a.plan.chunks + chunk) * tiles;
@@ -763,31 +796,44 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int index) {
     const int g0 = attend_group(begin, units, groups), g1 = attend_group(begin + tiles - 1, units, groups);
     if (g0 == g1) return;
     constexpr int R = NB * kAtTile;
+    const int row0 = (block % NB) * kAtTile;
     // the first group's part is the end of its run, the others' the beginning of theirs
     auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.share + share) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
+    for (int row = threadIdx.x >> 5; row < rows; row += kAtPrepNT / 32) {
+        const int lane = threadIdx.x & 31;
+        float m = kNoMax, l = 0.0f;
+        for (int g = g0 + lane; g <= g1; g += 32) {
+            const float2 ml = reinterpret_cast<const float2*>(part(g))[row0 + row];
+            const float top = fmaxf(m, ml.x);
+            l = l * exp2f((m - top) * a.c) + ml.y * exp2f((ml.x - top) * a.c);
+            m = top;
+        }
+        const float top = warp_max_redux(m);
+        l *= exp2f((m - top) * a.c);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) sh_row[row] = make_float2(top, 1.0f / l);
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < rows * (a.dim / 4); i += kAtPrepNT) {
-        const int row = i % rows, d = i / rows, at = (block % NB) * kAtTile + row;
-        float m = kNoMax;
-        for (int g = g0; g <= g1; ++g) m = fmaxf(m, reinterpret_cast<const float2*>(part(g))[at].x);
-        float l = 0.0f;
+        const int row = i % rows, d = i / rows;
+        const float2 of = sh_row[row];
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
         for (int g = g0; g <= g1; ++g) {
             const float* p = part(g);
-            const float2 ml = reinterpret_cast<const float2*>(p)[at];
-            const float f = exp2f((ml.x - m) * a.c);
-            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + at];
-            l += f * ml.y;
+            const float f = exp2f((reinterpret_cast<const float2*>(p)[row0 + row].x - of.x) * a.c) * of.y;
+            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + row0 + row];
             o.x += f * v.x;
             o.y += f * v.y;
             o.z += f * v.z;
             o.w += f * v.w;
         }
-        const int q = row0 + row, node = q / a.group;
+        const int node = row / a.group;
         uint2 v;
-        v.x = Pair<T>::put(o.x / l, o.y / l);
-        v.y = Pair<T>::put(o.z / l, o.w / l);
-        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node) * a.q_heads + head * a.group + (q - node * a.group)) * a.dim +
+        v.x = Pair<T>::put(o.x, o.y);
+        v.y = Pair<T>::put(o.z, o.w);
+        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
                                   d * 4) = v;
     }
 }
@@ -828,9 +874,9 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_consta
 
 static AttendPlan attend_plan(int N, int group, int ctas) {
     AttendPlan p;
-    const int64_t rows = (int64_t)N * group;
-    p.blocks = rows > kAtTile ? 2 : 1;
-    const int parts = (int)((rows + p.blocks * kAtTile - 1) / (p.blocks * kAtTile));
+    p.nodes = kAtTile / group;
+    p.blocks = N > p.nodes ? 2 : 1;
+    const int parts = (N + p.blocks * p.nodes - 1) / (p.blocks * p.nodes);
     p.chunks = (parts + kAtShare - 1) / kAtShare;
     p.share = (parts + p.chunks - 1) / p.chunks;
     p.groups = ctas / p.share;
@@ -853,13 +899,13 @@ static AttendSpace attend_space(int B, int N, int group, int dim) {
     return s;
 }
 
-// The map of a cache: dim innermost, then heads, entries and blocks by stride;
-// boxes of 64 values of `box` entries.  false: the driver refuses it.
-struct AttendMapOrder {
-    int head, entry;
+// A map of three dimensions of heads (sizes, strides in elements, boxes), 64
+// columns of a head at a time.  false: the driver refuses it.
+struct AttendDim {
+    int64_t size, stride;
+    int box;
 };
-static bool attend_map(CUtensorMap* map, const void* base, bool bf16, const spec_cache_layout* l, int box,
-                       AttendMapOrder* order) {
+static bool attend_map(CUtensorMap* map, const void* base, bool bf16, int dim, const AttendDim (&d)[3]) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -872,39 +918,23 @@ static bool attend_map(CUtensorMap* map, const void* base, bool bf16, const spec
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return false;
-    struct Dim {
-        cuuint64_t size;
-        int64_t stride;
-        cuuint32_t box;
-        int what;
-    } d[3] = {{(cuuint64_t)l->heads, l->head_stride, 1, 0},
-              {(cuuint64_t)l->page_size, l->entry_stride, (cuuint32_t)box, 1},
-              {(cuuint64_t)l->blocks, l->block_stride, 1, 2}};
-    for (Dim& x : d)
-        if (x.size == 1) x.stride = l->dim;  // not used, but has to be one
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-            if (d[j].stride > d[j + 1].stride) {
-                const Dim t = d[j];
-                d[j] = d[j + 1];
-                d[j + 1] = t;
-            }
-    cuuint64_t sizes[4] = {(cuuint64_t)l->dim}, strides[3];
+    cuuint64_t sizes[4] = {(cuuint64_t)dim}, strides[3];
     cuuint32_t boxes[4] = {64}, steps[4] = {1, 1, 1, 1};
     for (int i = 0; i < 3; ++i) {
-        sizes[i + 1] = d[i].size;
-        strides[i] = (cuuint64_t)d[i].stride * 2;
-        boxes[i + 1] = d[i].box;
-        if (d[i].what == 0) order->head = i + 1;
-        if (d[i].what == 1) order->entry = i + 1;
+        sizes[i + 1] = (cuuint64_t)d[i].size;
+        strides[i] = (cuuint64_t)(d[i].size == 1 ? dim : d[i].stride) * 2;  // one of size 1 is not used, but has to be there
+        boxes[i + 1] = (cuuint32_t)d[i].box;
     }
     return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
                   sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct AttendMaps {
+    CUtensorMap q, k, v;
+};
 template <typename T, int DT, int NB>
-static cudaError_t launch_attend(AttendArgs a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+static cudaError_t launch_attend(AttendArgs a, const AttendMaps& maps, cudaStream_t st) {
     LaunchShape shape;
     if (!launch_shape(reinterpret_cast<const void*>(k_attend<T, DT, NB>), kAttendSmem<DT>, kAtNT, &shape))
         return cudaErrorUnknown;
@@ -912,16 +942,17 @@ static cudaError_t launch_attend(AttendArgs a, const CUtensorMap& km, const CUte
     const int trees = !a.parent ? 0 : a.parent_stride ? a.B : 1;
     cudaError_t e = launch_dependent(k_attend_prepare, dim3(1 + trees), dim3(kAtPrepNT), 0, st, a);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.share), dim3(kAtNT), kAttendSmem<DT>, st, a, km, vm);
+    e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.share), dim3(kAtNT), kAttendSmem<DT>, st, a, maps.q,
+                         maps.k, maps.v);
     if (e != cudaSuccess) return e;
     const int64_t joins = (int64_t)a.B * a.kv_heads * a.plan.chunks * a.plan.share * NB;
     return launch_dependent(k_attend_finish<T, DT, NB>, dim3((unsigned)(1 + joins)), dim3(kAtPrepNT), 0, st, a);
 }
 template <typename T>
-static cudaError_t launch_attend(const AttendArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-    const bool two = (int64_t)a.N * a.group > kAtTile;
-    if (a.dim > 64) return two ? launch_attend<T, 128, 2>(a, km, vm, st) : launch_attend<T, 128, 1>(a, km, vm, st);
-    return two ? launch_attend<T, 64, 2>(a, km, vm, st) : launch_attend<T, 64, 1>(a, km, vm, st);
+static cudaError_t launch_attend(const AttendArgs& a, const AttendMaps& maps, cudaStream_t st) {
+    const bool two = a.plan.blocks == 2;
+    if (a.dim > 64) return two ? launch_attend<T, 128, 2>(a, maps, st) : launch_attend<T, 128, 1>(a, maps, st);
+    return two ? launch_attend<T, 64, 2>(a, maps, st) : launch_attend<T, 64, 1>(a, maps, st);
 }
 
 }  // namespace sv
@@ -950,7 +981,7 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
     const int group = q_heads / layout->heads;
     const int64_t capacity = (int64_t)max_blocks * layout->page_size;
     if (B > kMaxRequests || N > kMaxDraftNodes || layout->dim % 8 || layout->dim < 64 || layout->dim > 128 ||
-        q_heads > kMaxAttendHeads)
+        group > kAtTile)
         return SPEC_ERR_UNSUPPORTED;
     const AttendPlan plan = attend_plan(N, group, kAtMaxCtas);
     // units, and the last launch's CTAs, in 31 bits
@@ -969,19 +1000,23 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
     // a copy takes as many entries as lie together in every page and tile
     int box = 1;
     while (box < kAtTile && layout->page_size % (2 * box) == 0) box *= 2;
-    CUtensorMap km, vm;
-    AttendMapOrder order{};
     const bool bf16 = dtype == SPEC_BF16;
-    if (!attend_map(&km, k_cache, bf16, layout, box, &order) || !attend_map(&vm, v_cache, bf16, layout, box, &order))
+    const int dim = layout->dim;
+    const AttendDim queries[3] = {{q_heads, q_head_stride, group}, {N, q_node_stride, plan.nodes}, {B, q_request_stride, 1}};
+    const AttendDim cache[3] = {{layout->heads, layout->head_stride, 1},
+                                {layout->page_size, layout->entry_stride, box},
+                                {layout->blocks, layout->block_stride, 1}};
+    AttendMaps maps;
+    if (!attend_map(&maps.q, q, bf16, dim, queries) || !attend_map(&maps.k, k_cache, bf16, dim, cache) ||
+        !attend_map(&maps.v, v_cache, bf16, dim, cache))
         return SPEC_ERR_UNSUPPORTED;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     auto at = [&](size_t offset) { return reinterpret_cast<int32_t*>(w + offset); };
-    AttendArgs a{static_cast<const uint16_t*>(q), B, N, q_heads, layout->heads, group, layout->dim, q_request_stride,
-                 q_node_stride, q_head_stride, layout->blocks, layout->page_size, box, order.head, order.entry, block_table,
-                 table_stride, capacity, seq_lens, parent, parent_stride, n_nodes, (float)((double)scale * kLog2e),
+    AttendArgs a{B, N, q_heads, layout->heads, group, dim, layout->blocks, layout->page_size, box, block_table, table_stride,
+                 capacity, seq_lens, parent, parent_stride, n_nodes, (float)((double)scale * kLog2e),
                  static_cast<uint16_t*>(out), dev_error, plan, at(s.err), at(s.tree_err), at(s.first), at(s.late),
                  reinterpret_cast<uint32_t*>(w + s.masks), reinterpret_cast<float*>(w + s.part), (N + 31) / 32};
-    return (bf16 ? launch_attend<__nv_bfloat16>(a, km, vm, st) : launch_attend<__half>(a, km, vm, st)) == cudaSuccess
+    return (bf16 ? launch_attend<__nv_bfloat16>(a, maps, st) : launch_attend<__half>(a, maps, st)) == cudaSuccess
                ? SPEC_OK
                : SPEC_ERR_CUDA;
 }

@@ -86,37 +86,46 @@ __device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t* r) {
 // An operand in shared memory, in rows of 128 bytes swizzled in groups of 8
 // (1024 bytes).  Rows along M or N (the product runs along a row): `across` is
 // not used.  Rows along the product's axis (M or N runs along a row, 64 values
-// a row): `across` is the distance between blocks of 64 columns.
-__device__ __forceinline__ uint64_t mma_operand(uint32_t at, uint32_t across) {
-    return (uint64_t)((at & 0x3ffffu) >> 4) | ((uint64_t)(across >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// a row): `across` is the distance between blocks of 64 columns.  This is the
+// descriptor's low word; a step of n bytes adds n / 16.  The high word is the
+// same for all of them.
+__device__ __forceinline__ uint32_t mma_operand(uint32_t at, uint32_t across) {
+    return (at >> 4) | ((across >> 4) << 16);
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // groups of 8 rows, version, 128-byte swizzle
 // 128 rows by N columns, 16-bit inputs of one type, sums in 32 bits.
 template <bool BF16>
 __host__ __device__ constexpr uint32_t mma_shape(int n, bool b_across) {
     return (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((128u >> 4) << 24);
 }
+// These are called by a whole warp with the same values, and one lane, the same
+// every time, issues them: so the operands stay in uniform registers (a single
+// thread's branch took 86 clocks an operation, more than the operation does).
 // d (+)= a b over 16 values of the product's axis; a in shared memory, or in
 // tensor memory (two values a column).
-__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_shared(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
-__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
-// An arrival on bar when every matrix operation that this thread has issued is done.
+// An arrival on bar when every matrix operation that the warp has issued is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
 }
 
 }  // namespace sv
