@@ -11,6 +11,7 @@ constexpr int kAtTile = 128;  // cache entries of a tile; query rows of a block
 constexpr int kAtPrepNT = 256;
 constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, products, values, queries and mending
 constexpr int kAtMaxCtas = 160;
+constexpr int kAtPieces = 8;   // CTAs that join a block
 constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
 constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 #ifndef SV_LATE_ATTEND
@@ -326,25 +327,23 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
 // stream's next tile follows its product with the values of the tile before, so
 // a warpgroup's softmax runs beside the other stream's products.
 // NB = 1: the streams take turns, and what comes first is done first: scores as
-// soon as the keys are there, a product as soon as its weights are.
+// soon as the keys are there, a product as soon as its weights are.  An item's
+// first scores do not wait for the last one's products.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t queries,
                                                 uint32_t ring, uint32_t tmem) {
     using S = AttendShape<DT>;
     constexpr bool kBf16 = !std::is_same<T, __half>::value;
     constexpr uint32_t kScores = mma_shape<kBf16>(kAtTile, false), kValues = mma_shape<kBf16>(DT, true);
-    constexpr int kTurns = NB == 1 ? 2 : 1;  // query buffers
-    AttendItem x;
-    int J = 0, qi = 0;
-    uint32_t mended = 0;            // parity of each slot's next mending
-    uint32_t weights[2] = {0, 0};   // parity of p_full
+    uint32_t mended = 0;           // parity of each slot's next mending
+    uint32_t weights[2] = {0, 0};  // parity of p_full
     bool ok = true;
-    // O_w (+)= P_w V of tile t, the J-th; `last` stream of the tile gives the slot back
-    auto product = [&](int w, int t, int j, bool add, bool wait_values, bool last) {
-        const int slot = S::value_turn(j) % S::kStages;
+    // O_w (+)= P_w V of tile J; `last` stream of the tile gives the slot back
+    auto product = [&](int w, bool masked, int J, bool add, bool wait_values, bool last) {
+        const int slot = S::value_turn(J) % S::kStages;
         if (wait_values) {
-            if (!attend_wait_warp(c, &c->full[slot], S::value_turn(j) / S::kStages & 1)) return false;
-            if (x.masked(t)) {
+            if (!attend_wait_warp(c, &c->full[slot], S::value_turn(J) / S::kStages & 1)) return false;
+            if (masked) {
                 if (!attend_wait_warp(c, &c->mended[slot], (mended >> slot) & 1u)) return false;
                 mended ^= 1u << slot;
             }
@@ -362,9 +361,11 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
         if (last) mma_commit(&c->empty[slot]);
         return true;
     };
-    auto scores = [&](int w, uint32_t q_at, int j) {
+    auto keys = [&](int J) { return &c->full[S::key_turn(J) % S::kStages]; };
+    auto keys_parity = [&](int J) { return (uint32_t)(S::key_turn(J) / S::kStages & 1); };
+    auto scores = [&](int w, uint32_t q_at, int J) {
         const uint32_t q = mma_operand(q_at, 16),
-                       k0 = mma_operand(ring + S::key_turn(j) % S::kStages * S::kTileBytes, 16);
+                       k0 = mma_operand(ring + S::key_turn(J) % S::kStages * S::kTileBytes, 16);
 #pragma unroll
         for (int k = 0; k < DT / 16; ++k) {
             const uint32_t at = ((k / 4) * S::kBlockBytes + (k % 4) * 32) / 16;
@@ -372,55 +373,70 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
         }
         mma_commit(&c->s_full[w]);
     };
-    while (ok && walk.item(a, &x)) {
-        const int turn = qi % kTurns;
-        if (!attend_wait_warp(c, &c->q_full[turn], (qi / kTurns) & 1)) break;
-        ++qi;
-        tmem_fence_after();
-        const uint32_t q = queries + (NB == 1 ? turn * S::kTileBytes : 0);
-        const int n = x.t1 - x.t0, streams = NB == 2 && x.nodes > a.plan.nodes ? 2 : 1;
-        auto keys = [&](int j) { return &c->full[S::key_turn(J + j) % S::kStages]; };
-        auto keys_parity = [&](int j) { return (uint32_t)(S::key_turn(J + j) / S::kStages & 1); };
-        auto keys_done = [&](int j) {
-            mma_commit(&c->empty[S::key_turn(J + j) % S::kStages]);
-            if (j == n - 1) mma_commit(&c->q_empty[turn]);
-        };
-        if (NB == 1) {
-            long long since = clock64();
-            for (int s = 0, p = 0; ok && p < n;) {
-                if (p < s && __all_sync(0xffffffffu, mbar_test(&c->p_full[p & 1][0], weights[p & 1]))) {
-                    ok = product(p & 1, x.t0 + p, J + p, p >= 2, true, true);
-                    if (p >= n - 2) mma_commit(&c->o_full[p & 1]);
-                    ++p;
-                } else if (s < n && s < p + 2 && __all_sync(0xffffffffu, mbar_test(keys(s), keys_parity(s)))) {
-                    scores(s & 1, q, J + s);
-                    keys_done(s);
-                    ++s;
-                } else {
-                    if (__any_sync(0xffffffffu, c->dead != 0 || clock64() - since > kAtWaitClocks)) {
-                        c->dead = 1;
-                        ok = false;
-                    }
-                    continue;
+    if (NB == 1) {
+        // s: the tile whose scores come next, p: whose product; p <= s <= p + 2, and s may be an item ahead
+        AttendItem xs, xp;
+        AttendWalk walk_p = walk;
+        bool more_s = walk.item(a, &xs), more_p = walk_p.item(a, &xp);
+        int s = 0, p = 0, ts = xs.t0, tp = xp.t0, qi = 0, ready = -1;
+        long long since = clock64();
+        while (ok && more_p) {
+            const int w = p & 1;
+            if (p < s && __all_sync(0xffffffffu, mbar_test(&c->p_full[w][0], weights[w]))) {
+                ok = product(w, xp.masked(tp), p, tp - xp.t0 >= 2, true, true);
+                if (tp >= xp.t1 - 2) mma_commit(&c->o_full[w]);
+                ++p;
+                if (++tp == xp.t1) {
+                    more_p = walk_p.item(a, &xp);
+                    tp = xp.t0;
                 }
-                since = clock64();
+            } else if (more_s && s < p + 2 &&
+                       (ready == qi || __all_sync(0xffffffffu, mbar_test(&c->q_full[qi & 1], (qi >> 1) & 1))) &&
+                       __all_sync(0xffffffffu, mbar_test(keys(s), keys_parity(s)))) {
+                ready = qi;  // this item's queries are there
+                tmem_fence_after();
+                scores(s & 1, queries + (qi & 1) * S::kTileBytes, s);
+                mma_commit(&c->empty[S::key_turn(s) % S::kStages]);
+                ++s;
+                if (++ts == xs.t1) {
+                    mma_commit(&c->q_empty[qi & 1]);
+                    ++qi;
+                    more_s = walk.item(a, &xs);
+                    ts = xs.t0;
+                }
+            } else {
+                if (__any_sync(0xffffffffu, c->dead != 0 || clock64() - since > kAtWaitClocks)) {
+                    c->dead = 1;
+                    ok = false;
+                }
+                continue;
             }
-        } else {
+            since = clock64();
+        }
+    } else {
+        AttendItem x;
+        for (int J = 0, qi = 0; ok && walk.item(a, &x); ++qi) {
+            if (!attend_wait_warp(c, &c->q_full[0], qi & 1)) break;
+            tmem_fence_after();
+            const int n = x.t1 - x.t0, streams = x.nodes > a.plan.nodes ? 2 : 1;
             for (int j = 0; ok && j <= n; ++j)
                 for (int w = 0; ok && w < streams; ++w) {
                     // the values' product goes first: it gives back the slot that a coming tile waits for
-                    if (j >= 1) ok = product(w, x.t0 + j - 1, J + j - 1, j >= 2, w == 0, w == streams - 1);
+                    if (j >= 1) ok = product(w, x.masked(x.t0 + j - 1), J + j - 1, j >= 2, w == 0, w == streams - 1);
                     if (j == n) {
                         if (ok) mma_commit(&c->o_full[w]);
                         continue;
                     }
-                    if (w == 0) ok = ok && attend_wait_warp(c, keys(j), keys_parity(j));
+                    if (w == 0) ok = ok && attend_wait_warp(c, keys(J + j), keys_parity(J + j));
                     if (!ok) break;
-                    scores(w, q + w * S::kTileBytes, J + j);
-                    if (w == streams - 1) keys_done(j);
+                    scores(w, queries + w * S::kTileBytes, J + j);
+                    if (w == streams - 1) {
+                        mma_commit(&c->empty[S::key_turn(J + j) % S::kStages]);
+                        if (j == n - 1) mma_commit(&c->q_empty[0]);
+                    }
                 }
+            J += n;
         }
-        J += n;
     }
     // no product is on its way when tensor memory is freed
     mma_commit(&c->drain);
@@ -528,7 +544,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
     int J = 0;
     AttendItem x;
     while (walk.item(a, &x)) {
-        const int n = x.t1 - x.t0, first = NB == 2 ? w * a.plan.nodes : 0;  // the block's first node in the item
+        const int n = x.t1 - x.t0, J0 = J, first = NB == 2 ? w * a.plan.nodes : 0;  // the block's first node in the item
         const int live_rows = min(x.nodes - first, a.plan.nodes) * a.group;
         if (NB == 2 && live_rows <= 0) {  // the second block is empty
             for (int t = x.t0; t < x.t1; ++t, ++J)
@@ -547,7 +563,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
             const int slot = S::value_turn(J) % S::kStages;
             const uint32_t mend_parity = (mended >> slot) & 1u;
             if (masked) mended ^= 1u << slot;
-            if (NB == 1 && ((t - x.t0) & 1) != w) continue;
+            if (NB == 1 && (J & 1) != w) continue;
             if (!attend_wait_warp(c, &c->s_full[w], scored)) return;
             scored ^= 1u;
             if (masked && !attend_wait_warp(c, &c->mended[slot], mend_parity)) return;
@@ -627,25 +643,23 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         }
         // the item's end
         float total = l.x + l.y;
-        float f0 = 1.0f, f1 = 0.0f;  // factors of the streams' outputs
-        const bool both = NB == 1 && n >= 2;
+        float f[2] = {1.0f, 0.0f};  // factors of the streams' outputs
+        const bool used[2] = {n >= 2 || (J0 & 1) == 0, n >= 2 || (J0 & 1) == 1};
         if (NB == 1) {
             c->ml[w][row] = make_float2(m, total);
             attend_arrive_warp(&c->ml_full);
             if (!attend_wait_warp(c, &c->ml_full, met)) return;
             const float2 p = c->ml[0][row], q = c->ml[1][row];
             m = fmaxf(p.x, q.x);
-            f0 = exp2_fast((p.x - m) * a.c);
-            f1 = both ? exp2_fast((q.x - m) * a.c) : 0.0f;
-            total = p.y * f0 + (both ? q.y * f1 : 0.0f);
-        }
-        if (NB == 1) {
-            if (!attend_wait_warp(c, &c->o_full[0], done[0])) return;
-            done[0] ^= 1u;
-            if (both) {
-                if (!attend_wait_warp(c, &c->o_full[1], done[1])) return;
-                done[1] ^= 1u;
-            }
+            f[0] = used[0] ? exp2_fast((p.x - m) * a.c) : 0.0f;
+            f[1] = used[1] ? exp2_fast((q.x - m) * a.c) : 0.0f;
+            total = (used[0] ? p.y * f[0] : 0.0f) + (used[1] ? q.y * f[1] : 0.0f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (used[i]) {
+                    if (!attend_wait_warp(c, &c->o_full[i], done[i])) return;
+                    done[i] ^= 1u;
+                }
         } else {
             if (!attend_wait_warp(c, &c->o_full[w], done[0])) return;
             done[0] ^= 1u;
@@ -669,10 +683,10 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                 tmem_load16(o_at + col, reinterpret_cast<uint32_t*>(o));
                 if (NB == 1) {
                     float o1[16];
-                    if (both) tmem_load16(o_at + DT + col, reinterpret_cast<uint32_t*>(o1));
+                    tmem_load16(o_at + DT + col, reinterpret_cast<uint32_t*>(o1));
                     tmem_wait_load();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = o[k] * f0 + (both ? o1[k] * f1 : 0.0f);
+                    for (int k = 0; k < 16; ++k) o[k] = (used[0] ? o[k] * f[0] : 0.0f) + (used[1] ? o1[k] * f[1] : 0.0f);
                 } else {
                     tmem_wait_load();
                 }
@@ -779,97 +793,96 @@ __device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int gro
     return (int)(((unit + 1) * groups - 1) / units);
 }
 
-// Joins the results of items that several groups shared: a CTA per request, key
-// head and block.  A warp finds a row's reference and sum over the parts, then
-// every thread adds up four columns of a row, with the parts' loads in flight.
+// Joins the results of an item that several groups share: a CTA takes an eighth
+// of a block's (row, four columns) pairs.  The threads that share a row find its
+// reference and sum together, in the same order everywhere.
 template <typename T, int DT, int NB>
-__device__ __forceinline__ void attend_join(const AttendArgs& a, int index) {
-    __shared__ float2 sh_row[kAtTile];  // reference, 1 / sum
-    const int per = a.plan.chunks * a.plan.share * NB;  // blocks of a request's head
-    const int b = index / (a.kv_heads * per), head = index / per % a.kv_heads, block = index % per;
-    const AttendRequest r = attend_request(a, b);
-    const int tiles = attend_tiles(r), node0 = block * a.plan.nodes, rows = min(r.n - node0, a.plan.nodes) * a.group;
-    if (tiles == 0 || rows <= 0) return;
-    const int pair = block / NB, chunk = pair / a.plan.share, share = pair % a.plan.share;
-    const int64_t units = a.first[a.B], begin = a.first[b] + (int64_t)(head * a.plan.chunks + chunk) * tiles;
+__device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int share, int w, int piece, int* sh) {
+    const int tid = threadIdx.x;
+    const int64_t units = a.first[a.B];
     const int groups = attend_groups(a, units);
-    const int g0 = attend_group(begin, units, groups), g1 = attend_group(begin + tiles - 1, units, groups);
-    if (g0 == g1) return;
+    if (g0 + 1 >= groups) return;
+    // the item at the end of group g0's run, if it goes on and began in it
+    const int64_t run = units * g0 / groups, next = units * (g0 + 1) / groups;
+    for (int b = tid; b < a.B; b += kAtPrepNT)
+        if (a.first[b] < next && next <= a.first[b + 1]) *sh = b;  // the request of unit next - 1
+    __syncthreads();
+    const int b = *sh;
+    if (a.err[b] | (a.parent ? a.tree_err[a.parent_stride ? b : 0] : 0)) return;  // it gets zeros
+    const AttendRequest r = attend_request(a, b);
+    const int tiles = attend_tiles(r), i = (int)(next - 1 - a.first[b]) / tiles;
+    const int64_t begin = a.first[b] + (int64_t)i * tiles, end = begin + tiles;
+    if (end <= next || begin < run) return;
+    const int head = i / a.plan.chunks, block = ((i - head * a.plan.chunks) * a.plan.share + share) * NB + w;
+    const int node0 = block * a.plan.nodes, rows = min(r.n - node0, a.plan.nodes) * a.group;
+    if (rows <= 0) return;
+    const int g1 = attend_group(end - 1, units, groups);
     constexpr int R = NB * kAtTile;
-    const int row0 = (block % NB) * kAtTile;
     // the first group's part is the end of its run, the others' the beginning of theirs
     auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.share + share) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
-    for (int row = threadIdx.x >> 5; row < rows; row += kAtPrepNT / 32) {
-        const int lane = threadIdx.x & 31;
-        float m = kNoMax, l = 0.0f;
-        for (int g = g0 + lane; g <= g1; g += 32) {
-            const float2 ml = reinterpret_cast<const float2*>(part(g))[row0 + row];
-            const float top = fmaxf(m, ml.x);
-            l = l * exp2f((m - top) * a.c) + ml.y * exp2f((ml.x - top) * a.c);
-            m = top;
-        }
-        const float top = warp_max_redux(m);
-        l *= exp2f((m - top) * a.c);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) sh_row[row] = make_float2(top, 1.0f / l);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (a.dim / 4); i += kAtPrepNT) {
-        const int row = i % rows, d = i / rows;
-        const float2 of = sh_row[row];
+    const int pairs = rows * (a.dim / 4), each = (pairs + kAtPieces - 1) / kAtPieces;
+    for (int k = piece * each + tid; k < min(pairs, (piece + 1) * each); k += kAtPrepNT) {
+        const int d = k / rows, row = k - d * rows, at = w * kAtTile + row;
+        float m = kNoMax;
+#pragma unroll 8
+        for (int g = g0; g <= g1; ++g) m = fmaxf(m, reinterpret_cast<const float2*>(part(g))[at].x);
+        float l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
         for (int g = g0; g <= g1; ++g) {
             const float* p = part(g);
-            const float f = exp2f((reinterpret_cast<const float2*>(p)[row0 + row].x - of.x) * a.c) * of.y;
-            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + row0 + row];
+            const float2 ml = reinterpret_cast<const float2*>(p)[at];
+            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + at];
+            const float f = exp2f((ml.x - m) * a.c);
+            l += f * ml.y;
             o.x += f * v.x;
             o.y += f * v.y;
             o.z += f * v.z;
             o.w += f * v.w;
         }
+        const float inv = 1.0f / l;
         const int node = row / a.group;
         uint2 v;
-        v.x = Pair<T>::put(o.x, o.y);
-        v.y = Pair<T>::put(o.z, o.w);
+        v.x = Pair<T>::put(o.x * inv, o.y * inv);
+        v.y = Pair<T>::put(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
                                   d * 4) = v;
     }
 }
 
-// After the attention: joins, refused requests' zeros, and what was found.  The
-// first CTAs have a request's zeros or the error word, the others join.
+// After the attention: joins, then refused requests' zeros and what was found.
+// CTAs 0 .. zeros - 1 have every zeros-th request, the first the error word; the
+// others a group's last item each, in pieces.  (A CTA for every block of every request
+// took 41 us of 320 where 75 were to be joined, in turns of a microsecond.)
 template <typename T, int DT, int NB>
-__global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_constant__ AttendArgs a) {
-    __shared__ int sh_err;
+__global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_constant__ AttendArgs a, int zeros) {
+    __shared__ int sh;
     rows_begin();
     const int tid = threadIdx.x;
     auto err_of = [&](int b) { return a.err[b] | (a.parent ? a.tree_err[a.parent_stride ? b : 0] : 0); };
-    if (blockIdx.x > 0) {
-        const int index = blockIdx.x - 1, b = index / (a.kv_heads * a.plan.chunks * a.plan.share * NB);
-        const int err = err_of(b);
-        if (!err) {
-            attend_join<T, DT, NB>(a, index);
-            return;
-        }
-        // the CTAs of a refused request share its zeros
-        const AttendRequest r = attend_request(a, b);
-        const int n = r.n < 0 || r.n > a.N ? a.N : r.n, ctas = a.kv_heads * a.plan.chunks * a.plan.share * NB;
-        const int64_t each = (int64_t)a.q_heads * a.dim / 8;
-        uint4* out = reinterpret_cast<uint4*>(a.out) + (int64_t)b * a.N * each;
-        for (int64_t i = (int64_t)(index - b * ctas) * kAtPrepNT + tid; i < n * each; i += (int64_t)ctas * kAtPrepNT)
-            out[i] = make_uint4(0, 0, 0, 0);
+    if ((int)blockIdx.x >= zeros) {
+        const int i = blockIdx.x - zeros, piece = i % kAtPieces, w = i / kAtPieces % NB,
+                  share = i / (kAtPieces * NB) % a.plan.share;
+        attend_join<T, DT, NB>(a, i / (kAtPieces * NB) / a.plan.share, share, w, piece, &sh);
         return;
     }
-    if (!a.dev_error) return;
-    if (tid == 0) sh_err = *a.late;
-    __syncthreads();
-    int err = 0;
-    for (int b = tid; b < a.B; b += kAtPrepNT) err |= err_of(b);
-    if (err) atomicOr(&sh_err, err);
-    __syncthreads();
-    if (tid == 0) *a.dev_error = sh_err;
+    if (blockIdx.x == 0 && a.dev_error) {
+        if (tid == 0) sh = *a.late;
+        __syncthreads();
+        int err = 0;
+        for (int b = tid; b < a.B; b += kAtPrepNT) err |= err_of(b);
+        if (err) atomicOr(&sh, err);
+        __syncthreads();
+        if (tid == 0) *a.dev_error = sh;
+    }
+    const int64_t each = (int64_t)a.q_heads * a.dim / 8;
+    for (int b = blockIdx.x; b < a.B; b += zeros) {
+        if (!err_of(b)) continue;
+        const AttendRequest r = attend_request(a, b);
+        const int n = r.n < 0 || r.n > a.N ? a.N : r.n;
+        uint4* out = reinterpret_cast<uint4*>(a.out) + (int64_t)b * a.N * each;
+        for (int64_t i = tid; i < n * each; i += kAtPrepNT) out[i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
 static AttendPlan attend_plan(int N, int group, int ctas) {
@@ -945,8 +958,8 @@ static cudaError_t launch_attend(AttendArgs a, const AttendMaps& maps, cudaStrea
     e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.share), dim3(kAtNT), kAttendSmem<DT>, st, a, maps.q,
                          maps.k, maps.v);
     if (e != cudaSuccess) return e;
-    const int64_t joins = (int64_t)a.B * a.kv_heads * a.plan.chunks * a.plan.share * NB;
-    return launch_dependent(k_attend_finish<T, DT, NB>, dim3((unsigned)(1 + joins)), dim3(kAtPrepNT), 0, st, a);
+    const int zeros = a.B < 64 ? a.B : 64, joins = a.plan.groups * a.plan.share * NB * kAtPieces;
+    return launch_dependent(k_attend_finish<T, DT, NB>, dim3(zeros + joins), dim3(kAtPrepNT), 0, st, a, zeros);
 }
 template <typename T>
 static cudaError_t launch_attend(const AttendArgs& a, const AttendMaps& maps, cudaStream_t st) {
@@ -984,9 +997,9 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
         group > kAtTile)
         return SPEC_ERR_UNSUPPORTED;
     const AttendPlan plan = attend_plan(N, group, kAtMaxCtas);
-    // units, and the last launch's CTAs, in 31 bits
+    // units in 31 bits
     const int64_t parts = (int64_t)B * layout->heads * plan.chunks, tiles = (capacity + kAtTile - 1) / kAtTile;
-    if (tiles > 0x7fffffffLL || parts * plan.share * plan.blocks > 0x7ffffffeLL || parts > 0x7fffffffLL / tiles)
+    if (tiles > 0x7fffffffLL || parts > 0x7fffffffLL / tiles)
         return SPEC_ERR_UNSUPPORTED;
     if ((q_request_stride | q_node_stride | q_head_stride | layout->block_stride | layout->entry_stride |
          layout->head_stride) % 8 ||
