@@ -20,13 +20,16 @@ constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 
 // The query rows of a request and a key head: a block has as many whole nodes as
 // fit in 128 rows, row i * group + j being head h * group + j of its node i.  A
-// CTA takes one or two blocks (`blocks`) and a run of tiles.  Work is counted in
-// units: (request, key head, chunk of blocks, tile) in this order, shared out
-// evenly among `groups` groups of `share` CTAs; the CTAs of a group take the
-// chunk's blocks, over the same tiles.
+// CTA takes one or two blocks (`blocks`) of one head and a run of tiles.  The
+// CTAs of a group go over the same tiles at the same time, `heads` heads beside
+// each other and `share` parts of the blocks: entries of several heads lie
+// together in memory, and parts read the same ones.  Work is counted in units:
+// (request, set of heads, chunk of blocks, tile) in this order, shared out
+// evenly among `groups` groups.
 struct AttendPlan {
     int nodes;  // of a block
-    int blocks, chunks, share, groups;
+    int blocks, chunks, share, heads, groups;
+    __host__ __device__ int ctas() const { return share * heads; }  // of a group
 };
 
 struct AttendArgs {
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_prepare(AttendArgs a) {
     const int tid = threadIdx.x;
     if (blockIdx.x == 0) {
         const int each = (a.B + kAtPrepNT - 1) / kAtPrepNT, b0 = min(tid * each, a.B), b1 = min(b0 + each, a.B);
-        const int times = a.kv_heads * a.plan.chunks;
+        const int times = a.kv_heads / a.plan.heads * a.plan.chunks;
         int sum = 0;
         for (int b = b0; b < b1; ++b) {
             const AttendRequest r = attend_request(a, b);
@@ -133,7 +136,7 @@ __device__ __forceinline__ int attend_groups(const AttendArgs& a, int64_t units)
 }
 // The items of a CTA, one after the other; every role walks them for itself.
 struct AttendWalk {
-    int u, u1, b, start, next, share;
+    int u, u1, b, start, next, share, head;
     AttendRequest r;
     int tiles;
     __device__ __forceinline__ void request(const AttendArgs& a) {
@@ -142,7 +145,9 @@ struct AttendWalk {
     }
     // b0: the request of unit u0 (any value when there are no units)
     __device__ __forceinline__ AttendWalk(const AttendArgs& a, int u0, int end, int b0) : u(u0), u1(end), b(b0) {
-        share = blockIdx.x % a.plan.share;
+        const int i = blockIdx.x % a.plan.ctas();
+        head = i / a.plan.share;
+        share = i - head * a.plan.share;
         if (u >= u1) return;
         start = a.first[b];
         next = a.first[b + 1];
@@ -162,9 +167,9 @@ struct AttendWalk {
             x->t0 = at - i * tiles;
             x->t1 = min(tiles, x->t0 + (u1 - u));
             u += x->t1 - x->t0;
-            x->head = i / a.plan.chunks;
-            const int most = a.plan.blocks * a.plan.nodes;
-            x->node0 = ((i - x->head * a.plan.chunks) * a.plan.share + share) * most;
+            const int set = i / a.plan.chunks, most = a.plan.blocks * a.plan.nodes;
+            x->head = set * a.plan.heads + head;
+            x->node0 = ((i - set * a.plan.chunks) * a.plan.share + share) * most;
             x->nodes = min(r.n - x->node0, most);
             if (x->nodes <= 0) continue;  // a request of fewer nodes than N
             x->b = b;
@@ -760,7 +765,7 @@ __global__ void __launch_bounds__(kAtNT, 1)
     tmem_fence_after();
     const uint32_t tmem = c->tmem, queries = smem_addr(sh_attend), ring = queries + S::kQueryBytes;
     const int64_t units = a.first[a.B];
-    const int g = blockIdx.x / a.plan.share;
+    const int g = blockIdx.x / a.plan.ctas();
     const int groups = attend_groups(a, units);
     const int u0 = (int)(units * min(g, groups) / groups), u1 = (int)(units * min(g + 1, groups) / groups);
     if (u0 < u1)
@@ -797,7 +802,7 @@ __device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int gro
 // of a block's (row, four columns) pairs.  The threads that share a row find its
 // reference and sum together, in the same order everywhere.
 template <typename T, int DT, int NB>
-__device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int share, int w, int piece, int* sh) {
+__device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta, int w, int piece, int* sh) {
     const int tid = threadIdx.x;
     const int64_t units = a.first[a.B];
     const int groups = attend_groups(a, units);
@@ -813,13 +818,14 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int sha
     const int tiles = attend_tiles(r), i = (int)(next - 1 - a.first[b]) / tiles;
     const int64_t begin = a.first[b] + (int64_t)i * tiles, end = begin + tiles;
     if (end <= next || begin < run) return;
-    const int head = i / a.plan.chunks, block = ((i - head * a.plan.chunks) * a.plan.share + share) * NB + w;
+    const int set = i / a.plan.chunks, beside = cta / a.plan.share, share = cta - beside * a.plan.share;
+    const int head = set * a.plan.heads + beside, block = ((i - set * a.plan.chunks) * a.plan.share + share) * NB + w;
     const int node0 = block * a.plan.nodes, rows = min(r.n - node0, a.plan.nodes) * a.group;
     if (rows <= 0) return;
     const int g1 = attend_group(end - 1, units, groups);
     constexpr int R = NB * kAtTile;
     // the first group's part is the end of its run, the others' the beginning of theirs
-    auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.share + share) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
+    auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.ctas() + cta) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
     const int pairs = rows * (a.dim / 4), each = (pairs + kAtPieces - 1) / kAtPieces;
     for (int k = piece * each + tid; k < min(pairs, (piece + 1) * each); k += kAtPrepNT) {
         const int d = k / rows, row = k - d * rows, at = w * kAtTile + row;
@@ -862,8 +868,8 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_consta
     auto err_of = [&](int b) { return a.err[b] | (a.parent ? a.tree_err[a.parent_stride ? b : 0] : 0); };
     if ((int)blockIdx.x >= zeros) {
         const int i = blockIdx.x - zeros, piece = i % kAtPieces, w = i / kAtPieces % NB,
-                  share = i / (kAtPieces * NB) % a.plan.share;
-        attend_join<T, DT, NB>(a, i / (kAtPieces * NB) / a.plan.share, share, w, piece, &sh);
+                  cta = i / (kAtPieces * NB) % a.plan.ctas();
+        attend_join<T, DT, NB>(a, i / (kAtPieces * NB) / a.plan.ctas(), cta, w, piece, &sh);
         return;
     }
     if (blockIdx.x == 0 && a.dev_error) {
@@ -885,20 +891,24 @@ __global__ void __launch_bounds__(kAtPrepNT) k_attend_finish(const __grid_consta
     }
 }
 
-static AttendPlan attend_plan(int N, int group, int ctas) {
+static AttendPlan attend_plan(int N, int heads, int group, int ctas) {
     AttendPlan p;
     p.nodes = kAtTile / group;
     p.blocks = N > p.nodes ? 2 : 1;
     const int parts = (N + p.blocks * p.nodes - 1) / (p.blocks * p.nodes);
     p.chunks = (parts + kAtShare - 1) / kAtShare;
     p.share = (parts + p.chunks - 1) / p.chunks;
-    p.groups = ctas / p.share;
+    // the most heads, of up to 8, whose groups leave no more than a twentieth of the CTAs out
+    p.heads = 1;
+    for (int n = 2; n <= 8; ++n)
+        if (heads % n == 0 && ctas / (p.share * n) * (p.share * n) * 20 >= ctas * 19) p.heads = n;
+    p.groups = ctas / p.ctas();
     return p;
 }
 struct AttendSpace {
     size_t err, tree_err, first, late, masks, part, total;
 };
-static AttendSpace attend_space(int B, int N, int group, int dim) {
+static AttendSpace attend_space(int B, int N, int heads, int group, int dim) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     AttendSpace s;
     s.err = 0;
@@ -907,7 +917,7 @@ static AttendSpace attend_space(int B, int N, int group, int dim) {
     s.late = s.first + up(((size_t)B + 1) * 4);
     s.masks = s.late + 256;
     s.part = s.masks + up((size_t)B * N * ((N + 31) / 32) * 4);
-    const int rows = attend_plan(N, group, kAtMaxCtas).blocks * kAtTile, cols = dim > 64 ? 128 : 64;
+    const int rows = attend_plan(N, heads, group, kAtMaxCtas).blocks * kAtTile, cols = dim > 64 ? 128 : 64;
     s.total = s.part + (size_t)kAtMaxCtas * 2 * rows * (cols + 2) * 4;
     return s;
 }
@@ -951,14 +961,14 @@ static cudaError_t launch_attend(AttendArgs a, const AttendMaps& maps, cudaStrea
     LaunchShape shape;
     if (!launch_shape(reinterpret_cast<const void*>(k_attend<T, DT, NB>), kAttendSmem<DT>, kAtNT, &shape))
         return cudaErrorUnknown;
-    a.plan = attend_plan(a.N, a.group, shape.sms < kAtMaxCtas ? shape.sms : kAtMaxCtas);
+    a.plan = attend_plan(a.N, a.kv_heads, a.group, shape.sms < kAtMaxCtas ? shape.sms : kAtMaxCtas);
     const int trees = !a.parent ? 0 : a.parent_stride ? a.B : 1;
     cudaError_t e = launch_dependent(k_attend_prepare, dim3(1 + trees), dim3(kAtPrepNT), 0, st, a);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.share), dim3(kAtNT), kAttendSmem<DT>, st, a, maps.q,
+    e = launch_dependent(k_attend<T, DT, NB>, dim3(a.plan.groups * a.plan.ctas()), dim3(kAtNT), kAttendSmem<DT>, st, a, maps.q,
                          maps.k, maps.v);
     if (e != cudaSuccess) return e;
-    const int zeros = a.B < 64 ? a.B : 64, joins = a.plan.groups * a.plan.share * NB * kAtPieces;
+    const int zeros = a.B < 64 ? a.B : 64, joins = a.plan.groups * a.plan.ctas() * NB * kAtPieces;
     return launch_dependent(k_attend_finish<T, DT, NB>, dim3(zeros + joins), dim3(kAtPrepNT), 0, st, a, zeros);
 }
 template <typename T>
@@ -974,7 +984,7 @@ using namespace sv;
 
 extern "C" size_t spec_tree_attention_workspace(int B, int N, int q_heads, int kv_heads, int dim) {
     if (B < 1 || N < 1 || q_heads < 1 || kv_heads < 1 || dim < 1 || q_heads % kv_heads) return 0;
-    return attend_space(B, N, q_heads / kv_heads, dim).total;
+    return attend_space(B, N, kv_heads, q_heads / kv_heads, dim).total;
 }
 
 extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int B, int N, int q_heads,
@@ -996,7 +1006,7 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
     if (B > kMaxRequests || N > kMaxDraftNodes || layout->dim % 8 || layout->dim < 64 || layout->dim > 128 ||
         group > kAtTile)
         return SPEC_ERR_UNSUPPORTED;
-    const AttendPlan plan = attend_plan(N, group, kAtMaxCtas);
+    const AttendPlan plan = attend_plan(N, layout->heads, group, kAtMaxCtas);
     // units in 31 bits
     const int64_t parts = (int64_t)B * layout->heads * plan.chunks, tiles = (capacity + kAtTile - 1) / kAtTile;
     if (tiles > 0x7fffffffLL || parts > 0x7fffffffLL / tiles)
@@ -1006,7 +1016,7 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
         ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
           reinterpret_cast<uintptr_t>(out)) & 15u))
         return SPEC_ERR_UNSUPPORTED;
-    const AttendSpace s = attend_space(B, N, group, layout->dim);
+    const AttendSpace s = attend_space(B, N, layout->heads, group, layout->dim);
     if (!workspace || workspace_bytes < s.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPEC_ERR_WORKSPACE;
     if (!select_device_of(q)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
