@@ -683,7 +683,7 @@ typedef struct {
  *   y = seen ? (x > 0 ? x / repetition : x * repetition) : x
  *   y = y - (frequency * c + presence * [c > 0]) + sum of v's biases
  *   y = -inf where v is not allowed (whatever x is; x is not read there).
- * In 32 bits, rounded once.  c is held up to 2^31 - 1.
+ * In 32 bits, rounded once.
  *
  *  logits, out  B * R rows of V elements, row r at r * row_stride (out:
  *               out_stride), bf16 or fp32; out may be logits itself with the
@@ -696,7 +696,7 @@ typedef struct {
  *  the request's paths empty (SPEC_DEVERR_PARENT).  Parameters that are no
  *  numbers act by the formula.
  *  B == 0 is valid.  Limits: V <= 524,280, R <= 1024, bias_count <= 1024,
- *  B <= 65,535 (SPEC_ERR_UNSUPPORTED).
+ *  history_capacity <= 536,000,000, B <= 65,535 (SPEC_ERR_UNSUPPORTED).
  */
 spec_status spec_adjust_logits(const void* logits, spec_dtype dtype, int B, int R, int V, int64_t row_stride,
                                const spec_adjustments* adjustments, void* out, int64_t out_stride,

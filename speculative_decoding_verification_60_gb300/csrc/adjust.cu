@@ -8,9 +8,13 @@ namespace sv {
 constexpr int kAdNT = 256;
 constexpr int kAdSlice = 4096;  // tokens of a CTA's slice
 constexpr int kAdMaxBias = 1024;
-constexpr int kAdAhead = 8;  // tokens of the history of a thread on their way at once
+constexpr int kAdMaxHistory = 536000000;  // with a path, below 2^29
+constexpr int kAdAhead = 8;     // tokens of the history of a lane on their way at once
+constexpr int kAdHistory = 32 * kAdAhead * 2;  // tokens of the history that a warp takes at a time
 constexpr int kAdFixes = 4;  // adjusted logits of a thread on their way at once
-constexpr uint32_t kAdSeen = 0x80000000u;  // a count's top bit: in the prompt
+// A token's cell: how often it was said (the prompt apart), and whether it is in
+// the prompt, was drafted, is biased.  Nothing happens to a token of cell 0.
+constexpr uint32_t kAdPrompt = 1u << 31, kAdDrafted = 1u << 30, kAdBiased = 1u << 29, kAdCount = kAdBiased - 1;
 
 struct AdjustArgs {
     const void* in;
@@ -21,22 +25,30 @@ struct AdjustArgs {
     int32_t* dev_error;
 };
 
-// What a slice keeps in shared memory: counts, biases (if there are any), which
-// tokens were drafted and which are biased, the tokens that anything happens to,
-// the draft's tokens and parents [R], and the slice's biases (id, value).
+// What a slice keeps in shared memory: its tokens' cells and biases (if there
+// are any), a list of tokens, the draft's tokens and parents [R], and the
+// slice's biases (place, value).  Cells and biases are laid out for lanes that
+// have a vector of VE tokens each: the token at place `at` is in row at % VE,
+// column at / VE.
 struct AdjustSlice {
-    uint32_t* count;
+    uint32_t* cell;
     float* bias;
-    uint32_t *drafted, *biased;
     uint16_t* list;
     int *token, *parent;
     int2* entry;
 };
+constexpr int kAdCells = kAdSlice + 8;
+template <int VE> __device__ __forceinline__ int adjust_cell(int at) { return (at % VE) * (kAdSlice / VE + 1) + at / VE; }
+template <int VE> __device__ __forceinline__ int adjust_place(int cell) {
+    const int row = cell / (kAdSlice / VE + 1);
+    return (cell - row * (kAdSlice / VE + 1)) * VE + row;
+}
 __host__ __device__ inline size_t adjust_smem(const AdjustArgs& a) {
-    return kAdSlice * (a.p.bias_ids ? 8 : 4) + kAdSlice / 4 + kAdSlice * 2 + (a.p.bias_ids ? (size_t)a.p.bias_count * 8 : 0) +
+    return kAdCells * (a.p.bias_ids ? 8 : 4) + kAdSlice * 2 + (a.p.bias_ids ? (size_t)a.p.bias_count * 8 : 0) +
            (a.p.drafted ? (size_t)a.R * 8 : 0);
 }
 
+// A request's penalties.
 struct Penalties {
     float repetition, frequency, presence;
 };
@@ -51,6 +63,18 @@ __device__ __forceinline__ float adjust_value(float x, uint32_t count, bool seen
 template <typename T> struct Logit;
 template <> struct Logit<__nv_bfloat16> {
     static constexpr int kVec = 8;
+    __device__ static __forceinline__ void get(const uint4& q, float* x) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+    __device__ static __forceinline__ uint4 put(const float* x) {
+        return make_uint4(Pair<__nv_bfloat16>::put(x[0], x[1]), Pair<__nv_bfloat16>::put(x[2], x[3]),
+                          Pair<__nv_bfloat16>::put(x[4], x[5]), Pair<__nv_bfloat16>::put(x[6], x[7]));
+    }
     // -inf where a bit of ok is not set
     __device__ static __forceinline__ void rule_out(uint4& q, uint32_t ok) {
         uint32_t* w = &q.x;
@@ -66,6 +90,15 @@ template <> struct Logit<__nv_bfloat16> {
 };
 template <> struct Logit<float> {
     static constexpr int kVec = 4;
+    __device__ static __forceinline__ void get(const uint4& q, float* x) {
+        x[0] = __uint_as_float(q.x);
+        x[1] = __uint_as_float(q.y);
+        x[2] = __uint_as_float(q.z);
+        x[3] = __uint_as_float(q.w);
+    }
+    __device__ static __forceinline__ uint4 put(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
     __device__ static __forceinline__ void rule_out(uint4& q, uint32_t ok) {
         uint32_t* w = &q.x;
 #pragma unroll
@@ -75,47 +108,57 @@ template <> struct Logit<float> {
     __device__ static __forceinline__ void store(float* p, float y) { *p = y; }
 };
 
-// A CTA takes a slice of the vocabulary for some rows of a request.  It counts
-// the request's history there once and lists the slice's tokens that anything
-// happens to (seen, drafted, biased).  Then it streams the rows with the mask
-// alone (a vector that the mask rules out is written without being read), and
-// then goes over the listed tokens of every row, which are still in L2: they
-// are one in a hundred, but some lane of a warp nearly always has one, so
-// adjusting them within the stream took three times as long, with branches or
-// without.  What a row's path adds to a count is found by walking up the tree.
+// A CTA takes a slice of the vocabulary for some rows of a request.  Its warps
+// draw their work from a counter: parts of the request's history, whose tokens
+// are counted where they fall into the slice, and parts of the rows, streamed
+// with the mask alone (a vector that the mask rules out is written without being
+// read).  After that, the slice's tokens that anything happens to (seen,
+// drafted, biased) are listed and adjusted in every row, which is still in L2:
+// they are one in a hundred, but some lane of a warp nearly always has one, so
+// adjusting them within the stream took 482 us where this takes 290 (256
+// requests of 9 rows), with or without branches.  Only where the history is
+// long next to the vocabulary, so that many tokens are seen, is it counted
+// first and every token computed within the stream.  What a row's path adds to
+// a count is found by walking up the tree.
 template <typename T>
-__global__ void __launch_bounds__(kAdNT) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
+__global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
+    constexpr int VE = Logit<T>::kVec;
     extern __shared__ __align__(16) uint32_t sh_adjust[];
-    __shared__ int sh_listed, sh_entries;
+    __shared__ int sh_listed, sh_task, sh_part;
     rows_begin();
     const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
     const int v0 = blockIdx.x * kAdSlice, v1 = min(v0 + kAdSlice, a.V), width = v1 - v0;
     const spec_adjustments& p = a.p;
     AdjustSlice s;
-    s.count = sh_adjust;
-    s.bias = reinterpret_cast<float*>(s.count + kAdSlice);
-    s.drafted = s.count + kAdSlice * (p.bias_ids ? 2 : 1);
-    s.biased = s.drafted + kAdSlice / 32;
-    s.list = reinterpret_cast<uint16_t*>(s.biased + kAdSlice / 32);
+    s.cell = sh_adjust;
+    s.bias = reinterpret_cast<float*>(s.cell + kAdCells);
+    s.list = reinterpret_cast<uint16_t*>(s.cell + kAdCells * (p.bias_ids ? 2 : 1));
     s.entry = reinterpret_cast<int2*>(s.list + kAdSlice);
     s.token = reinterpret_cast<int*>(s.entry + (p.bias_ids ? p.bias_count : 0));
     s.parent = s.token + a.R;
     int err = 0;
-    int rows = a.R;
-    if (p.n_nodes) {
-        rows = p.n_nodes[b];
-        if (rows < 0 || rows > a.R) {
-            err |= kDevErrLength;
-            rows = a.R;
-        }
-    }
+    int rows = p.n_nodes ? p.n_nodes[b] : a.R;
+    int told = p.history ? p.history_lens[b] : 0, said = p.history && p.prompt_lens ? p.prompt_lens[b] : 0;
     const Penalties q{p.repetition ? p.repetition[b] : 1.0f, p.frequency ? p.frequency[b] : 0.0f,
                       p.presence ? p.presence[b] : 0.0f};
     const bool penalties = q.repetition != 1.0f || q.frequency != 0.0f || q.presence != 0.0f;
-    if (penalties)
-        for (int i = tid; i < kAdSlice / 4; i += kAdNT) reinterpret_cast<uint4*>(s.count)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < kAdSlice / 32 * 2; i += kAdNT) s.drafted[i] = 0;
-    if (tid == 0) sh_listed = sh_entries = 0;
+    if (rows < 0 || rows > a.R) {
+        err |= kDevErrLength;
+        rows = a.R;
+    }
+    if (!penalties) told = said = 0;
+    if (told < 0 || told > p.history_capacity) {
+        err |= kDevErrLength;
+        told = 0;
+    }
+    if (said < 0 || said > told) {
+        err |= kDevErrLength;
+        said = said < 0 ? 0 : told;
+    }
+    const bool dense = (int64_t)told * 4 > a.V;
+    if (penalties || p.bias_ids)
+        for (int i = tid; i < kAdCells / 4; i += kAdNT) reinterpret_cast<uint4*>(s.cell)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sh_listed = sh_task = sh_part = 0;
     bool tree = true;
     if (p.drafted && penalties) {
         if (p.parent) tree = tree_part_ok(p.parent + b * p.parent_stride, rows, tid, kAdNT);
@@ -126,59 +169,27 @@ __global__ void __launch_bounds__(kAdNT) k_adjust_logits(const __grid_constant__
     }
     tree = __syncthreads_and(tree);
     if (!tree) err |= kDevErrParent;
-    if (p.history && penalties) {
-        int n = p.history_lens[b];
-        if (n < 0 || n > p.history_capacity) {
-            err |= kDevErrLength;
-            n = 0;
-        }
-        int said = p.prompt_lens ? p.prompt_lens[b] : 0;
-        if (said < 0 || said > n) {
-            err |= kDevErrLength;
-            said = said < 0 ? 0 : n;
-        }
-        const int32_t* ids = p.history + b * p.history_stride;
-        for (int i0 = tid; i0 < n; i0 += kAdNT * kAdAhead) {
-            int v[kAdAhead];
-#pragma unroll
-            for (int k = 0; k < kAdAhead; ++k) v[k] = ids[min(i0 + k * kAdNT, n - 1)];
-#pragma unroll
-            for (int k = 0; k < kAdAhead; ++k) {
-                const uint32_t at = (uint32_t)(v[k] - v0);
-                if ((uint32_t)v[k] >= (uint32_t)a.V) err |= kDevErrToken;
-                const int i = i0 + k * kAdNT;
-                if (at >= (uint32_t)width || i >= n) continue;
-                if (i >= said) atomicAdd(s.count + at, 1u);
-                else atomicOr(s.count + at, kAdSeen);
-            }
-        }
-    }
     if (p.drafted && penalties && tree)
         for (int i = 1 + tid; i < rows; i += kAdNT) {
             const int v = s.token[i];
             if (v < 0 || v >= a.V) err |= kDevErrToken;
-            if (v >= v0 && v < v1) atomicOr(s.drafted + ((v - v0) >> 5), 1u << ((v - v0) & 31));
+            if (v >= v0 && v < v1) atomicOr(s.cell + adjust_cell<VE>(v - v0), kAdDrafted);
         }
-    if (p.bias_ids) {
-        // the first warp picks the slice's biases, in order
-        if (tid < 32) {
-            const int32_t* ids = p.bias_ids + (int64_t)b * p.bias_count;
-            const float* values = p.bias_values + (int64_t)b * p.bias_count;
-            int n = 0;
-            for (int j0 = 0; j0 < p.bias_count; j0 += 32) {
-                const int j = j0 + lane, v = j < p.bias_count ? ids[j] : -1;
-                if (v < -1 || v >= a.V) err |= kDevErrToken;
-                const bool in = v >= v0 && v < v1;
-                const uint32_t all = __ballot_sync(0xffffffffu, in);
-                if (in) s.entry[n + __popc(all & ((1u << lane) - 1u))] = make_int2(v - v0, __float_as_int(values[j]));
-                n += __popc(all);
-            }
-            if (lane == 0) sh_entries = n;
+    if (p.bias_ids && tid < 32) {
+        // the first warp picks the slice's biases, in order; the first entry of an id sums them all
+        const int32_t* ids = p.bias_ids + (int64_t)b * p.bias_count;
+        const float* values = p.bias_values + (int64_t)b * p.bias_count;
+        int n = 0;
+        for (int j0 = 0; j0 < p.bias_count; j0 += 32) {
+            const int j = j0 + lane, v = j < p.bias_count ? ids[j] : -1;
+            if (v < -1 || v >= a.V) err |= kDevErrToken;
+            const bool in = v >= v0 && v < v1;
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            if (in) s.entry[n + __popc(all & ((1u << lane) - 1u))] = make_int2(v - v0, __float_as_int(values[j]));
+            n += __popc(all);
         }
-        __syncthreads();
-        // the first entry of an id sums them all, in order
-        const int n = sh_entries;
-        for (int j = tid; j < n; j += kAdNT) {
+        __syncwarp();
+        for (int j = lane; j < n; j += 32) {
             const int at = s.entry[j].x;
             float sum = 0.0f;
             bool first = true;
@@ -188,91 +199,158 @@ __global__ void __launch_bounds__(kAdNT) k_adjust_logits(const __grid_constant__
                     sum = k == j ? __int_as_float(s.entry[k].y) : sum + __int_as_float(s.entry[k].y);
                 }
             if (!first) continue;
-            s.bias[at] = sum;
-            atomicOr(s.biased + (at >> 5), 1u << (at & 31));
-        }
-    }
-    if (err) set_error(a.dev_error, err);
-    __syncthreads();
-    if (penalties || p.bias_ids) {
-        for (int i = tid; i < kAdSlice; i += kAdNT) {  // 32 tokens of a warp
-            const bool hit = ((s.drafted[i >> 5] | s.biased[i >> 5]) >> lane & 1u) || (penalties && s.count[i] != 0);
-            const uint32_t all = __ballot_sync(0xffffffffu, hit);
-            if (!all) continue;
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&sh_listed, __popc(all));
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1u));
-            if (hit) s.list[at] = (uint16_t)i;
+            s.bias[adjust_cell<VE>(at)] = sum;
+            atomicOr(s.cell + adjust_cell<VE>(at), kAdBiased);
         }
     }
 
-    constexpr int VE = Logit<T>::kVec;
+    // parts of the history
+    const int32_t* ids = p.history + b * p.history_stride;
+    auto history = [&](int part) {
+        const int first = part * kAdHistory + lane, end = min((part + 1) * kAdHistory, told);
+        for (int i0 = first; i0 < end; i0 += 32 * kAdAhead) {
+            int v[kAdAhead];
+#pragma unroll
+            for (int k = 0; k < kAdAhead; ++k) v[k] = ids[min(i0 + k * 32, end - 1)];
+#pragma unroll
+            for (int k = 0; k < kAdAhead; ++k) {
+                const uint32_t at = (uint32_t)(v[k] - v0);
+                if ((uint32_t)v[k] >= (uint32_t)a.V) err |= kDevErrToken;
+                const int i = i0 + k * 32;
+                if (at >= (uint32_t)width || i >= end) continue;
+                uint32_t* cell = s.cell + adjust_cell<VE>((int)at);
+                if (i >= said) atomicAdd(cell, 1u);
+                else atomicOr(cell, kAdPrompt);
+            }
+        }
+    };
+    // parts of the rows: 32 lanes of kAcross vectors
+    constexpr int kAcross = 8, kPart = 32 * kAcross, kParts = kAdSlice / VE / kPart;
+    constexpr uint32_t kAll = (1u << VE) - 1;
     const int r0 = blockIdx.z * a.rows, r1 = min(r0 + a.rows, rows);
     const int last_word = (a.V - 1) >> 5;
     auto row_of = [&](int r) { return (int64_t)b * a.R + r; };
     auto in_of = [&](int r) { return static_cast<const T*>(a.in) + row_of(r) * a.in_stride + v0; };
     auto out_of = [&](int r) { return static_cast<T*>(a.out) + row_of(r) * a.out_stride + v0; };
     auto allowed_of = [&](int r) { return reinterpret_cast<const uint32_t*>(p.allowed) + row_of(r) * p.allowed_stride; };
-    // a thread has kAcross vectors of a row, and kRows rows on their way at once
-    constexpr int kAcross = kAdSlice / VE / kAdNT, kRows = 4 / kAcross;
-    constexpr uint32_t kAll = (1u << VE) - 1;
-    for (int rb = r0; rb < r1; rb += kRows) {
-        const uint4* from[kRows];
-        uint4* to[kRows];
-        const uint32_t* allowed[kRows];
-        int head[kRows], vecs[kRows];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int r = min(rb + k, r1 - 1);
-            const T* in = in_of(r);
-            T* out = out_of(r);
-            allowed[k] = p.allowed ? allowed_of(r) : nullptr;
-            const uint32_t skew = (uint32_t)(reinterpret_cast<uintptr_t>(in) & 15u);
-            // vectors lie on 16 bytes in both; where in and out differ in alignment there are none
-            const bool same = skew == (uint32_t)(reinterpret_cast<uintptr_t>(out) & 15u);
-            head[k] = same ? min(width, (int)((16u - skew) & 15u) / (int)sizeof(T)) : width;
-            vecs[k] = rb + k < r1 ? (width - head[k]) / VE : 0;
-            from[k] = reinterpret_cast<const uint4*>(in + head[k]);
-            to[k] = reinterpret_cast<uint4*>(out + head[k]);
-            if (rb + k >= r1) continue;
+    // a logit of row r, by what the history, the path and the biases say
+    auto adjusted = [&](float x, int at, uint32_t cell, int r) {
+        uint32_t count = cell & kAdCount;
+        bool seen = (cell & (kAdCount | kAdPrompt)) != 0;
+        if (cell & kAdDrafted)
+            for (int i = r; i > 0; i = s.parent[i])
+                if (s.token[i] == v0 + at) {
+                    seen = true;
+                    ++count;
+                }
+        return adjust_value(x, count, seen, cell & kAdBiased ? s.bias[adjust_cell<VE>(at)] : 0.0f, q);
+    };
+    auto row_part = [&](int r, int part) {
+        const T* in = in_of(r);
+        T* out = out_of(r);
+        const uint32_t* allowed = p.allowed ? allowed_of(r) + (v0 >> 5) : nullptr;  // of the slice
+        const uint32_t skew = (uint32_t)reinterpret_cast<uintptr_t>(in) & 15u;
+        // vectors lie on 16 bytes in both; where in and out differ in alignment there are none
+        const bool same = skew == ((uint32_t)reinterpret_cast<uintptr_t>(out) & 15u);
+        const int head = same ? min(width, (int)((16u - skew) & 15u) / (int)sizeof(T)) : width;
+        const int vecs = (width - head) / VE, tail = head + vecs * VE;
+        if (head | (width - tail)) {
             auto single = [&](int at) {
-                const int v = v0 + at;
-                if (allowed[k] && !((allowed[k][v >> 5] >> (v & 31)) & 1u)) Logit<T>::store(out + at, -INFINITY);
+                const uint32_t cell = dense ? s.cell[adjust_cell<VE>(at)] : 0u;
+                if (allowed && !((allowed[at >> 5] >> (at & 31)) & 1u)) Logit<T>::store(out + at, -INFINITY);
+                else if (cell) Logit<T>::store(out + at, adjusted(Logit<T>::load(in + at), at, cell, r));
                 else out[at] = in[at];
             };
-            for (int at = tid; at < head[k]; at += kAdNT) single(at);
-            const int tail = head[k] + vecs[k] * VE;
-            if (tid < width - tail) single(tail + tid);
+            if (part == 0)
+                for (int at = lane; at < head; at += 32) single(at);
+            if (part == kParts - 1 && lane < width - tail) single(tail + lane);
         }
-        uint4 x[kRows][kAcross];
-        uint32_t ok[kRows][kAcross];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k)
+        const int i0 = part * kPart + lane;
+        const uint4* from = reinterpret_cast<const uint4*>(in + head) + i0;
+        uint4* to = reinterpret_cast<uint4*>(out + head) + i0;
+        uint4 x[kAcross];
+        uint32_t ok[kAcross];
+        if (allowed) {
+            const int last = last_word - (v0 >> 5);
+            uint32_t word[kAcross], next[kAcross];
 #pragma unroll
             for (int u = 0; u < kAcross; ++u) {
-                const int i = tid + u * kAdNT;
-                ok[k][u] = i < vecs[k] ? kAll : 0u;
-                if (p.allowed && i < vecs[k]) {
-                    const int v = v0 + head[k] + i * VE, w = v >> 5;
-                    ok[k][u] = __funnelshift_r(allowed[k][w], allowed[k][min(w + 1, last_word)], v & 31) & kAll;
-                }
+                const int w = min((head + (i0 + u * 32) * VE) >> 5, last);
+                word[u] = allowed[w];
+                next[u] = head % VE ? allowed[min(w + 1, last)] : 0u;  // a vector may end in the next word
             }
-#pragma unroll
-        for (int k = 0; k < kRows; ++k)
 #pragma unroll
             for (int u = 0; u < kAcross; ++u)
-                if (ok[k][u]) x[k][u] = from[k][tid + u * kAdNT];
+                ok[u] = i0 + u * 32 < vecs ? __funnelshift_r(word[u], next[u], (head + (i0 + u * 32) * VE) & 31) & kAll : 0u;
+        } else {
 #pragma unroll
-        for (int k = 0; k < kRows; ++k)
+            for (int u = 0; u < kAcross; ++u) ok[u] = i0 + u * 32 < vecs ? kAll : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kAcross; ++u)
+            if (ok[u]) x[u] = from[u * 32];
+        if (dense) {
 #pragma unroll
             for (int u = 0; u < kAcross; ++u) {
-                if (tid + u * kAdNT >= vecs[k]) continue;
-                if (ok[k][u] != kAll) Logit<T>::rule_out(x[k][u], ok[k][u]);
-                to[k][tid + u * kAdNT] = x[k][u];
+                if (!ok[u]) continue;
+                float y[VE];
+                Logit<T>::get(x[u], y);
+                const int at = head + (i0 + u * 32) * VE;
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    const uint32_t cell = s.cell[adjust_cell<VE>(at + k)];
+                    if (cell) y[k] = adjusted(y[k], at + k, cell, r);
+                }
+                x[u] = Logit<T>::put(y);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kAcross; ++u) {
+            if (i0 + u * 32 >= vecs) continue;
+            if (ok[u] != kAll) Logit<T>::rule_out(x[u], ok[u]);
+            to[u * 32] = x[u];
+        }
+    };
+    const int histories = (told + kAdHistory - 1) / kAdHistory, parts = max(r1 - r0, 0) * kParts;
+    auto draw = [&](int* counter) {
+        int t = 0;
+        if (lane == 0) t = atomicAdd(counter, 1);
+        return __shfl_sync(0xffffffffu, t, 0);
+    };
+    for (int t; (t = draw(&sh_task)) < histories + (dense ? 0 : parts);) {
+        if (t < histories) history(t);
+        else row_part(r0 + (t - histories) / kParts, (t - histories) % kParts);
+        __syncwarp();
     }
-    __syncthreads();  // the rows are written, and the list
-
+    if (err) set_error(a.dev_error, err);
+    __syncthreads();  // the counts are whole; the rows are written, but for a dense request's
+    if (dense) {
+        for (int t; (t = draw(&sh_part)) < parts;) {
+            row_part(r0 + t / kParts, t % kParts);
+            __syncwarp();
+        }
+        return;
+    }
+    if (!penalties && !p.bias_ids) return;
+    // the list: a thread looks at four cells at a time
+    constexpr int kLooks = (kAdCells / 4 + kAdNT - 1) / kAdNT;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int k = 0; k < kLooks; ++k) {
+        const int i = tid + k * kAdNT;
+        if (i >= kAdCells / 4) continue;
+        const uint4 c = reinterpret_cast<const uint4*>(s.cell)[i];
+        hits |= ((c.x != 0) | (c.y != 0) << 1 | (c.z != 0) << 2 | (c.w != 0) << 3) << (4 * k);
+    }
+    const int mine = __popc(hits), upto = warp_inclusive_scan_i(mine);
+    int to = 0;
+    if (lane == 31) to = atomicAdd(&sh_listed, upto);
+    to = __shfl_sync(0xffffffffu, to, 31) + upto - mine;
+    for (; hits; hits &= hits - 1) {
+        const int k = __ffs(hits) - 1;
+        s.list[to++] = (uint16_t)adjust_place<VE>((tid + (k >> 2) * kAdNT) * 4 + (k & 3));
+    }
+    __syncthreads();
     // a thread has every `places`-th listed token, in every `phases`-th row
     const int listed = sh_listed;
     int places = kAdNT;
@@ -280,10 +358,7 @@ __global__ void __launch_bounds__(kAdNT) k_adjust_logits(const __grid_constant__
     const int phases = kAdNT / places, phase = tid / places;
     for (int i = tid - phase * places; i < listed; i += places) {
         const int at = s.list[i], v = v0 + at;
-        auto marked = [&](const uint32_t* map) { return map[at >> 5] >> (at & 31) & 1u; };
-        const uint32_t n = penalties ? s.count[at] : 0u;
-        const bool drafted = marked(s.drafted);
-        const float bias = marked(s.biased) ? s.bias[at] : 0.0f;
+        const uint32_t cell = s.cell[adjust_cell<VE>(at)];
         const T* in = in_of(r0 + phase) + at;
         T* out = out_of(r0 + phase) + at;
         const uint32_t* allowed = p.allowed ? allowed_of(r0 + phase) + (v >> 5) : nullptr;
@@ -299,18 +374,8 @@ __global__ void __launch_bounds__(kAdNT) k_adjust_logits(const __grid_constant__
                 if (allowed) live[k] = allowed[k * allowed_step] >> (v & 31) & 1u;
             }
 #pragma unroll
-            for (int k = 0; k < kAdFixes; ++k) {
-                if (!live[k]) continue;
-                uint32_t count = n & ~kAdSeen;
-                bool seen = n != 0;
-                if (drafted)
-                    for (int i = r + k * phases; i > 0; i = s.parent[i])
-                        if (s.token[i] == v) {
-                            seen = true;
-                            ++count;
-                        }
-                Logit<T>::store(out + k * out_step, adjust_value(x[k], count, seen, bias, q));
-            }
+            for (int k = 0; k < kAdFixes; ++k)
+                if (live[k]) Logit<T>::store(out + k * out_step, adjusted(x[k], at, cell, r + k * phases));
             in += kAdFixes * in_step;
             out += kAdFixes * out_step;
             if (allowed) allowed += kAdFixes * allowed_step;
@@ -359,7 +424,7 @@ extern "C" spec_status spec_adjust_logits(const void* logits, spec_dtype dtype, 
     if (p.allowed && p.allowed_stride < (V + 31) / 32) return SPEC_ERR_INVALID_ARG;
     if (B > 0 && out == logits && out_stride != row_stride) return SPEC_ERR_INVALID_ARG;
     if ((int64_t)V > kRowsMaxVocab || R > kMaxDraftNodes || B > kMaxRequests ||
-        (p.bias_ids && p.bias_count > kAdMaxBias))
+        (p.bias_ids && p.bias_count > kAdMaxBias) || (p.history && p.history_capacity > kAdMaxHistory))
         return SPEC_ERR_UNSUPPORTED;
     if (B == 0 && !dev_error) return SPEC_OK;
     if (!select_device_of(B > 0 ? logits : dev_error)) return SPEC_ERR_INVALID_ARG;
