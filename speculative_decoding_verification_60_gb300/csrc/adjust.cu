@@ -7,6 +7,7 @@ namespace sv {
 
 constexpr int kAdNT = 256;
 constexpr int kAdSlice = 4096;  // tokens of a CTA's slice
+constexpr int kAdWaves = 2;     // of CTAs that rows are shared out for
 constexpr int kAdMaxBias = 1024;
 constexpr int kAdMaxHistory = 536000000;  // with a path, below 2^29
 constexpr int kAdAhead = 8;     // tokens of the history of a lane on their way at once
@@ -48,18 +49,36 @@ __host__ __device__ inline size_t adjust_smem(const AdjustArgs& a) {
            (a.p.drafted ? (size_t)a.R * 8 : 0);
 }
 
-// A request's penalties.
+// A request's penalties.  A product with 1 / repetition stands for the division
+// where neither leaves the range of 32 bits: 2^-23.4 of the value at most, and a
+// third of the time that the division takes over a row of seen tokens.
 struct Penalties {
-    float repetition, frequency, presence;
+    float repetition, inverse, frequency, presence;
+    bool divides;
 };
-__device__ __forceinline__ float adjust_value(float x, uint32_t count, bool seen, float bias, const Penalties& q) {
-    float y = x;
-    if (seen) {
-        y = x > 0.0f ? x / q.repetition : x * q.repetition;
-        y -= q.frequency * (float)count + (count ? q.presence : 0.0f);
-    }
-    return y + bias;
+__device__ __forceinline__ float adjust_value(float x, uint32_t cell, const Penalties& q) {
+    const uint32_t count = cell & kAdCount;
+    const float y = cell & (kAdCount | kAdPrompt) ? x * (x > 0.0f ? q.inverse : q.repetition) : x;
+    return count ? y - fmaf(q.frequency, (float)count, q.presence) : y;
 }
+// The same with all that is rare: a draft's tokens (those on the path to node i
+// count), biases, repetitions that have to be divided by.
+__device__ __noinline__ float adjust_rare(float x, int v, uint32_t cell, float bias, int i, const int* token,
+                                          const int* parent, const Penalties& q) {
+    uint32_t count = cell & kAdCount;
+    bool seen = (cell & (kAdCount | kAdPrompt)) != 0;
+    if (cell & kAdDrafted)
+        for (; i > 0; i = parent[i])
+            if (token[i] == v) {
+                seen = true;
+                ++count;
+            }
+    float y = x;
+    if (seen) y = x > 0.0f ? x / q.repetition : x * q.repetition;
+    if (count) y -= fmaf(q.frequency, (float)count, q.presence);
+    return cell & kAdBiased ? y + bias : y;
+}
+
 template <typename T> struct Logit;
 template <> struct Logit<__nv_bfloat16> {
     static constexpr int kVec = 8;
@@ -118,13 +137,14 @@ template <> struct Logit<float> {
 // adjusting them within the stream took 482 us where this takes 290 (256
 // requests of 9 rows), with or without branches.  Only where the history is
 // long next to the vocabulary, so that many tokens are seen, is it counted
-// first and every token computed within the stream.  What a row's path adds to
-// a count is found by walking up the tree.
+// first and the counts applied within the stream; then drafted and biased tokens
+// alone are listed.  What a row's path adds to a count is found by walking up
+// the tree.
 template <typename T>
 __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
     constexpr int VE = Logit<T>::kVec;
     extern __shared__ __align__(16) uint32_t sh_adjust[];
-    __shared__ int sh_listed, sh_task, sh_part;
+    __shared__ int sh_listed, sh_task, sh_part, sh_entries;
     rows_begin();
     const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
     const int v0 = blockIdx.x * kAdSlice, v1 = min(v0 + kAdSlice, a.V), width = v1 - v0;
@@ -139,8 +159,12 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
     int err = 0;
     int rows = p.n_nodes ? p.n_nodes[b] : a.R;
     int told = p.history ? p.history_lens[b] : 0, said = p.history && p.prompt_lens ? p.prompt_lens[b] : 0;
-    const Penalties q{p.repetition ? p.repetition[b] : 1.0f, p.frequency ? p.frequency[b] : 0.0f,
-                      p.presence ? p.presence[b] : 0.0f};
+    Penalties q;
+    q.repetition = p.repetition ? p.repetition[b] : 1.0f;
+    q.frequency = p.frequency ? p.frequency[b] : 0.0f;
+    q.presence = p.presence ? p.presence[b] : 0.0f;
+    q.inverse = 1.0f / q.repetition;
+    q.divides = !(fabsf(q.repetition) > 0x1p-100f && fabsf(q.repetition) < 0x1p100f);
     const bool penalties = q.repetition != 1.0f || q.frequency != 0.0f || q.presence != 0.0f;
     if (rows < 0 || rows > a.R) {
         err |= kDevErrLength;
@@ -155,10 +179,17 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
         err |= kDevErrLength;
         said = said < 0 ? 0 : told;
     }
-    const bool dense = (int64_t)told * 4 > a.V;
+    const bool dense = (int64_t)told * 16 > a.V;
     if (penalties || p.bias_ids)
         for (int i = tid; i < kAdCells / 4; i += kAdNT) reinterpret_cast<uint4*>(s.cell)[i] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) sh_listed = sh_task = sh_part = 0;
+    if (tid == 0) sh_listed = sh_task = sh_part = sh_entries = 0;
+    int bias_id[kAdMaxBias / kAdNT];
+    if (p.bias_ids)
+#pragma unroll
+        for (int k = 0; k < kAdMaxBias / kAdNT; ++k) {
+            const int j = tid + k * kAdNT;
+            bias_id[k] = j < p.bias_count ? p.bias_ids[(int64_t)b * p.bias_count + j] : -1;
+        }
     bool tree = true;
     if (p.drafted && penalties) {
         if (p.parent) tree = tree_part_ok(p.parent + b * p.parent_stride, rows, tid, kAdNT);
@@ -175,32 +206,14 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
             if (v < 0 || v >= a.V) err |= kDevErrToken;
             if (v >= v0 && v < v1) atomicOr(s.cell + adjust_cell<VE>(v - v0), kAdDrafted);
         }
-    if (p.bias_ids && tid < 32) {
-        // the first warp picks the slice's biases, in order; the first entry of an id sums them all
-        const int32_t* ids = p.bias_ids + (int64_t)b * p.bias_count;
-        const float* values = p.bias_values + (int64_t)b * p.bias_count;
-        int n = 0;
-        for (int j0 = 0; j0 < p.bias_count; j0 += 32) {
-            const int j = j0 + lane, v = j < p.bias_count ? ids[j] : -1;
+    if (p.bias_ids) {
+#pragma unroll
+        for (int k = 0; k < kAdMaxBias / kAdNT; ++k) {
+            const int v = bias_id[k];
             if (v < -1 || v >= a.V) err |= kDevErrToken;
-            const bool in = v >= v0 && v < v1;
-            const uint32_t all = __ballot_sync(0xffffffffu, in);
-            if (in) s.entry[n + __popc(all & ((1u << lane) - 1u))] = make_int2(v - v0, __float_as_int(values[j]));
-            n += __popc(all);
-        }
-        __syncwarp();
-        for (int j = lane; j < n; j += 32) {
-            const int at = s.entry[j].x;
-            float sum = 0.0f;
-            bool first = true;
-            for (int k = 0; k < n; ++k)
-                if (s.entry[k].x == at) {
-                    first = first && k >= j;
-                    sum = k == j ? __int_as_float(s.entry[k].y) : sum + __int_as_float(s.entry[k].y);
-                }
-            if (!first) continue;
-            s.bias[adjust_cell<VE>(at)] = sum;
-            atomicOr(s.cell + adjust_cell<VE>(at), kAdBiased);
+            if (v < v0 || v >= v1) continue;
+            s.entry[atomicAdd(&sh_entries, 1)] = make_int2(v - v0, tid + k * kAdNT);
+            atomicOr(s.cell + adjust_cell<VE>(v - v0), kAdBiased);
         }
     }
 
@@ -234,16 +247,10 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
     auto out_of = [&](int r) { return static_cast<T*>(a.out) + row_of(r) * a.out_stride + v0; };
     auto allowed_of = [&](int r) { return reinterpret_cast<const uint32_t*>(p.allowed) + row_of(r) * p.allowed_stride; };
     // a logit of row r, by what the history, the path and the biases say
+    const uint32_t rare = q.divides ? 0xffffffffu : kAdDrafted | kAdBiased;
     auto adjusted = [&](float x, int at, uint32_t cell, int r) {
-        uint32_t count = cell & kAdCount;
-        bool seen = (cell & (kAdCount | kAdPrompt)) != 0;
-        if (cell & kAdDrafted)
-            for (int i = r; i > 0; i = s.parent[i])
-                if (s.token[i] == v0 + at) {
-                    seen = true;
-                    ++count;
-                }
-        return adjust_value(x, count, seen, cell & kAdBiased ? s.bias[adjust_cell<VE>(at)] : 0.0f, q);
+        if (!(cell & rare)) return adjust_value(x, cell, q);
+        return adjust_rare(x, v0 + at, cell, cell & kAdBiased ? s.bias[adjust_cell<VE>(at)] : 0.0f, r, s.token, s.parent, q);
     };
     auto row_part = [&](int r, int part) {
         const T* in = in_of(r);
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
             auto single = [&](int at) {
                 const uint32_t cell = dense ? s.cell[adjust_cell<VE>(at)] : 0u;
                 if (allowed && !((allowed[at >> 5] >> (at & 31)) & 1u)) Logit<T>::store(out + at, -INFINITY);
-                else if (cell) Logit<T>::store(out + at, adjusted(Logit<T>::load(in + at), at, cell, r));
+                else if (cell && !(cell & rare)) Logit<T>::store(out + at, adjust_value(Logit<T>::load(in + at), cell, q));
                 else out[at] = in[at];
             };
             if (part == 0)
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
 #pragma unroll
                 for (int k = 0; k < VE; ++k) {
                     const uint32_t cell = s.cell[adjust_cell<VE>(at + k)];
-                    if (cell) y[k] = adjusted(y[k], at + k, cell, r);
+                    y[k] = cell & rare ? y[k] : adjust_value(y[k], cell, q);
                 }
                 x[u] = Logit<T>::put(y);
             }
@@ -329,10 +336,35 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
             row_part(r0 + t / kParts, t % kParts);
             __syncwarp();
         }
-        return;
     }
     if (!penalties && !p.bias_ids) return;
-    // the list: a thread looks at four cells at a time
+    if (p.bias_ids) {
+        // of the slice's biases of one id the first adds them all up, in order
+        const float* values = p.bias_values + (int64_t)b * p.bias_count;
+        const int n = sh_entries;
+        for (int i = tid; i < n; i += kAdNT) {
+            const int2 e = s.entry[i];
+            bool first = true, more = false;
+            for (int k = 0; k < n; ++k)
+                if (s.entry[k].x == e.x) {
+                    first = first && s.entry[k].y >= e.y;
+                    more = more || s.entry[k].y > e.y;
+                }
+            if (!first) continue;
+            float sum = values[e.y];
+            for (int last = e.y; more;) {
+                int next = kAdMaxBias;
+                for (int k = 0; k < n; ++k)
+                    if (s.entry[k].x == e.x && s.entry[k].y > last) next = min(next, s.entry[k].y);
+                more = next < kAdMaxBias;
+                if (more) sum += values[next];
+                last = next;
+            }
+            s.bias[adjust_cell<VE>(e.x)] = sum;
+        }
+    }
+    // the list (a dense request's: what the stream left): a thread looks at four cells at a time
+    const uint32_t listable = dense ? rare : 0xffffffffu;
     constexpr int kLooks = (kAdCells / 4 + kAdNT - 1) / kAdNT;
     uint32_t hits = 0;
 #pragma unroll
@@ -340,7 +372,8 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
         const int i = tid + k * kAdNT;
         if (i >= kAdCells / 4) continue;
         const uint4 c = reinterpret_cast<const uint4*>(s.cell)[i];
-        hits |= ((c.x != 0) | (c.y != 0) << 1 | (c.z != 0) << 2 | (c.w != 0) << 3) << (4 * k);
+        hits |= (((c.x & listable) != 0) | ((c.y & listable) != 0) << 1 | ((c.z & listable) != 0) << 2 |
+                 ((c.w & listable) != 0) << 3) << (4 * k);
     }
     const int mine = __popc(hits), upto = warp_inclusive_scan_i(mine);
     int to = 0;
@@ -395,9 +428,10 @@ static cudaError_t launch_adjust(AdjustArgs a, int B, cudaStream_t st) {
     most.p.bias_count = kAdMaxBias;
     if (!launch_shape(kernel, adjust_smem(most), kAdNT, &shape)) return cudaErrorUnknown;
     const int slices = (a.V + kAdSlice - 1) / kAdSlice;
-    // rows of a request are shared out only where its slices do not fill the GPU
+    // Rows of a request are shared out only where its slices do not fill the GPU.  Each CTA counts the history again:
+    // 12 requests of 60 rows took 113 us in one wave, 103 in two, 118 in four.
     const long long want = (long long)shape.sms * shape.per_sm, have = (long long)slices * B;
-    int parts = (int)(have >= want ? 1 : (want + have - 1) / have);
+    int parts = (int)(have >= want ? 1 : kAdWaves * want / have);
     parts = parts < a.R ? parts : a.R;
     a.rows = (a.R + parts - 1) / parts;
     parts = (a.R + a.rows - 1) / a.rows;
