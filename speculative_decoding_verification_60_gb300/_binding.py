@@ -9,6 +9,7 @@ when the library has not been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -574,26 +575,27 @@ def _half_code(t, name) -> int:
     raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
 
 
-def _cache(t, name, device=None) -> CacheLayout:
-    """Layout of a cache [blocks, page_size, heads, dim] whose dim is contiguous; the other dimensions may lie in any
-    order and be parts of a wider buffer, but must not overlap."""
-    if not t.is_cuda:
+def _cache(t, name, device=None):
+    """Layout of a cache [blocks, page_size, heads, dim] whose dim is contiguous, as the arguments of a CacheLayout; the
+    other dimensions may lie in any order and be parts of a wider buffer, but must not overlap."""
+    shape, stride, on = t.shape, t.stride(), t.get_device()
+    if on < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or t.numel() == 0:
-        raise ValueError(f"{name} must have shape [blocks, page_size, heads, dim], got {tuple(t.shape)}")
-    if device is not None and t.get_device() != device:
+    if len(shape) != 4 or 0 in shape:
+        raise ValueError(f"{name} must have shape [blocks, page_size, heads, dim], got {tuple(shape)}")
+    if device is not None and on != device:
         raise ValueError(f"{name} must be on cuda:{device}")
-    shape, stride = t.shape, t.stride()
-    if shape[3] > 1 and stride[3] != 1:
+    blocks, page, heads, dim = shape
+    if dim > 1 and stride[3] != 1:
         raise ValueError(f"{name} must have contiguous heads")
-    room = shape[3]
-    steps = [0, 0, 0]
-    for s, n, i in sorted((stride[i], shape[i], i) for i in range(3)):
+    steps = [s if n > 1 else 0 for s, n in zip(stride, (blocks, page, heads))]
+    room = dim
+    for s, n in sorted(zip(steps, (blocks, page, heads))):
         if n > 1:
             if s < room:
                 raise ValueError(f"{name} must have entries that do not overlap")
-            steps[i], room = s, s * (n - 1) + room
-    return CacheLayout(shape[0], shape[1], shape[2], shape[3], *steps)
+            room += s * (n - 1)
+    return (blocks, page, heads, dim, *steps)
 
 
 def _caches(k_cache, v_cache, device):
@@ -601,11 +603,11 @@ def _caches(k_cache, v_cache, device):
     layout = _cache(k_cache, "k_cache", device)
     if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have one dtype and shape")
-    other = _cache(v_cache, "v_cache", device)
-    if (layout.block_stride, layout.entry_stride, layout.head_stride) != (
-            other.block_stride, other.entry_stride, other.head_stride):
+    if v_cache.stride() != k_cache.stride() and _cache(v_cache, "v_cache", device) != layout:
         raise ValueError("k_cache and v_cache must have the same strides")
-    return layout
+    if v_cache.get_device() != device:
+        raise ValueError(f"v_cache must be on cuda:{device}")
+    return CacheLayout(*layout)
 
 
 def _heads(t, name, dtype, shape, device):
@@ -616,10 +618,10 @@ def _heads(t, name, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device}" if t.is_cuda else f"{name} must be a CUDA tensor")
-    stride = t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
+    *stride, last = t.stride()
+    if shape[-1] > 1 and last != 1:
         raise ValueError(f"{name} must have contiguous heads")
-    return t.data_ptr(), [s if n > 1 else 0 for s, n in zip(stride[:-1], shape[:-1])]
+    return t.data_ptr(), [s if n > 1 else 0 for s, n in zip(stride, shape)]
 
 
 def _table(block_table, B, device):
@@ -791,6 +793,9 @@ def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, dra
     return out
 
 
+_ALIKE = (operator.attrgetter("dtype"), torch.Tensor.size, torch.Tensor.stride, torch.Tensor.get_device)
+
+
 def keep_path(planes, path_nodes, accepted_len, seq_lens, block_table, out=None, stream=None) -> dict:
     """``spec_keep_path`` on torch tensors: planes, a sequence of caches [blocks, page_size, heads, dim] of one layout
     and dtype (keys and values of all layers), changed in place; path_nodes [B, W] and accepted_len [B] as verify_tree
@@ -803,24 +808,25 @@ def keep_path(planes, path_nodes, accepted_len, seq_lens, block_table, out=None,
     if not path_nodes.is_cuda:
         raise ValueError("path_nodes must be a CUDA tensor")
     B, W = path_nodes.shape
-    planes = list(planes)
+    planes = tuple(planes)
     if not planes:
         raise ValueError("planes must name at least one cache")
     head = planes[0]
-    layout = _cache(head, "planes[0]", device)
-    shape, stride, dtype = head.shape, head.stride(), head.dtype
-    for i, t in enumerate(planes):
-        if t.shape != shape or t.stride() != stride or t.dtype is not dtype or t.get_device() != device:
-            raise ValueError(f"planes[{i}] must have the dtype, shape, strides and device of planes[0]")
+    layout = CacheLayout(*_cache(head, "planes[0]", device))
+    for of in _ALIKE:  # a pass for each: no Python of its own for a plane, of which there are two a layer
+        each = list(map(of, planes))
+        if each.count(each[0]) != len(each):
+            raise ValueError("planes must have one dtype, shape, device and set of strides")
     each = torch.Size((B,))
     table, M, step = _table(block_table, B, device)
     out = {} if out is None else out
     st = lib.spec_keep_path(
-        (ctypes.c_void_p * len(planes))(*[t.data_ptr() for t in planes]), len(planes), head.element_size(),
+        (ctypes.c_void_p * len(planes))(*map(torch.Tensor.data_ptr, planes)), len(planes), head.element_size(),
         ctypes.byref(layout), B, W, _at(path_nodes, "path_nodes", _I32, path_nodes.shape, device),
         _at(accepted_len, "accepted_len", _I32, each, device), _at(seq_lens, "seq_lens", _I32, each, device), table, M,
         step, _to(out, "dev_error", _I32, _ONE, device, stream),
-        _handle(stream, device, *planes, path_nodes, accepted_len, seq_lens, block_table, *out.values()))
+        _handle(stream, device, *(planes if stream is not None else ()), path_nodes, accepted_len, seq_lens, block_table,
+                *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_keep_path", st)
     return out

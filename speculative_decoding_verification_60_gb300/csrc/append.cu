@@ -5,9 +5,10 @@
 
 namespace sv {
 
-constexpr int kApNT = 256;
+constexpr int kApNT = 128;
 constexpr int kApMaxDim = 256;
-constexpr int kApUnroll = 3;  // heads of a thread on their way at once
+constexpr int kApUnroll = 2;  // heads of a thread on their way at once
+constexpr int kApCtas = 6;    // of an SM
 
 struct AppendArgs {
     const uint16_t *q, *k, *v;
@@ -40,19 +41,22 @@ __device__ __forceinline__ uint64_t turn_unit(float inv) {
     return __double2ull_rz((hi - whole) * 0x1p64) + (uint64_t)__double2ll_rn(lo * 0x1p64);
 }
 
-// One CTA per token.  L lanes share a head, each with two vectors of VE
-// elements: a pair of vectors that turn together (i and i + half), or two
-// neighbours.  Cosines and sines are computed once per token, while the first
-// heads are on their way.  Bound by memory: every value is read and written
-// once.
+// Persistent CTAs, a token at a time.  L lanes share a head, each with two
+// vectors of VE elements: a pair of vectors that turn together (i and i + half),
+// or two neighbours.  A pair's unit is found once per CTA; a token's cosines and
+// sines are computed once, by as many threads as there are pairs, and its first
+// heads are on their way while the token before is turned.  Bound by memory:
+// every value is read and written once.  16384 tokens of 64 + 2 * 8 heads of
+// 128: 126 us, 0.78 of the copy rate, with 6 CTAs of 128 threads an SM (134 with
+// 4 of three heads a thread, 162 with 2 of 256 threads, 158 with a CTA a token).
 template <typename T, int VE, bool INTERLEAVED>
-__global__ void __launch_bounds__(kApNT) k_append(AppendArgs a, int lanes) {
+__global__ void __launch_bounds__(kApNT, kApCtas) k_append(const __grid_constant__ AppendArgs a, int lanes) {
     using V = typename Vec<VE>::type;
     constexpr int W = VE / 2;  // words of a vector
-    __shared__ float2 turn[kApMaxDim / 2];
-    __shared__ int64_t sh_entry;
+    __shared__ float2 turn[2][kApMaxDim / 2];
+    __shared__ int64_t sh_entry[2];
     rows_begin();
-    const int t = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x;
     const int per = kApNT / lanes, sub = tid % lanes, first = tid / lanes;
     const int heads = (a.q ? a.q_heads : 0), all = heads + 2 * a.kv_heads;
     // this lane's two vectors; a vector past the head's end is not there
@@ -69,128 +73,149 @@ __global__ void __launch_bounds__(kApNT) k_append(AppendArgs a, int lanes) {
         e1 = e0 + VE;
     }
     const bool has0 = e0 < a.dim, has1 = e1 < a.dim;
-    auto source = [&](int h) -> const uint16_t* {
-        if (h < heads) return a.q + (int64_t)t * a.q_token + (int64_t)h * a.q_head;
-        h -= heads;
-        if (h < a.kv_heads) return a.k + (int64_t)t * a.k_token + (int64_t)h * a.k_head;
-        return a.v + (int64_t)t * a.v_token + (int64_t)(h - a.kv_heads) * a.v_head;
-    };
     union Two {
         V v[2];
         uint32_t w[2][W];
     };
-    Two x[kApUnroll];
-    auto load = [&](int h0) {
+    auto load = [&](Two* x, int t, int h0) {
 #pragma unroll
         for (int u = 0; u < kApUnroll; ++u) {
-            const int h = h0 + u * per;
-            if (h < all) {
-                const uint16_t* s = source(h);
-                if (has0) x[u].v[0] = *reinterpret_cast<const V*>(s + e0);
-                if (has1) x[u].v[1] = *reinterpret_cast<const V*>(s + e1);
-            }
+            int h = h0 + u * per;
+            if (h >= all) continue;
+            const uint16_t* s;
+            if (h < heads) s = a.q + (int64_t)t * a.q_token + (int64_t)h * a.q_head;
+            else if ((h -= heads) < a.kv_heads) s = a.k + (int64_t)t * a.k_token + (int64_t)h * a.k_head;
+            else s = a.v + (int64_t)t * a.v_token + (int64_t)(h - a.kv_heads) * a.v_head;
+            if (has0) x[u].v[0] = *reinterpret_cast<const V*>(s + e0);
+            if (has1) x[u].v[1] = *reinterpret_cast<const V*>(s + e1);
         }
     };
-    load(first);
-    for (int i = tid; i < a.half; i += kApNT) {
-        const uint64_t angle = (uint64_t)(int64_t)a.positions[t] * turn_unit(a.inv_freq[i]);
-        float s, c;
-        sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
-        turn[i] = make_float2(c, s);
+    // a thread of a pair has its unit; the last has the slots
+    const bool turns_pair = tid < a.half, has_slot = tid == kApNT - 1;
+    const uint64_t unit = turns_pair ? turn_unit(a.inv_freq[tid]) : 0;
+    int position = 0;
+    int64_t slot = -1;
+    auto look = [&](int t) {
+        if (turns_pair) position = a.positions[t];
+        if (has_slot) slot = a.slots[t];
+    };
+    Two ahead[kApUnroll];
+    int t = blockIdx.x;
+    if (t < a.T) {
+        look(t);
+        load(ahead, t, first);
     }
-    if (tid == 0) {
-        const int64_t slot = a.slots[t];
-        int64_t entry = -1;
-        if (slot >= a.entries) {
-            set_error(a.dev_error, kDevErrCapacity);
-        } else if (slot >= 0) {
-            const int64_t block = slot / a.page;
-            entry = block * a.block_stride + (slot - block * a.page) * a.entry_stride;
-        }
-        sh_entry = entry;
-    }
-    __syncthreads();
-    const int64_t entry = sh_entry;
-    float2 cs[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) cs[i] = pairs + i < a.half ? turn[pairs + i] : make_float2(1.0f, 0.0f);
     const int rot = 2 * a.half;
-    for (int base = 0; base < all; base += per * kApUnroll) {  // the same turns for every lane of a warp
-        const int h0 = base + first;
-        if (base > 0) load(h0);
+    for (int buf = 0; t < a.T; t += gridDim.x, buf ^= 1) {
+        if (turns_pair) {
+            const uint64_t angle = (uint64_t)(int64_t)position * unit;
+            float s, c;
+            sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
+            turn[buf][tid] = make_float2(c, s);
+        }
+        if (has_slot) {
+            int64_t entry = -1;
+            if (slot >= a.entries) {
+                set_error(a.dev_error, kDevErrCapacity);
+            } else if (slot >= 0) {
+                const int64_t block = slot / a.page;
+                entry = block * a.block_stride + (slot - block * a.page) * a.entry_stride;
+            }
+            sh_entry[buf] = entry;
+        }
+        __syncthreads();  // two buffers: the next token's are written by threads that have passed the next one
+        const int64_t entry = sh_entry[buf];
+        float2 cs[VE];
 #pragma unroll
-        for (int u = 0; u < kApUnroll; ++u) {
-            const int h = h0 + u * per;
-            const bool live = h < all, turns = live && h < heads + a.kv_heads;
-            if (__any_sync(0xffffffffu, turns)) {
-                float2 f[2][W];
+        for (int i = 0; i < VE; ++i) cs[i] = pairs + i < a.half ? turn[buf][pairs + i] : make_float2(1.0f, 0.0f);
+        for (int base = 0; base < all; base += per * kApUnroll) {  // the same turns for every lane of a warp
+            const int h0 = base + first;
+            Two x[kApUnroll];
+            if (base > 0) {
+                load(x, t, h0);
+            } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    f[0][i] = turns && has0 ? Pair<T>::get(x[u].w[0][i]) : make_float2(0.0f, 0.0f);
-                    f[1][i] = turns && has1 ? Pair<T>::get(x[u].w[1][i]) : make_float2(0.0f, 0.0f);
+                for (int u = 0; u < kApUnroll; ++u) x[u] = ahead[u];
+                const int next = t + gridDim.x;
+                if (next < a.T) {
+                    look(next);
+                    load(ahead, next, first);
                 }
-                if (a.k_norm) {
-                    float sum = 0.0f;
+            }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int i = 0; i < W; ++i) sum += f[j][i].x * f[j][i].x + f[j][i].y * f[j][i].y;
-                    for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    const float r = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
-                    const uint16_t* norm = h < heads ? a.q_norm : a.k_norm;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (j == 0 ? !has0 : !has1) continue;
-                        Two n;
-                        n.v[0] = *reinterpret_cast<const V*>(norm + (j == 0 ? e0 : e1));
-#pragma unroll
-                        for (int i = 0; i < W; ++i) {
-                            const float2 w = Pair<T>::get(n.w[0][i]);
-                            f[j][i].x *= r * w.x;
-                            f[j][i].y *= r * w.y;
-                        }
-                    }
-                }
-                if (INTERLEAVED) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if ((j == 0 ? e0 : e1) < rot) {
-#pragma unroll
-                            for (int i = 0; i < W; ++i) {
-                                const float2 c = cs[j * W + i], p = f[j][i];
-                                f[j][i] = make_float2(p.x * c.x - p.y * c.y, p.y * c.x + p.x * c.y);
-                            }
-                        }
-                } else if (pairs < a.half) {
+            for (int u = 0; u < kApUnroll; ++u) {
+                const int h = h0 + u * per;
+                const bool live = h < all, turns = live && h < heads + a.kv_heads;
+                if (__any_sync(0xffffffffu, turns)) {
+                    float2 f[2][W];
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        const float2 c = cs[2 * i], d = cs[2 * i + 1], p = f[0][i], q = f[1][i];
-                        f[0][i] = make_float2(p.x * c.x - q.x * c.y, p.y * d.x - q.y * d.y);
-                        f[1][i] = make_float2(q.x * c.x + p.x * c.y, q.y * d.x + p.y * d.y);
+                        f[0][i] = turns && has0 ? Pair<T>::get(x[u].w[0][i]) : make_float2(0.0f, 0.0f);
+                        f[1][i] = turns && has1 ? Pair<T>::get(x[u].w[1][i]) : make_float2(0.0f, 0.0f);
+                    }
+                    if (a.k_norm) {
+                        float2 squares = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < W; ++i) squares = __ffma2_rn(f[j][i], f[j][i], squares);
+                        float sum = squares.x + squares.y;
+                        for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        const float r = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+                        const uint16_t* norm = h < heads ? a.q_norm : a.k_norm;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (j == 0 ? !has0 : !has1) continue;
+                            Two n;
+                            n.v[0] = *reinterpret_cast<const V*>(norm + (j == 0 ? e0 : e1));
+#pragma unroll
+                            for (int i = 0; i < W; ++i)
+                                f[j][i] = __fmul2_rn(f[j][i], __fmul2_rn(Pair<T>::get(n.w[0][i]), make_float2(r, r)));
+                        }
+                    }
+                    if (INTERLEAVED) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if ((j == 0 ? e0 : e1) < rot) {
+#pragma unroll
+                                for (int i = 0; i < W; ++i) {
+                                    const float2 c = cs[j * W + i], p = f[j][i];
+                                    f[j][i] = make_float2(p.x * c.x - p.y * c.y, p.y * c.x + p.x * c.y);
+                                }
+                            }
+                    } else if (pairs < a.half) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const float2 c = make_float2(cs[2 * i].x, cs[2 * i + 1].x), s = make_float2(cs[2 * i].y, cs[2 * i + 1].y);
+                            const float2 p = f[0][i], q = f[1][i], minus = make_float2(-s.x, -s.y);
+                            f[0][i] = __ffma2_rn(q, minus, __fmul2_rn(p, c));
+                            f[1][i] = __ffma2_rn(p, s, __fmul2_rn(q, c));
+                        }
+                    }
+                    // values that neither the norm nor the turn touches keep their bits
+                    if (turns && (a.k_norm || e0 < rot)) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) x[u].w[0][i] = Pair<T>::put(f[0][i].x, f[0][i].y);
+                    }
+                    if (turns && (a.k_norm || e1 < rot)) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) x[u].w[1][i] = Pair<T>::put(f[1][i].x, f[1][i].y);
                     }
                 }
-                // values that neither the norm nor the turn touches keep their bits
-                if (turns && (a.k_norm || e0 < rot)) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) x[u].w[0][i] = Pair<T>::put(f[0][i].x, f[0][i].y);
+                if (!live) continue;
+                uint16_t* to;
+                if (h < heads) {
+                    to = a.out_q + ((int64_t)t * heads + h) * a.dim;
+                } else {
+                    if (entry < 0) continue;
+                    const int g = h - heads;
+                    to = g < a.kv_heads ? a.k_cache + entry + g * a.head_stride
+                                        : a.v_cache + entry + (g - a.kv_heads) * a.head_stride;
                 }
-                if (turns && (a.k_norm || e1 < rot)) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) x[u].w[1][i] = Pair<T>::put(f[1][i].x, f[1][i].y);
-                }
+                if (has0) *reinterpret_cast<V*>(to + e0) = x[u].v[0];
+                if (has1) *reinterpret_cast<V*>(to + e1) = x[u].v[1];
             }
-            if (!live) continue;
-            uint16_t* to;
-            if (h < heads) {
-                to = a.out_q + ((int64_t)t * heads + h) * a.dim;
-            } else {
-                if (entry < 0) continue;
-                const int g = h - heads;
-                to = g < a.kv_heads ? a.k_cache + entry + g * a.head_stride
-                                    : a.v_cache + entry + (g - a.kv_heads) * a.head_stride;
-            }
-            if (has0) *reinterpret_cast<V*>(to + e0) = x[u].v[0];
-            if (has1) *reinterpret_cast<V*>(to + e1) = x[u].v[1];
+            __syncwarp();
         }
     }
 }
@@ -202,8 +227,12 @@ static cudaError_t launch_append(const AppendArgs& a, bool interleaved, cudaStre
     const int slots = turned + (a.dim - 2 * turned * VE + 2 * VE - 1) / (2 * VE);
     int lanes = 1;
     while (lanes < slots) lanes *= 2;
-    return interleaved ? launch_clusters(k_append<T, VE, true>, a.T, 1, kApNT, 0, true, st, a, lanes)
-                       : launch_clusters(k_append<T, VE, false>, a.T, 1, kApNT, 0, true, st, a, lanes);
+    int grid;
+    if (!(interleaved ? launch_grid(k_append<T, VE, true>, 0, a.T, &grid, kApNT)
+                      : launch_grid(k_append<T, VE, false>, 0, a.T, &grid, kApNT)))
+        return cudaErrorUnknown;
+    return interleaved ? launch_clusters(k_append<T, VE, true>, grid, 1, kApNT, 0, true, st, a, lanes)
+                       : launch_clusters(k_append<T, VE, false>, grid, 1, kApNT, 0, true, st, a, lanes);
 }
 
 }  // namespace sv
