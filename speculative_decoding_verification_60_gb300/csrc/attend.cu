@@ -11,6 +11,7 @@ constexpr int kAtTile = 128;  // cache entries of a tile; query rows of a block
 constexpr int kAtPrepNT = 256;
 constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, products, values, queries and mending
 constexpr int kAtMaxCtas = 160;
+constexpr int kAtMaskedTiles = kMaxDraftNodes / kAtTile + 1;  // tiles that reach behind a sequence, at most
 constexpr int kAtPieces = 8;   // CTAs that join a block
 constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
 constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
@@ -195,8 +196,9 @@ template <int DT> struct AttendShape {
 };
 struct AttendCtrl {
     uint64_t full[10], empty[10], mend[10], mended[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], ml_full, read, drain;
-    uint32_t poison[10][4];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], ml_full, read, judged[2], drain;
+    uint32_t poison[2][kAtMaskedTiles][4];  // of every other item: entries that are not finite
+    uint32_t poisoned[2];                   // whether there are any
     float2 ml[2][kAtTile];
     uint32_t tmem;
     int b0;
@@ -255,9 +257,14 @@ __device__ __forceinline__ uint32_t attend_sees(const AttendArgs& a, const uint3
 // up: the copy reads outside the cache there, which gives zeros.  (One warp for
 // both took 3900 clocks a tile of eight pages, 75 a copy, and the products
 // waited.)
-template <int DT, int KV>
-__device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* map, AttendWalk walk, AttendCtrl* c,
-                                            uint32_t ring) {
+//
+// The warp of the values copies the queries, too, between an item's last values
+// and the next one's first: one box of a block's nodes and heads for every 64
+// columns; nodes behind the last read as zeros or as rows that nothing is
+// written for.
+template <int DT, int NB, int KV>
+__device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorMap* map, const CUtensorMap* qm,
+                                            AttendWalk walk, AttendCtrl* c, uint32_t queries, uint32_t ring) {
     using S = AttendShape<DT>;
     constexpr int kCopies = kAtTile / 32 * (DT / 64);  // of a lane, at most
     // a lane takes every 32nd of the tile's copies, (box, 64 columns) each
@@ -283,8 +290,31 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
             }
         }
     };
+    // with two turns of queries the next item's are on their way during this one, with one they wait for its end
+    constexpr int kTurns = NB == 1 ? 2 : 1;
+    int qi = 0;
+    auto copy_queries = [&](const AttendItem& x) {
+        const int turn = qi % kTurns, use = qi / kTurns;
+        ++qi;
+        if (use > 0 && !attend_wait_warp(c, &c->q_empty[turn], (use - 1) & 1)) return false;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&c->q_full[turn], NB * kWide * a.plan.nodes * a.group * 128);
+            for (int w = 0; w < NB; ++w)
+                for (int d = 0; d < kWide; ++d)
+                    tma_load_4d(queries + (turn + w) * S::kTileBytes + d * S::kBlockBytes, qm, d * 64, x.head * a.group,
+                                x.node0 + w * a.plan.nodes, x.b, &c->q_full[turn]);
+        }
+        return true;
+    };
+    AttendItem ahead;
+    AttendWalk walk_ahead = walk;
+    if (KV == 1 && NB == 1 && walk_ahead.item(a, &ahead)) ok = copy_queries(ahead);
     while (ok && walk.item(a, &x)) {
         look_up(x.t0);
+        if (KV == 1) {
+            if (NB == 2) ok = copy_queries(x);
+            else if (walk_ahead.item(a, &ahead)) ok = copy_queries(ahead);
+        }
         for (int t = x.t0; ok && t < x.t1; ++t) {
             int to_block[kCopies], to_entry[kCopies];
 #pragma unroll
@@ -324,6 +354,7 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
         const int turn = KV ? S::value_turn(j) : S::key_turn(j);
         mbar_wait(&c->full[turn % S::kStages], (turn / S::kStages) & 1, kDrainNs);
     }
+    for (int i = max(0, qi - kTurns); i < qi; ++i) mbar_wait(&c->q_full[i % kTurns], (i / kTurns) & 1, kDrainNs);
     __syncwarp();
 }
 
@@ -449,43 +480,27 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
     __syncwarp();
 }
 
-// The warp that copies queries and mends values.  An item's queries are one box
-// of its block's nodes and heads for every 64 columns; nodes behind the last
-// read as zeros or as rows that nothing is written for.
-//
-// Mending: in tiles that reach behind the sequence, values that no product may
-// meet.  A weight of zero does not hide an infinity or a NaN, so entries behind
-// the last node, and nodes' entries that are not finite, become zeros; the
-// latter's places are told to the softmax, which makes the rows that see them
-// NaN.
-template <typename T, int DT, int NB>
-__device__ __forceinline__ void attend_mend(const AttendArgs& a, const CUtensorMap* map, AttendWalk walk, AttendCtrl* c,
-                                            uint8_t* queries, uint8_t* ring) {
+// The mending warp: in tiles that reach behind the sequence, values that no
+// product may meet.  A weight of zero does not hide an infinity or a NaN, so
+// entries behind the last node, and nodes' entries that are not finite, become
+// zeros; the latter's places are kept for the item's end, where the rows that
+// see them become NaN.
+template <typename T, int DT>
+__device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint8_t* ring) {
     using S = AttendShape<DT>;
-    constexpr int kTurns = NB == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31;
-    auto copy = [&](const AttendItem& x, int qi) {
-        const int turn = qi % kTurns, use = qi / kTurns;
-        if (use > 0 && !attend_wait_warp(c, &c->q_empty[turn], (use - 1) & 1)) return false;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&c->q_full[turn], NB * (DT / 64) * a.plan.nodes * a.group * 128);
-            for (int w = 0; w < NB; ++w)
-                for (int d = 0; d < DT / 64; ++d)
-                    tma_load_4d(smem_addr(queries) + (turn + w) * S::kTileBytes + d * S::kBlockBytes, map, d * 64,
-                                x.head * a.group, x.node0 + w * a.plan.nodes, x.b, &c->q_full[turn]);
-        }
-        return true;
-    };
-    AttendItem x, ahead;
-    int J = 0, qi = 0;
+    AttendItem x;
+    bool ok = true;
     uint32_t parity = 0;  // of each slot's next tile to mend
-    bool more = walk.item(a, &ahead), ok = !more || NB == 2 || copy(ahead, qi++);
-    while (ok && more) {
-        x = ahead;
-        more = walk.item(a, &ahead);
-        // with two turns the next item's queries are on their way during this one; with one they wait for its end
-        if (NB == 2) ok = copy(x, qi++);
-        else if (more) ok = copy(ahead, qi++);
+    for (int J = 0, item = 0; ok && walk.item(a, &x); ++item) {
+        const int turn = item & 1, use = item >> 1;
+        // every item's end in order, so that none is taken for another
+        if (use > 0 && !attend_wait_warp(c, &c->judged[turn], (use - 1) & 1)) break;
+        if (!x.masked(x.t1 - 1)) {
+            J += x.t1 - x.t0;
+            continue;
+        }
+        if (lane == 0) c->poisoned[turn] = 0;
         for (int t = x.t0; ok && t < x.t1; ++t, ++J) {
             if (!x.masked(t)) continue;
             // This warp does not follow the ring.  Once the copy warp has named
@@ -522,15 +537,15 @@ __device__ __forceinline__ void attend_mend(const AttendArgs& a, const CUtensorM
                             make_uint4(0, 0, 0, 0);
                 }
                 const uint32_t all = __ballot_sync(0xffffffffu, bad);
-                if (lane == 0) c->poison[slot][k] = all;
+                if (lane == 0) {
+                    c->poison[turn][t - x.len / kAtTile][k] = all;
+                    if (all) c->poisoned[turn] = 1;
+                }
             }
             fence_async_shared();
             attend_arrive_warp(&c->mended[slot]);
         }
     }
-    // no queries are on their way either
-    for (int i = max(0, qi - kTurns); i < qi; ++i) mbar_wait(&c->q_full[i % kTurns], (i / kTurns) & 1, kDrainNs);
-    __syncwarp();
 }
 
 // A warpgroup of the softmax: a thread has a query row.  The scores of a tile
@@ -540,20 +555,19 @@ __device__ __forceinline__ void attend_mend(const AttendArgs& a, const CUtensorM
 // outputs stay in 32 bits.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t tmem) {
-    using S = AttendShape<DT>;
     const int w = threadIdx.x >> 7, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = quarter * 32 + lane;  // of the block
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * 128;
-    uint32_t scored = 0, done[2] = {0, 0}, met = 0, mended = 0;  // parities
+    uint32_t scored = 0, done[2] = {0, 0}, met = 0;  // parities
     int J = 0;
     AttendItem x;
-    while (walk.item(a, &x)) {
+    for (int item = 0; walk.item(a, &x); ++item) {
         const int n = x.t1 - x.t0, J0 = J, first = NB == 2 ? w * a.plan.nodes : 0;  // the block's first node in the item
         const int live_rows = min(x.nodes - first, a.plan.nodes) * a.group;
         if (NB == 2 && live_rows <= 0) {  // the second block is empty
-            for (int t = x.t0; t < x.t1; ++t, ++J)
-                if (x.masked(t)) mended ^= 1u << (S::value_turn(J) % S::kStages);
+            J += n;
+            attend_arrive_warp(&c->judged[item & 1]);
             continue;
         }
         const bool live = quarter * 32 < live_rows;  // this warp has a row
@@ -564,14 +578,18 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         float2 l = make_float2(0.0f, 0.0f);  // two sums of a row's weights
         bool begun = false;
         for (int t = x.t0; t < x.t1; ++t, ++J) {
-            const bool masked = x.masked(t);
-            const int slot = S::value_turn(J) % S::kStages;
-            const uint32_t mend_parity = (mended >> slot) & 1u;
-            if (masked) mended ^= 1u << slot;
             if (NB == 1 && (J & 1) != w) continue;
+            const bool masked = x.masked(t);
+            uint32_t sees[4];  // on their way while the scores are waited for
+            if (masked && live) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t base = (int64_t)t * kAtTile + i * 32 - x.len;
+                    sees[i] = attend_sees(a, mask, node, base < -32 ? -32 : (int)base);
+                }
+            }
             if (!attend_wait_warp(c, &c->s_full[w], scored)) return;
             scored ^= 1u;
-            if (masked && !attend_wait_warp(c, &c->mended[slot], mend_parity)) return;
             tmem_fence_after();
             if (live) {
                 float s[kAtTile];
@@ -581,11 +599,8 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                 if (masked) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int64_t base = (int64_t)t * kAtTile + i * 32 - x.len;
-                        const uint32_t sees = attend_sees(a, mask, node, base < -32 ? -32 : (int)base);
-                        if (sees & c->poison[slot][i]) l.x = NAN;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[i * 32 + k] = (sees >> k) & 1u ? s[i * 32 + k] : -INFINITY;
+                        for (int k = 0; k < 32; ++k) s[i * 32 + k] = (sees[i] >> k) & 1u ? s[i * 32 + k] : -INFINITY;
                     }
                 }
                 float top[4];
@@ -670,6 +685,16 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
             done[0] ^= 1u;
         }
         tmem_fence_after();
+        // every tile's values are mended by now
+        if (x.masked(x.t1 - 1) && c->poisoned[item & 1])
+            for (int t = max(x.t0, x.len / kAtTile); t < x.t1; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t base = (int64_t)t * kAtTile + i * 32 - x.len;
+                    if (attend_sees(a, mask, node, base < -32 ? -32 : (int)base) & c->poison[item & 1][t - x.len / kAtTile][i])
+                        total = NAN;
+                }
+        attend_arrive_warp(&c->judged[item & 1]);
         if (live) {
             const bool there = row < live_rows;
             constexpr int kCols = NB == 1 ? DT / 2 : DT;  // of this thread
@@ -748,6 +773,8 @@ __global__ void __launch_bounds__(kAtNT, 1)
         }
         mbar_init(&c->ml_full, 8);
         mbar_init(&c->read, 8);
+        mbar_init(&c->judged[0], 8);
+        mbar_init(&c->judged[1], 8);
         mbar_init(&c->drain, 1);
         c->dead = 0;
         c->b0 = 0;
@@ -776,13 +803,13 @@ __global__ void __launch_bounds__(kAtNT, 1)
     if (warp < 8) {
         attend_softmax<T, DT, NB>(a, walk, c, tmem);
     } else if (warp == 8) {
-        attend_copy<DT, 0>(a, &km, walk, c, ring);
+        attend_copy<DT, NB, 0>(a, &km, &qm, walk, c, queries, ring);
     } else if (warp == 9) {
         attend_products<T, DT, NB>(a, walk, c, queries, ring, tmem);
     } else if (warp == 10) {
-        attend_copy<DT, 1>(a, &vm, walk, c, ring);
+        attend_copy<DT, NB, 1>(a, &vm, &qm, walk, c, queries, ring);
     } else {
-        attend_mend<T, DT, NB>(a, &qm, walk, c, sh_attend, sh_attend + S::kQueryBytes);
+        attend_mend<T, DT>(a, walk, c, sh_attend + S::kQueryBytes);
     }
     tmem_fence_before();
     __syncthreads();
