@@ -135,23 +135,36 @@ struct AttendItem {
 __device__ __forceinline__ int attend_groups(const AttendArgs& a, int64_t units) {
     return units < a.plan.groups ? max((int)units, 1) : a.plan.groups;
 }
+// The first requests of a CTA's run, in shared memory: what the next item is must
+// not take two reads of global memory at the end of every request.
+constexpr int kAtNear = 20;
+struct AttendNear {
+    int b0, first[kAtNear + 1], len[kAtNear], n[kAtNear];
+};
 // The items of a CTA, one after the other; every role walks them for itself.
 struct AttendWalk {
+    const AttendNear* near;
     int u, u1, b, start, next, share, head;
-    AttendRequest r;
-    int tiles;
-    __device__ __forceinline__ void request(const AttendArgs& a) {
-        r = attend_request(a, b);
-        tiles = attend_tiles(r);
+    int len, n, tiles;
+    __device__ __forceinline__ int first(const AttendArgs& a, int b) const {
+        const int i = b - near->b0;
+        return i <= kAtNear ? near->first[i] : a.first[b];
     }
-    // b0: the request of unit u0 (any value when there are no units)
-    __device__ __forceinline__ AttendWalk(const AttendArgs& a, int u0, int end, int b0) : u(u0), u1(end), b(b0) {
+    __device__ __forceinline__ void request(const AttendArgs& a) {
+        const int i = b - near->b0;
+        len = i < kAtNear ? near->len[i] : a.lens[b];
+        n = i < kAtNear ? near->n[i] : a.n_nodes ? a.n_nodes[b] : a.N;
+        tiles = attend_tiles({len, n, 0});  // requests that are refused have no units
+    }
+    // near->b0: the request of unit u0 (any one when there are no units)
+    __device__ __forceinline__ AttendWalk(const AttendArgs& a, int u0, int end, const AttendNear* requests)
+        : near(requests), u(u0), u1(end), b(requests->b0) {
         const int i = blockIdx.x % a.plan.ctas();
         head = i / a.plan.share;
         share = i - head * a.plan.share;
         if (u >= u1) return;
-        start = a.first[b];
-        next = a.first[b + 1];
+        start = first(a, b);
+        next = first(a, b + 1);
         request(a);
     }
     __device__ __forceinline__ bool item(const AttendArgs& a, AttendItem* x) {
@@ -160,7 +173,7 @@ struct AttendWalk {
                 do {
                     ++b;
                     start = next;
-                    next = a.first[b + 1];
+                    next = first(a, b + 1);
                 } while (u >= next);
                 request(a);
             }
@@ -171,11 +184,11 @@ struct AttendWalk {
             const int set = i / a.plan.chunks, most = a.plan.blocks * a.plan.nodes;
             x->head = set * a.plan.heads + head;
             x->node0 = ((i - set * a.plan.chunks) * a.plan.share + share) * most;
-            x->nodes = min(r.n - x->node0, most);
+            x->nodes = min(n - x->node0, most);
             if (x->nodes <= 0) continue;  // a request of fewer nodes than N
             x->b = b;
-            x->len = r.len;
-            x->n = r.n;
+            x->len = len;
+            x->n = n;
             x->tiles = tiles;
             return true;
         }
@@ -201,8 +214,8 @@ struct AttendCtrl {
     uint32_t poisoned[2];                   // whether there are any
     float2 ml[2][kAtTile];
     uint32_t tmem;
-    int b0;
     volatile int dead;
+    AttendNear near;
 };
 template <int DT> constexpr size_t kAttendSmem = AttendShape<DT>::kTiles + sizeof(AttendCtrl);
 static_assert(kAttendSmem<128> <= 232448 && kAttendSmem<64> <= 232448, "a CTA's shared memory");
@@ -777,7 +790,7 @@ __global__ void __launch_bounds__(kAtNT, 1)
         mbar_init(&c->judged[1], 8);
         mbar_init(&c->drain, 1);
         c->dead = 0;
-        c->b0 = 0;
+        c->near.b0 = 0;
         mbar_fence_init();
         mbar_arrive(&c->full[1]);  // turn 1 is over
         mbar_arrive(&c->empty[1]);
@@ -797,9 +810,18 @@ __global__ void __launch_bounds__(kAtNT, 1)
     const int u0 = (int)(units * min(g, groups) / groups), u1 = (int)(units * min(g + 1, groups) / groups);
     if (u0 < u1)
         for (int b = tid; b < a.B; b += kAtNT)
-            if (a.first[b] <= u0 && u0 < a.first[b + 1]) c->b0 = b;
+            if (a.first[b] <= u0 && u0 < a.first[b + 1]) c->near.b0 = b;
     __syncthreads();
-    const AttendWalk walk(a, u0, u1, c->b0);
+    if (tid <= kAtNear) {
+        const int b = c->near.b0 + tid;
+        if (b <= a.B) c->near.first[tid] = a.first[b];
+        if (tid < kAtNear && b < a.B) {
+            c->near.len[tid] = a.lens[b];
+            c->near.n[tid] = a.n_nodes ? a.n_nodes[b] : a.N;
+        }
+    }
+    __syncthreads();
+    const AttendWalk walk(a, u0, u1, &c->near);
     if (warp < 8) {
         attend_softmax<T, DT, NB>(a, walk, c, tmem);
     } else if (warp == 8) {
