@@ -135,6 +135,20 @@ struct AttendItem {
 __device__ __forceinline__ int attend_groups(const AttendArgs& a, int64_t units) {
     return units < a.plan.groups ? max((int)units, 1) : a.plan.groups;
 }
+// The group that has a unit.
+__device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int groups) {
+    return (int)(((unit + 1) * groups - 1) / units);
+}
+// A CTA's partial results: the reference and sum of the rows of its two blocks
+// (or, with one block, of its two halves of columns, alike), then four columns
+// at a time of its rows.  Part 1 is the beginning of an item at the end of the
+// CTA's run, part 0 what goes on from the group before.
+constexpr int kAtPartSums = 2 * kAtTile;
+template <int DT, int NB> constexpr int kAtPartFloats = 2 * kAtPartSums + NB * kAtTile * DT;
+template <int DT, int NB>
+__device__ __forceinline__ float* attend_part(const AttendArgs& a, int group, int cta, bool begins) {
+    return a.part + ((int64_t)(group * a.plan.ctas() + cta) * 2 + begins) * kAtPartFloats<DT, NB>;
+}
 // The first requests of a CTA's run, in shared memory: what the next item is must
 // not take two reads of global memory at the end of every request.
 constexpr int kAtNear = 20;
@@ -713,10 +727,9 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
             constexpr int kCols = NB == 1 ? DT / 2 : DT;  // of this thread
             const int col0 = NB == 1 ? w * kCols : 0, rows = NB * kAtTile, at_row = (NB == 2 ? w * kAtTile : 0) + row;
             const uint32_t o_at = tmem + lanes + 256 + (NB == 2 ? w * DT : 0);
-            float* part = a.part + ((int64_t)blockIdx.x * 2 + (x.t0 == 0 ? 1 : 0)) * (rows * (DT + 2));
-            if (!x.whole() && there && (NB == 2 || w == 0))
-                reinterpret_cast<float2*>(part)[at_row] = make_float2(m, total);
-            float4* part_o = reinterpret_cast<float4*>(part + 2 * rows) + at_row;
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + (x.t0 == 0)) * kAtPartFloats<DT, NB>;
+            if (!x.whole() && there) reinterpret_cast<float2*>(part)[w * kAtTile + row] = make_float2(m, total);
+            float4* part_o = reinterpret_cast<float4*>(part + 2 * kAtPartSums) + at_row;
             const float inv = 1.0f / total;
             uint16_t* out = a.out + (((int64_t)x.b * a.N + node) * a.q_heads + x.head * a.group + (row - at_node * a.group)) * a.dim;
 #pragma unroll 1
@@ -842,13 +855,10 @@ __global__ void __launch_bounds__(kAtNT, 1)
     }
 }
 
-// The group that has a unit.
-__device__ __forceinline__ int attend_group(int64_t unit, int64_t units, int groups) {
-    return (int)(((unit + 1) * groups - 1) / units);
-}
-
 // Joins the results of an item that several groups share: a CTA takes an eighth
-// of a block's (row, four columns) pairs.  The threads that share a row find its
+// of a block's (row, four columns) pairs.  (The warps that wrote a row's parts,
+// the last one at a time, took as long again as this launch: a lane has a row
+// to itself there.)  The threads that share a row find its
 // reference and sum together, in the same order everywhere.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta, int w, int piece, int* sh) {
@@ -871,23 +881,29 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta
     const int head = set * a.plan.heads + beside, block = ((i - set * a.plan.chunks) * a.plan.share + share) * NB + w;
     const int node0 = block * a.plan.nodes, rows = min(r.n - node0, a.plan.nodes) * a.group;
     if (rows <= 0) return;
-    const int g1 = attend_group(end - 1, units, groups);
+    const int g1 = attend_group(end - 1, units, groups), count = g1 - g0 + 1;
     constexpr int R = NB * kAtTile;
-    // the first group's part is the end of its run, the others' the beginning of theirs
-    auto part = [&](int g) { return a.part + ((int64_t)(g * a.plan.ctas() + cta) * 2 + (g == g0 ? 1 : 0)) * (R * (DT + 2)); };
+    auto part = [&](int g) { return attend_part<DT, NB>(a, g, cta, g == g0); };
+    // as many threads for a pair as are to spare, each with every so many-th part
     const int pairs = rows * (a.dim / 4), each = (pairs + kAtPieces - 1) / kAtPieces;
-    for (int k = piece * each + tid; k < min(pairs, (piece + 1) * each); k += kAtPrepNT) {
-        const int d = k / rows, row = k - d * rows, at = w * kAtTile + row;
-        float m = kNoMax;
-#pragma unroll 8
-        for (int g = g0; g <= g1; ++g) m = fmaxf(m, reinterpret_cast<const float2*>(part(g))[at].x);
-        float l = 0.0f;
+    int beside_pair = 1;
+    while (beside_pair < 32 && beside_pair < count && each * beside_pair * 2 <= kAtPrepNT) beside_pair *= 2;
+    const int lane = tid & (beside_pair - 1), per = kAtPrepNT / beside_pair, last = min(pairs, (piece + 1) * each);
+    for (int k0 = piece * each; k0 < last; k0 += per) {  // the same turns for every thread
+        const int k = min(k0 + tid / beside_pair, last - 1);
+        const int d = k / rows, row = k - d * rows;
+        // with one block a part's sums are there twice, alike
+        const int at = w * kAtTile + row;
+        float m = kNoMax, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int g = g0; g <= g1; ++g) {
+#pragma unroll 4
+        for (int g = g0 + lane; g <= g1; g += beside_pair) m = fmaxf(m, reinterpret_cast<const float2*>(part(g))[at].x);
+        for (int s = 1; s < beside_pair; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+#pragma unroll 4
+        for (int g = g0 + lane; g <= g1; g += beside_pair) {
             const float* p = part(g);
             const float2 ml = reinterpret_cast<const float2*>(p)[at];
-            const float4 v = reinterpret_cast<const float4*>(p + 2 * R)[d * R + at];
+            const float4 v = reinterpret_cast<const float4*>(p + 2 * kAtPartSums)[d * R + at];
             const float f = exp2f((ml.x - m) * a.c);
             l += f * ml.y;
             o.x += f * v.x;
@@ -895,13 +911,21 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta
             o.z += f * v.z;
             o.w += f * v.w;
         }
+        for (int s = 1; s < beside_pair; s *= 2) {
+            l += __shfl_xor_sync(0xffffffffu, l, s);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, s);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, s);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, s);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, s);
+        }
         const float inv = 1.0f / l;
         const int node = row / a.group;
         uint2 v;
         v.x = Pair<T>::put(o.x * inv, o.y * inv);
         v.y = Pair<T>::put(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
-                                  d * 4) = v;
+        if (lane == 0)
+            *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
+                                      d * 4) = v;
     }
 }
 
@@ -966,8 +990,10 @@ static AttendSpace attend_space(int B, int N, int heads, int group, int dim) {
     s.late = s.first + up(((size_t)B + 1) * 4);
     s.masks = s.late + 256;
     s.part = s.masks + up((size_t)B * N * ((N + 31) / 32) * 4);
-    const int rows = attend_plan(N, heads, group, kAtMaxCtas).blocks * kAtTile, cols = dim > 64 ? 128 : 64;
-    s.total = s.part + (size_t)kAtMaxCtas * 2 * rows * (cols + 2) * 4;
+    const bool two = attend_plan(N, heads, group, kAtMaxCtas).blocks == 2;
+    const int floats = dim > 64 ? (two ? kAtPartFloats<128, 2> : kAtPartFloats<128, 1>)
+                                : (two ? kAtPartFloats<64, 2> : kAtPartFloats<64, 1>);
+    s.total = s.part + (size_t)kAtMaxCtas * 2 * floats * 4;
     return s;
 }
 

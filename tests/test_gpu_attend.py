@@ -124,6 +124,18 @@ def test_counts(form):
     run(make(7, 20, 4, 2, 64, 16, [100, 0, 0, 129, 128, 300, 5], form=form, counts=[20, 0, 1, 3, 19, 7, 12]))
 
 
+@pytest.mark.parametrize("N,heads,kv,B", [(3, 8, 8, 30), (1, 16, 2, 100), (40, 8, 2, 20), (9, 48, 2, 12)])
+def test_many_requests(N, heads, kv, B):
+    """More tiles than there are CTAs: runs that end within items, requests without nodes between."""
+    rng = np.random.default_rng(B)
+    counts = rng.integers(0, N + 1, B)
+    counts[0], counts[1] = N, 0
+    lens = rng.integers(0, 900, B)
+    lens[2] = 3000
+    run(make(B, N, heads, kv, 64, 64, lens, counts=counts, form="dynamic", seed=B))
+    run(make(B, N, heads, kv, 64, 64, lens, seed=B + 1))
+
+
 def test_one_long_sequence():
     run(make(1, 2, 2, 1, 64, 64, [9000], seed=5))
 
