@@ -42,12 +42,15 @@
  *    current for its own launches and puts the caller's current device
  *    back before it returns.
  *  - The linear calls, the draft-side sampler and the calls around a
- *    verification (log probabilities, distillation, cache slots) use
+ *    verification (log probabilities, distillation, cache slots, the paged
+ *    cache, logit adjustment) use
  *    dependent launches:
  *    a launch may be scheduled while the kernel before it on the stream is
  *    ending, and waits for that kernel to complete before it reads or
  *    writes anything.  Stream order is kept; after any other stream
  *    operation (a copy, an event) they are ordinary launches.
+ *  - spec_append_kv, spec_adjust_logits and spec_keep_path take no workspace,
+ *    and their results do not depend on the batch.
  *  - spec_token_logprobs, spec_distill_topk and spec_advance_blocks take no
  *    workspace.  The same call gives the same bits every time.  Ids, ranks
  *    and error bits of a row do not depend on the other rows; its floats
@@ -611,7 +614,7 @@ spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dty
  *               [B, N] with parent_stride >= N: as in the tree verification.
  *  n_nodes      [B] int32 in 0 .. N, or NULL (N each).  Rows from n_b on have
  *               no influence and are not written.
- *  scale        > 0, finite.
+ *  scale        > 0; scale * log2(e) finite.
  *  out          [B, N, q_heads, dim] out, contiguous; must not overlap the
  *               inputs.
  *  Entries that a node does not see have no influence on it, whatever they
@@ -683,7 +686,10 @@ typedef struct {
  *   y = seen ? (x > 0 ? x / repetition : x * repetition) : x
  *   y = y - (frequency * c + presence * [c > 0]) + sum of v's biases
  *   y = -inf where v is not allowed (whatever x is; x is not read there).
- * In 32 bits, rounded once.
+ * In 32 bits, rounded once; x / repetition is taken as a product with 1 /
+ * repetition (2^-23.4 of it) where neither leaves the range of 32 bits.  Where a
+ * request's penalties are 1, 0 and 0, its history and drafted tokens are neither
+ * read nor checked.
  *
  *  logits, out  B * R rows of V elements, row r at r * row_stride (out:
  *               out_stride), bf16 or fp32; out may be logits itself with the

@@ -379,9 +379,10 @@ __device__ __forceinline__ void attend_copy(const AttendArgs& a, const CUtensorM
     constexpr int kLast = S::kStages % 2 == 0 ? S::kStages / 2 : KV ? (S::kStages + 3) / 2 : (S::kStages - 3) / 2;
     for (int j = max(0, J - kLast); j < J; ++j) {
         const int turn = KV ? S::value_turn(j) : S::key_turn(j);
-        mbar_wait(&c->full[turn % S::kStages], (turn / S::kStages) & 1, kDrainNs);
+        if (!mbar_wait(&c->full[turn % S::kStages], (turn / S::kStages) & 1, kDrainNs)) break;
     }
-    for (int i = max(0, qi - kTurns); i < qi; ++i) mbar_wait(&c->q_full[i % kTurns], (i / kTurns) & 1, kDrainNs);
+    for (int i = max(0, qi - kTurns); i < qi; ++i)
+        if (!mbar_wait(&c->q_full[i % kTurns], (i / kTurns) & 1, kDrainNs)) break;
     __syncwarp();
 }
 
@@ -1074,7 +1075,7 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !layout_ok(layout)) return SPEC_ERR_INVALID_ARG;
     if (B < 1 || N < 1 || q_heads < 1 || q_heads % layout->heads || max_blocks < 1 || table_stride < max_blocks ||
         q_request_stride < 0 || q_node_stride < 0 || q_head_stride < 0 ||
-        (parent && parent_stride != 0 && parent_stride < N) || !(scale > 0.0f) || !(scale < INFINITY))
+        (parent && parent_stride != 0 && parent_stride < N) || !(scale > 0.0f) || !(scale * (float)kLog2e < INFINITY))
         return SPEC_ERR_INVALID_ARG;
     const int group = q_heads / layout->heads;
     const int64_t capacity = (int64_t)max_blocks * layout->page_size;
