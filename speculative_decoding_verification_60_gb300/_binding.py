@@ -8,6 +8,7 @@ when the library has not been built: there is no fallback path.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import operator
 import os
@@ -817,11 +818,12 @@ def keep_path(planes, path_nodes, accepted_len, seq_lens, block_table, out=None,
         each = list(map(of, planes))
         if each.count(each[0]) != len(each):
             raise ValueError("planes must have one dtype, shape, device and set of strides")
+    pointers = array.array("Q", map(torch.Tensor.data_ptr, planes))
     each = torch.Size((B,))
     table, M, step = _table(block_table, B, device)
     out = {} if out is None else out
     st = lib.spec_keep_path(
-        (ctypes.c_void_p * len(planes))(*map(torch.Tensor.data_ptr, planes)), len(planes), head.element_size(),
+        pointers.buffer_info()[0], len(planes), head.element_size(),
         ctypes.byref(layout), B, W, _at(path_nodes, "path_nodes", _I32, path_nodes.shape, device),
         _at(accepted_len, "accepted_len", _I32, each, device), _at(seq_lens, "seq_lens", _I32, each, device), table, M,
         step, _to(out, "dev_error", _I32, _ONE, device, stream),

@@ -399,6 +399,7 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
     using S = AttendShape<DT>;
     constexpr bool kBf16 = !std::is_same<T, __half>::value;
     constexpr uint32_t kScores = mma_shape<kBf16>(kAtTile, false), kValues = mma_shape<kBf16>(DT, true);
+    const bool leader = elect_lane();
     uint32_t mended = 0;           // parity of each slot's next mending
     uint32_t weights[2] = {0, 0};  // parity of p_full
     bool ok = true;
@@ -412,30 +413,30 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                 mended ^= 1u << slot;
             }
         }
-        const uint32_t v = mma_operand(ring + slot * S::kTileBytes, S::kBlockBytes);
+        const uint32_t v = uniform(mma_operand(ring + slot * S::kTileBytes, S::kBlockBytes));
 #pragma unroll
         for (int k = 0; k < kAtTile / 16; ++k) {
             if (k % 4 == 0) {  // the weights come in halves
                 if (!attend_wait_warp(c, &c->p_full[w][k / 4], weights[w])) return false;
                 tmem_fence_after();
             }
-            mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, v + k * (2048 / 16), kValues, add || k > 0);
+            mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, v + k * (2048 / 16), kValues, add || k > 0, leader);
         }
         weights[w] ^= 1u;
-        if (last) mma_commit(&c->empty[slot]);
+        if (last) mma_commit(&c->empty[slot], leader);
         return true;
     };
     auto keys = [&](int J) { return &c->full[S::key_turn(J) % S::kStages]; };
     auto keys_parity = [&](int J) { return (uint32_t)(S::key_turn(J) / S::kStages & 1); };
     auto scores = [&](int w, uint32_t q_at, int J) {
-        const uint32_t q = mma_operand(q_at, 16),
-                       k0 = mma_operand(ring + S::key_turn(J) % S::kStages * S::kTileBytes, 16);
+        const uint32_t q = uniform(mma_operand(q_at, 16)),
+                       k0 = uniform(mma_operand(ring + S::key_turn(J) % S::kStages * S::kTileBytes, 16));
 #pragma unroll
         for (int k = 0; k < DT / 16; ++k) {
             const uint32_t at = ((k / 4) * S::kBlockBytes + (k % 4) * 32) / 16;
-            mma_shared(tmem + w * 128, q + at, k0 + at, kScores, k > 0);
+            mma_shared(tmem + w * 128, q + at, k0 + at, kScores, k > 0, leader);
         }
-        mma_commit(&c->s_full[w]);
+        mma_commit(&c->s_full[w], leader);
     };
     if (NB == 1) {
         // s: the tile whose scores come next, p: whose product; p <= s <= p + 2, and s may be an item ahead
@@ -448,7 +449,7 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
             const int w = p & 1;
             if (p < s && __all_sync(0xffffffffu, mbar_test(&c->p_full[w][0], weights[w]))) {
                 ok = product(w, xp.masked(tp), p, tp - xp.t0 >= 2, true, true);
-                if (tp >= xp.t1 - 2) mma_commit(&c->o_full[w]);
+                if (tp >= xp.t1 - 2) mma_commit(&c->o_full[w], leader);
                 ++p;
                 if (++tp == xp.t1) {
                     more_p = walk_p.item(a, &xp);
@@ -460,10 +461,10 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                 ready = qi;  // this item's queries are there
                 tmem_fence_after();
                 scores(s & 1, queries + (qi & 1) * S::kTileBytes, s);
-                mma_commit(&c->empty[S::key_turn(s) % S::kStages]);
+                mma_commit(&c->empty[S::key_turn(s) % S::kStages], leader);
                 ++s;
                 if (++ts == xs.t1) {
-                    mma_commit(&c->q_empty[qi & 1]);
+                    mma_commit(&c->q_empty[qi & 1], leader);
                     ++qi;
                     more_s = walk.item(a, &xs);
                     ts = xs.t0;
@@ -488,22 +489,22 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                     // the values' product goes first: it gives back the slot that a coming tile waits for
                     if (j >= 1) ok = product(w, x.masked(x.t0 + j - 1), J + j - 1, j >= 2, w == 0, w == streams - 1);
                     if (j == n) {
-                        if (ok) mma_commit(&c->o_full[w]);
+                        if (ok) mma_commit(&c->o_full[w], leader);
                         continue;
                     }
                     if (w == 0) ok = ok && attend_wait_warp(c, keys(J + j), keys_parity(J + j));
                     if (!ok) break;
                     scores(w, queries + w * S::kTileBytes, J + j);
                     if (w == streams - 1) {
-                        mma_commit(&c->empty[S::key_turn(J + j) % S::kStages]);
-                        if (j == n - 1) mma_commit(&c->q_empty[0]);
+                        mma_commit(&c->empty[S::key_turn(J + j) % S::kStages], leader);
+                        if (j == n - 1) mma_commit(&c->q_empty[0], leader);
                     }
                 }
             J += n;
         }
     }
     // no product is on its way when tensor memory is freed
-    mma_commit(&c->drain);
+    mma_commit(&c->drain, leader);
     mbar_wait(&c->drain, 0, kDrainNs);
     __syncwarp();
 }

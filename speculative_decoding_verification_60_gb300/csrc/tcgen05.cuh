@@ -100,32 +100,42 @@ __host__ __device__ constexpr uint32_t mma_shape(int n, bool b_across) {
            ((128u >> 4) << 24);
 }
 // These are called by a whole warp with the same values, and one lane, the same
-// every time, issues them: so the operands stay in uniform registers (a single
-// thread's branch took 86 clocks an operation, more than the operation does).
+// every time, issues them (leader: whether this one does): so the operands stay
+// in uniform registers (a single thread's branch took 86 clocks an operation,
+// more than the operation does).
 // d (+)= a b over 16 values of the product's axis; a in shared memory, or in
 // tensor memory (two values a column).
-__device__ __forceinline__ void mma_shared(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_shared(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, bool leader) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
-        "mov.b64 b, {%2, %5};\n\telect.sync _|q, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh)
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh), "r"((uint32_t)leader)
         : "memory");
 }
-__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, bool leader) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh)
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kOperandHigh), "r"((uint32_t)leader)
         : "memory");
 }
 // An arrival on bar when every matrix operation that the warp has issued is done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, bool leader) {
     asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"((uint32_t)leader)
         : "memory");
 }
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// A value that is the same in every lane, as one that the compiler knows to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 }  // namespace sv
