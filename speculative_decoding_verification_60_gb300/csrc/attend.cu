@@ -216,6 +216,9 @@ template <int DT> struct AttendShape {
     static constexpr int kStages = 5 * 128 / DT;             // 160 KiB of keys and values
     static constexpr int kQueryBytes = 2 * kTileBytes;       // two blocks, or two turns of one
     static constexpr int kTiles = kQueryBytes + kStages * kTileBytes;
+    // Weights of a tile that are handed over first.  A short first part starts the product sooner; two streams of many
+    // rows keep the matrix unit busy anyway.
+    __host__ __device__ static constexpr int first(int blocks) { return blocks == 1 ? 32 : 64; }
     // The ring's turns of the J-th tile.  Values are needed later than keys by
     // more than a tile's time, so they come a tile later.  Turn 1 is nobody's.
     __device__ static __forceinline__ int key_turn(int J) { return 2 * J; }
@@ -398,14 +401,16 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                                                 uint32_t ring, uint32_t tmem) {
     using S = AttendShape<DT>;
     constexpr bool kBf16 = !std::is_same<T, __half>::value;
+    constexpr int kFirst = S::first(NB);
     constexpr uint32_t kScores = mma_shape<kBf16>(kAtTile, false), kValues = mma_shape<kBf16>(DT, true);
     const bool leader = elect_lane();
     uint32_t mended = 0;           // parity of each slot's next mending
     uint32_t weights[2] = {0, 0};  // parity of p_full
     bool ok = true;
-    // O_w (+)= P_w V of tile J; `last` stream of the tile gives the slot back
-    auto product = [&](int w, bool masked, int J, bool add, bool wait_values, bool last) {
+    // O_w (+)= P_w V of tile J
+    auto product = [&](int w, bool masked, int J, bool add, bool wait_values) {
         const int slot = S::value_turn(J) % S::kStages;
+        const uint32_t v = uniform(mma_operand(ring + slot * S::kTileBytes, S::kBlockBytes));
         if (wait_values) {
             if (!attend_wait_warp(c, &c->full[slot], S::value_turn(J) / S::kStages & 1)) return false;
             if (masked) {
@@ -413,24 +418,22 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                 mended ^= 1u << slot;
             }
         }
-        const uint32_t v = uniform(mma_operand(ring + slot * S::kTileBytes, S::kBlockBytes));
 #pragma unroll
         for (int k = 0; k < kAtTile / 16; ++k) {
-            if (k % 4 == 0) {  // the weights come in halves
-                if (!attend_wait_warp(c, &c->p_full[w][k / 4], weights[w])) return false;
+            if (k == 0 || k == kFirst / 16) {  // the weights come in two parts
+                if (!attend_wait_warp(c, &c->p_full[w][k != 0], weights[w])) return false;
                 tmem_fence_after();
             }
             mma_tensor(tmem + 256 + w * DT, tmem + w * 128 + k * 8, v + k * (2048 / 16), kValues, add || k > 0, leader);
         }
         weights[w] ^= 1u;
-        if (last) mma_commit(&c->empty[slot], leader);
         return true;
     };
+    auto values_done = [&](int J) { mma_commit(&c->empty[S::value_turn(J) % S::kStages], leader); };
     auto keys = [&](int J) { return &c->full[S::key_turn(J) % S::kStages]; };
     auto keys_parity = [&](int J) { return (uint32_t)(S::key_turn(J) / S::kStages & 1); };
-    auto scores = [&](int w, uint32_t q_at, int J) {
-        const uint32_t q = uniform(mma_operand(q_at, 16)),
-                       k0 = uniform(mma_operand(ring + S::key_turn(J) % S::kStages * S::kTileBytes, 16));
+    auto keys_at = [&](int J) { return uniform(mma_operand(ring + S::key_turn(J) % S::kStages * S::kTileBytes, 16)); };
+    auto scores = [&](int w, uint32_t q, uint32_t k0) {
 #pragma unroll
         for (int k = 0; k < DT / 16; ++k) {
             const uint32_t at = ((k / 4) * S::kBlockBytes + (k % 4) * 32) / 16;
@@ -448,7 +451,10 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
         while (ok && more_p) {
             const int w = p & 1;
             if (p < s && __all_sync(0xffffffffu, mbar_test(&c->p_full[w][0], weights[w]))) {
-                ok = product(w, xp.masked(tp), p, tp - xp.t0 >= 2, true, true);
+                // after a wait that ran out nothing is given back: a second arrival in a slot's turn is a fault
+                ok = product(w, xp.masked(tp), p, tp - xp.t0 >= 2, true);
+                if (!ok) break;
+                values_done(p);
                 if (tp >= xp.t1 - 2) mma_commit(&c->o_full[w], leader);
                 ++p;
                 if (++tp == xp.t1) {
@@ -460,7 +466,7 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
                        __all_sync(0xffffffffu, mbar_test(keys(s), keys_parity(s)))) {
                 ready = qi;  // this item's queries are there
                 tmem_fence_after();
-                scores(s & 1, queries + (qi & 1) * S::kTileBytes, s);
+                scores(s & 1, uniform(mma_operand(queries + (qi & 1) * S::kTileBytes, 16)), keys_at(s));
                 mma_commit(&c->empty[S::key_turn(s) % S::kStages], leader);
                 ++s;
                 if (++ts == xs.t1) {
@@ -487,14 +493,17 @@ __device__ __forceinline__ void attend_products(const AttendArgs& a, AttendWalk 
             for (int j = 0; ok && j <= n; ++j)
                 for (int w = 0; ok && w < streams; ++w) {
                     // the values' product goes first: it gives back the slot that a coming tile waits for
-                    if (j >= 1) ok = product(w, x.masked(x.t0 + j - 1), J + j - 1, j >= 2, w == 0, w == streams - 1);
+                    if (j >= 1) {
+                        ok = product(w, x.masked(x.t0 + j - 1), J + j - 1, j >= 2, w == 0);
+                        if (!ok) break;
+                        if (w == streams - 1) values_done(J + j - 1);
+                    }
                     if (j == n) {
-                        if (ok) mma_commit(&c->o_full[w], leader);
+                        mma_commit(&c->o_full[w], leader);
                         continue;
                     }
-                    if (w == 0) ok = ok && attend_wait_warp(c, keys(J + j), keys_parity(J + j));
-                    if (!ok) break;
-                    scores(w, queries + w * S::kTileBytes, J + j);
+                    if (w == 0 && !(ok = attend_wait_warp(c, keys(J + j), keys_parity(J + j)))) break;
+                    scores(w, uniform(mma_operand(queries + w * S::kTileBytes, 16)), keys_at(J + j));
                     if (w == streams - 1) {
                         mma_commit(&c->empty[S::key_turn(J + j) % S::kStages], leader);
                         if (j == n - 1) mma_commit(&c->q_empty[0], leader);
@@ -675,7 +684,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                         p[k] = Pair<T>::put(e.x, e.y);
                     }
                     tmem_store16(s_at + i * 16, p);
-                    if (i == 1) {  // the product with the tile's first 64 values may begin
+                    if (i == AttendShape<DT>::first(NB) / 32 - 1) {  // the product with the tile's first values may begin
                         tmem_wait_store();
                         tmem_fence_before();
                         attend_arrive_warp(&c->p_full[w][0]);
