@@ -134,14 +134,19 @@ template <> struct Logit<float> {
 // read).  After that, the slice's tokens that anything happens to (seen,
 // drafted, biased) are listed and adjusted in every row, which is still in L2:
 // they are one in a hundred, but some lane of a warp nearly always has one, so
-// adjusting them within the stream took 482 us where this takes 290 (256
-// requests of 9 rows), with or without branches.  Only where the history is
-// long next to the vocabulary, so that many tokens are seen, is it counted
-// first and the counts applied within the stream; then drafted and biased tokens
-// alone are listed.  What a row's path adds to a count is found by walking up
-// the tree.
+// adjusting them within the stream took 482 us, with branches or without, where
+// this took 290 (256 requests of 9 rows).  Only where the history has more than
+// a 16th as many tokens as the vocabulary is it counted first and the counts
+// applied within the stream (12 requests of 60 rows, 7,500 to 30,000 tokens of
+// 50,021: 103 us, 160 without); then drafted and biased tokens alone are listed.
+// What a row's path adds to a count is found by walking up the tree.
+// Bound by latency: 256 rows of 9 at V = 128,256 take 275 us, 0.58 of the copy
+// rate for what has to be moved.  A copy without history, masks and biases runs
+// at 0.82; what is missing is the time in which a CTA's warps wait for each
+// other around its list.  Slices of 8,192 tokens 304 us, 512 threads 308, eight
+// vectors a lane and 3 CTAs an SM 281.
 template <typename T>
-__global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
+__global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
     constexpr int VE = Logit<T>::kVec;
     extern __shared__ __align__(16) uint32_t sh_adjust[];
     __shared__ int sh_listed, sh_task, sh_part, sh_entries;
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
         }
     };
     // parts of the rows: 32 lanes of kAcross vectors
-    constexpr int kAcross = 8, kPart = 32 * kAcross, kParts = kAdSlice / VE / kPart;
+    constexpr int kAcross = 4, kPart = 32 * kAcross, kParts = kAdSlice / VE / kPart;
     constexpr uint32_t kAll = (1u << VE) - 1;
     const int r0 = blockIdx.z * a.rows, r1 = min(r0 + a.rows, rows);
     const int last_word = (a.V - 1) >> 5;

@@ -785,6 +785,27 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
     }
 }
 
+// softmax(scale q K^T) V for blocks of 128 query rows against tiles of 128
+// entries, on the tensor cores: S = Q K^T with both operands in shared memory
+// and S in tensor memory; weights 2^((s - m) c) in 16 bits over S; O += P V with
+// P read from tensor memory and O kept there.  One persistent CTA an SM, its
+// roles on warps of their own, joined by mbarriers: copies, products and softmax
+// overlap, within an item and from one to the next.
+// Bound, with few rows a head, by memory: 64 requests of 5 nodes at lengths of
+// 2048 to 8192, 8 heads of 128, pages of 16: 256 us, 5.3 TB/s or 0.78 of the copy
+// rate; two sequences of 32768 and 131072: 128 us, 0.77 (the runs' ends and the
+// other two launches are 15 us of it).  With many rows by the chain of S, softmax
+// and P V: 32 requests of 60 nodes (480 rows a head): 285 us, 1.13 PFLOP/s or 0.59
+// of the measured bf16 rate; a tile takes 2800 clocks where its products take 2048.
+// Found on the way (us for these three cases): a CTA per query row on CUDA cores
+// 17341, 38333, 93667; this scheme 400, 158, 453; values' products before the next
+// keys are waited for, 32-bit page look-ups a tile ahead and waits timed by the
+// SM's clock (the global timer's read takes longer than the wait) 330, 131, 402; a
+// copy warp each for keys and values 283, 133, 372; products by a whole warp 308,
+// 141, 354; an item's scores beside the last one's products, joins by runs' ends
+// 273, 136, 337; a group's CTAs on neighbouring heads 272, 132, 329; queries by
+// tiled copies from the values' warp, masks read ahead 269, 132, 314; operands
+// known to be uniform 268, 133, 289; a short first part of the weights 256, 128.
 template <typename T, int DT, int NB>
 __global__ void __launch_bounds__(kAtNT, 1)
     k_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qm,
