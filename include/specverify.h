@@ -717,7 +717,8 @@ spec_status spec_adjust_logits(const void* logits, spec_dtype dtype, int B, int 
  * entries stay; a linear draft needs no such call.
  *
  *  planes       HOST array of n_planes device pointers, key and value caches of
- *               all layers, of one layout; read before the call returns.
+ *               all layers, of one layout, none of which overlap; read before
+ *               the call returns.
  *  element_size 1, 2 or 4 bytes.
  *  path_nodes   [B, W], accepted_len [B]: as the tree verification gives them,
  *               on the block_table and seq_lens of its attention.

@@ -819,6 +819,8 @@ def keep_path(planes, path_nodes, accepted_len, seq_lens, block_table, out=None,
         if each.count(each[0]) != len(each):
             raise ValueError("planes must have one dtype, shape, device and set of strides")
     pointers = array.array("Q", map(torch.Tensor.data_ptr, planes))
+    if len(set(pointers)) != len(planes):
+        raise ValueError("planes must be distinct")
     each = torch.Size((B,))
     table, M, step = _table(block_table, B, device)
     out = {} if out is None else out

@@ -136,6 +136,21 @@ def test_many_requests(N, heads, kv, B):
     run(make(B, N, heads, kv, 64, 64, lens, seed=B + 1))
 
 
+@pytest.mark.parametrize("form", ["chain", "tree"])
+def test_the_largest_draft(form):
+    run(make(1, 1024, 2, 2, 64, 64, [70], form=form, seed=13))
+
+
+@pytest.mark.parametrize("heads,N", [(128, 3), (100, 2), (65, 5), (127, 1)])
+def test_many_heads_a_key_head(heads, N):
+    run(make(2, N, heads, 1, 64, 16, [140, 3], form="tree", seed=heads))
+
+
+def test_more_short_requests_than_a_run_keeps_at_hand():
+    rng = np.random.default_rng(14)
+    run(make(1500, 1, 8, 8, 64, 8, rng.integers(0, 12, 1500), counts=rng.integers(0, 2, 1500), seed=14))
+
+
 def test_one_long_sequence():
     run(make(1, 2, 2, 1, 64, 64, [9000], seed=5))
 

@@ -117,3 +117,16 @@ def test_a_graph():
     for x, y in zip(caches, want):
         ref.keep(y, path, accepted, lens, table)
         assert np.array_equal(x.cpu().numpy(), y)
+
+
+def test_planes_that_cannot_be_taken():
+    lens, accepted, table, path, blocks = make(2, 3, 6, 4, [3, 2], [2, 1])
+    c = lambda a: torch.as_tensor(a).cuda()  # noqa: E731
+    args = (c(path), c(accepted), c(lens), c(table))
+    a = torch.randn(blocks, 4, 2, 64, device="cuda")
+    for planes in ([a, a], [a, a[:-1]], [a, a.bfloat16()], [a, torch.empty(blocks, 2, 4, 64, device="cuda").transpose(1, 2)],
+                   [a, a.cpu()], []):
+        with pytest.raises(ValueError):
+            _svp().keep_path(planes, *args)
+    with pytest.raises(ValueError, match="overlap"):
+        _svp().keep_path([a[:1].expand(blocks, -1, -1, -1)], *args)

@@ -102,9 +102,10 @@ def test_attention_refusals(lib):
     for change in (dict(q=None), dict(dtype=1), dict(B=0), dict(N=0), dict(heads=3), dict(heads=0), dict(qr=-8),
                    dict(k=None), dict(v=None), dict(layout=None), dict(table=None), dict(M=0), dict(step=3),
                    dict(lens=None), dict(parent=d, pstep=4), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-                   dict(scale=float("inf")), dict(out=None)):
+                   dict(scale=float("inf")), dict(scale=3e38), dict(out=None)):
         assert bad(**change) == 1, change
-    for change in (dict(N=1025), dict(B=65536), dict(layout=_layout(dim=56)), dict(layout=_layout(dim=136)),
+    for change in (dict(N=1025), dict(B=65536), dict(heads=258), 
+                   dict(M=2**31 - 1, step=2**31 - 1, layout=_layout(page_size=1024, block_stride=2**17)), dict(layout=_layout(dim=56)), dict(layout=_layout(dim=136)),
                    dict(layout=_layout(dim=68)), dict(qn=260), dict(k=ctypes.c_void_p(4104)),
                    dict(q=ctypes.c_void_p(4104)), dict(layout=_layout(entry_stride=132))):
         assert bad(**change) == 2, change
