@@ -632,7 +632,7 @@ spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dty
  *  in their last bits with the other requests of its batch.
  *  workspace    spec_tree_attention_workspace() bytes on 256, for this call
  *               alone until it has completed; needs no initial value.
- *  Limits (SPEC_ERR_UNSUPPORTED): dim a multiple of 8 in 64 .. 128, N <= 1024,
+ *  Limits (SPEC_ERR_UNSUPPORTED): dim a multiple of 8 up to 128, N <= 1024,
  *  q_heads / heads <= 128, B <= 65,535, strides of the caches multiples of 16 bytes, caches on 16 bytes,
  *  q on 16 bytes with strides of multiples of 16 bytes.
  */

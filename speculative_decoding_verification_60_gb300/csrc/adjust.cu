@@ -273,8 +273,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
                 else if (cell && !(cell & rare)) Logit<T>::store(out + at, adjust_value(Logit<T>::load(in + at), cell, q));
                 else out[at] = in[at];
             };
-            if (part == 0)
-                for (int at = lane; at < head; at += 32) single(at);
+            for (int at = part * 32 + lane; at < head; at += 32 * kParts) single(at);
             if (part == kParts - 1 && lane < width - tail) single(tail + lane);
         }
         const int i0 = part * kPart + lane;

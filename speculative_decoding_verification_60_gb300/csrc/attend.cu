@@ -9,7 +9,7 @@ namespace sv {
 
 constexpr int kAtTile = 128;  // cache entries of a tile; query rows of a block
 constexpr int kAtPrepNT = 256;
-constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, products, values, queries and mending
+constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, products, values with queries, mending
 constexpr int kAtMaxCtas = 160;
 constexpr int kAtMaskedTiles = kMaxDraftNodes / kAtTile + 1;  // tiles that reach behind a sequence, at most
 constexpr int kAtPieces = 8;   // CTAs that join a block
@@ -1110,7 +1110,7 @@ extern "C" spec_status spec_tree_attention(const void* q, spec_dtype dtype, int 
         return SPEC_ERR_INVALID_ARG;
     const int group = q_heads / layout->heads;
     const int64_t capacity = (int64_t)max_blocks * layout->page_size;
-    if (B > kMaxRequests || N > kMaxDraftNodes || layout->dim % 8 || layout->dim < 64 || layout->dim > 128 ||
+    if (B > kMaxRequests || N > kMaxDraftNodes || layout->dim % 8 || layout->dim > 128 ||
         group > kAtTile)
         return SPEC_ERR_UNSUPPORTED;
     const AttendPlan plan = attend_plan(N, layout->heads, group, kAtMaxCtas);

@@ -96,7 +96,7 @@ def test_lengths(lens, N):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("heads,kv,dim", [(1, 1, 64), (6, 6, 72), (8, 2, 80), (10, 2, 96), (7, 1, 128), (16, 2, 128)])
+@pytest.mark.parametrize("heads,kv,dim", [(2, 1, 8), (4, 2, 32), (3, 3, 40), (1, 1, 64), (6, 6, 72), (8, 2, 80), (10, 2, 96), (7, 1, 128), (16, 2, 128)])
 def test_heads_and_types(dtype, heads, kv, dim):
     run(make(2, 4, heads, kv, dim, 16, [300, 77], dtype))
 

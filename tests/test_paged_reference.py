@@ -105,7 +105,7 @@ def test_attention_refusals(lib):
                    dict(scale=float("inf")), dict(scale=3e38), dict(out=None)):
         assert bad(**change) == 1, change
     for change in (dict(N=1025), dict(B=65536), dict(heads=258), 
-                   dict(M=2**31 - 1, step=2**31 - 1, layout=_layout(page_size=1024, block_stride=2**17)), dict(layout=_layout(dim=56)), dict(layout=_layout(dim=136)),
+                   dict(M=2**31 - 1, step=2**31 - 1, layout=_layout(page_size=1024, block_stride=2**17)), dict(layout=_layout(dim=136)),
                    dict(layout=_layout(dim=68)), dict(qn=260), dict(k=ctypes.c_void_p(4104)),
                    dict(q=ctypes.c_void_p(4104)), dict(layout=_layout(entry_stride=132))):
         assert bad(**change) == 2, change
