@@ -587,6 +587,8 @@ def _cache(t, name, device=None):
     if device is not None and on != device:
         raise ValueError(f"{name} must be on cuda:{device}")
     blocks, page, heads, dim = shape
+    if t.is_contiguous():
+        return (blocks, page, heads, dim, page * heads * dim, heads * dim, dim)
     if dim > 1 and stride[3] != 1:
         raise ValueError(f"{name} must have contiguous heads")
     steps = [s if n > 1 else 0 for s, n in zip(stride, (blocks, page, heads))]
@@ -600,7 +602,7 @@ def _cache(t, name, device=None):
 
 
 def _caches(k_cache, v_cache, device):
-    """The one layout of a key and a value cache."""
+    """The one layout of a key and a value cache, as _cache's."""
     layout = _cache(k_cache, "k_cache", device)
     if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have one dtype and shape")
@@ -608,21 +610,23 @@ def _caches(k_cache, v_cache, device):
         raise ValueError("k_cache and v_cache must have the same strides")
     if v_cache.get_device() != device:
         raise ValueError(f"v_cache must be on cuda:{device}")
-    return CacheLayout(*layout)
+    return layout
 
 
 def _heads(t, name, dtype, shape, device):
-    """(pointer, strides) of a tensor [..., heads, dim] whose heads are contiguous."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on cuda:{device}" if t.is_cuda else f"{name} must be a CUDA tensor")
-    *stride, last = t.stride()
-    if shape[-1] > 1 and last != 1:
+    """(pointer, strides but the last) of a tensor [..., heads, dim] whose heads are contiguous."""
+    stride = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or (stride[-1] != 1 and shape[-1] > 1):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}" if t.is_cuda else f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} must have contiguous heads")
-    return t.data_ptr(), [s if n > 1 else 0 for s, n in zip(stride, shape)]
+    if 1 in shape:  # a stride that is not used may be any number
+        stride = [s if n > 1 else 0 for s, n in zip(stride, shape)]
+    return t.data_ptr(), stride[:-1]
 
 
 def _table(block_table, B, device):
@@ -652,33 +656,33 @@ def append_kv(q, k, v, positions, slots, k_cache, v_cache, inv_freq=None, q_norm
     float32 or None (no turn); q_norm and k_norm [dim] or None.  Returns a dict: q (turned; out["q"] may be q itself),
     dev_error [1]."""
     lib = load()
-    dt = _half_code(k, "k")
-    if k.dim() != 3 or (q is not None and q.dim() != 3):
+    dt, dtype, shape, device = _half_code(k, "k"), k.dtype, k.shape, k.get_device()
+    if len(shape) != 3 or (q is not None and q.dim() != 3):
         raise ValueError("q, k and v must have shape [T, heads, dim]")
-    device, (T, H, D) = k.get_device(), k.shape
-    if not k.is_cuda:
+    if device < 0:
         raise ValueError("k must be a CUDA tensor")
+    T, H, D = shape
     layout = _caches(k_cache, v_cache, device)
-    if k_cache.dtype is not k.dtype or (layout.heads, layout.dim) != (H, D):
-        raise ValueError(f"caches must be {k.dtype} of {H} heads of {D}")
+    if k_cache.dtype is not dtype or layout[2:4] != (H, D):
+        raise ValueError(f"caches must be {dtype} of {H} heads of {D}")
     out = {} if out is None else out
     q_heads = 0 if q is None else q.shape[1]
     wide = torch.Size((T, q_heads, D))
-    q_ptr, (q_token, q_head) = (None, (0, 0)) if q is None else _heads(q, "q", k.dtype, wide, device)
-    k_ptr, (k_token, k_head) = _heads(k, "k", k.dtype, k.shape, device)
-    v_ptr, (v_token, v_head) = _heads(v, "v", k.dtype, k.shape, device)
+    q_ptr, (q_token, q_head) = (None, (0, 0)) if q is None else _heads(q, "q", dtype, wide, device)
+    k_ptr, (k_token, k_head) = _heads(k, "k", dtype, shape, device)
+    v_ptr, (v_token, v_head) = _heads(v, "v", dtype, shape, device)
     one, each = torch.Size((D,)), torch.Size((T,))
     rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
     if inv_freq is not None and positions is None:
         raise ValueError("positions are required with inv_freq")
     st = lib.spec_append_kv(
         q_ptr, k_ptr, v_ptr, dt, T, q_heads, q_token, q_head, k_token, k_head, v_token, v_head,
-        _at(q_norm, "q_norm", k.dtype, one, device), _at(k_norm, "k_norm", k.dtype, one, device), eps,
+        _at(q_norm, "q_norm", dtype, one, device), _at(k_norm, "k_norm", dtype, one, device), eps,
         _at(positions, "positions", _I32, each, device),
         None if inv_freq is None else _at(inv_freq, "inv_freq", _F32, torch.Size((rot // 2,)), device), rot,
         bool(interleaved), _at(slots, "slots", torch.int64, each, device),
-        None if q is None else _to(out, "q", k.dtype, wide, device, stream), k_cache.data_ptr(), v_cache.data_ptr(),
-        ctypes.byref(layout), _to(out, "dev_error", _I32, _ONE, device, stream),
+        None if q is None else _to(out, "q", dtype, wide, device, stream), k_cache.data_ptr(), v_cache.data_ptr(),
+        ctypes.byref(CacheLayout(*layout)), _to(out, "dev_error", _I32, _ONE, device, stream),
         _handle(stream, device, q, k, v, positions, slots, k_cache, v_cache, inv_freq, q_norm, k_norm, *out.values()))
     if st != SPEC_OK:
         raise SpecError("spec_append_kv", st)
@@ -699,11 +703,12 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_lens, parent=None, n_no
         raise ValueError(f"q must have shape [B, N, q_heads, dim], got {tuple(q.shape)}")
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    device, (B, N, H, D) = q.get_device(), q.shape
+    device, shape, dtype = q.get_device(), q.shape, q.dtype
+    B, N, H, D = shape
     layout = _caches(k_cache, v_cache, device)
-    if k_cache.dtype is not q.dtype or layout.dim != D or H % layout.heads:
-        raise ValueError(f"caches must be {q.dtype} of heads that divide {H}, of {D}")
-    q_ptr, (q_request, q_node, q_head) = _heads(q, "q", q.dtype, q.shape, device)
+    if k_cache.dtype is not dtype or layout[3] != D or H % layout[2]:
+        raise ValueError(f"caches must be {dtype} of heads that divide {H}, of {D}")
+    q_ptr, (q_request, q_node, q_head) = _heads(q, "q", dtype, shape, device)
     table, M, step = _table(block_table, B, device)
     tree, tree_step = _tree(parent, B, N, device)
     out = {} if out is None else out
@@ -711,16 +716,16 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_lens, parent=None, n_no
     if "out" not in out and n_nodes is not None:
         with torch.cuda.stream(stream):  # no effect for None
             out["out"] = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    need = lib.spec_tree_attention_workspace(B, N, H, layout.heads, D)
+    need = lib.spec_tree_attention_workspace(B, N, H, layout[2], D)
     space = out.get("workspace")
     if space is None or space.numel() < need or space.get_device() != device:
         with torch.cuda.stream(stream):
             space = out["workspace"] = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = lib.spec_tree_attention(
-        q_ptr, dt, B, N, H, q_request, q_node, q_head, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(layout),
-        table, M, step, _at(seq_lens, "seq_lens", _I32, each, device), tree, tree_step,
+        q_ptr, dt, B, N, H, q_request, q_node, q_head, k_cache.data_ptr(), v_cache.data_ptr(),
+        ctypes.byref(CacheLayout(*layout)), table, M, step, _at(seq_lens, "seq_lens", _I32, each, device), tree, tree_step,
         _at(n_nodes, "n_nodes", _I32, each, device), D ** -0.5 if scale is None else scale,
-        _to(out, "out", q.dtype, q.shape, device, stream), _to(out, "dev_error", _I32, _ONE, device, stream),
+        _to(out, "out", dtype, shape, device, stream), _to(out, "dev_error", _I32, _ONE, device, stream),
         space.data_ptr(), space.numel(),
         _handle(stream, device, q, k_cache, v_cache, block_table, seq_lens, parent, n_nodes, *out.values()))
     if st != SPEC_OK:

@@ -56,7 +56,16 @@ __global__ void __launch_bounds__(kApNT, kApCtas) k_append(const __grid_constant
     __shared__ float2 turn[2][kApMaxDim / 2];
     __shared__ int64_t sh_entry[2];
     rows_begin();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, extra = a.dev_error ? 1 : 0, ctas = gridDim.x - extra;
+    if ((int)blockIdx.x < extra) {
+        // this CTA looks over all slots for the error word: a launch that clears it first would be on every call's way
+        int64_t most = -1;
+#pragma unroll 16
+        for (int t = tid; t < a.T; t += kApNT) most = max(most, a.slots[t]);
+        const bool bad = __syncthreads_or(most >= a.entries);
+        if (tid == 0) *a.dev_error = bad ? kDevErrCapacity : 0;
+        return;
+    }
     const int per = kApNT / lanes, sub = tid % lanes, first = tid / lanes;
     const int heads = (a.q ? a.q_heads : 0), all = heads + 2 * a.kv_heads;
     // this lane's two vectors; a vector past the head's end is not there
@@ -100,13 +109,13 @@ __global__ void __launch_bounds__(kApNT, kApCtas) k_append(const __grid_constant
         if (has_slot) slot = a.slots[t];
     };
     Two ahead[kApUnroll];
-    int t = blockIdx.x;
+    int t = blockIdx.x - extra;
     if (t < a.T) {
         look(t);
         load(ahead, t, first);
     }
     const int rot = 2 * a.half;
-    for (int buf = 0; t < a.T; t += gridDim.x, buf ^= 1) {
+    for (int buf = 0; t < a.T; t += ctas, buf ^= 1) {
         if (turns_pair) {
             const uint64_t angle = (uint64_t)(int64_t)position * unit;
             float s, c;
@@ -115,9 +124,7 @@ __global__ void __launch_bounds__(kApNT, kApCtas) k_append(const __grid_constant
         }
         if (has_slot) {
             int64_t entry = -1;
-            if (slot >= a.entries) {
-                set_error(a.dev_error, kDevErrCapacity);
-            } else if (slot >= 0) {
+            if (slot >= 0 && slot < a.entries) {
                 const int64_t block = slot / a.page;
                 entry = block * a.block_stride + (slot - block * a.page) * a.entry_stride;
             }
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kApNT, kApCtas) k_append(const __grid_constant
             } else {
 #pragma unroll
                 for (int u = 0; u < kApUnroll; ++u) x[u] = ahead[u];
-                const int next = t + gridDim.x;
+                const int next = t + ctas;
                 if (next < a.T) {
                     look(next);
                     load(ahead, next, first);
@@ -227,10 +234,12 @@ static cudaError_t launch_append(const AppendArgs& a, bool interleaved, cudaStre
     const int slots = turned + (a.dim - 2 * turned * VE + 2 * VE - 1) / (2 * VE);
     int lanes = 1;
     while (lanes < slots) lanes *= 2;
+    // one CTA more for the error word, all of them at once
     int grid;
-    if (!(interleaved ? launch_grid(k_append<T, VE, true>, 0, a.T, &grid, kApNT)
-                      : launch_grid(k_append<T, VE, false>, 0, a.T, &grid, kApNT)))
+    if (!(interleaved ? launch_grid(k_append<T, VE, true>, 0, (long long)a.T + 1, &grid, kApNT)
+                      : launch_grid(k_append<T, VE, false>, 0, (long long)a.T + 1, &grid, kApNT)))
         return cudaErrorUnknown;
+    if (!a.dev_error && grid > a.T) grid = a.T;
     return interleaved ? launch_clusters(k_append<T, VE, true>, grid, 1, kApNT, 0, true, st, a, lanes)
                        : launch_clusters(k_append<T, VE, false>, grid, 1, kApNT, 0, true, st, a, lanes);
 }
@@ -267,8 +276,6 @@ extern "C" spec_status spec_append_kv(const void* q, const void* k, const void* 
     if (T == 0 && !dev_error) return SPEC_OK;
     if (!select_device_of(k_cache)) return SPEC_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const spec_status cleared = clear_error(dev_error, st);
-    if (cleared != SPEC_OK || T == 0) return cleared;
     auto in = [](const void* x) { return static_cast<const uint16_t*>(x); };
     auto out = [](void* x) { return static_cast<uint16_t*>(x); };
     AppendArgs a{in(q), in(k), in(v), T, q_heads, layout->heads, layout->dim, rot_dim / 2,
