@@ -37,6 +37,7 @@ struct AdjustSlice {
     uint16_t* list;
     int *token, *parent;
     int2* entry;
+    uint32_t* kept;  // a dense request's listed tokens' cells
 };
 constexpr int kAdCells = kAdSlice + 8;
 template <int VE> __device__ __forceinline__ int adjust_cell(int at) { return (at % VE) * (kAdSlice / VE + 1) + at / VE; }
@@ -45,8 +46,8 @@ template <int VE> __device__ __forceinline__ int adjust_place(int cell) {
     return (cell - row * (kAdSlice / VE + 1)) * VE + row;
 }
 __host__ __device__ inline size_t adjust_smem(const AdjustArgs& a) {
-    return kAdCells * (a.p.bias_ids ? 8 : 4) + kAdSlice * 2 + (a.p.bias_ids ? (size_t)a.p.bias_count * 8 : 0) +
-           (a.p.drafted ? (size_t)a.R * 8 : 0);
+    return kAdCells * (a.p.bias_ids ? 8 : 4) + kAdSlice * 2 + (a.p.bias_ids ? (size_t)a.p.bias_count * 12 : 0) +
+           (a.p.drafted ? (size_t)a.R * 12 : 0);
 }
 
 // A request's penalties.  A product with 1 / repetition stands for the division
@@ -60,6 +61,17 @@ __device__ __forceinline__ float adjust_value(float x, uint32_t cell, const Pena
     const uint32_t count = cell & kAdCount;
     const float y = cell & (kAdCount | kAdPrompt) ? x * (x > 0.0f ? q.inverse : q.repetition) : x;
     return count ? y - fmaf(q.frequency, (float)count, q.presence) : y;
+}
+// The same from what a dense request's cells become: what is taken off the logit,
+// as a float; the bits of zero stand for a token that was not seen, -0 for a
+// seen one that nothing is taken off.
+__device__ __forceinline__ uint32_t adjust_pack(uint32_t cell, const Penalties& q) {
+    const uint32_t count = cell & kAdCount;
+    const uint32_t less = count ? __float_as_uint(fmaf(q.frequency, (float)count, q.presence)) : 0u;
+    return cell == 0 ? 0u : less == 0 ? 0x80000000u : less;
+}
+__device__ __forceinline__ float adjust_packed(float x, uint32_t pack, const Penalties& q) {
+    return (pack ? x * (x > 0.0f ? q.inverse : q.repetition) : x) - __uint_as_float(pack);
 }
 // The same with all that is rare: a draft's tokens (those on the path to node i
 // count), biases, repetitions that have to be divided by.
@@ -138,7 +150,7 @@ template <> struct Logit<float> {
 // this took 290 (256 requests of 9 rows).  Only where the history has more than
 // a 16th as many tokens as the vocabulary is it counted first and the counts
 // applied within the stream (12 requests of 60 rows, 7,500 to 30,000 tokens of
-// 50,021: 103 us, 160 without); then drafted and biased tokens alone are listed.
+// 50,021: 99 us, 160 without); then drafted and biased tokens alone are listed.
 // What a row's path adds to a count is found by walking up the tree.
 // Bound by latency: 256 rows of 9 at V = 128,256 take 275 us, 0.58 of the copy
 // rate for what has to be moved.  A copy without history, masks and biases runs
@@ -161,6 +173,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
     s.entry = reinterpret_cast<int2*>(s.list + kAdSlice);
     s.token = reinterpret_cast<int*>(s.entry + (p.bias_ids ? p.bias_count : 0));
     s.parent = s.token + a.R;
+    s.kept = reinterpret_cast<uint32_t*>(s.token + (p.drafted ? 2 * a.R : 0));
     int err = 0;
     int rows = p.n_nodes ? p.n_nodes[b] : a.R;
     int told = p.history ? p.history_lens[b] : 0, said = p.history && p.prompt_lens ? p.prompt_lens[b] : 0;
@@ -184,7 +197,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
         err |= kDevErrLength;
         said = said < 0 ? 0 : told;
     }
-    const bool dense = (int64_t)told * 16 > a.V;
+    const bool dense = (int64_t)told * 16 > a.V && !q.divides;
     if (penalties || p.bias_ids)
         for (int i = tid; i < kAdCells / 4; i += kAdNT) reinterpret_cast<uint4*>(s.cell)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) sh_listed = sh_task = sh_part = sh_entries = 0;
@@ -268,9 +281,8 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
         const int vecs = (width - head) / VE, tail = head + vecs * VE;
         if (head | (width - tail)) {
             auto single = [&](int at) {
-                const uint32_t cell = dense ? s.cell[adjust_cell<VE>(at)] : 0u;
                 if (allowed && !((allowed[at >> 5] >> (at & 31)) & 1u)) Logit<T>::store(out + at, -INFINITY);
-                else if (cell && !(cell & rare)) Logit<T>::store(out + at, adjust_value(Logit<T>::load(in + at), cell, q));
+                else if (dense) Logit<T>::store(out + at, adjust_packed(Logit<T>::load(in + at), s.cell[adjust_cell<VE>(at)], q));
                 else out[at] = in[at];
             };
             for (int at = part * 32 + lane; at < head; at += 32 * kParts) single(at);
@@ -308,10 +320,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
                 Logit<T>::get(x[u], y);
                 const int at = head + (i0 + u * 32) * VE;
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const uint32_t cell = s.cell[adjust_cell<VE>(at + k)];
-                    y[k] = cell & rare ? y[k] : adjust_value(y[k], cell, q);
-                }
+                for (int k = 0; k < VE; ++k) y[k] = adjust_packed(y[k], s.cell[adjust_cell<VE>(at + k)], q);
                 x[u] = Logit<T>::put(y);
             }
         }
@@ -335,12 +344,6 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
     }
     if (err) set_error(a.dev_error, err);
     __syncthreads();  // the counts are whole; the rows are written, but for a dense request's
-    if (dense) {
-        for (int t; (t = draw(&sh_part)) < parts;) {
-            row_part(r0 + t / kParts, t % kParts);
-            __syncwarp();
-        }
-    }
     if (!penalties && !p.bias_ids) return;
     if (p.bias_ids) {
         // of the slice's biases of one id the first adds them all up, in order
@@ -367,8 +370,8 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
             s.bias[adjust_cell<VE>(e.x)] = sum;
         }
     }
-    // the list (a dense request's: what the stream left): a thread looks at four cells at a time
-    const uint32_t listable = dense ? rare : 0xffffffffu;
+    // the list (a dense request's: the rare, which the stream leaves): a thread looks at four cells at a time
+    const uint32_t listable = dense ? kAdDrafted | kAdBiased : 0xffffffffu;
     constexpr int kLooks = (kAdCells / 4 + kAdNT - 1) / kAdNT;
     uint32_t hits = 0;
 #pragma unroll
@@ -384,8 +387,25 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
     if (lane == 31) to = atomicAdd(&sh_listed, upto);
     to = __shfl_sync(0xffffffffu, to, 31) + upto - mine;
     for (; hits; hits &= hits - 1) {
-        const int k = __ffs(hits) - 1;
-        s.list[to++] = (uint16_t)adjust_place<VE>((tid + (k >> 2) * kAdNT) * 4 + (k & 3));
+        const int k = __ffs(hits) - 1, i = (tid + (k >> 2) * kAdNT) * 4 + (k & 3);
+        if (dense) s.kept[to] = s.cell[i];
+        s.list[to++] = (uint16_t)adjust_place<VE>(i);
+    }
+    if (dense) {
+        // this thread's cells become what the stream takes off
+#pragma unroll
+        for (int k = 0; k < kLooks; ++k) {
+            const int i = tid + k * kAdNT;
+            if (i >= kAdCells / 4) continue;
+            const uint4 c = reinterpret_cast<const uint4*>(s.cell)[i];
+            auto pack = [&](uint32_t cell) { return cell & listable ? 0u : adjust_pack(cell, q); };
+            reinterpret_cast<uint4*>(s.cell)[i] = make_uint4(pack(c.x), pack(c.y), pack(c.z), pack(c.w));
+        }
+        __syncthreads();
+        for (int t; (t = draw(&sh_part)) < parts;) {
+            row_part(r0 + t / kParts, t % kParts);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // a thread has every `places`-th listed token, in every `phases`-th row
@@ -395,7 +415,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
     const int phases = kAdNT / places, phase = tid / places;
     for (int i = tid - phase * places; i < listed; i += places) {
         const int at = s.list[i], v = v0 + at;
-        const uint32_t cell = s.cell[adjust_cell<VE>(at)];
+        const uint32_t cell = dense ? s.kept[i] : s.cell[adjust_cell<VE>(at)];
         const T* in = in_of(r0 + phase) + at;
         T* out = out_of(r0 + phase) + at;
         const uint32_t* allowed = p.allowed ? allowed_of(r0 + phase) + (v >> 5) : nullptr;
@@ -433,7 +453,7 @@ static cudaError_t launch_adjust(AdjustArgs a, int B, cudaStream_t st) {
     if (!launch_shape(kernel, adjust_smem(most), kAdNT, &shape)) return cudaErrorUnknown;
     const int slices = (a.V + kAdSlice - 1) / kAdSlice;
     // Rows of a request are shared out only where its slices do not fill the GPU.  Each CTA counts the history again:
-    // 12 requests of 60 rows took 113 us in one wave, 103 in two, 118 in four.
+    // 12 requests of 60 rows took 152 us in one wave, 99 in two, 104 in three, 109 in four.
     const long long want = (long long)shape.sms * shape.per_sm, have = (long long)slices * B;
     int parts = (int)(have >= want ? 1 : kAdWaves * want / have);
     parts = parts < a.R ? parts : a.R;
