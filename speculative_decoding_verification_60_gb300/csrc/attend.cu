@@ -13,6 +13,7 @@ constexpr int kAtNT = 384;     // 2 warpgroups for the softmax, warps for keys, 
 constexpr int kAtMaxCtas = 160;
 constexpr int kAtMaskedTiles = kMaxDraftNodes / kAtTile + 1;  // tiles that reach behind a sequence, at most
 constexpr int kAtPieces = 8;   // CTAs that join a block
+constexpr int kAtFew = 4;      // parts that a thread joins by itself
 constexpr int kAtShare = 4;    // CTAs that share a tile's read through L2, at most
 constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 #ifndef SV_LATE_ATTEND
@@ -916,11 +917,50 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta
     const int g1 = attend_group(end - 1, units, groups), count = g1 - g0 + 1;
     constexpr int R = NB * kAtTile;
     auto part = [&](int g) { return attend_part<DT, NB>(a, g, cta, g == g0); };
+    const int pairs = rows * (a.dim / 4), each = (pairs + kAtPieces - 1) / kAtPieces, last = min(pairs, (piece + 1) * each);
+    auto write = [&](int row, int d, float4 o, float l) {
+        const float inv = 1.0f / l;
+        const int node = row / a.group;
+        uint2 v;
+        v.x = Pair<T>::put(o.x * inv, o.y * inv);
+        v.y = Pair<T>::put(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
+                                  d * 4) = v;
+    };
+    if (count <= kAtFew) {
+        // mostly two parts: all that a pair needs is on its way at once
+        for (int k = piece * each + tid; k < last; k += kAtPrepNT) {
+            const int d = k / rows, row = k - d * rows, at = w * kAtTile + row;
+            float2 ml[kAtFew];
+            float4 v[kAtFew];
+#pragma unroll
+            for (int i = 0; i < kAtFew; ++i) {
+                ml[i] = make_float2(kNoMax, 0.0f);
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i >= count) continue;
+                const float* p = part(g0 + i);
+                ml[i] = reinterpret_cast<const float2*>(p)[at];
+                v[i] = reinterpret_cast<const float4*>(p + 2 * kAtPartSums)[d * R + at];
+            }
+            float m = kNoMax, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kAtFew; ++i) m = fmaxf(m, ml[i].x);
+#pragma unroll
+            for (int i = 0; i < kAtFew; ++i) {
+                if (i >= count) continue;
+                const float f = exp2f((ml[i].x - m) * a.c);
+                l += f * ml[i].y;
+                o = make_float4(o.x + f * v[i].x, o.y + f * v[i].y, o.z + f * v[i].z, o.w + f * v[i].w);
+            }
+            write(row, d, o, l);
+        }
+        return;
+    }
     // as many threads for a pair as are to spare, each with every so many-th part
-    const int pairs = rows * (a.dim / 4), each = (pairs + kAtPieces - 1) / kAtPieces;
     int beside_pair = 1;
     while (beside_pair < 32 && beside_pair < count && each * beside_pair * 2 <= kAtPrepNT) beside_pair *= 2;
-    const int lane = tid & (beside_pair - 1), per = kAtPrepNT / beside_pair, last = min(pairs, (piece + 1) * each);
+    const int lane = tid & (beside_pair - 1), per = kAtPrepNT / beside_pair;
     for (int k0 = piece * each; k0 < last; k0 += per) {  // the same turns for every thread
         const int k = min(k0 + tid / beside_pair, last - 1);
         const int d = k / rows, row = k - d * rows;
@@ -950,14 +990,7 @@ __device__ __forceinline__ void attend_join(const AttendArgs& a, int g0, int cta
             o.z += __shfl_xor_sync(0xffffffffu, o.z, s);
             o.w += __shfl_xor_sync(0xffffffffu, o.w, s);
         }
-        const float inv = 1.0f / l;
-        const int node = row / a.group;
-        uint2 v;
-        v.x = Pair<T>::put(o.x * inv, o.y * inv);
-        v.y = Pair<T>::put(o.z * inv, o.w * inv);
-        if (lane == 0)
-            *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.N + node0 + node) * a.q_heads + head * a.group + (row - node * a.group)) * a.dim +
-                                      d * 4) = v;
+        if (lane == 0) write(row, d, o, l);
     }
 }
 
