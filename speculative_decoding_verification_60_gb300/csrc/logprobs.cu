@@ -731,8 +731,8 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int r, const LpR
 
 // A row by a CTA, or by a cluster whose first CTA finishes it.  Bound by
 // memory, one read of the row, while rows are many: 2048 rows of 128256 bf16
-// without alternatives take 86.8 us, 0.89 of the measured copy bandwidth; 3072
-// live rows of 129280 with 8 alternatives 141 us, 0.83.  The rest is the rows'
+// without alternatives take 86.8 us, 0.89 of the measured copy bandwidth; 4096
+// rows of 129280, a quarter skipped, with 8 alternatives 141 us, 0.83.  The rest is the rows'
 // ends, where a CTA has nothing on its way: four CTAs an SM (60 registers, 24 KB
 // of tiles each) cover each other's.  Fewer, larger CTAs with a ring of copies
 // and teams of finishing warps took 137 and 230 us, rows split over CTAs that

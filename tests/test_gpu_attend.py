@@ -253,3 +253,19 @@ def test_another_stream_and_a_graph():
                                               "n_nodes", "scale")])
     # request 1's and 0's nodes now lie where their sequences were
     assert bool(((out["out"].double().cpu() - want).abs() <= bound)[:2].all())
+
+
+def test_two_calls_at_once():
+    """On two streams, with buffers of their own, again and again: the same bits as alone."""
+    cases = [on_gpu(make(4, 5, 8, 2, 128, 16, [900, 30, 2000, 0], seed=20)),
+             on_gpu(make(3, 40, 8, 2, 64, 64, [700, 50, 1500], form="dynamic", seed=21))]
+    want = [_svp().tree_attention(**c)["out"] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [{} for _ in cases]
+    for _ in range(20):
+        for c, out, stream in zip(cases, outs, streams):
+            _svp().tree_attention(**c, out=out, stream=stream)
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out["out"], w) and int(out["dev_error"]) == 0
