@@ -50,6 +50,11 @@ __host__ __device__ inline size_t adjust_smem(const AdjustArgs& a) {
            (a.p.drafted ? (size_t)a.R * 12 : 0);
 }
 
+// Bytes (a multiple of 16, on 16) on their way into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // A request's penalties.  A product with 1 / repetition stands for the division
 // where neither leaves the range of 32 bits: 2^-23.4 of the value at most, and a
 // third of the time that the division takes over a row of seen tokens.
@@ -152,13 +157,13 @@ template <> struct Logit<float> {
 // applied within the stream (12 requests of 60 rows, 7,500 to 30,000 tokens of
 // 50,021: 99 us, 160 without); then drafted and biased tokens alone are listed.
 // What a row's path adds to a count is found by walking up the tree.
-// Bound by latency: 256 rows of 9 at V = 128,256 take 275 us, 0.58 of the copy
-// rate for what has to be moved.  A copy without history, masks and biases runs
-// at 0.82; what is missing is the time in which a CTA's warps wait for each
-// other around its list.  Slices of 8,192 tokens 304 us, 512 threads 308, eight
-// vectors a lane and 3 CTAs an SM 281.
+// Bound by latency: 256 requests of 9 rows at V = 128,256 take 234 us, 0.67 of the
+// copy rate for what has to be moved.  A copy without history, masks and biases
+// runs at 0.86; what is missing is the time in which a CTA's warps wait for each
+// other around its list.  Slices of 8,192 tokens 255 us, four CTAs an SM 242, five
+// of four vectors a lane 257.
 template <typename T>
-__global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
+__global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constant__ AdjustArgs a) {
     constexpr int VE = Logit<T>::kVec;
     extern __shared__ __align__(16) uint32_t sh_adjust[];
     __shared__ int sh_listed, sh_task, sh_part, sh_entries;
@@ -235,6 +240,25 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
         }
     }
 
+    // A row's slice is asked for before the warps get to it (256 requests of 9 rows: 234 us, 281 without), but not
+    // where the mask rules most of it out, nor where the history comes first.
+    if (!dense)
+        for (int r = blockIdx.z * a.rows + (tid >> 5); r < min((int)(blockIdx.z + 1) * a.rows, rows); r += kAdNT / 32) {
+            const int64_t row = (int64_t)b * a.R + r;
+            const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.in) + row * a.in_stride + v0);
+            const uintptr_t begin = (from + 15) & ~(uintptr_t)15, end = (from + (uintptr_t)width * sizeof(T)) & ~(uintptr_t)15;
+            int open = width;
+            if (p.allowed) {
+                const uint32_t* allowed = reinterpret_cast<const uint32_t*>(p.allowed) + row * p.allowed_stride + (v0 >> 5);
+                open = 0;
+#pragma unroll
+                for (int w = 0; w < kAdSlice / 32 / 32; ++w)
+                    if (w * 32 + lane < (width + 31) / 32) open += __popc(allowed[w * 32 + lane]);
+                open = __reduce_add_sync(0xffffffffu, open);
+            }
+            if (lane == 0 && open * 8 > width && end > begin) prefetch_l2(reinterpret_cast<const void*>(begin), (uint32_t)(end - begin));
+        }
+
     // parts of the history
     const int32_t* ids = p.history + b * p.history_stride;
     auto history = [&](int part) {
@@ -256,7 +280,7 @@ __global__ void __launch_bounds__(kAdNT, 5) k_adjust_logits(const __grid_constan
         }
     };
     // parts of the rows: 32 lanes of kAcross vectors
-    constexpr int kAcross = 4, kPart = 32 * kAcross, kParts = kAdSlice / VE / kPart;
+    constexpr int kAcross = 8, kPart = 32 * kAcross, kParts = kAdSlice / VE / kPart;
     constexpr uint32_t kAll = (1u << VE) - 1;
     const int r0 = blockIdx.z * a.rows, r1 = min(r0 + a.rows, rows);
     const int last_word = (a.V - 1) >> 5;
