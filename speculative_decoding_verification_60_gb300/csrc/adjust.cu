@@ -10,7 +10,8 @@ constexpr int kAdSlice = 4096;  // tokens of a CTA's slice
 constexpr int kAdWaves = 2;     // of CTAs that rows are shared out for
 constexpr int kAdMaxBias = 1024;
 constexpr int kAdMaxHistory = 536000000;  // with a path, below 2^29
-constexpr int kAdAhead = 8;     // tokens of the history of a lane on their way at once
+// Tokens of the history of a lane on their way at once: 12 requests of 60 rows 97.5 us, 100 with 8, 99 with 32.
+constexpr int kAdAhead = 16;
 constexpr int kAdHistory = 32 * kAdAhead * 2;  // tokens of the history that a warp takes at a time
 constexpr int kAdFixes = 4;  // adjusted logits of a thread on their way at once
 // A token's cell: how often it was said (the prompt apart), and whether it is in
@@ -155,9 +156,9 @@ template <> struct Logit<float> {
 // this took 290 (256 requests of 9 rows).  Only where the history has more than
 // a 16th as many tokens as the vocabulary is it counted first and the counts
 // applied within the stream (12 requests of 60 rows, 7,500 to 30,000 tokens of
-// 50,021: 99 us, 160 without); then drafted and biased tokens alone are listed.
+// 50,021: 97.5 us, 160 without); then drafted and biased tokens alone are listed.
 // What a row's path adds to a count is found by walking up the tree.
-// Bound by latency: 256 requests of 9 rows at V = 128,256 take 234 us, 0.67 of the
+// Bound by latency: 256 requests of 9 rows at V = 128,256 take 232 us, 0.68 of the
 // copy rate for what has to be moved.  A copy without history, masks and biases
 // runs at 0.86; what is missing is the time in which a CTA's warps wait for each
 // other around its list.  Slices of 8,192 tokens 255 us, four CTAs an SM 242, five
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kAdNT, 3) k_adjust_logits(const __grid_constan
         }
     }
 
-    // A row's slice is asked for before the warps get to it (256 requests of 9 rows: 234 us, 281 without), but not
+    // A row's slice is asked for before the warps get to it (256 requests of 9 rows: 232 us, 281 without), but not
     // where the mask rules most of it out, nor where the history comes first.
     if (!dense)
         for (int r = blockIdx.z * a.rows + (tid >> 5); r < min((int)(blockIdx.z + 1) * a.rows, rows); r += kAdNT / 32) {
