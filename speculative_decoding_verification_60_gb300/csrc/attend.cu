@@ -19,6 +19,11 @@ constexpr long long kAtWaitClocks = 4000000000ll;  // two seconds
 #ifndef SV_LATE_ATTEND
 #define SV_LATE_ATTEND false
 #endif
+// Nanoseconds that a thread loses before each of its waits; a test sets it for a
+// library of its own, so that roles come late to what others wait for.
+#ifndef SV_SLOW_ATTEND
+#define SV_SLOW_ATTEND 0
+#endif
 
 // The query rows of a request and a key head: a block has as many whole nodes as
 // fit in 128 rows, row i * group + j being head h * group + j of its node i.  A
@@ -131,6 +136,8 @@ struct AttendItem {
     int t0, t1, tiles;
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
     __device__ __forceinline__ bool masked(int t) const { return (t + 1) * (int64_t)kAtTile > len; }
+    // Whether values are mended in it.  All items but a run's last one: that may end before the sequence does.
+    __device__ __forceinline__ bool mends() const { return masked(t1 - 1); }
 };
 // Groups that have units: as many as there are units, if those are fewer.
 __device__ __forceinline__ int attend_groups(const AttendArgs& a, int64_t units) {
@@ -255,6 +262,7 @@ __device__ __forceinline__ bool attend_wait(AttendCtrl* c, uint64_t* bar, uint32
         c->dead = 1;
         return false;
     }
+    if (SV_SLOW_ATTEND) __nanosleep(SV_SLOW_ATTEND);
     return mbar_test(bar, parity) || attend_wait_long(c, bar, parity);
 }
 __device__ __forceinline__ bool attend_wait_warp(AttendCtrl* c, uint64_t* bar, uint32_t parity) {
@@ -532,13 +540,12 @@ __device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk
     bool ok = true;
     uint32_t parity = 0;  // of each slot's next tile to mend
     for (int J = 0, item = 0; ok && walk.item(a, &x); ++item) {
+        // An item without mending is the run's last.  Nobody would hold its end back for a warp that still waits for
+        // the item two before, whose phase of `judged` would then be taken for the one not yet over: it has none.
+        if (!x.mends()) break;
         const int turn = item & 1, use = item >> 1;
         // every item's end in order, so that none is taken for another
         if (use > 0 && !attend_wait_warp(c, &c->judged[turn], (use - 1) & 1)) break;
-        if (!x.masked(x.t1 - 1)) {
-            J += x.t1 - x.t0;
-            continue;
-        }
         if (lane == 0) c->poisoned[turn] = 0;
         for (int t = x.t0; ok && t < x.t1; ++t, ++J) {
             if (!x.masked(t)) continue;
@@ -606,7 +613,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         const int live_rows = min(x.nodes - first, a.plan.nodes) * a.group;
         if (NB == 2 && live_rows <= 0) {  // the second block is empty
             J += n;
-            attend_arrive_warp(&c->judged[item & 1]);
+            if (x.mends()) attend_arrive_warp(&c->judged[item & 1]);
             continue;
         }
         const bool live = quarter * 32 < live_rows;  // this warp has a row
@@ -725,7 +732,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         }
         tmem_fence_after();
         // every tile's values are mended by now
-        if (x.masked(x.t1 - 1) && c->poisoned[item & 1])
+        if (x.mends() && c->poisoned[item & 1])
             for (int t = max(x.t0, x.len / kAtTile); t < x.t1; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -733,7 +740,7 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
                     if (attend_sees(a, mask, node, base < -32 ? -32 : (int)base) & c->poison[item & 1][t - x.len / kAtTile][i])
                         total = NAN;
                 }
-        attend_arrive_warp(&c->judged[item & 1]);
+        if (x.mends()) attend_arrive_warp(&c->judged[item & 1]);
         if (live) {
             const bool there = row < live_rows;
             constexpr int kCols = NB == 1 ? DT / 2 : DT;  // of this thread
