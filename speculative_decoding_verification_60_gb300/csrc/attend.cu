@@ -613,7 +613,12 @@ __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk w
         const int live_rows = min(x.nodes - first, a.plan.nodes) * a.group;
         if (NB == 2 && live_rows <= 0) {  // the second block is empty
             J += n;
-            if (x.mends()) attend_arrive_warp(&c->judged[item & 1]);
+            // Nothing else holds this warpgroup back: it must not arrive for an item before the one two before it is over,
+            // or it alone would count for both.
+            if (x.mends()) {
+                if (item >= 2 && !attend_wait_warp(c, &c->judged[item & 1], ((item >> 1) - 1) & 1)) return;
+                attend_arrive_warp(&c->judged[item & 1]);
+            }
             continue;
         }
         const bool live = quarter * 32 < live_rows;  // this warp has a row

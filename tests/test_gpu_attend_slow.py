@@ -70,7 +70,30 @@ def test_many_items(slow, who, N, heads, kv, dim, longest):
     """Runs of many items; of sequences of several tiles, so that runs end within items, some of them after one tile."""
     rng = np.random.default_rng(longest)
     c = make(100, N, heads, kv, dim, 16, rng.integers(0, longest, 100), seed=N + dim)
-    for b in (3, 4, 5, 40, 70):  # what the mending finds must not be lost
-        t = int(c["seq_lens"][b]) + N - 1
-        c["v_cache"][int(c["block_table"][b, t // 16]), t % 16, b % kv, 7] = float("nan")
+    nan_in_nodes(c, (3, 4, 5, 40, 70))
+    alike(slow, who, c)
+
+
+def nan_in_nodes(c, requests):
+    """What the mending finds must not be lost: in the last node of these requests, if they have one."""
+    N, kv = c["q"].shape[1], c["k_cache"].shape[2]
+    for b in requests:
+        n = N if c["n_nodes"] is None else int(c["n_nodes"][b])
+        t = int(c["seq_lens"][b]) + n - 1
+        if n > 0:
+            c["v_cache"][int(c["block_table"][b, t // 16]), t % 16, b % kv, 7] = float("nan")
+
+
+@pytest.mark.parametrize("who", list(WHO))
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("longest", [60, 700])
+@pytest.mark.parametrize("nodes", ["33", "1 to 16", "16 or 17", "0 to 40"])
+def test_empty_second_blocks(slow, who, dim, longest, nodes):
+    """Items whose second block of rows is empty: always, in a share's CTAs alone, and now and then."""
+    rng = np.random.default_rng(dim + longest)
+    B, counts = 120, dict([("33", None), ("1 to 16", rng.integers(1, 17, 120)), ("16 or 17", rng.integers(16, 18, 120)),
+                           ("0 to 40", rng.integers(0, 41, 120))])[nodes]
+    N = {"33": 33, "1 to 16": 32, "16 or 17": 32, "0 to 40": 40}[nodes]
+    c = make(B, N, 64, 8, dim, 16, rng.integers(0, longest, B), form="dynamic", counts=counts, seed=dim)
+    nan_in_nodes(c, range(3, B, 7))
     alike(slow, who, c)
