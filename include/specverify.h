@@ -684,7 +684,8 @@ typedef struct {
  *   seen(v): v in the history or on the path;  c(v): times v occurs in the
  *            history from prompt_lens[b] on, and on the path
  *   y = seen ? (x > 0 ? x / repetition : x * repetition) : x
- *   y = y - (frequency * c + presence * [c > 0]) + sum of v's biases
+ *   y = c > 0 ? y - (frequency * c + presence) : y
+ *   y = y + the sum of v's biases
  *   y = -inf where v is not allowed (whatever x is; x is not read there).
  * In 32 bits, rounded once; x / repetition is taken as a product with 1 /
  * repetition (2^-23.4 of it) where neither leaves the range of 32 bits.  Where a
@@ -699,8 +700,8 @@ typedef struct {
  *  outside 0 .. history_capacity counts as 0, prompt_lens[b] outside
  *  0 .. history_lens[b] as the nearer end, n_nodes[b] outside 0 .. R as R
  *  (SPEC_DEVERR_LENGTH); a parent array that is not a tree (see above) makes
- *  the request's paths empty (SPEC_DEVERR_PARENT).  Parameters that are no
- *  numbers act by the formula.
+ *  the request's paths empty (SPEC_DEVERR_PARENT).  Infinite and NaN parameters
+ *  act by the formula: a penalty on the tokens that it is for, not on others.
  *  B == 0 is valid.  Limits: V <= 524,280, R <= 1024, bias_count <= 1024,
  *  history_capacity <= 536,000,000, B <= 65,535 (SPEC_ERR_UNSUPPORTED).
  */
