@@ -688,9 +688,9 @@ typedef struct {
  *   y = y + the sum of v's biases
  *   y = -inf where v is not allowed (whatever x is; x is not read there).
  * In 32 bits, rounded once; x / repetition is taken as a product with 1 /
- * repetition (2^-23.4 of it) where neither leaves the range of 32 bits.  Where a
- * request's penalties are 1, 0 and 0, its history and drafted tokens are neither
- * read nor checked.
+ * repetition (off by 2^-23 of it at most) where neither leaves the range of 32
+ * bits.  Where a request's penalties are 1, 0 and 0, its history and drafted
+ * tokens are neither read nor checked.
  *
  *  logits, out  B * R rows of V elements, row r at r * row_stride (out:
  *               out_stride), bf16 or fp32; out may be logits itself with the

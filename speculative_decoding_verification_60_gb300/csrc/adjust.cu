@@ -57,8 +57,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 }
 
 // A request's penalties.  A product with 1 / repetition stands for the division
-// where neither leaves the range of 32 bits: 2^-23.4 of the value at most, and a
-// third of the time that the division takes over a row of seen tokens.
+// where neither leaves the range of 32 bits: two roundings, 2^-23 of the value at
+// most, and a third of the time that the division takes over a row of seen tokens.
 struct Penalties {
     float repetition, inverse, frequency, presence;
     bool divides;
