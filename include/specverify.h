@@ -571,9 +571,10 @@ typedef struct {
  *               inv_freq[i], (x, y) <- (x cos - y sin, y cos + x sin).  Pair i
  *               is elements (i, i + rot_dim / 2) of a head, or with
  *               `interleaved` (2i, 2i + 1); elements from rot_dim on stay.
- *               The angle is taken modulo a turn in 64-bit fixed point: exact
- *               to 2^-33 turns at any position.  In a tree, a node's position
- *               is its request's length plus its depth.
+ *               The angle is taken modulo a turn in 64-bit fixed point and
+ *               rounded to 32 bits there: to 2^-25.9 turns (1e-7 radians) at
+ *               any position.  In a tree, a node's position is its request's
+ *               length plus its depth.
  *  slots        [T] int64 cache slots; a negative one stores nothing (its
  *               queries are still turned).  Slots are distinct: an entry named
  *               twice holds either token's values, per 16 bytes.

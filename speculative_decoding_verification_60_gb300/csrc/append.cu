@@ -33,7 +33,9 @@ template <> struct Vec<4> { using type = uint2; };
 // inv / 2 pi as a fraction of a turn, in units of 2^-64 turns.  A position
 // times it, modulo 2^64, is the angle modulo a turn: positions are whole
 // numbers, so nothing is lost however far they are.  The product is taken in
-// two parts (1 / 2 pi to 106 bits), so the unit is right to a few 2^-64.
+// two parts (1 / 2 pi to 106 bits), so the unit is right to 1.5 * 2^-64 and the
+// angle to 2^-32.4 turns at any position.  As a float of its upper half, which is
+// what sine and cosine are taken of in 32 bits, it is right to 2^-25.9.
 __device__ __forceinline__ uint64_t turn_unit(float inv) {
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
     const double x = (double)inv, hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;

@@ -1,5 +1,7 @@
 """How far results of the calls over a paged cache and the logits may be off, as the header states it."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -29,3 +31,40 @@ def test_repetitions(L):
     off = np.abs(y / want - 1)
     assert off.max() <= 2.0**-23 + 2.0**-47
     assert (off[:, L:] == 0).all()
+
+
+def turn(position, inv):
+    """position * inv modulo a turn, in radians within half a turn of 0, from whole numbers."""
+    two_pi = Fraction("6.28318530717958647692528676655900576839433879875021164194988918461563281257241799725606965068423413")
+    turns = Fraction(position) * Fraction(float(inv)) / two_pi
+    return float((turns - round(turns)) * two_pi)
+
+
+@pytest.mark.parametrize("theta", [10000.0, 1e8])
+def test_angles(theta):
+    """The angle to 2^-25.9 turns at any position.  Pairs that are turned to where one of the two nearly vanishes show
+    it: fp16 holds 6e4 sin(delta) to 2^-12 and less there."""
+    import speculative_decoding_verification_60_gb300 as svp
+
+    rng = np.random.default_rng(8)
+    T, D = 400, 128
+    inv = np.array([theta ** (-2.0 * i / D) for i in range(D // 2)], np.float32)
+    positions = rng.integers(0, 2**31, T)
+    positions[:100] = rng.integers(0, 131072, 100)
+    angle = np.array([[turn(int(p), f) for f in inv] for p in positions])
+    x = np.zeros((T, 1, D))
+    x[:, 0, :64], x[:, 0, 64:] = 4e4 * np.sin(angle), 4e4 * np.cos(angle)  # turned, the first is near 0
+    k = torch.tensor(x).half()
+    cache = [torch.zeros(T, 1, 1, D, dtype=torch.float16, device="cuda") for _ in range(2)]
+    got = svp.append_kv(k.cuda(), k.cuda(), k.cuda(), torch.tensor(positions, dtype=torch.int32, device="cuda"),
+                        torch.arange(T, device="cuda"), *cache, torch.tensor(inv, device="cuda"))
+    assert int(got["dev_error"]) == 0
+    a, b = [k.double().numpy()[:, 0, s] for s in (slice(0, 64), slice(64, 128))]
+    want = np.concatenate([a * np.cos(angle) - b * np.sin(angle), b * np.cos(angle) + a * np.sin(angle)], 1)
+    size = np.hypot(a, b)
+    # the angle; sine and cosine to a unit in their last place each (2^-24 below 1); a product rounded to 2^-24; its sum
+    # with the other rounded, and the type
+    far = size * (2 * np.pi * 2.0**-25.9 + (2**0.5 + 1) * 2.0**-24)
+    for turned in (got["q"], cache[0][:, 0]):
+        off = np.abs(turned.double().cpu().numpy()[:, 0] - want)
+        assert (off <= np.tile(far, 2) + np.abs(want) * (2.0**-11 + 2.0**-24) * 1.01 + 2.0**-25).all()
