@@ -577,7 +577,7 @@ typedef struct {
  *               length plus its depth.
  *  slots        [T] int64 cache slots; a negative one stores nothing (its
  *               queries are still turned).  Slots are distinct: an entry named
- *               twice holds either token's values, per 16 bytes.
+ *               twice holds either token's values, per 8 bytes.
  *  out_q        [T, q_heads, dim] out, contiguous; may be q itself when that
  *               is contiguous.
  *  k_cache, v_cache  out: caches of one layout (heads = the kv heads).

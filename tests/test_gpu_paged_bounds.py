@@ -68,3 +68,24 @@ def test_angles(theta):
     for turned in (got["q"], cache[0][:, 0]):
         off = np.abs(turned.double().cpu().numpy()[:, 0] - want)
         assert (off <= np.tile(far, 2) + np.abs(want) * (2.0**-11 + 2.0**-24) * 1.01 + 2.0**-25).all()
+
+
+@pytest.mark.parametrize("pad", [0, 4])  # vectors of 16 bytes, and of 8
+def test_a_slot_named_twice(pad):
+    """Every 8 bytes of the entry are one of the tokens'; the entries beside it stay."""
+    import speculative_decoding_verification_60_gb300 as svp
+
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, H, D = 300, 3, 64
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    k, v = rand(T, H, D + pad)[..., pad:], rand(T, H, D + pad)[..., pad:]
+    caches = [rand(4, 8, H, D) for _ in range(2)]
+    before = [c.clone() for c in caches]
+    got = svp.append_kv(None, k, v, None, torch.full((T,), 13, device="cuda"), *caches)
+    assert int(got["dev_error"]) == 0
+    for x, cache, old in zip((k, v), caches, before):
+        flat, old = cache.flatten(0, 1), old.flatten(0, 1)
+        eights = x.contiguous().view(torch.int64)
+        assert bool((eights == flat[13].contiguous().view(torch.int64)).any(0).all())
+        rest = torch.arange(32, device="cuda") != 13
+        assert torch.equal(flat[rest], old[rest])
