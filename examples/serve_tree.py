@@ -64,7 +64,9 @@ class Server:
         self.accepted = None
         shape = (B * max_blocks, page, model.kv_heads, model.dim)
         self.caches = [[torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)] for _ in model.qkv]
-        self.history, self.said = torch.zeros(B, history, **i32), torch.zeros(B, **i32)
+        # tokens so far; what has no place there goes into one more column, which nobody reads
+        self.tokens, self.said = torch.zeros(B, history + 1, **i32), torch.zeros(B, **i32)
+        self.history = self.tokens[:, :history]
         self.errors = []
 
     def step(self, tokens, repetition=1.1, temperature=0.0, seed=0):
@@ -92,13 +94,16 @@ class Server:
         kept = sv.keep_path([c for both in self.caches for c in both], verified["path_nodes"], self.accepted, self.lens,
                             self.table)
         self.errors += [slots["dev_error"], adjusted["dev_error"], verified["dev_error"], kept["dev_error"]]
-        # what was emitted joins the history
-        new = verified["out_tokens"]
-        at = self.said[:, None] + torch.arange(new.shape[1], device=self.device)
-        keep = (new >= 0) & (at < self.history.shape[1])
-        self.history.scatter_(1, torch.where(keep, at, 0).long(), torch.where(keep, new, self.history[:, :1]))
-        self.said = torch.clamp(self.said + self.accepted + 1, max=self.history.shape[1])
+        self.remember(verified["out_tokens"], self.accepted + 1)
         return verified, adjusted["logits"]
+
+    def remember(self, tokens, counts):
+        """The first counts[b] of tokens[b] join the history, as far as there is room."""
+        most = self.history.shape[1]
+        i = torch.arange(tokens.shape[1], device=self.device)
+        at = torch.where(i < counts[:, None], self.said[:, None] + i, most).clamp_(max=most)
+        self.tokens.scatter_(1, at.long(), tokens)
+        self.said = torch.clamp(self.said + counts, max=most)
 
     def drafts(self, verified, logits):
         """The next trees: the last emitted token, and below every node the best tokens of the row that emitted it."""
