@@ -72,6 +72,8 @@ class Server:
     def step(self, tokens, repetition=1.1, temperature=0.0, seed=0):
         """tokens [B, nodes]: every request's tree, node 0 its last token.  Returns the verification and the logits."""
         m, B, N = self.model, tokens.shape[0], self.nodes
+        if self.accepted is None:  # the first root; later ones are remembered when they are emitted
+            self.remember(tokens[:, :1], torch.ones_like(self.said))
         slots = sv.advance_blocks(self.lens, torch.full_like(self.lens, N), self.table, self.held, self.free,
                                   self.free_count, self.page, B * N, accepted_len=self.accepted)
         self.lens, self.held, self.free_count = slots["seq_lens"], slots["held"], slots["free_count"]
