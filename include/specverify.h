@@ -687,7 +687,7 @@ typedef struct {
  *   y = seen ? (x > 0 ? x / repetition : x * repetition) : x
  *   y = c > 0 ? y - (frequency * c + presence) : y
  *   y = y + the sum of v's biases
- *   y = -inf where v is not allowed (whatever x is; x is not read there).
+ *   y = -inf where v is not allowed, whatever x is.
  * In 32 bits, rounded once; x / repetition is taken as a product with 1 /
  * repetition (off by 2^-23 of it at most) where neither leaves the range of 32
  * bits.  Where a request's penalties are 1, 0 and 0, its history and drafted
