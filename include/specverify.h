@@ -622,7 +622,9 @@ spec_status spec_append_kv(const void* q, const void* k, const void* v, spec_dty
  *  hold.  An entry of this step's nodes whose values are not all finite makes
  *  the whole head row of each node that sees it NaN.  Scores, softmax sums and
  *  outputs are held in 32 bits; the weights of the products with the values are
- *  rounded to the type.
+ *  rounded to the type, half a step of it each.  In fp16 small weights are off
+ *  by more, by 2^-25 of the row's largest: weights of 2^-20 of it, of a long
+ *  tail beside one dominant entry, by 2^-5 of themselves.
  *  A request with seq_lens[b] < 0, n_b outside 0 .. N or more positions than
  *  max_blocks blocks hold (SPEC_DEVERR_LENGTH), a parent array that is not a
  *  tree rooted at 0 with parent[i] < i (SPEC_DEVERR_PARENT), or a block outside

@@ -598,7 +598,11 @@ __device__ __forceinline__ void attend_mend(const AttendArgs& a, AttendWalk walk
 // come from tensor memory, the weights go back over them in 16 bits.  The
 // reference of the exponentials follows the running maximum only when that has
 // grown by more than 8 (in powers of two), so that O is rarely scaled; sums and
-// outputs stay in 32 bits.
+// outputs stay in 32 bits.  Weights are rounded to the type because the matrix
+// unit takes nothing wider beside values of 16 bits: half a step each, so that a
+// result is off by 1.4 times its own rounding.  The row's sum is of the weights
+// before that.  In fp16 weights below 2^-14 of the reference are subnormal, off
+// by 2^-25; the reference is never above the row's maximum.
 template <typename T, int DT, int NB>
 __device__ __forceinline__ void attend_softmax(const AttendArgs& a, AttendWalk walk, AttendCtrl* c, uint32_t tmem) {
     const int w = threadIdx.x >> 7, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;

@@ -89,3 +89,34 @@ def test_a_slot_named_twice(pad):
         assert bool((eights == flat[13].contiguous().view(torch.int64)).any(0).all())
         rest = torch.arange(32, device="cuda") != 13
         assert torch.equal(flat[rest], old[rest])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("at", [0, 19999])
+def test_a_long_tail(dtype, at):
+    """One dominant entry, first or last, beside 20,000 of 2^-20 of its weight: half a step of the type for each weight,
+    and in fp16, where they are subnormal, 2^-25 of the dominant one."""
+    import speculative_decoding_verification_60_gb300 as svp
+
+    L, D, page = 20000, 64, 64
+    g = torch.Generator().manual_seed(10)
+    blocks = L // page + 1
+    k = torch.zeros(blocks * page, 1, D, dtype=dtype)
+    k[:, 0, 0] = -20 * np.log(2)
+    k[at, 0, 0] = 0.0
+    v = (torch.rand(blocks * page, 1, D, generator=g) + 0.5).to(dtype)  # of one sign: errors of one sign add up
+    q = torch.zeros(1, 1, 2, D, dtype=dtype)
+    q[..., 0] = 1.0
+    table = torch.arange(blocks, dtype=torch.int32)[None]
+    args = [q, k.view(blocks, page, 1, D), v.view(blocks, page, 1, D), table, torch.tensor([L - 1], dtype=torch.int32)]
+    got = svp.tree_attention(*[t.cuda() for t in args], scale=1.0)
+    assert int(got["dev_error"]) == 0
+    s = k[:L, 0, 0].double()
+    w = torch.exp(s - s.max())
+    want = (w @ v[:L, 0].double()) / w.sum()
+    u = torch.finfo(dtype).eps / 2
+    # sums of 20,000 terms in 32 bits in an order of the kernel's: at most 2^-24 of the sum a term
+    far = (u * want * 2 + L * 2.0**-24 * want) * 1.01
+    if dtype is torch.float16:
+        far = far + L * 2.0**-25 * v[:L, 0].double().amax(0)
+    assert bool(((got["out"][0, 0].double().cpu() - want).abs() <= far).all())
