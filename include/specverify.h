@@ -669,7 +669,8 @@ typedef struct {
     const int32_t* n_nodes;
     /* [B] each */
     const float *repetition, *frequency, *presence;
-    /* [B, bias_count] ids (-1: none) and what is added to their logits; an id given twice gets both */
+    /* [B, bias_count] ids (-1: none, to fill a list up) and what is added to their logits; an id given twice gets both
+     * (one id's n entries are added up in order by one thread, in n^2 steps: 0.6 ms for 300 of one id) */
     const int32_t* bias_ids;
     const float* bias_values;
     int32_t bias_count;
